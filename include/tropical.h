@@ -10,6 +10,8 @@
  *   tropical_contract_pair         one pairwise einsum built from the three
  *   tropical_tree_run              a contraction tree of pairwise einsums
  *                                  with every intermediate kept on device
+ * and the operators of a training step around them (see "Training
+ * operators" below): layer norm, linear cross entropy, AdamW.
  *
  * Sources (web pages the method is taken from):
  *   [PR35]  tropical-gemm PR #35 "feat: batched GPU ops with DLPack zero-copy
@@ -94,7 +96,9 @@ typedef enum {
  * float32, a max-mul term must exceed the zero element 0 to win.
  */
 typedef enum { TROP_MAX_PLUS = 0, TROP_MIN_PLUS = 1, TROP_MAX_MUL = 2 } trop_semiring;
-typedef enum { TROP_F32 = 0, TROP_I32 = 1 } trop_dtype;
+/* TROP_BF16 is taken by the training operators only (layer norm, linear
+ * cross entropy, AdamW); the contraction calls refuse it. */
+typedef enum { TROP_F32 = 0, TROP_I32 = 1, TROP_BF16 = 2 } trop_dtype;
 
 /* Strides of a batched matrix X[b][r][c] = base[b*batch + r*row + c*col]. */
 typedef struct {
@@ -477,6 +481,165 @@ TROP_API trop_status tropical_tree_run(trop_tree_plan plan, const void* const* i
  * the sum of the intermediate results' sizes, into buf (truncated).
  */
 TROP_API trop_status tropical_tree_describe(trop_tree_plan plan, char* buf, size_t buflen);
+
+/*
+ * ---- Training operators ----
+ *
+ * What a program that trains (max, +) layers needs around the product and
+ * its backward: a normalisation (a max-plus output is defined up to the
+ * constants added to its operands), a loss over a large label set with its
+ * gradient, and the step that applies the gradients.  Matrices are float32
+ * or bfloat16; statistics, sums, states and master weights are float32.  A
+ * bfloat16 output is rounded once (to nearest even) from a float32 value.
+ * Matrices are row-major with unit stride along a row and any row stride
+ * >= the row's length (in elements); every element alignment is served.
+ * Outputs must not overlap inputs or each other unless stated.  No kernel
+ * uses atomics: a call gives the same bits every time on one device model.
+ * Their kernels are a code object of their own, loaded once per device by
+ * the first such call (or tropical_train_init, which code that captures
+ * graphs calls beforehand).
+ */
+TROP_API trop_status tropical_train_init(int device);
+
+/*
+ * Layer norm of the rows of x (rows x cols, row stride ldx):
+ *   mean[r] = sum_c x[r][c] / cols
+ *   rstd[r] = 1 / sqrt(sum_c (x[r][c] - mean[r])^2 / cols + eps)
+ *   y[r][c] = (x[r][c] - mean[r]) rstd[r] gamma[c] + beta[c]
+ * The variance is summed about the mean.  A non-finite element makes its own
+ * row's outputs non-finite and no other's.
+ * x, y: `dtype` (y has row stride ldy and may be x itself, with ldy == ldx).
+ * gamma, beta: cols elements of `param_dtype` (float32 or `dtype`), either
+ *   may be NULL (1 and 0).
+ * mean, rstd: float32, rows elements each, either may be NULL.
+ * rows, cols >= 0; eps >= 0 and finite.
+ * Errors: TROP_ERR_INVALID_ARGUMENT (bad enum, negative size, row stride
+ *   below cols, eps), TROP_ERR_NOT_DEVICE_MEMORY, TROP_ERR_HIP.
+ */
+TROP_API trop_status tropical_layer_norm_forward(trop_dtype dtype, trop_dtype param_dtype, const void* x,
+                                        int64_t ldx, const void* gamma, const void* beta, float eps, void* y,
+                                        int64_t ldy, float* mean, float* rstd, int64_t rows, int64_t cols,
+                                        void* stream);
+
+/*
+ * Workspace (bytes) of tropical_layer_norm_backward for this shape: the
+ * partial column sums of dgamma and dbeta (with_params != 0), else 0.
+ * Host-only.  Errors: TROP_ERR_INVALID_ARGUMENT (negative size, NULL bytes).
+ */
+TROP_API trop_status tropical_layer_norm_backward_workspace_size(int64_t rows, int64_t cols, int with_params,
+                                                        size_t* bytes);
+
+/*
+ * Backward of tropical_layer_norm_forward.  With h = (x - mean) rstd and
+ * w = dy gamma (gamma 1 when NULL):
+ *   dx[r][c]  = rstd[r] (w - sum_c w / cols - h sum_c (w h) / cols)
+ *   dgamma[c] = sum_r dy[r][c] h[r][c],  dbeta[c] = sum_r dy[r][c]
+ * x, mean, rstd: the forward's input and float32 statistics.  dy, dx have
+ * `dtype`; dx may be dy itself (lddx == lddy).  dgamma, dbeta have
+ * `param_dtype`.  dx, dgamma and dbeta may each be NULL (not computed).
+ * With rows == 0, dgamma and dbeta are zero.  The column sums are added in
+ * a fixed order.
+ * workspace: at least tropical_layer_norm_backward_workspace_size bytes
+ *   (NULL when neither dgamma nor dbeta is asked for), used only by work on
+ *   `stream`.
+ * Errors: as the forward, and TROP_ERR_WORKSPACE_TOO_SMALL.
+ */
+TROP_API trop_status tropical_layer_norm_backward(trop_dtype dtype, trop_dtype param_dtype, const void* dy,
+                                         int64_t lddy, const void* x, int64_t ldx, const float* mean,
+                                         const float* rstd, const void* gamma, void* dx, int64_t lddx,
+                                         void* dgamma, void* dbeta, int64_t rows, int64_t cols,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One AdamW step over many tensors at once, in place.  With g the gradient
+ * and q the float32 weight (master when given, else param):
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   q = (1 - lr weight_decay) q
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * every operation one IEEE float32 operation in this order (the scalar
+ * factors are computed in float64 and rounded once).  param then holds q,
+ * rounded to `dtype`.
+ */
+typedef struct {
+    void* param;        /* elements of `dtype`; read unless master is given */
+    const void* grad;   /* elements of `dtype`                              */
+    float* exp_avg;     /* m                                                */
+    float* exp_avg_sq;  /* v                                                */
+    float* master;      /* float32 weights, or NULL                         */
+    int64_t elements;   /* 0: skipped                                       */
+} trop_adamw_tensor;
+
+/*
+ * The same with m and v held in 8 bits: blocks of TROP_ADAMW_BLOCK
+ * consecutive elements (the last one may be short) share a float32 scale a.
+ *   exp_avg code c in [-127, 127] stands for a (c/127) |c/127|,
+ *     a = max |m| of the block, c = sign(m) rint(127 sqrt(|m| / a))
+ *   exp_avg_sq code c in [0, 255] stands for a (c/255)^4,
+ *     a = max v of the block, c = rint(255 (v / a)^(1/4)), at least 1 for
+ *     v > 0 (so that no positive v is taken for zero)
+ * A block of zeros has scale 0.  The step uses m and v before they are
+ * rounded to codes.  A non-finite gradient makes its block's state NaN.
+ */
+#define TROP_ADAMW_BLOCK 256
+typedef struct {
+    void* param;
+    const void* grad;
+    int8_t* exp_avg;
+    float* exp_avg_scale;     /* ceil(elements / TROP_ADAMW_BLOCK) values */
+    uint8_t* exp_avg_sq;
+    float* exp_avg_sq_scale;  /* likewise */
+    float* master;
+    int64_t elements;
+} trop_adamw8_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step; /* counted from 1 */
+} trop_adamw_hyper;
+
+/*
+ * tensors: `count` host entries, copied into the launches' arguments (tens
+ * of tensors a launch).  dtype: float32 or bfloat16.  No two tensors may
+ * overlap.  All checks of all tensors precede the first launch.
+ * Errors: TROP_ERR_INVALID_ARGUMENT (bad enum, NULL table, negative count or
+ *   size, betas outside [0, 1), step < 1, lr, eps or weight_decay negative
+ *   or not finite), TROP_ERR_NOT_DEVICE_MEMORY, TROP_ERR_HIP.
+ */
+TROP_API trop_status tropical_adamw_step(trop_dtype dtype, const trop_adamw_tensor* tensors, int64_t count,
+                                const trop_adamw_hyper* hyper, void* stream);
+TROP_API trop_status tropical_adamw8_step(trop_dtype dtype, const trop_adamw8_tensor* tensors, int64_t count,
+                                 const trop_adamw_hyper* hyper, void* stream);
+
+/*
+ * The values that 8-bit states stand for (for checkpoints and inspection):
+ * m into exp_avg_values[i], v into exp_avg_sq_values[i], float32 tensors of
+ * tensors[i].elements; an entry may be NULL (skipped).  param, grad and
+ * master of the entries are not looked at.
+ */
+TROP_API trop_status tropical_adamw8_unpack(const trop_adamw8_tensor* tensors, int64_t count,
+                                   float* const* exp_avg_values, float* const* exp_avg_sq_values, void* stream);
+
+/* Kernel families of the training operators, counted apart from trop_stats. */
+typedef enum {
+    TROP_T_LAYER_NORM_FORWARD = 0,
+    TROP_T_LAYER_NORM_BACKWARD = 1,  /* row gradients and partial column sums, and their sum */
+    TROP_T_CE_PACK = 2,              /* kept tokens listed, operands packed */
+    TROP_T_CE_LOGITS = 3,            /* logits of a piece and what is made of them */
+    TROP_T_CE_MERGE = 4,             /* statistics and partial gradients joined */
+    TROP_T_CE_GRAD = 5,              /* the gradients' products */
+    TROP_T_ADAMW = 6,
+    TROP_T_FAMILIES = 7
+} trop_train_family;
+
+typedef struct {
+    uint64_t module_loads;
+    uint64_t launches_total;
+    uint64_t launches[TROP_T_FAMILIES];
+} trop_train_stats;
+
+/* Copy the process-wide counters of the training operators (tropical_reset_stats
+ * zeroes their launch counters too). */
+TROP_API trop_status tropical_get_train_stats(trop_train_stats* out);
 
 /* Text of the calling thread's last error ("" if none). */
 TROP_API const char* tropical_last_error(void);

@@ -10,6 +10,7 @@ Output tensors are allocated with torch when the caller passes none; torch
 is used only for device memory and streams.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -22,10 +23,12 @@ STATUS_NAMES = {0: "TROP_OK", 1: "TROP_ERR_INVALID_ARGUMENT", 2: "TROP_ERR_UNSUP
                 3: "TROP_ERR_NOT_DEVICE_MEMORY", 4: "TROP_ERR_WORKSPACE_TOO_SMALL",
                 5: "TROP_ERR_HIP"}
 SEMIRINGS = {"max_plus": 0, "min_plus": 1, "max_mul": 2}
-F32, I32 = 0, 1
+F32, I32, BF16 = 0, 1, 2
 KERNEL_FAMILIES = ["gemm_tiled", "gemm_simple", "fill", "gather_copy", "gather_tiled",
                    "gather_naive", "gather_reduce", "gemm_backward", "gemm_splitk_merge",
                    "argmax_compose", "gemm_domain"]
+TRAIN_FAMILIES = ["layer_norm_forward", "layer_norm_backward", "ce_pack", "ce_logits", "ce_merge", "ce_grad",
+                  "adamw"]
 MAX_DIMS = 8
 
 
@@ -50,6 +53,26 @@ class trop_tree_step(ctypes.Structure):
 class trop_stats(ctypes.Structure):
     _fields_ = [("module_loads", ctypes.c_uint64), ("launches_total", ctypes.c_uint64),
                 ("launches", ctypes.c_uint64 * 11)]
+
+
+class trop_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "exp_avg", "exp_avg_sq", "master")] + [
+        ("elements", ctypes.c_int64)]
+
+
+class trop_adamw8_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "exp_avg", "exp_avg_scale", "exp_avg_sq",
+                                               "exp_avg_sq_scale", "master")] + [("elements", ctypes.c_int64)]
+
+
+class trop_adamw_hyper(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int64)]
+
+
+class trop_train_stats(ctypes.Structure):
+    _fields_ = [("module_loads", ctypes.c_uint64), ("launches_total", ctypes.c_uint64),
+                ("launches", ctypes.c_uint64 * 7)]
 
 
 _lib = None
@@ -116,6 +139,20 @@ def lib():
     vp, i64 = ctypes.c_void_p, ctypes.c_int64
     L.tropical_gemm_strided_batched.argtypes = [ctypes.c_int, ctypes.c_int, vp, trop_strides, vp, trop_strides,
                                                 vp, trop_strides, vp, i64, i64, i64, i64, vp]
+    f32 = ctypes.c_float
+    L.tropical_train_init.argtypes = [i32]
+    L.tropical_layer_norm_forward.argtypes = [i32, i32, vp, i64, vp, vp, f32, vp, i64, vp, vp, i64, i64, vp]
+    L.tropical_layer_norm_backward_workspace_size.argtypes = [i64, i64, i32, PP(sz)]
+    L.tropical_layer_norm_backward.argtypes = [i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, i64,
+                                               vp, sz, vp]
+    L.tropical_adamw_step.argtypes = [i32, PP(trop_adamw_tensor), i64, PP(trop_adamw_hyper), vp]
+    L.tropical_adamw8_step.argtypes = [i32, PP(trop_adamw8_tensor), i64, PP(trop_adamw_hyper), vp]
+    L.tropical_adamw8_unpack.argtypes = [PP(trop_adamw8_tensor), i64, PP(vp), PP(vp), vp]
+    L.tropical_get_train_stats.argtypes = [PP(trop_train_stats)]
+    for fn in ("tropical_train_init", "tropical_layer_norm_forward", "tropical_layer_norm_backward_workspace_size",
+               "tropical_layer_norm_backward",
+               "tropical_adamw_step", "tropical_adamw8_step", "tropical_adamw8_unpack", "tropical_get_train_stats"):
+        getattr(L, fn).restype = ctypes.c_int
     _lib = L
     return L
 
@@ -503,6 +540,250 @@ def tropical_tree_run(plan, inputs, out=None, argmax=False, workspace=None, stre
                                  _stream(stream))
     _check(st, "tropical_tree_run")
     return out, ams
+
+
+# ---------------------------------------------------------------------------
+# training operators
+
+_TRAIN_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _tdt(t, what):
+    dt = _TRAIN_DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
+    return dt
+
+
+def _row_stride(t, what):
+    """Row stride of a 2-d tensor with unit stride along its rows."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-d, got {t.dim()}-d")
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{what} must have unit stride along its rows")
+    return ld if rows > 1 else max(ld, cols)
+
+
+def _flat(t, what, n, dtype):
+    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous 1-d {dtype} tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _out_like(t, shape, dtype, device, what):
+    """The caller's output tensor, checked, or a new one for True / None."""
+    if t is None or t is True:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}")
+    return t
+
+
+def _workspace(workspace, nbytes, device):
+    """(tensor to keep alive, pointer, bytes) of a workspace given or made."""
+    if workspace is None:
+        if not nbytes:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _on_stream(fn):
+    """With a `stream` argument, run the call with that stream current, so
+    that the outputs and the workspace it allocates belong to that stream."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def tropical_train_init(device=0):
+    _check(lib().tropical_train_init(int(device)), "tropical_train_init")
+
+
+@_on_stream
+def tropical_layer_norm_forward(x, gamma=None, beta=None, eps=1e-5, y=None, mean=None, rstd=None):
+    """Layer norm of the rows of x (rows, cols): (y, mean, rstd).
+
+    x: float32 or bfloat16, unit stride along the rows, any row stride.
+    gamma, beta: cols elements, float32 or x's type (one type), or None.
+    mean, rstd: float32 statistics for the backward.  Outputs are allocated
+    when not given; y may be x.
+    """
+    dt = _tdt(x, "x")
+    ldx = _row_stride(x, "x")
+    rows, cols = x.shape
+    par = gamma if gamma is not None else beta
+    pdt = _tdt(par, "gamma and beta") if par is not None else F32
+    pg = _flat(gamma, "gamma", cols, par.dtype) if gamma is not None else None
+    pb = _flat(beta, "beta", cols, par.dtype) if beta is not None else None
+    y = _out_like(y, (rows, cols), x.dtype, x.device, "y")
+    mean = _out_like(mean, (rows,), torch.float32, x.device, "mean")
+    rstd = _out_like(rstd, (rows,), torch.float32, x.device, "rstd")
+    st = lib().tropical_layer_norm_forward(dt, pdt, x.data_ptr(), ldx, pg, pb, eps, y.data_ptr(),
+                                           _row_stride(y, "y"), _flat(mean, "mean", rows, torch.float32),
+                                           _flat(rstd, "rstd", rows, torch.float32), rows, cols,
+                                           _stream_ptr(None, x))
+    if st != OK:
+        _check(st, "tropical_layer_norm_forward")
+    return y, mean, rstd
+
+
+def tropical_layer_norm_backward_workspace_size(rows, cols, with_params=True):
+    nb = ctypes.c_size_t(0)
+    _check(lib().tropical_layer_norm_backward_workspace_size(int(rows), int(cols), 1 if with_params else 0,
+                                                             ctypes.byref(nb)),
+           "tropical_layer_norm_backward_workspace_size")
+    return nb.value
+
+
+@_on_stream
+def tropical_layer_norm_backward(dy, x, mean, rstd, gamma=None, dx=True, dgamma=True, dbeta=True, workspace=None):
+    """Gradients of a layer norm: (dx, dgamma, dbeta).
+
+    x, mean, rstd: the forward's.  dx (x's type), dgamma and dbeta (gamma's
+    type, float32 without gamma): True to allocate, a tensor to fill, or None
+    to skip.  dx may be dy.  The workspace is allocated with torch when not
+    given.
+    """
+    dt = _tdt(x, "x")
+    rows, cols = x.shape
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must have the shape and type of x")
+    ptype = gamma.dtype if gamma is not None else torch.float32
+    pdt = _tdt(gamma, "gamma") if gamma is not None else F32
+    pg = _flat(gamma, "gamma", cols, ptype) if gamma is not None else None
+    dev = x.device
+    dx = _out_like(dx, (rows, cols), x.dtype, dev, "dx") if dx is not None else None
+    dgamma = _out_like(dgamma, (cols,), ptype, dev, "dgamma") if dgamma is not None else None
+    dbeta = _out_like(dbeta, (cols,), ptype, dev, "dbeta") if dbeta is not None else None
+    need = 0
+    if workspace is None and (dgamma is not None or dbeta is not None):
+        need = tropical_layer_norm_backward_workspace_size(rows, cols)
+    workspace, wp, wn = _workspace(workspace, need, dev)
+    st = lib().tropical_layer_norm_backward(
+        dt, pdt, dy.data_ptr(), _row_stride(dy, "dy"), x.data_ptr(), _row_stride(x, "x"),
+        _flat(mean, "mean", rows, torch.float32), _flat(rstd, "rstd", rows, torch.float32), pg,
+        dx.data_ptr() if dx is not None else None, _row_stride(dx, "dx") if dx is not None else 0,
+        _flat(dgamma, "dgamma", cols, ptype) if dgamma is not None else None,
+        _flat(dbeta, "dbeta", cols, ptype) if dbeta is not None else None, rows, cols, wp, wn,
+        _stream_ptr(None, x))
+    if st != OK:
+        _check(st, "tropical_layer_norm_backward")
+    return dx, dgamma, dbeta
+
+
+def _adamw_table(kind, columns, params, grads, masters):
+    """The ctypes table of `kind` and the elements' type.  columns: (field,
+    tensors, type, elements per scale or 0)."""
+    n = len(params)
+    if not n:
+        return (kind * 1)(), F32
+    dtype = params[0].dtype
+    dt = _tdt(params[0], "params")
+    columns = [("param", params, dtype, 0), ("grad", grads, dtype, 0)] + columns
+    if masters is not None:
+        columns = columns + [("master", masters, torch.float32, 0)]
+    for name, ts, ty, block in columns:
+        if len(ts) != n:
+            raise ValueError(f"{name}: {len(ts)} tensors for {n} parameters")
+    rows = []
+    ptrs = {}
+    counts = [p.numel() for p in params]
+    for name, ts, ty, block in columns:
+        col = []
+        for t, e in zip(ts, counts):
+            want = (e + block - 1) // block if block else e
+            if t.dtype != ty or t.numel() != want or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {ty} tensors of the parameters' sizes")
+            col.append(t.data_ptr())
+        ptrs[name] = col
+    names = [f[0] for f in kind._fields_[:-1]]
+    cols = [ptrs.get(name, [None] * n) for name in names]
+    rows = list(zip(*cols, counts))
+    return (kind * n)(*rows), dt
+
+
+def _adamw_hyper(lr, beta1, beta2, eps, weight_decay, step):
+    return trop_adamw_hyper(lr, beta1, beta2, eps, weight_decay, step)
+
+
+@_on_stream
+def tropical_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr, beta1=0.9, beta2=0.999, eps=1e-8,
+                        weight_decay=0.0, step=1, masters=None):
+    """One AdamW step over lists of tensors, in place (see
+    include/tropical.h).  params and grads: float32 or bfloat16, one type;
+    states and masters float32; all contiguous.  step counts from 1."""
+    f = torch.float32
+    table, dt = _adamw_table(trop_adamw_tensor, [("exp_avg", exp_avgs, f, 0), ("exp_avg_sq", exp_avg_sqs, f, 0)],
+                             params, grads, masters)
+    h = _adamw_hyper(lr, beta1, beta2, eps, weight_decay, step)
+    st = lib().tropical_adamw_step(dt, table, len(params), ctypes.byref(h),
+                                   _stream_ptr(None, params[0]) if params else None)
+    if st != OK:
+        _check(st, "tropical_adamw_step")
+
+
+ADAMW_BLOCK = 256  # TROP_ADAMW_BLOCK in include/tropical.h
+
+
+def _adamw8_columns(m, m_scales, v, v_scales):
+    f = torch.float32
+    return [("exp_avg", m, torch.int8, 0), ("exp_avg_scale", m_scales, f, ADAMW_BLOCK),
+            ("exp_avg_sq", v, torch.uint8, 0), ("exp_avg_sq_scale", v_scales, f, ADAMW_BLOCK)]
+
+
+@_on_stream
+def tropical_adamw8_step(params, grads, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, lr, beta1=0.9,
+                         beta2=0.999, eps=1e-8, weight_decay=0.0, step=1, masters=None):
+    """tropical_adamw_step with 8-bit states: int8 exp_avgs and uint8
+    exp_avg_sqs with a float32 scale for each ADAMW_BLOCK elements (zeros
+    everywhere are the state before the first step)."""
+    table, dt = _adamw_table(trop_adamw8_tensor, _adamw8_columns(exp_avgs, exp_avg_scales, exp_avg_sqs,
+                                                                 exp_avg_sq_scales), params, grads, masters)
+    h = _adamw_hyper(lr, beta1, beta2, eps, weight_decay, step)
+    st = lib().tropical_adamw8_step(dt, table, len(params), ctypes.byref(h),
+                                    _stream_ptr(None, params[0]) if params else None)
+    if st != OK:
+        _check(st, "tropical_adamw8_step")
+
+
+@_on_stream
+def tropical_adamw8_unpack(exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, exp_avg_values=None,
+                           exp_avg_sq_values=None):
+    """The float32 values that 8-bit states stand for: two lists of tensors
+    (allocated when not given)."""
+    n = len(exp_avgs)
+    if exp_avg_values is None:
+        exp_avg_values = [torch.empty(t.shape, dtype=torch.float32, device=t.device) for t in exp_avgs]
+    if exp_avg_sq_values is None:
+        exp_avg_sq_values = [torch.empty(t.shape, dtype=torch.float32, device=t.device) for t in exp_avg_sqs]
+    if not n:
+        return exp_avg_values, exp_avg_sq_values
+    # the values' tensors stand where a step's float32 parameters would
+    table, _ = _adamw_table(trop_adamw8_tensor, _adamw8_columns(exp_avgs, exp_avg_scales, exp_avg_sqs,
+                                                                exp_avg_sq_scales), exp_avg_values,
+                            exp_avg_sq_values, None)
+    mv = (ctypes.c_void_p * n)(*[r.param for r in table])
+    vv = (ctypes.c_void_p * n)(*[r.grad for r in table])
+    st = lib().tropical_adamw8_unpack(table, n, mv, vv, _stream_ptr(None, exp_avgs[0]))
+    if st != OK:
+        _check(st, "tropical_adamw8_unpack")
+    return exp_avg_values, exp_avg_sq_values
+
+
+def tropical_get_train_stats():
+    s = trop_train_stats()
+    _check(lib().tropical_get_train_stats(ctypes.byref(s)), "tropical_get_train_stats")
+    return {"module_loads": s.module_loads, "launches_total": s.launches_total,
+            "launches": {name: s.launches[i] for i, name in enumerate(TRAIN_FAMILIES)}}
 
 
 def tropical_get_stats():

@@ -1,9 +1,11 @@
 """Build libtropical.so: gfx950 code object + host runtime.
 
-1. hipcc --genco compiles csrc/kernels/kernels.hip for gfx950 only.  Packed
-   FP32 instructions are disabled (-packed-fp32-ops) and nothing enables
-   fast math, FTZ or FMA contraction: every tropical term is one IEEE op.
-2. The code object is embedded into the library with an assembler .incbin.
+1. hipcc --genco compiles csrc/kernels/kernels.hip (the contraction) and
+   csrc/kernels/train_kernels.hip (the training operators) for gfx950 only,
+   one code object each.  Packed FP32 instructions are disabled
+   (-packed-fp32-ops) and nothing enables fast math, FTZ or FMA contraction:
+   every tropical term is one IEEE op.
+2. The code objects are embedded into the library with an assembler .incbin.
 3. The host runtime (C++17, HIP runtime API only, no kernels) is compiled
    with g++ and linked against libamdhip64; its one source with device data
    (the allocation-free call's scratch array) is compiled by hipcc.
@@ -31,7 +33,7 @@ DEVICE_FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17",
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wextra", "-Wno-unused-parameter",
               "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]
 RUNTIME_SRCS = ["status.cpp", "module.cpp", "validate.cpp", "gemm.cpp", "gather.cpp", "contract.cpp",
-                "backward.cpp", "tree.cpp"]
+                "backward.cpp", "tree.cpp", "train_module.cpp", "layer_norm.cpp", "adamw.cpp"]
 # host runtime sources with device data (compiled by hipcc, gfx950 only)
 RUNTIME_HIP_SRCS = ["noalloc.hip"]
 
@@ -43,9 +45,9 @@ def _run(cmd):
     return res
 
 
-def build_code_object(out=None):
+def build_code_object(out=None, source="kernels.hip"):
     out = out or os.path.join(BUILD, "tropical_kernels.co")
-    src = os.path.join(HERE, "kernels", "kernels.hip")
+    src = os.path.join(HERE, "kernels", source)
     _run([HIPCC, *DEVICE_FLAGS, "--genco", "--no-gpu-bundle-output", src, "-o", out])
     return out
 
@@ -54,6 +56,7 @@ def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     co = os.path.join(BUILD, "tropical_kernels.co")
+    train_co = os.path.join(BUILD, "train_kernels.co")
     blob = os.path.join(BUILD, "co_blob.S")
 
     def compile_host(name):
@@ -69,24 +72,26 @@ def build(verbose=False):
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, len(RUNTIME_SRCS) + 2)) as ex:
-        fut_co = ex.submit(build_code_object, co)
+        fut_co = [ex.submit(build_code_object, co), ex.submit(build_code_object, train_co, "train_kernels.hip")]
         fut_hip = [ex.submit(compile_hip_host, n) for n in RUNTIME_HIP_SRCS]
         objs = list(ex.map(compile_host, RUNTIME_SRCS))
         objs += [f.result() for f in fut_hip]
-        fut_co.result()
+        for f in fut_co:
+            f.result()
 
     with open(blob, "w") as f:
-        f.write(
-            "    .section .rodata\n"
-            "    .balign 4096\n"
-            "    .globl trop_code_object\n"
-            "    .type trop_code_object, @object\n"
-            "trop_code_object:\n"
-            f"    .incbin \"{co}\"\n"
-            "    .globl trop_code_object_end\n"
-            "trop_code_object_end:\n"
-            "    .byte 0\n"
-            "    .section .note.GNU-stack,\"\",@progbits\n")
+        f.write("    .section .rodata\n")
+        for symbol, path in (("trop_code_object", co), ("trop_train_code_object", train_co)):
+            f.write(
+                "    .balign 4096\n"
+                f"    .globl {symbol}\n"
+                f"    .type {symbol}, @object\n"
+                f"{symbol}:\n"
+                f"    .incbin \"{path}\"\n"
+                f"    .globl {symbol}_end\n"
+                f"{symbol}_end:\n"
+                "    .byte 0\n")
+        f.write("    .section .note.GNU-stack,\"\",@progbits\n")
     blob_obj = os.path.join(BUILD, "co_blob.o")
     _run(["gcc", "-c", blob, "-o", blob_obj])
     tmp = LIB + ".tmp"

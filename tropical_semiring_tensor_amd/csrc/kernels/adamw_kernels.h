@@ -1,0 +1,190 @@
+// AdamW over many tensors in one launch.
+//
+// Per element a dozen operations on 28 bytes (32-bit state) or 16 (8-bit
+// state): bound by HBM.  A launch's argument block lists up to 72 (56)
+// tensors with the running count of their 4096-element chunks; a workgroup
+// takes one chunk and finds its tensor by bisection over those counts
+// (scalar loads of the argument block), so small and large tensors fill the
+// device together.  All arithmetic is one IEEE float32 operation at a time,
+// in the order the header states.
+#pragma once
+#include "train_common.h"
+
+namespace trop {
+
+template <typename PARAMS>
+__device__ __forceinline__ int find_tensor(const PARAMS& p, uint32_t chunk) {
+    int lo = 0, hi = p.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (chunk < p.chunk_end[mid])
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ void adamw_element(const TropAdamwScalars& s, float g, float& m, float& v, float& q) {
+    m = m * s.beta1 + g * s.one_minus_beta1;
+    v = v * s.beta2 + (g * g) * s.one_minus_beta2;
+    q = q * s.keep - (m / (sqrtf(v) * s.root + s.eps)) * s.step_size;
+}
+
+// MASTER: q is the float32 master weight, param only receives its rounding.
+template <typename T, bool MASTER>
+__device__ __forceinline__ void adamw_body(const TropAdamwParams& p) {
+    const int ti = find_tensor(p, blockIdx.x);
+    const TropAdamwEntry& e = p.t[ti];
+    const int64_t base = (int64_t)(blockIdx.x - (ti ? p.chunk_end[ti - 1] : 0u)) * TROP_ADAMW_CHUNK;
+    constexpr int U = TROP_ADAMW_CHUNK / (256 * 4);
+    FloatVec<4> q[U], m[U], v[U];
+    typename VecOf<T, 4>::raw g[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = base + (u * 256 + threadIdx.x) * 4;
+        g[u] = load_row<T, 4>(static_cast<const T*>(e.grad), c, e.n);
+        m[u] = load_row<float, 4>(e.m, c, e.n);
+        v[u] = load_row<float, 4>(e.v, c, e.n);
+        if constexpr (MASTER)
+            q[u] = load_row<float, 4>(e.master, c, e.n);
+        else
+            q[u] = to_float<T, 4>(load_row<T, 4>(static_cast<const T*>(e.param), c, e.n));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = base + (u * 256 + threadIdx.x) * 4;
+        const FloatVec<4> gf = to_float<T, 4>(g[u]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mm = m[u][i], vv = v[u][i], qq = q[u][i];
+            adamw_element(p.s, gf[i], mm, vv, qq);
+            m[u][i] = mm;
+            v[u][i] = vv;
+            q[u][i] = qq;
+        }
+        if (c < e.n) {
+            store_row<float, 4>(e.m, c, e.n, m[u]);
+            store_row<float, 4>(e.v, c, e.n, v[u]);
+            if constexpr (MASTER) store_row<float, 4>(e.master, c, e.n, q[u]);
+            store_row<T, 4>(static_cast<T*>(e.param), c, e.n, from_float<T, 4>(q[u]));
+        }
+    }
+}
+
+// Values of the 8-bit codes (t4: (c / 255)^4 by two squarings).
+__device__ __forceinline__ float adamw8_m(float code, float a) {
+    const float t = code * (1.0f / 127.0f);
+    return (a * t) * fabsf(t);
+}
+__device__ __forceinline__ float adamw8_v(float code, float a) {
+    const float t = code * (1.0f / 255.0f), t2 = t * t;
+    return a * (t2 * t2);
+}
+// Codes of m and v in a block of scale a (0: every element is zero).  A NaN
+// ratio takes code 0: the block's scale is NaN then, and so are its values.
+__device__ __forceinline__ int adamw8_code_m(float m, float a) {
+    const float r = fabsf(m) / (a > 0.f ? a : 1.f);
+    const float c = rintf(sqrtf(r) * 127.0f);
+    const int k = c <= 127.f ? (int)c : 0;
+    return m < 0.f ? -k : k;
+}
+__device__ __forceinline__ int adamw8_code_v(float v, float a) {
+    const float r = v / (a > 0.f ? a : 1.f);
+    const float c = rintf(sqrtf(sqrtf(r)) * 255.0f);
+    const int k = c <= 255.f ? (int)c : 0;
+    return v > 0.f ? (k > 1 ? k : 1) : 0;
+}
+
+// One wave per block of 256 elements, four a lane: the block's scale is a
+// wave reduction, no LDS.
+template <typename T, bool MASTER>
+__device__ __forceinline__ void adamw8_body(const TropAdamw8Params& p) {
+    const int ti = find_tensor(p, blockIdx.x);
+    const TropAdamw8Entry& e = p.t[ti];
+    const int64_t base = (int64_t)(blockIdx.x - (ti ? p.chunk_end[ti - 1] : 0u)) * TROP_ADAMW_CHUNK;
+    constexpr int U = TROP_ADAMW_CHUNK / (256 * 4);
+    FloatVec<4> q[U];
+    typename VecOf<T, 4>::raw g[U];
+    typename VecOf<int8_t, 4>::raw mc[U];
+    typename VecOf<uint8_t, 4>::raw vc[U];
+    float ma[U], va[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = base + (u * 256 + threadIdx.x) * 4;
+        g[u] = load_row<T, 4>(static_cast<const T*>(e.grad), c, e.n);
+        mc[u] = load_row<int8_t, 4>(e.m, c, e.n);
+        vc[u] = load_row<uint8_t, 4>(e.v, c, e.n);
+        ma[u] = c < e.n ? e.m_scale[c / TROP_ADAMW_BLOCK_ELEMS] : 0.f;
+        va[u] = c < e.n ? e.v_scale[c / TROP_ADAMW_BLOCK_ELEMS] : 0.f;
+        if constexpr (MASTER)
+            q[u] = load_row<float, 4>(e.master, c, e.n);
+        else
+            q[u] = to_float<T, 4>(load_row<T, 4>(static_cast<const T*>(e.param), c, e.n));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = base + (u * 256 + threadIdx.x) * 4;
+        const FloatVec<4> gf = to_float<T, 4>(g[u]);
+        float m[4], v[4];
+        float am = 0.f, av = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = adamw8_m((float)mc[u][i], ma[u]);
+            v[i] = adamw8_v((float)vc[u][i], va[u]);
+            float qq = q[u][i];
+            adamw_element(p.s, gf[i], m[i], v[i], qq);
+            q[u][i] = qq;
+            if (c + i >= e.n) m[i] = v[i] = 0.f;
+            am = nan_max(am, fabsf(m[i]));
+            av = nan_max(av, v[i]);
+        }
+        am = wave_nan_max(am);
+        av = wave_nan_max(av);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mc[u][i] = (int8_t)adamw8_code_m(m[i], am);
+            vc[u][i] = (uint8_t)adamw8_code_v(v[i], av);
+        }
+        if (c < e.n) {
+            store_row<int8_t, 4>(e.m, c, e.n, mc[u]);
+            store_row<uint8_t, 4>(e.v, c, e.n, vc[u]);
+            if ((threadIdx.x & 63) == 0) {
+                e.m_scale[c / TROP_ADAMW_BLOCK_ELEMS] = am;
+                e.v_scale[c / TROP_ADAMW_BLOCK_ELEMS] = av;
+            }
+            if constexpr (MASTER) store_row<float, 4>(e.master, c, e.n, q[u]);
+            store_row<T, 4>(static_cast<T*>(e.param), c, e.n, from_float<T, 4>(q[u]));
+        }
+    }
+}
+
+// The codes' values: m into `param`, v into `master` (either may be null).
+__device__ __forceinline__ void adamw8_unpack_body(const TropAdamw8Params& p) {
+    const int ti = find_tensor(p, blockIdx.x);
+    const TropAdamw8Entry& e = p.t[ti];
+    const int64_t base = (int64_t)(blockIdx.x - (ti ? p.chunk_end[ti - 1] : 0u)) * TROP_ADAMW_CHUNK;
+    constexpr int U = TROP_ADAMW_CHUNK / (256 * 4);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = base + (u * 256 + threadIdx.x) * 4;
+        if (c >= e.n) return;
+        FloatVec<4> o;
+        if (e.param) {
+            const auto k = load_row<int8_t, 4>(e.m, c, e.n);
+            const float a = e.m_scale[c / TROP_ADAMW_BLOCK_ELEMS];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = adamw8_m((float)k[i], a);
+            store_row<float, 4>(static_cast<float*>(e.param), c, e.n, o);
+        }
+        if (e.master) {
+            const auto k = load_row<uint8_t, 4>(e.v, c, e.n);
+            const float a = e.v_scale[c / TROP_ADAMW_BLOCK_ELEMS];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = adamw8_v((float)k[i], a);
+            store_row<float, 4>(e.master, c, e.n, o);
+        }
+    }
+}
+
+}  // namespace trop

@@ -1,0 +1,75 @@
+// Types and wave reductions shared by the training operators' kernels.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "../train_params.h"
+
+namespace trop {
+
+using bf16 = __bf16;
+
+// N consecutive elements at any element-aligned address.  The target's
+// unaligned access mode serves these as single wide accesses, so one path
+// covers every row stride and offset.
+template <typename T, int N>
+struct VecOf {
+    typedef T raw __attribute__((ext_vector_type(N)));
+    typedef raw type __attribute__((aligned(sizeof(T))));
+};
+template <int N>
+using FloatVec = typename VecOf<float, N>::raw;
+
+template <typename T, int N>
+__device__ __forceinline__ typename VecOf<T, N>::raw load_vec(const T* p) {
+    return *reinterpret_cast<const typename VecOf<T, N>::type*>(p);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_vec(T* p, typename VecOf<T, N>::raw v) {
+    *reinterpret_cast<typename VecOf<T, N>::type*>(p) = v;
+}
+template <typename T, int N>
+__device__ __forceinline__ FloatVec<N> to_float(typename VecOf<T, N>::raw v) {
+    return __builtin_convertvector(v, FloatVec<N>);
+}
+template <typename T, int N>
+__device__ __forceinline__ typename VecOf<T, N>::raw from_float(FloatVec<N> v) {
+    return __builtin_convertvector(v, typename VecOf<T, N>::raw);
+}
+
+// Elements [c, c + N) of a row of n elements, zeros past its end.
+template <typename T, int N>
+__device__ __forceinline__ typename VecOf<T, N>::raw load_row(const T* row, int64_t c, int64_t n) {
+    if (c + N <= n) return load_vec<T, N>(row + c);
+    typename VecOf<T, N>::raw v = {};
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        if (c + e < n) v[e] = row[c + e];
+    return v;
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T* row, int64_t c, int64_t n, typename VecOf<T, N>::raw v) {
+    if (c + N <= n) {
+        store_vec<T, N>(row + c, v);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        if (c + e < n) row[c + e] = v[e];
+}
+
+// Butterfly reductions: every lane ends with the wave's result, the same
+// order of operations in every lane pair, so all lanes hold the same bits.
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+    return x;
+}
+// Maximum that keeps a NaN (fmaxf would drop it).
+__device__ __forceinline__ float nan_max(float a, float b) { return (a > b || a != a) ? a : b; }
+__device__ __forceinline__ float wave_nan_max(float x) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x = nan_max(x, __shfl_xor(x, o, 64));
+    return x;
+}
+
+}  // namespace trop

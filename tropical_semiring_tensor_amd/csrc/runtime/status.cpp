@@ -3,7 +3,7 @@
 #include <cstring>
 #include <string>
 
-#include "internal.h"
+#include "train.h"
 
 namespace trop {
 
@@ -49,4 +49,5 @@ extern "C" trop_status tropical_get_stats(trop_stats* out) {
 extern "C" void tropical_reset_stats(void) {
     trop::g_launches_total.store(0);
     for (int i = 0; i < TROP_K_FAMILIES; ++i) trop::g_launches[i].store(0);
+    trop::reset_train_launches();
 }

@@ -1,0 +1,70 @@
+// Internal interfaces of the training operators' host runtime.
+#pragma once
+#include <exception>
+#include <string>
+
+#include "../train_params.h"
+#include "internal.h"
+
+namespace trop {
+
+// Kernels of the training code object.  A family has one entry point per
+// (element type, weights' type), in ln_index / ce_index order.
+enum TrainKernelId : int {
+    TK_LN_FWD_WAVE = 0,  // + ln_index: f32 f32, bf16 bf16, bf16 f32
+    TK_LN_FWD_BLOCK = TK_LN_FWD_WAVE + 3,
+    TK_LN_FWD_WIDE = TK_LN_FWD_BLOCK + 3,
+    TK_LN_FWD_LOOP = TK_LN_FWD_WIDE + 3,
+    TK_LN_BWD_WAVE = TK_LN_FWD_LOOP + 3,
+    TK_LN_BWD_BLOCK = TK_LN_BWD_WAVE + 3,
+    TK_LN_BWD_WIDE = TK_LN_BWD_BLOCK + 3,
+    TK_LN_BWD_LOOP = TK_LN_BWD_WIDE + 3,
+    TK_LN_COLUMNS = TK_LN_BWD_LOOP + 3,  // + (bf16 ? 1 : 0)
+    TK_LN_MERGE = TK_LN_COLUMNS + 2,
+    TK_ADAMW = TK_LN_MERGE + 2,  // + 2 (bf16) + (master ? 1 : 0)
+    TK_ADAMW8 = TK_ADAMW + 4,
+    TK_ADAMW8_UNPACK = TK_ADAMW8 + 4,
+    TK_COUNT
+};
+
+// Current device with the training code object loaded on it.
+trop_status train_device(int* dev);
+trop_status train_launch(int dev, TrainKernelId id, trop_train_family fam, int64_t grid, uint32_t block,
+                         const void* params, hipStream_t stream);
+int train_cu_count(int dev);
+void reset_train_launches();
+
+inline size_t elem_size(trop_dtype dt) { return dt == TROP_BF16 ? 2 : 4; }
+
+// `p` must hold a row-major rows x cols matrix of row stride ld (all >= 1,
+// ld >= cols) in device memory of `dev`, aligned to its elements.
+trop_status check_matrix(const void* p, int dev, int64_t rows, int64_t cols, int64_t ld, size_t elem_bytes,
+                         const char* what);
+
+// Extents and allocations of one call: a pointer inside the range that the
+// call checked last needs no further query (many tensors share a segment).
+class SpanChecker {
+   public:
+    explicit SpanChecker(int dev) : dev_(dev) {}
+    trop_status check(const void* p, int64_t elems, size_t elem_bytes, const char* what, int64_t index);
+
+   private:
+    int dev_;
+    uintptr_t lo_ = 1, hi_ = 0;
+};
+
+// A C entry point's body: no C++ exception leaves the library.
+template <typename F>
+trop_status guarded(const char* what, F&& body) {
+    try {
+        return body();
+    } catch (const std::exception& e) {
+        try {
+            return fail(TROP_ERR_HIP, std::string(what) + ": " + e.what());
+        } catch (...) {
+            return TROP_ERR_HIP;
+        }
+    }
+}
+
+}  // namespace trop

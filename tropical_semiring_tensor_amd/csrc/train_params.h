@@ -1,0 +1,90 @@
+// Argument blocks of the training operators' kernels, passed by value to
+// every launch (host runtime and device code agree on the layout; no pointer
+// in them is kept after a call returns).
+#pragma once
+#include <stdint.h>
+
+// ---- layer norm ------------------------------------------------------------
+// Partial column sums (dgamma, dbeta) a backward call makes at most.
+#define TROP_LN_MAX_PARTS 512
+// Columns a wave / 256 threads / 1024 threads hold in registers (16 each).
+#define TROP_LN_COLS_WAVE 1024
+#define TROP_LN_COLS_BLOCK 4096
+#define TROP_LN_COLS_WIDE 16384
+
+struct TropLayerNormParams {
+    const void* x;
+    const void* dy;     // backward
+    const void* gamma;  // may be null
+    const void* beta;   // forward, may be null
+    void* y;            // forward: y; backward: dx (may be null)
+    float* mean;        // forward: written, may be null; backward: read
+    float* rstd;
+    float* part;        // backward: [2][parts][cols], null without dgamma and dbeta
+    int64_t ldx, lddy, ldy;
+    int64_t rows, cols;
+    float eps, inv_cols;
+    int32_t parts;      // workgroups of the backward
+    int32_t pad_;
+};
+
+struct TropLayerNormMergeParams {
+    const float* part;
+    void* dgamma;  // may be null
+    void* dbeta;   // may be null
+    int64_t cols;
+    int32_t parts;
+    int32_t pad_;
+};
+
+// ---- AdamW -----------------------------------------------------------------
+// Elements of one workgroup's chunk of a tensor, and of a scale's block.
+#define TROP_ADAMW_CHUNK 4096
+#define TROP_ADAMW_BLOCK_ELEMS 256
+// Tensors of one launch (a 4 KiB argument block).
+#define TROP_ADAMW_TENSORS 72
+#define TROP_ADAMW8_TENSORS 56
+
+struct TropAdamwScalars {
+    float beta1, one_minus_beta1, beta2, one_minus_beta2;
+    float keep;       // 1 - lr weight_decay
+    float step_size;  // lr / (1 - beta1^step)
+    float root;       // 1 / sqrt(1 - beta2^step)
+    float eps;
+};
+
+struct TropAdamwEntry {
+    void* param;
+    const void* grad;
+    float* m;
+    float* v;
+    float* master;
+    int64_t n;
+};
+
+struct TropAdamwParams {
+    TropAdamwScalars s;
+    int32_t count, pad_;
+    uint32_t chunk_end[TROP_ADAMW_TENSORS];  // chunks of this tensor and all before it
+    TropAdamwEntry t[TROP_ADAMW_TENSORS];
+};
+
+struct TropAdamw8Entry {
+    void* param;        // unpack: float values of m (may be null)
+    const void* grad;
+    int8_t* m;
+    float* m_scale;
+    uint8_t* v;
+    float* v_scale;
+    float* master;      // unpack: float values of v (may be null)
+    int64_t n;
+};
+
+struct TropAdamw8Params {
+    TropAdamwScalars s;
+    int32_t count, pad_;
+    uint32_t chunk_end[TROP_ADAMW8_TENSORS];
+    TropAdamw8Entry t[TROP_ADAMW8_TENSORS];
+};
+
+static_assert(sizeof(TropAdamwParams) <= 4096 && sizeof(TropAdamw8Params) <= 4096, "kernel argument block");
