@@ -551,6 +551,63 @@ TROP_API trop_status tropical_layer_norm_backward(trop_dtype dtype, trop_dtype p
                                          void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Softmax cross entropy of tokens over a label set, from hidden states and
+ * the label matrix, without the logits ever being kept:
+ *   l[n][v] = sum_d x[n][d] w[v][d]
+ *   lse[n]  = log sum_v exp(l[n][v]),  loss[n] = lse[n] - l[n][target[n]]
+ * A token whose target is `ignore_index` or outside [0, vocab) does not
+ * count: its loss and lse are 0, its row of grad_x is 0, and whatever its
+ * row of x holds (NaN included) reaches no output.
+ *
+ * x (tokens x width, row stride ldx), w (vocab x width, row stride ldw):
+ *   `dtype` (float32 or bfloat16) both.  float32 products keep float32
+ *   accuracy; sums are float32 for both.
+ * target: target_bytes 4 (int32) or 8 (int64), tokens elements.
+ * loss, lse: float32, tokens elements each.
+ * workspace: at least tropical_linear_cross_entropy_workspace_size bytes of
+ *   device memory, used only by work on `stream`.
+ * tokens, width, vocab >= 0 (vocab >= 1 and width >= 1 when tokens > 0).
+ * Errors: TROP_ERR_INVALID_ARGUMENT, TROP_ERR_NOT_DEVICE_MEMORY,
+ *   TROP_ERR_WORKSPACE_TOO_SMALL, TROP_ERR_HIP.
+ */
+TROP_API trop_status tropical_linear_cross_entropy_forward(trop_dtype dtype, const void* x, int64_t ldx,
+                                                  const void* w, int64_t ldw, const void* target,
+                                                  int target_bytes, int64_t ignore_index, float* loss,
+                                                  float* lse, int64_t tokens, int64_t width, int64_t vocab,
+                                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace (bytes) of the linear cross entropy calls for this shape:
+ * backward == 0 for the forward, else for the backward.  It holds packed
+ * operands, per-tile softmax statistics and, for the backward, one piece of
+ * the label set's gradients of the logits; never tokens x vocab values.
+ * The size serves every row stride and alignment.  Host-only.
+ * Errors: TROP_ERR_INVALID_ARGUMENT (bad dtype, negative size, NULL bytes).
+ */
+TROP_API trop_status tropical_linear_cross_entropy_workspace_size(trop_dtype dtype, int64_t tokens, int64_t width,
+                                                         int64_t vocab, int backward, size_t* bytes);
+
+/*
+ * Gradients of sum_n grad_loss[n] loss[n]:
+ *   G[n][v] = grad_loss[n] (exp(l[n][v] - lse[n]) - [v = target[n]])
+ *   grad_x[n][d] = sum_v G[n][v] w[v][d],  grad_w[v][d] = sum_n G[n][v] x[n][d]
+ * with the logits computed again in pieces of the label set.  lse: the
+ * forward's.  grad_loss: float32, element n at n * grad_loss_stride (0: one
+ * value for every token; 1: one each).  grad_x (tokens x width, row stride
+ * ldgx) and grad_w (vocab x width, row stride ldgw) have `dtype`; either may
+ * be NULL (not computed).  Every element of a requested gradient is written;
+ * tokens that do not count add nothing.
+ * Errors: as the forward.
+ */
+TROP_API trop_status tropical_linear_cross_entropy_backward(trop_dtype dtype, const void* x, int64_t ldx,
+                                                   const void* w, int64_t ldw, const void* target,
+                                                   int target_bytes, int64_t ignore_index, const float* lse,
+                                                   const float* grad_loss, int64_t grad_loss_stride,
+                                                   void* grad_x, int64_t ldgx, void* grad_w, int64_t ldgw,
+                                                   int64_t tokens, int64_t width, int64_t vocab,
+                                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * One AdamW step over many tensors at once, in place.  With g the gradient
  * and q the float32 weight (master when given, else param):
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2

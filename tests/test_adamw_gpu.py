@@ -5,7 +5,7 @@ whose float32 root is the correctly rounded one; torch's CPU root is not).
 Tolerances against 64 bits, u = 2^-24: m is two products and a sum of float32
 factors (5 u of its terms), v one product more (6 u); the update divides m by
 a root and a sum (16 u of its size) and joins q in two more roundings (4 u);
-a bfloat16 parameter is rounded once (2^-8 of it, doubled).
+a bfloat16 parameter is rounded once (2^-8 of it).
 """
 import math
 

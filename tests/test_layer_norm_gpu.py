@@ -1,7 +1,7 @@
 """Layer norm forward and backward on the GPU against the formulas in 64 bits.
 
 Tolerances, with u = 2^-24 (one float32 rounding, relative) and half = 2^-8
-(one rounding to bfloat16 is at most 2^-9 of the value, doubled):
+(one rounding to bfloat16, which has 8 significant bits):
   - a sum over a row is a tree: at most 16 sequential terms per thread, 6
     lane levels, 16 waves; with the product and the factor 1/cols fewer than
     48 roundings touch a term, so its error is below 48 u sum|terms|; rows

@@ -145,12 +145,18 @@ def lib():
     L.tropical_layer_norm_backward_workspace_size.argtypes = [i64, i64, i32, PP(sz)]
     L.tropical_layer_norm_backward.argtypes = [i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, i64,
                                                vp, sz, vp]
+    L.tropical_linear_cross_entropy_forward.argtypes = [i32, vp, i64, vp, i64, vp, i32, i64, vp, vp, i64, i64, i64,
+                                                        vp, sz, vp]
+    L.tropical_linear_cross_entropy_workspace_size.argtypes = [i32, i64, i64, i64, i32, PP(sz)]
+    L.tropical_linear_cross_entropy_backward.argtypes = [i32, vp, i64, vp, i64, vp, i32, i64, vp, vp, i64, vp, i64,
+                                                         vp, i64, i64, i64, i64, vp, sz, vp]
     L.tropical_adamw_step.argtypes = [i32, PP(trop_adamw_tensor), i64, PP(trop_adamw_hyper), vp]
     L.tropical_adamw8_step.argtypes = [i32, PP(trop_adamw8_tensor), i64, PP(trop_adamw_hyper), vp]
     L.tropical_adamw8_unpack.argtypes = [PP(trop_adamw8_tensor), i64, PP(vp), PP(vp), vp]
     L.tropical_get_train_stats.argtypes = [PP(trop_train_stats)]
     for fn in ("tropical_train_init", "tropical_layer_norm_forward", "tropical_layer_norm_backward_workspace_size",
-               "tropical_layer_norm_backward",
+               "tropical_layer_norm_backward", "tropical_linear_cross_entropy_forward",
+               "tropical_linear_cross_entropy_workspace_size", "tropical_linear_cross_entropy_backward",
                "tropical_adamw_step", "tropical_adamw8_step", "tropical_adamw8_unpack", "tropical_get_train_stats"):
         getattr(L, fn).restype = ctypes.c_int
     _lib = L
@@ -678,6 +684,92 @@ def tropical_layer_norm_backward(dy, x, mean, rstd, gamma=None, dx=True, dgamma=
     if st != OK:
         _check(st, "tropical_layer_norm_backward")
     return dx, dgamma, dbeta
+
+
+def tropical_linear_cross_entropy_workspace_size(dtype, tokens, width, vocab, backward=False):
+    """Workspace bytes of a cross entropy call (dtype: torch.float32 or
+    torch.bfloat16)."""
+    if dtype not in _TRAIN_DTYPES:
+        raise TypeError(f"float32 or bfloat16 only, got {dtype}")
+    nb = ctypes.c_size_t(0)
+    _check(lib().tropical_linear_cross_entropy_workspace_size(_TRAIN_DTYPES[dtype], int(tokens), int(width),
+                                                              int(vocab), 1 if backward else 0, ctypes.byref(nb)),
+           "tropical_linear_cross_entropy_workspace_size")
+    return nb.value
+
+
+def _ce_operands(x, w, target):
+    dt = _tdt(x, "x")
+    if w.dtype != x.dtype:
+        raise TypeError("w must have the type of x")
+    ldx, ldw = _row_stride(x, "x"), _row_stride(w, "w")
+    tokens, width = x.shape
+    if w.shape[1] != width:
+        raise ValueError(f"x has a width of {width}, w of {w.shape[1]}")
+    if target.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"target must be int32 or int64, got {target.dtype}")
+    pt = _flat(target, "target", tokens, target.dtype)
+    return dt, ldx, ldw, tokens, width, w.shape[0], pt, target.element_size()
+
+
+@_on_stream
+def tropical_linear_cross_entropy_forward(x, w, target, ignore_index=-100, loss=None, lse=None, workspace=None):
+    """Softmax cross entropy of tokens over a label set: (loss, lse), float32
+    per token, with logits x @ w.T that are never kept.
+
+    x (tokens, width), w (vocab, width): float32 or bfloat16, unit stride
+    along the rows.  target: int32 or int64; a token whose target is
+    ignore_index or outside the vocabulary does not count (loss and lse 0).
+    The workspace is allocated with torch when not given.
+    """
+    dt, ldx, ldw, tokens, width, vocab, pt, tbytes = _ce_operands(x, w, target)
+    dev = x.device
+    loss = _out_like(loss, (tokens,), torch.float32, dev, "loss")
+    lse = _out_like(lse, (tokens,), torch.float32, dev, "lse")
+    need = 0
+    if workspace is None:
+        need = tropical_linear_cross_entropy_workspace_size(x.dtype, tokens, width, vocab)
+    workspace, wp, wn = _workspace(workspace, need, dev)
+    st = lib().tropical_linear_cross_entropy_forward(
+        dt, x.data_ptr(), ldx, w.data_ptr(), ldw, pt, tbytes, ignore_index,
+        _flat(loss, "loss", tokens, torch.float32), _flat(lse, "lse", tokens, torch.float32), tokens, width, vocab,
+        wp, wn, _stream_ptr(None, x))
+    if st != OK:
+        _check(st, "tropical_linear_cross_entropy_forward")
+    return loss, lse
+
+
+@_on_stream
+def tropical_linear_cross_entropy_backward(x, w, target, lse, grad_loss, ignore_index=-100, grad_x=True, grad_w=True,
+                                           workspace=None):
+    """Gradients of sum(grad_loss * loss): (grad_x, grad_w) in x's type.
+
+    lse: the forward's.  grad_loss: float32, one per token (any stride, an
+    expanded scalar too) or a 0-d tensor for all.  grad_x, grad_w: True to
+    allocate, a tensor to fill, or None to skip.
+    """
+    dt, ldx, ldw, tokens, width, vocab, pt, tbytes = _ce_operands(x, w, target)
+    dev = x.device
+    if grad_loss.dtype != torch.float32 or grad_loss.dim() > 1 or (grad_loss.dim() == 1 and
+                                                                   grad_loss.shape[0] != tokens):
+        raise ValueError(f"grad_loss must be float32, 0-d or of {tokens} elements")
+    gstride = grad_loss.stride(0) if grad_loss.dim() == 1 and tokens > 1 else 0
+    grad_x = _out_like(grad_x, (tokens, width), x.dtype, dev, "grad_x") if grad_x is not None else None
+    grad_w = _out_like(grad_w, (vocab, width), x.dtype, dev, "grad_w") if grad_w is not None else None
+    need = 0
+    if workspace is None:
+        need = tropical_linear_cross_entropy_workspace_size(x.dtype, tokens, width, vocab, backward=True)
+    workspace, wp, wn = _workspace(workspace, need, dev)
+    st = lib().tropical_linear_cross_entropy_backward(
+        dt, x.data_ptr(), ldx, w.data_ptr(), ldw, pt, tbytes, ignore_index, _flat(lse, "lse", tokens, torch.float32),
+        grad_loss.data_ptr(), gstride, grad_x.data_ptr() if grad_x is not None else None,
+        _row_stride(grad_x, "grad_x") if grad_x is not None else 0,
+        grad_w.data_ptr() if grad_w is not None else None,
+        _row_stride(grad_w, "grad_w") if grad_w is not None else 0, tokens, width, vocab, wp, wn,
+        _stream_ptr(None, x))
+    if st != OK:
+        _check(st, "tropical_linear_cross_entropy_backward")
+    return grad_x, grad_w
 
 
 def _adamw_table(kind, columns, params, grads, masters):

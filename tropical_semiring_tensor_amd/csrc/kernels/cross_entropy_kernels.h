@@ -1,0 +1,657 @@
+// Softmax cross entropy of tokens over a large label set, from the hidden
+// states x and the label matrix w, without keeping the logits l = x w^T.
+//
+//   lse_n = log sum_v exp l_nv           loss_n = lse_n - l_n,target
+//   G_nv = g_n (exp(l_nv - lse_n) - [v = target_n])
+//   grad_x = G w                         grad_w = G^T x
+//
+// Forward: the product's tiles end in their rows' maximum and sum of
+// exponentials (8 bytes a token and tile); a merge joins them.  Backward:
+// the label set is taken in pieces; a piece's logits are computed again and
+// end as G in 16 bits, which two more products consume.  8 N V D operations
+// in all, 2 more than with kept logits; the 4 N V bytes of logits are never
+// written.  For many tokens the matrix cores bound it, for few the read of w.
+//
+// Tokens that do not count are left out: the kept ones are listed first
+// (ordered, by one workgroup), and x is packed in that order, so masked
+// tokens cost nothing and what they hold cannot reach a sum.  Packing also
+// pads x with zeros to whole tiles and, for float32, splits it.
+//
+// float32 operands go through the matrix cores as two float16 planes of the
+// value scaled by one power of two per matrix (largest magnitude in [2^14,
+// 2^15)): 22 bits of every element above 2^-18 of its matrix's largest, an
+// absolute 2^-39 of that largest below; three 16-bit products at 1/16 of the
+// float32 units' cost each.  G is split the same way, scaled by 2^15 from
+// [-1, 1]: elements below 2^-30 of the largest token gradient lose digits.
+//
+// G is stored in quads of labels ([label / 4][token][4]): four consecutive
+// labels of a token are what a lane of the logits' product holds, so it
+// stores 8 bytes next to its neighbours' without a transpose, and both
+// products that follow read quads directly (along k, or across it with the
+// transposing LDS read).  It is scaled by grad_loss / max |grad_loss|, a
+// power that the float32 sums get back at the end, so that with equal token
+// weights only exp(l - lse) itself is rounded to 16 bits.
+#pragma once
+#include "mfma_gemm.h"
+
+namespace trop {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float CE_LOG2E = 1.44269504088896340736f;
+
+// exp of a difference of logits.  bfloat16 operands: the exponent's rounding
+// (2^-24 of it) is far below the products' own error.  float32: expf.
+template <int PLANES>
+__device__ __forceinline__ float ce_exp(float x) {
+    if constexpr (PLANES == 1)
+        return __builtin_amdgcn_exp2f(x * CE_LOG2E);
+    else
+        return expf(x);
+}
+
+__device__ __forceinline__ int64_t ce_target(const TropCeParams& p, int64_t n) {
+    return p.target_bytes == 8 ? static_cast<const int64_t*>(p.target)[n]
+                               : (int64_t)static_cast<const int32_t*>(p.target)[n];
+}
+__device__ __forceinline__ bool ce_counts(const TropCeParams& p, int64_t t) {
+    return t != p.ignore_index && t >= 0 && t < p.vocab;
+}
+
+// ---- which tokens count ----------------------------------------------------
+// One workgroup of 1024: each thread takes a run of consecutive tokens, a
+// scan over the runs' counts gives their places.
+__device__ __forceinline__ void ce_keep_body(const TropCeParams& p) {
+    __shared__ int32_t wave_count[16];
+    __shared__ float wave_max[16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t run = (p.tokens + 1023) / 1024;
+    const int64_t n0 = min((int64_t)threadIdx.x * run, p.tokens), n1 = min(n0 + run, p.tokens);
+    int32_t count = 0;
+    float gmax = 0.f;
+    for (int64_t n = n0; n < n1; ++n) {
+        if (!ce_counts(p, ce_target(p, n))) continue;
+        ++count;
+        if (p.backward) gmax = fmaxf(gmax, fabsf(p.grad_loss[n * p.grad_loss_stride]));
+    }
+    int32_t before = count;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int32_t v = __shfl_up(before, o, 64);
+        if (lane >= o) before += v;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) gmax = fmaxf(gmax, __shfl_xor(gmax, o, 64));
+    if (lane == 63) wave_count[wave] = before;
+    if (lane == 0) wave_max[wave] = gmax;
+    __syncthreads();
+    int32_t base = 0, total = 0;
+    gmax = 0.f;
+    for (int w = 0; w < 16; ++w) {
+        if (w < wave) base += wave_count[w];
+        total += wave_count[w];
+        gmax = fmaxf(gmax, wave_max[w]);
+    }
+    if (!(gmax > 0.f) || gmax > 3.0e38f) gmax = 1.f;  // nothing to scale, or an infinite weight
+    int32_t at = base + before - count;
+    for (int64_t n = n0; n < n1; ++n) {
+        const int64_t t = ce_target(p, n);
+        const bool keep = ce_counts(p, t);
+        p.slot[n] = keep ? at : -1;
+        if (keep) {
+            p.rows[at] = (int32_t)n;
+            p.kept_target[at] = (int32_t)t;
+            if (p.backward) {
+                p.kept_lse[at] = p.lse_in[n];
+                p.kept_grad[at] = p.grad_loss[n * p.grad_loss_stride] / gmax;
+            }
+            ++at;
+        } else if (!p.backward) {
+            p.loss[n] = 0.f;
+            p.lse[n] = 0.f;
+        }
+    }
+    if (threadIdx.x == 0) {
+        p.control->kept = total;
+        p.control->grad_max = gmax;
+        p.control->x_exp = p.control->w_exp = 0;
+    }
+}
+
+// ---- float32: the matrices' largest magnitudes -----------------------------
+// Partial maxima over the finite elements of the kept rows of x and of w.
+__device__ __forceinline__ void ce_magnitude_body(const TropCeParams& p) {
+    __shared__ float lds[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    for (int which = 0; which < 2; ++which) {
+        const float* m = static_cast<const float*>(which ? p.w : p.x);
+        const int64_t ld = which ? p.ldw : p.ldx, rows = which ? p.vocab : p.control->kept;
+        float best = 0.f;
+        // a wave to a row
+        for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < rows; r += (int64_t)p.max_parts * 4) {
+            const float* row = m + (which ? r : (int64_t)p.rows[r]) * ld;
+            for (int64_t c = lane * 4; c < p.width; c += 256) {
+                const FloatVec<4> v = load_row<float, 4>(row, c, p.width);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = fabsf(v[e]);
+                    best = a < 3.4e38f ? fmaxf(best, a) : best;
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor(best, o, 64));
+        if (lane == 0) lds[wave] = best;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            p.magnitude[which * TROP_CE_MAX_PARTS + blockIdx.x] = fmaxf(fmaxf(lds[0], lds[1]), fmaxf(lds[2], lds[3]));
+        __syncthreads();
+    }
+}
+
+// Exponent e with largest 2^e in [2^14, 2^15) (0 for a matrix of zeros).
+__device__ __forceinline__ int32_t ce_scale_exp(float largest) {
+    if (!(largest > 0.f)) return 0;
+    return 15 - (__builtin_amdgcn_frexp_expf(largest));
+}
+
+// value 2^e as h + l, both float16.
+__device__ __forceinline__ void ce_split(float scaled, _Float16& h, _Float16& l) {
+    h = (_Float16)scaled;
+    l = (_Float16)(scaled - (float)h);
+}
+
+// ---- packing ---------------------------------------------------------------
+// 8 elements of a row [c, c + 8), zeros past its end, into the planes.
+template <int PLANES>
+__device__ __forceinline__ void ce_pack8(const void* row, int64_t c, int64_t width, int32_t e, char* out,
+                                         int64_t plane_bytes) {
+    if constexpr (PLANES == 1) {
+        *reinterpret_cast<VecOf<bf16, 8>::raw*>(out) = load_row<bf16, 8>(static_cast<const bf16*>(row), c, width);
+    } else {
+        f16x8 h, l;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const FloatVec<4> v = load_row<float, 4>(static_cast<const float*>(row), c + q * 4, width);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                _Float16 a, b;
+                ce_split(ldexpf(v[i], e), a, b);
+                h[q * 4 + i] = a;
+                l[q * 4 + i] = b;
+            }
+        }
+        *reinterpret_cast<f16x8*>(out) = h;
+        *reinterpret_cast<f16x8*>(out + plane_bytes) = l;
+    }
+}
+
+// Kept rows of x, in order, and zero rows up to a whole tile.  A workgroup
+// takes a row; for float32 each reduces the partial maxima, and the first
+// leaves the exponents for the kernels after it.
+template <int PLANES>
+__device__ __forceinline__ void ce_pack_x_body(const TropCeParams& p) {
+    const int64_t kept = p.control->kept, i = blockIdx.x;
+    __shared__ float lds[2][4];
+    int32_t e = 0;
+    if constexpr (PLANES == 2) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+        float best[2];
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float b = 0.f;
+            for (int q = threadIdx.x; q < p.max_parts; q += 256) b = fmaxf(b, p.magnitude[which * TROP_CE_MAX_PARTS + q]);
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) b = fmaxf(b, __shfl_xor(b, o, 64));
+            if (lane == 0) lds[which][wave] = b;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int which = 0; which < 2; ++which)
+            best[which] = fmaxf(fmaxf(lds[which][0], lds[which][1]), fmaxf(lds[which][2], lds[which][3]));
+        e = ce_scale_exp(best[0]);
+        if (i == 0 && threadIdx.x == 0) {
+            p.control->x_exp = e;
+            p.control->w_exp = ce_scale_exp(best[1]);
+        }
+    }
+    if (i >= (kept + 255) / 256 * 256) return;
+    const size_t eb = PLANES == 1 ? 2 : 4;
+    const char* row = i < kept ? static_cast<const char*>(p.x) + (int64_t)p.rows[i] * p.ldx * eb : nullptr;
+    char* out = static_cast<char*>(p.xp) + i * p.width_p * 2;
+    for (int64_t c = threadIdx.x * 8; c < p.width_p; c += 256 * 8)
+        ce_pack8<PLANES>(row, c, row ? p.width : 0, e, out + c * 2, p.padded * p.width_p * 2);
+}
+
+// Rows [v0, v0 + piece) of w (its last row again past the vocabulary).
+template <int PLANES>
+__device__ __forceinline__ void ce_pack_w_body(const TropCeParams& p) {
+    const size_t eb = PLANES == 1 ? 2 : 4;
+    const int32_t e = p.control->w_exp;
+    for (int64_t r = blockIdx.x; r < p.piece; r += gridDim.x) {
+        const char* row = static_cast<const char*>(p.w) + min(p.v0 + r, p.vocab - 1) * p.ldw * eb;
+        char* out = static_cast<char*>(p.wp) + r * p.width_p * 2;
+        for (int64_t c = threadIdx.x * 8; c < p.width_p; c += 256 * 8)
+            ce_pack8<PLANES>(row, c, p.width, e, out + c * 2, p.piece * p.width_p * 2);
+    }
+}
+
+// ---- tiles -----------------------------------------------------------------
+// Workgroup -> tile of an active tm x tn grid (false: none).  Each XCD (a
+// workgroup's id modulo 8) takes a consecutive range of the tiles, which run
+// down groups of 8 tile rows, so the tiles that an XCD works on at a time
+// share operand panels in its L2.
+__device__ __forceinline__ bool ce_tile(int64_t id, int64_t tm, int64_t tn, int64_t& mi, int64_t& ni) {
+    const int64_t total = tm * tn, per = total / 8, rest = total % 8;
+    const int64_t xcd = id % 8, k = id / 8;
+    if (k >= per + (xcd < rest ? 1 : 0)) return false;
+    const int64_t t = xcd * per + min(xcd, rest) + k;
+    const int64_t group = t / (8 * tn), in = t - group * 8 * tn, rows = min((int64_t)8, tm - group * 8);
+    mi = group * 8 + in % rows;
+    ni = in / rows;
+    return true;
+}
+
+// The label matrix's rows from piece row r0 on as a KM operand (along the width).
+template <int PLANES>
+__device__ __forceinline__ MgOperand ce_w_rows(const TropCeParams& p, int64_t r0) {
+    MgOperand o;
+    o.k_bytes = MG_BK * 2;
+    if (PLANES == 2 || p.w_packed) {
+        o.base = static_cast<const char*>(p.wp) + r0 * p.width_p * 2;
+        o.ld = p.width_p;
+        o.plane_bytes = p.piece * p.width_p * 2;
+        o.last_row = 0x7fffffff;
+        o.last_k = 0x7fffffff;
+    } else {
+        o.base = static_cast<const char*>(p.w) + (p.v0 + r0) * p.ldw * 2;
+        o.ld = p.ldw;
+        o.plane_bytes = 0;
+        o.last_row = (int32_t)min(p.vocab - 1 - (p.v0 + r0), (int64_t)0x7fffffff);
+        o.last_k = (int32_t)(p.width / 8 - 1);
+    }
+    return o;
+}
+
+enum CeEpilogue { CE_STATS, CE_GRAD };
+
+// Logits of a BM-label x BN-token tile, and their row statistics or G.
+template <typename C, CeEpilogue EPI>
+__device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds) {
+    const int64_t kept = p.control->kept;
+    int64_t mi, ni;
+    if (!ce_tile(blockIdx.x, p.piece / C::BM, (kept + C::BN - 1) / C::BN, mi, ni)) return;
+    MgOperand b;
+    b.base = static_cast<const char*>(p.xp) + ni * C::BN * p.width_p * 2;
+    b.ld = p.width_p;
+    b.plane_bytes = p.padded * p.width_p * 2;
+    b.k_bytes = MG_BK * 2;
+    b.last_row = b.last_k = 0x7fffffff;
+    f32x16 acc[C::FM][C::FN];
+    mg_walk<C>(acc, ce_w_rows<C::PLANES>(p, mi * C::BM), b, (int)(p.width_p / MG_BK), lds);
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t v_wave = p.v0 + mi * C::BM + (wave / C::WN) * (C::BM / C::WM);  // label of the wave's row 0
+    const int n_wave = (wave % C::WN) * (C::BN / C::WN);                          // token of its column 0 in the tile
+    if constexpr (C::PLANES == 2) {
+        const int32_t e = -(p.control->x_exp + p.control->w_exp);
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = ldexpf(acc[i][j][r], e);
+    }
+    // labels past the vocabulary (the last tile only)
+    const bool ragged = v_wave + C::BM / C::WM > p.vocab;
+    if (ragged) {
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int64_t v = v_wave + 32 * i + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j) acc[i][j][r] = v < p.vocab ? acc[i][j][r] : -INFINITY;
+            }
+    }
+    // rows of the targets within this lane's block column j: register r of
+    // block i where 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4 is the target's row
+    int64_t n[C::FN];
+    int32_t trow[C::FN];
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+        n[j] = ni * C::BN + n_wave + 32 * j + (lane & 31);
+        const int64_t d = n[j] < kept ? p.kept_target[n[j]] - v_wave : -1;
+        trow[j] = d >= 0 && d < C::BM / C::WM && ((d >> 2) & 1) == lane / 32 ? (int32_t)d : -1;
+    }
+    if constexpr (EPI == CE_STATS) {
+        float2* part = reinterpret_cast<float2*>(lds);  // [WM][BN]
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+            if (__any(trow[j] >= 0)) {
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (trow[j] == 32 * i + 8 * (r / 4) + 4 * (lane / 32) + r % 4)
+                            p.target_logit[n[j]] = acc[i][j][r];
+            }
+            float m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) m = nan_max(m, acc[i][j][r]);
+            m = nan_max(m, __shfl_xor(m, 32, 64));
+            // (a block of -inf has nothing to sum; its logits minus 0 stay -inf)
+            const float base = m == -INFINITY ? 0.f : m;
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s += ce_exp<C::PLANES>(acc[i][j][r] - base);
+            s += __shfl_xor(s, 32, 64);
+            if (lane < 32) part[(wave / C::WN) * C::BN + n_wave + 32 * j + lane] = make_float2(m, s);
+        }
+        __syncthreads();
+        if (threadIdx.x < C::BN) {
+            const int64_t tok = ni * C::BN + threadIdx.x;
+            float2 a = part[threadIdx.x];
+#pragma unroll
+            for (int q = 1; q < C::WM; ++q) {
+                const float2 o = part[q * C::BN + threadIdx.x];
+                const float m = nan_max(a.x, o.x), base = m == -INFINITY ? 0.f : m;
+                a.y = a.y * ce_exp<C::PLANES>(a.x - base) + o.y * ce_exp<C::PLANES>(o.x - base);
+                a.x = m;
+            }
+            if (tok < kept) reinterpret_cast<float2*>(p.stats)[tok * p.tiles + p.tile0 + mi] = a;
+        }
+    } else {
+        const int64_t plane = p.piece * p.padded * 2;  // bytes
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+            const bool on = n[j] < kept;
+            const float lse = on ? p.kept_lse[n[j]] : 0.f, weight = on ? p.kept_grad[n[j]] : 0.f;
+            const bool hit = __any(trow[j] >= 0);
+            char* out = static_cast<char*>(p.g) +
+                        (((v_wave - p.v0) / 4 + lane / 32) * p.padded + n[j]) * 8;
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float g[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        g[e] = ce_exp<C::PLANES>(acc[i][j][4 * q + e] - lse);
+                        if (hit && trow[j] == 32 * i + 8 * q + 4 * (lane / 32) + e) g[e] -= 1.f;
+                        g[e] = on ? g[e] * weight : 0.f;
+                    }
+                    char* o = out + (int64_t)(8 * i + 2 * q) * p.padded * 8;
+                    if constexpr (C::PLANES == 1) {
+                        FloatVec<4> f = {g[0], g[1], g[2], g[3]};
+                        *reinterpret_cast<VecOf<bf16, 4>::raw*>(o) = from_float<bf16, 4>(f);
+                    } else {
+                        _Float16 __attribute__((ext_vector_type(4))) h, l;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            _Float16 a, b;
+                            ce_split(g[e] * 32768.f, a, b);
+                            h[e] = a;
+                            l[e] = b;
+                        }
+                        *reinterpret_cast<decltype(h)*>(o) = h;
+                        *reinterpret_cast<decltype(l)*>(o + plane) = l;
+                    }
+                }
+        }
+    }
+}
+
+// grad_x of a BM-token x BN-column tile over part `split` of the piece's
+// labels, into (or added to) the part's float32 sums.
+template <typename C>
+__device__ __forceinline__ void ce_grad_x_body(const TropCeParams& p, char* lds) {
+    const int64_t kept = p.control->kept;
+    const int64_t tm = (kept + C::BM - 1) / C::BM, tn = (p.width + C::BN - 1) / C::BN;
+    int64_t mi, q;
+    if (!ce_tile(blockIdx.x, tm, tn * p.splits, mi, q)) return;
+    const int64_t ni = q % tn, split = q / tn;
+    // (k tiles that hold a label: a part past them is empty, its sums zero)
+    const int64_t ktiles = (min(p.piece, p.vocab - p.v0) + MG_BK - 1) / MG_BK;
+    const int64_t kt0 = min(split * p.split_tiles, ktiles), kt1 = min(kt0 + p.split_tiles, ktiles);
+    const int64_t k0 = kt0 * MG_BK;
+    MgOperand a, b;
+    a.base = static_cast<const char*>(p.g) + (k0 / 4 * p.padded + mi * C::BM) * 8;
+    a.ld = p.padded;
+    a.plane_bytes = p.piece * p.padded * 2;
+    a.k_bytes = (MG_BK / 4) * p.padded * 8;
+    a.last_row = a.last_k = 0;
+    if (C::PLANES == 2 || p.w_packed) {
+        b.base = static_cast<const char*>(p.wp) + (k0 * p.width_p + ni * C::BN) * 2;
+        b.ld = p.width_p;
+        b.plane_bytes = p.piece * p.width_p * 2;
+        b.last_row = (int32_t)((p.width_p - ni * C::BN) / 8 - 1);
+        b.last_k = 0x7fffffff;
+    } else {
+        b.base = static_cast<const char*>(p.w) + ((p.v0 + k0) * p.ldw + ni * C::BN) * 2;
+        b.ld = p.ldw;
+        b.plane_bytes = 0;
+        b.last_row = (int32_t)((p.width - ni * C::BN) / 8 - 1);
+        b.last_k = (int32_t)min(p.vocab - 1 - (p.v0 + k0), (int64_t)0x7fffffff);
+    }
+    b.k_bytes = MG_BK * b.ld * 2;
+    f32x16 acc[C::FM][C::FN];
+    mg_walk<C>(acc, a, b, (int)(kt1 - kt0), lds);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t r0 = mi * C::BM + (wave / C::WN) * (C::BM / C::WM) + 4 * (lane / 32);
+    const int64_t c0 = ni * C::BN + (wave % C::WN) * (C::BN / C::WN) + (lane & 31);
+    float* out = p.gx_part + (split * p.padded + r0) * p.width_p + c0;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+        if (c0 + 32 * j >= p.width_p) continue;
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float* o = out + (int64_t)(32 * i + 8 * (r / 4) + r % 4) * p.width_p + 32 * j;
+                *o = p.accumulate ? *o + acc[i][j][r] : acc[i][j][r];
+            }
+    }
+}
+
+// grad_w of a BM-label x BN-column tile: the whole sum over the kept tokens.
+template <typename C, typename T>
+__device__ __forceinline__ void ce_grad_w_body(const TropCeParams& p, char* lds) {
+    const int64_t kept = p.control->kept;
+    int64_t mi, ni;
+    if (!ce_tile(blockIdx.x, (min(p.piece, p.vocab - p.v0) + C::BM - 1) / C::BM, (p.width + C::BN - 1) / C::BN, mi, ni))
+        return;
+    MgOperand a, b;
+    a.base = static_cast<const char*>(p.g) + mi * (C::BM / 4) * p.padded * 8;
+    a.ld = p.padded;
+    a.plane_bytes = p.piece * p.padded * 2;
+    a.k_bytes = MG_BK * 8;
+    a.last_row = a.last_k = 0;
+    b.base = static_cast<const char*>(p.xp) + ni * C::BN * 2;
+    b.ld = p.width_p;
+    b.plane_bytes = p.padded * p.width_p * 2;
+    b.k_bytes = MG_BK * p.width_p * 2;
+    b.last_row = (int32_t)((p.width_p - ni * C::BN) / 8 - 1);
+    b.last_k = 0x7fffffff;
+    f32x16 acc[C::FM][C::FN];
+    mg_walk<C>(acc, a, b, (int)((kept + MG_BK - 1) / MG_BK), lds);
+    float scale = p.control->grad_max;
+    if constexpr (C::PLANES == 2) scale = ldexpf(scale, -15 - p.control->x_exp);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t v0 = p.v0 + mi * C::BM + (wave / C::WN) * (C::BM / C::WM) + 4 * (lane / 32);
+    const int64_t c0 = ni * C::BN + (wave % C::WN) * (C::BN / C::WN) + (lane & 31);
+    T* out = static_cast<T*>(p.grad_w) + v0 * p.ldgw + c0;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+        if (c0 + 32 * j >= p.width) continue;
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = 32 * i + 8 * (r / 4) + r % 4;
+                if (v0 + row < p.vocab) out[(int64_t)row * p.ldgw + 32 * j] = (T)(acc[i][j][r] * scale);
+            }
+    }
+}
+
+// grad_x rows: the parts' sums in order, scaled; zeros for tokens that do
+// not count.  A workgroup takes a row.
+template <typename T, int PLANES>
+__device__ __forceinline__ void ce_finish_body(const TropCeParams& p) {
+    const int64_t n = blockIdx.x;
+    const int32_t i = p.slot[n];
+    float scale = p.control->grad_max;
+    if constexpr (PLANES == 2) scale = ldexpf(scale, -15 - p.control->w_exp);
+    T* out = static_cast<T*>(p.grad_x) + n * p.ldgx;
+    for (int64_t c = threadIdx.x * 4; c < p.width; c += 256 * 4) {
+        FloatVec<4> s = {0.f, 0.f, 0.f, 0.f};
+        if (i >= 0) {
+            const float* q = p.gx_part + (int64_t)i * p.width_p + c;
+            s = load_vec<float, 4>(q);  // width_p is a multiple of 64
+            for (int k = 1; k < p.splits; ++k) {
+                q += p.padded * p.width_p;
+                const FloatVec<4> o = load_vec<float, 4>(q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] += o[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] *= scale;
+        }
+        store_row<T, 4>(out, c, p.width, from_float<T, 4>(s));
+    }
+}
+
+// ---- few tokens ------------------------------------------------------------
+// Up to 64 tokens: w is streamed once from HBM into the 16 x 16 matrix
+// instructions' registers, no LDS, no packing: a wave takes 16 RF labels and
+// all tokens (16 per block column).  A lane reads 16 bytes of row lane % 16
+// at k chunk lane / 16, so a row's four lanes read 64 consecutive bytes.
+// float32 stays float32 (four 16x16x4 instructions per 16 k; the order of k
+// within them is the same for both operands and otherwise free).
+template <typename T, int RF, int NB>
+__device__ __forceinline__ void ce_few_body(const TropCeParams& p) {
+    constexpr int VEC = 16 / sizeof(T), KSTEP = 4 * VEC, U = 4;
+    using V = typename VecOf<T, VEC>::raw;
+    __shared__ float2 part[4][NB * 16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t v_wave = ((int64_t)blockIdx.x * 4 + wave) * 16 * RF;
+    const T* wr[RF];
+    const T* xr[NB];
+#pragma unroll
+    for (int i = 0; i < RF; ++i)
+        wr[i] = static_cast<const T*>(p.w) + min(v_wave + 16 * i + (lane & 15), p.vocab - 1) * p.ldw;
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+        xr[j] = static_cast<const T*>(p.x) + min((int64_t)(16 * j + (lane & 15)), p.tokens - 1) * p.ldx;
+    f32x4 acc[RF][NB] = {};
+    auto step = [&](const V (&a)[RF], const V (&b)[NB]) {
+#pragma unroll
+        for (int i = 0; i < RF; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                if constexpr (sizeof(T) == 2) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][e], b[j][e], acc[i][j], 0, 0, 0);
+                }
+            }
+    };
+    const int kl = (lane / 16) * VEC;
+    int64_t k = 0;
+    for (; k + U * KSTEP <= p.width; k += U * KSTEP) {
+        V a[U][RF], b[U][NB];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < RF; ++i) a[u][i] = load_vec<T, VEC>(wr[i] + k + kl + u * KSTEP);
+#pragma unroll
+            for (int j = 0; j < NB; ++j) b[u][j] = load_vec<T, VEC>(xr[j] + k + kl + u * KSTEP);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) step(a[u], b[u]);
+    }
+    for (; k < p.width; k += KSTEP) {
+        V a[RF], b[NB];
+#pragma unroll
+        for (int i = 0; i < RF; ++i) a[i] = load_row<T, VEC>(wr[i], k + kl, p.width);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) b[j] = load_row<T, VEC>(xr[j], k + kl, p.width);
+        step(a, b);
+    }
+    // row 16 i + 4 (lane / 16) + r, column 16 j + lane % 16
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        const int64_t n = 16 * j + (lane & 15);
+        const int64_t t = n < p.tokens ? ce_target(p, n) : -1;
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < RF; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int64_t v = v_wave + 16 * i + 4 * (lane / 16) + r;
+                if (v == t && v < p.vocab) p.target_logit[n] = acc[i][j][r];
+                if (v >= p.vocab) acc[i][j][r] = -INFINITY;
+                m = nan_max(m, acc[i][j][r]);
+            }
+        m = nan_max(m, __shfl_xor(m, 16, 64));
+        m = nan_max(m, __shfl_xor(m, 32, 64));
+        const float base = m == -INFINITY ? 0.f : m;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < RF; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s += expf(acc[i][j][r] - base);
+        s += __shfl_xor(s, 16, 64);
+        s += __shfl_xor(s, 32, 64);
+        if (lane < 16) part[wave][16 * j + lane] = make_float2(m, s);
+    }
+    __syncthreads();
+    if (threadIdx.x < NB * 16 && threadIdx.x < p.tokens) {
+        float2 a = part[0][threadIdx.x];
+#pragma unroll
+        for (int q = 1; q < 4; ++q) {
+            const float2 o = part[q][threadIdx.x];
+            const float m = nan_max(a.x, o.x), base = m == -INFINITY ? 0.f : m;
+            a.y = a.y * expf(a.x - base) + o.y * expf(o.x - base);
+            a.x = m;
+        }
+        reinterpret_cast<float2*>(p.stats)[threadIdx.x * p.tiles + blockIdx.x] = a;
+    }
+}
+
+// ---- statistics joined -----------------------------------------------------
+// A wave takes a token: its tiles' maxima and sums, then loss and lse.
+__device__ __forceinline__ void ce_merge_body(const TropCeParams& p) {
+    const int lane = threadIdx.x & 63;
+    const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    const int64_t kept = p.identity ? p.tokens : (int64_t)p.control->kept;
+    if (i >= kept) return;
+    const int64_t n = p.identity ? i : (int64_t)p.rows[i];
+    if (p.identity && !ce_counts(p, ce_target(p, n))) {
+        if (lane == 0) p.loss[n] = p.lse[n] = 0.f;
+        return;
+    }
+    const float2* q = reinterpret_cast<const float2*>(p.stats) + i * p.tiles;
+    float m = -INFINITY, s = 0.f;
+    for (int64_t t = lane; t < p.tiles; t += 64) {
+        const float2 a = q[t];
+        const float top = nan_max(m, a.x), base = top == -INFINITY ? 0.f : top;
+        s = s * expf(m - base) + a.y * expf(a.x - base);
+        m = top;
+    }
+    const float top = wave_nan_max(m), base = top == -INFINITY ? 0.f : top;
+    s = wave_sum(s * expf(m - base));
+    if (lane == 0) {
+        const float lse = top + logf(s);
+        p.lse[n] = lse;
+        p.loss[n] = lse - p.target_logit[i];
+    }
+}
+
+}  // namespace trop

@@ -2,6 +2,7 @@
 // point.  Built with hipcc --genco and embedded in the library beside the
 // contraction's; loaded once per device by the first training call.
 #include "adamw_kernels.h"
+#include "cross_entropy_kernels.h"
 #include "layer_norm_kernels.h"
 
 using namespace trop;
@@ -59,3 +60,51 @@ TROP_ADAMW_ENTRIES(bf16, bf16, false)
 TROP_ADAMW_ENTRIES(bf16_master, bf16, true)
 
 extern "C" __global__ __launch_bounds__(256) void trop_adamw8_unpack(TropAdamw8Params p) { adamw8_unpack_body(p); }
+
+extern "C" __global__ __launch_bounds__(1024) void trop_ce_keep(TropCeParams p) { ce_keep_body(p); }
+extern "C" __global__ __launch_bounds__(256) void trop_ce_magnitude(TropCeParams p) { ce_magnitude_body(p); }
+extern "C" __global__ __launch_bounds__(256) void trop_ce_merge(TropCeParams p) { ce_merge_body(p); }
+
+// one product tile: its LDS and the body's workgroup
+#define TROP_CE_TILE(NAME, CONFIG, BODY)                                                          \
+    extern "C" __global__ __launch_bounds__(CONFIG::THREADS) void trop_ce_##NAME(TropCeParams p) { \
+        __shared__ __align__(1024) char lds[CONFIG::LDS_BYTES];                                    \
+        BODY(p, lds);                                                                              \
+    }
+#define TROP_CE_ENTRIES(NAME, T, PLANES)                                                               \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_pack_x_##NAME(TropCeParams p) {           \
+        ce_pack_x_body<PLANES>(p);                                                                      \
+    }                                                                                                   \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_pack_w_##NAME(TropCeParams p) {           \
+        ce_pack_w_body<PLANES>(p);                                                                      \
+    }                                                                                                   \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_finish_##NAME(TropCeParams p) {           \
+        ce_finish_body<T, PLANES>(p);                                                                   \
+    }                                                                                                   \
+    using Logits256_##NAME = MgConfig<256, 256, 2, 4, KM, KM, PLANES>;                                  \
+    using Logits128_##NAME = MgConfig<128, 128, 2, 2, KM, KM, PLANES>;                                  \
+    using Logits64_##NAME = MgConfig<128, 64, 4, 1, KM, KM, PLANES>;                                    \
+    using GradX256_##NAME = MgConfig<256, 256, 2, 4, QK, MM, PLANES>;                                   \
+    using GradX128_##NAME = MgConfig<128, 128, 2, 2, QK, MM, PLANES>;                                   \
+    using GradX64_##NAME = MgConfig<64, 128, 1, 4, QK, MM, PLANES>;                                     \
+    using GradW256_##NAME = MgConfig<256, 256, 2, 4, QM, MM, PLANES>;                                   \
+    using GradW128_##NAME = MgConfig<128, 128, 2, 2, QM, MM, PLANES>;                                   \
+    TROP_CE_TILE(stats256_##NAME, Logits256_##NAME, (ce_logits_body<Logits256_##NAME, CE_STATS>))       \
+    TROP_CE_TILE(stats128_##NAME, Logits128_##NAME, (ce_logits_body<Logits128_##NAME, CE_STATS>))       \
+    TROP_CE_TILE(grad256_##NAME, Logits256_##NAME, (ce_logits_body<Logits256_##NAME, CE_GRAD>))         \
+    TROP_CE_TILE(grad128_##NAME, Logits128_##NAME, (ce_logits_body<Logits128_##NAME, CE_GRAD>))         \
+    TROP_CE_TILE(grad64_##NAME, Logits64_##NAME, (ce_logits_body<Logits64_##NAME, CE_GRAD>))            \
+    TROP_CE_TILE(gx256_##NAME, GradX256_##NAME, ce_grad_x_body<GradX256_##NAME>)                        \
+    TROP_CE_TILE(gx128_##NAME, GradX128_##NAME, ce_grad_x_body<GradX128_##NAME>)                        \
+    TROP_CE_TILE(gx64_##NAME, GradX64_##NAME, ce_grad_x_body<GradX64_##NAME>)                           \
+    TROP_CE_TILE(gw256_##NAME, GradW256_##NAME, (ce_grad_w_body<GradW256_##NAME, T>))                   \
+    TROP_CE_TILE(gw128_##NAME, GradW128_##NAME, (ce_grad_w_body<GradW128_##NAME, T>))                   \
+    TROP_CE_FEW(NAME, T, 1, 1) TROP_CE_FEW(NAME, T, 1, 2) TROP_CE_FEW(NAME, T, 1, 4)                    \
+    TROP_CE_FEW(NAME, T, 2, 1) TROP_CE_FEW(NAME, T, 2, 2) TROP_CE_FEW(NAME, T, 2, 4)
+// few tokens: blocks of 16 labels a wave, of 16 tokens
+#define TROP_CE_FEW(NAME, T, RF, NB)                                                                          \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_few_r##RF##_n##NB##_##NAME(TropCeParams p) {     \
+        ce_few_body<T, RF, NB>(p);                                                                             \
+    }
+TROP_CE_ENTRIES(f32, float, 2)
+TROP_CE_ENTRIES(bf16, bf16, 1)

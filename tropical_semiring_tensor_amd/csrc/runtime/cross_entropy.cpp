@@ -1,0 +1,380 @@
+// Linear cross entropy: argument checks, the plan of a call (tiles, pieces
+// of the label set, workspace layout) and its launches (see
+// cross_entropy_kernels.h).
+#include <string>
+
+#include "train.h"
+
+namespace trop {
+namespace {
+
+constexpr int64_t kBK = 64;               // k of a product's tile
+constexpr int64_t kPieceBytes = 256 << 20;  // of a piece of G, and of packed w
+constexpr int64_t kMaxTokens = 1 << 22, kMaxWidth = 1 << 22;  // 32-bit offsets within a tile
+constexpr int64_t kMaxVocab = ((int64_t)1 << 31) - 512;       // label indices are 32-bit
+constexpr int kFill = 192;  // workgroups that count as filling the device with 256 x 256 tiles
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// A piece's labels when a label takes `bytes` of a kPieceBytes buffer: equal
+// pieces, multiples of 256.
+int64_t piece_labels(int64_t vocab, int64_t bytes) {
+    int64_t most = kPieceBytes / bytes / 256 * 256;
+    if (most < 256) most = 256;
+    return round_up(ceil_div(vocab, ceil_div(vocab, most)), 256);
+}
+
+struct CePlan {
+    int64_t planes, padded, width_p;
+    bool few;           // forward of few tokens: no packing
+    bool packed;        // w is read from packed pieces
+    int64_t piece;      // labels of a piece (a multiple of 256; forward unpacked: all)
+    int logits_tile, gx_tile, gw_tile;  // 0: 256, 1: 128, 2: 64 tokens
+    int few_rows, few_tokens;           // the streaming kernel's blocks (16 each)
+    int64_t tiles;      // statistics per token
+    int64_t splits;
+    int64_t max_parts;
+    // workspace offsets
+    size_t control, rows, slot, kept_target, kept_lse, kept_grad, magnitude, stats, target_logit, xp, wp, g, gx_part;
+    size_t bytes;
+};
+
+int64_t logits_bm(const CePlan& c) { return c.logits_tile == 0 ? 256 : 128; }
+int64_t logits_bn(const CePlan& c) { return c.logits_tile == 0 ? 256 : c.logits_tile == 1 ? 128 : 64; }
+
+bool take(CePlan* c, size_t* at, int64_t bytes) {
+    *at = c->bytes;
+    int64_t next;
+    if (__builtin_add_overflow((int64_t)c->bytes, bytes, &next) || next > ((int64_t)1 << 62)) return false;
+    c->bytes = (size_t)round_up(next, 256);
+    return true;
+}
+
+// tokens, width, vocab in range (check_sizes), vocab and width >= 1.
+bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool backward, bool packed, CePlan* c) {
+    *c = CePlan();
+    c->planes = dt == TROP_BF16 ? 1 : 2;
+    c->padded = round_up(tokens > 0 ? tokens : 1, 256);
+    c->width_p = round_up(width, kBK);
+    c->packed = packed;
+    c->bytes = 256;  // room to align the caller's pointer
+    c->few = !backward && tokens <= TROP_CE_FEW;
+    bool ok = true;
+    if (c->few) {
+        c->few_tokens = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
+        // two blocks of labels a wave reuse its token registers; one where
+        // there would be fewer than two workgroups for each CU
+        c->few_rows = vocab >= 512 * 128 ? 2 : 1;
+        c->tiles = ceil_div(vocab, 64 * c->few_rows);
+        ok &= take(c, &c->stats, tokens * c->tiles * 8);
+        ok &= take(c, &c->target_logit, tokens * 4);
+        return ok;
+    }
+    const int64_t w_row = c->width_p * 2 * c->planes, g_label = c->padded * 2 * c->planes;
+    const bool whole = !backward && !packed;  // one launch over all labels
+    c->piece = round_up(vocab, 256);
+    if (!whole) {
+        int64_t bytes = packed ? w_row : 0;
+        if (backward && g_label > bytes) bytes = g_label;
+        c->piece = piece_labels(vocab, bytes);
+    }
+    const int64_t labels = c->piece < vocab ? c->piece : vocab;
+    // 256 x 256 tiles have the best rate; smaller ones where they would
+    // leave CUs without a tile
+    c->logits_tile = ceil_div(labels, 256) * ceil_div(tokens, 256) >= kFill ? 0 : tokens > 64 || !backward ? 1 : 2;
+    ok &= take(c, &c->control, sizeof(TropCeControl));
+    ok &= take(c, &c->rows, c->padded * 4);
+    ok &= take(c, &c->slot, c->padded * 4);
+    ok &= take(c, &c->kept_target, c->padded * 4);
+    if (c->planes == 2) {
+        c->max_parts = TROP_CE_MAX_PARTS;
+        ok &= take(c, &c->magnitude, 2 * TROP_CE_MAX_PARTS * 4);
+    }
+    ok &= take(c, &c->xp, c->padded * c->width_p * 2 * c->planes);
+    if (packed) ok &= take(c, &c->wp, c->piece * w_row);
+    if (!backward) {
+        c->tiles = ceil_div(vocab, logits_bm(*c));
+        ok &= take(c, &c->stats, tokens * c->tiles * 8);
+        ok &= take(c, &c->target_logit, c->padded * 4);
+        return ok;
+    }
+    ok &= take(c, &c->kept_lse, c->padded * 4);
+    ok &= take(c, &c->kept_grad, c->padded * 4);
+    // (the weight's 256-label tiles may read past a piece that ends at 128)
+    ok &= take(c, &c->g, (c->piece + 256) * g_label);
+    const int64_t ktiles = ceil_div(labels, kBK);
+    // grad_x: parts along the labels until the device is full, each of 8 k
+    // tiles at least; 256 tiles where that fills it
+    int64_t tiles = ceil_div(tokens > 0 ? tokens : 1, 256) * ceil_div(width, 256);
+    const int64_t most = ktiles / 8 > 1 ? ktiles / 8 : 1;
+    c->gx_tile = tiles * (most < 16 ? most : 16) >= kFill && tokens > 128 ? 0 : tokens > 64 ? 1 : 2;
+    int64_t want = 256;
+    if (c->gx_tile) {
+        tiles = ceil_div(tokens > 0 ? tokens : 1, c->gx_tile == 1 ? 128 : 64) * ceil_div(width, 128);
+        want = 512;
+    }
+    c->splits = want / tiles;
+    if (c->splits > most) c->splits = most;
+    if (c->splits > 16) c->splits = 16;
+    if (c->splits < 1) c->splits = 1;
+    ok &= take(c, &c->gx_part, c->splits * c->padded * c->width_p * 4);
+    c->gw_tile = ceil_div(labels, 256) * ceil_div(width, 256) >= kFill ? 0 : 1;
+    return ok;
+}
+
+trop_status check_sizes(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab) {
+    if (dt != TROP_F32 && dt != TROP_BF16)
+        return fail(TROP_ERR_INVALID_ARGUMENT,
+                    "linear cross entropy takes float32 or bfloat16, got dtype " + std::to_string((int)dt));
+    if (tokens < 0 || width < 0 || vocab < 0) return fail(TROP_ERR_INVALID_ARGUMENT, "negative size");
+    if (tokens > 0 && (width < 1 || vocab < 1))
+        return fail(TROP_ERR_INVALID_ARGUMENT, "tokens need a width and a vocabulary of at least 1");
+    if (tokens > kMaxTokens || width > kMaxWidth || vocab > kMaxVocab)
+        return fail(TROP_ERR_UNSUPPORTED, "more than 2^22 tokens, a width above 2^22 or 2^31 labels");
+    return TROP_OK;
+}
+
+// Can the products read w where it lies?  16-byte rows, and row offsets
+// within a tile that fit 32 bits.
+bool direct_w(trop_dtype dt, const void* w, int64_t ldw, int64_t width) {
+    return dt == TROP_BF16 && width % 8 == 0 && ldw % 8 == 0 && ldw <= kMaxWidth &&
+           reinterpret_cast<uintptr_t>(w) % 16 == 0;
+}
+
+struct CeCall {
+    trop_dtype dt;
+    const void *x, *w, *target;
+    int64_t ldx, ldw;
+    int target_bytes;
+    int64_t ignore_index;
+    int64_t tokens, width, vocab;
+    void* workspace;
+    size_t workspace_bytes;
+    void* stream;
+};
+
+trop_status check_inputs(const CeCall& a, int dev) {
+    const size_t eb = elem_size(a.dt);
+    trop_status st;
+    if (a.tokens > 0) {
+        if ((st = check_matrix(a.x, dev, a.tokens, a.width, a.ldx, eb, "x")) != TROP_OK) return st;
+        if ((st = check_matrix(a.target, dev, 1, a.tokens, a.tokens, a.target_bytes, "target")) != TROP_OK) return st;
+    }
+    return check_matrix(a.w, dev, a.vocab, a.width, a.ldw, eb, "w");
+}
+
+trop_status check_workspace(const CeCall& a, const CePlan& c, int dev, char** base) {
+    if (!a.workspace || a.workspace_bytes < c.bytes)
+        return fail(TROP_ERR_WORKSPACE_TOO_SMALL,
+                    "linear cross entropy needs " + std::to_string(c.bytes) + " workspace bytes, got " +
+                        std::to_string(a.workspace ? a.workspace_bytes : 0));
+    const trop_status st = check_device_span(a.workspace, dev, (int64_t)c.bytes, 1, "workspace");
+    *base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(a.workspace) + 255) / 256 * 256);
+    return st;
+}
+
+TropCeParams params(const CeCall& a, const CePlan& c, char* ws) {
+    TropCeParams p = {};
+    p.x = a.x;
+    p.w = a.w;
+    p.target = a.target;
+    p.ldx = a.ldx;
+    p.ldw = a.ldw;
+    p.target_bytes = a.target_bytes;
+    p.ignore_index = a.ignore_index;
+    p.tokens = a.tokens;
+    p.width = a.width;
+    p.vocab = a.vocab;
+    ws -= 256;  // (offsets start after the room for alignment)
+    p.control = reinterpret_cast<TropCeControl*>(ws + c.control);
+    p.rows = reinterpret_cast<int32_t*>(ws + c.rows);
+    p.slot = reinterpret_cast<int32_t*>(ws + c.slot);
+    p.kept_target = reinterpret_cast<int32_t*>(ws + c.kept_target);
+    p.kept_lse = reinterpret_cast<float*>(ws + c.kept_lse);
+    p.kept_grad = reinterpret_cast<float*>(ws + c.kept_grad);
+    p.magnitude = reinterpret_cast<float*>(ws + c.magnitude);
+    p.stats = reinterpret_cast<float*>(ws + c.stats);
+    p.target_logit = reinterpret_cast<float*>(ws + c.target_logit);
+    p.xp = ws + c.xp;
+    p.wp = ws + c.wp;
+    p.g = ws + c.g;
+    p.gx_part = reinterpret_cast<float*>(ws + c.gx_part);
+    p.padded = c.padded;
+    p.width_p = c.width_p;
+    p.tiles = c.tiles;
+    p.w_packed = c.packed;
+    p.splits = (int32_t)c.splits;
+    p.max_parts = (int32_t)c.max_parts;
+    return p;
+}
+
+TrainKernelId typed(int id, trop_dtype dt) { return (TrainKernelId)(id + (dt == TROP_BF16 ? 1 : 0)); }
+
+// List the kept tokens and pack them.
+trop_status prepare_tokens(int dev, const CeCall& a, const CePlan& c, const TropCeParams& p, hipStream_t s) {
+    trop_status st = train_launch(dev, TK_CE_KEEP, TROP_T_CE_PACK, 1, 1024, &p, s);
+    if (st == TROP_OK && c.planes == 2)
+        st = train_launch(dev, TK_CE_MAGNITUDE, TROP_T_CE_PACK, c.max_parts, 256, &p, s);
+    if (st == TROP_OK) st = train_launch(dev, typed(TK_CE_PACK_X, a.dt), TROP_T_CE_PACK, c.padded, 256, &p, s);
+    return st;
+}
+
+// This piece's labels into p, and w packed if it has to be.
+trop_status prepare_piece(int dev, const CeCall& a, const CePlan& c, int64_t v0, TropCeParams& p, hipStream_t s) {
+    const int64_t labels = a.vocab - v0 < c.piece ? a.vocab - v0 : c.piece;
+    p.v0 = v0;
+    p.piece = round_up(labels, logits_bm(c));
+    p.tile0 = v0 / logits_bm(c);
+    if (!c.packed) return TROP_OK;
+    return train_launch(dev, typed(TK_CE_PACK_W, a.dt), TROP_T_CE_PACK, p.piece < 4096 ? p.piece : 4096, 256, &p, s);
+}
+
+trop_status ce_forward(const CeCall& a, float* loss, float* lse) {
+    trop_status st = check_sizes(a.dt, a.tokens, a.width, a.vocab);
+    if (st != TROP_OK) return st;
+    if (a.target_bytes != 4 && a.target_bytes != 8)
+        return fail(TROP_ERR_INVALID_ARGUMENT, "targets have 4 or 8 bytes");
+    if (a.tokens == 0) return ok();
+    int dev = -1;
+    if ((st = train_device(&dev)) != TROP_OK) return st;
+    if ((st = check_inputs(a, dev)) != TROP_OK) return st;
+    if ((st = check_matrix(loss, dev, 1, a.tokens, a.tokens, 4, "loss")) != TROP_OK) return st;
+    if ((st = check_matrix(lse, dev, 1, a.tokens, a.tokens, 4, "lse")) != TROP_OK) return st;
+    CePlan c;
+    if (!plan(a.dt, a.tokens, a.width, a.vocab, false, !direct_w(a.dt, a.w, a.ldw, a.width), &c))
+        return fail(TROP_ERR_UNSUPPORTED, "workspace size overflows");
+    char* ws = nullptr;
+    if ((st = check_workspace(a, c, dev, &ws)) != TROP_OK) return st;
+    TropCeParams p = params(a, c, ws);
+    p.loss = loss;
+    p.lse = lse;
+    const hipStream_t s = static_cast<hipStream_t>(a.stream);
+    if (c.few) {
+        p.identity = 1;
+        const int id = TK_CE_FEW + 2 * (3 * (c.few_rows - 1) + (c.few_tokens == 4 ? 2 : c.few_tokens - 1));
+        st = train_launch(dev, typed(id, a.dt), TROP_T_CE_LOGITS, c.tiles, 256, &p, s);
+    } else {
+        st = prepare_tokens(dev, a, c, p, s);
+        for (int64_t v0 = 0; st == TROP_OK && v0 < a.vocab; v0 += c.piece) {
+            st = prepare_piece(dev, a, c, v0, p, s);
+            if (st == TROP_OK)
+                st = train_launch(dev, typed(TK_CE_STATS + 2 * c.logits_tile, a.dt), TROP_T_CE_LOGITS,
+                                  p.piece / logits_bm(c) * ceil_div(a.tokens, logits_bn(c)),
+                                  c.logits_tile == 0 ? 512 : 256, &p, s);
+        }
+    }
+    if (st == TROP_OK) st = train_launch(dev, TK_CE_MERGE, TROP_T_CE_MERGE, ceil_div(a.tokens, 4), 256, &p, s);
+    return st == TROP_OK ? ok() : st;
+}
+
+trop_status ce_backward(const CeCall& a, const float* lse, const float* grad_loss, int64_t grad_loss_stride,
+                        void* grad_x, int64_t ldgx, void* grad_w, int64_t ldgw) {
+    trop_status st = check_sizes(a.dt, a.tokens, a.width, a.vocab);
+    if (st != TROP_OK) return st;
+    if (a.target_bytes != 4 && a.target_bytes != 8)
+        return fail(TROP_ERR_INVALID_ARGUMENT, "targets have 4 or 8 bytes");
+    if (grad_loss_stride < 0) return fail(TROP_ERR_INVALID_ARGUMENT, "negative stride for grad_loss");
+    if (a.tokens == 0) grad_x = nullptr;
+    if (a.width == 0 || a.vocab == 0 || (!grad_x && !grad_w)) return ok();
+    int dev = -1;
+    if ((st = train_device(&dev)) != TROP_OK) return st;
+    const size_t eb = elem_size(a.dt);
+    if ((st = check_inputs(a, dev)) != TROP_OK) return st;
+    if (a.tokens > 0) {
+        if ((st = check_matrix(lse, dev, 1, a.tokens, a.tokens, 4, "lse")) != TROP_OK) return st;
+        // one element every grad_loss_stride
+        if ((st = check_matrix(grad_loss, dev, a.tokens, grad_loss_stride ? 1 : 0, grad_loss_stride, 4,
+                               "grad_loss")) != TROP_OK)
+            return st;
+        if (!grad_loss_stride && (st = check_matrix(grad_loss, dev, 1, 1, 1, 4, "grad_loss")) != TROP_OK) return st;
+    }
+    if (grad_x && (st = check_matrix(grad_x, dev, a.tokens, a.width, ldgx, eb, "grad_x")) != TROP_OK) return st;
+    if (grad_w && (st = check_matrix(grad_w, dev, a.vocab, a.width, ldgw, eb, "grad_w")) != TROP_OK) return st;
+    CePlan c;
+    if (!plan(a.dt, a.tokens, a.width, a.vocab, true, !direct_w(a.dt, a.w, a.ldw, a.width), &c))
+        return fail(TROP_ERR_UNSUPPORTED, "workspace size overflows");
+    char* ws = nullptr;
+    if ((st = check_workspace(a, c, dev, &ws)) != TROP_OK) return st;
+    TropCeParams p = params(a, c, ws);
+    p.backward = 1;
+    p.lse_in = lse;
+    p.grad_loss = grad_loss;
+    p.grad_loss_stride = grad_loss_stride;
+    p.grad_x = grad_x;
+    p.grad_w = grad_w;
+    p.ldgx = ldgx;
+    p.ldgw = ldgw;
+    const hipStream_t s = static_cast<hipStream_t>(a.stream);
+    const int64_t tokens = a.tokens > 0 ? a.tokens : 1;
+    st = prepare_tokens(dev, a, c, p, s);
+    for (int64_t v0 = 0; st == TROP_OK && v0 < a.vocab; v0 += c.piece) {
+        st = prepare_piece(dev, a, c, v0, p, s);
+        if (st == TROP_OK && a.tokens > 0)
+            st = train_launch(dev, typed(TK_CE_GRAD + 2 * c.logits_tile, a.dt), TROP_T_CE_LOGITS,
+                              p.piece / logits_bm(c) * ceil_div(tokens, logits_bn(c)),
+                              c.logits_tile == 0 ? 512 : 256, &p, s);
+        if (st == TROP_OK && grad_x) {
+            const int64_t bm = c.gx_tile == 0 ? 256 : c.gx_tile == 1 ? 128 : 64, bn = c.gx_tile == 0 ? 256 : 128;
+            const int64_t labels = a.vocab - v0 < c.piece ? a.vocab - v0 : c.piece;
+            p.split_tiles = (int32_t)ceil_div(ceil_div(labels, kBK), c.splits);
+            p.accumulate = v0 > 0;
+            st = train_launch(dev, typed(TK_CE_GX + 2 * c.gx_tile, a.dt), TROP_T_CE_GRAD,
+                              ceil_div(tokens, bm) * ceil_div(a.width, bn) * c.splits, c.gx_tile == 0 ? 512 : 256, &p,
+                              s);
+        }
+        if (st == TROP_OK && grad_w) {
+            const int64_t b = c.gw_tile == 0 ? 256 : 128;
+            st = train_launch(dev, typed(TK_CE_GW + 2 * c.gw_tile, a.dt), TROP_T_CE_GRAD,
+                              ceil_div(p.piece, b) * ceil_div(a.width, b), c.gw_tile == 0 ? 512 : 256, &p, s);
+        }
+    }
+    if (st == TROP_OK && grad_x)
+        st = train_launch(dev, typed(TK_CE_FINISH, a.dt), TROP_T_CE_MERGE, a.tokens, 256, &p, s);
+    return st == TROP_OK ? ok() : st;
+}
+
+}  // namespace
+}  // namespace trop
+
+extern "C" trop_status tropical_linear_cross_entropy_forward(trop_dtype dtype, const void* x, int64_t ldx,
+                                                             const void* w, int64_t ldw, const void* target,
+                                                             int target_bytes, int64_t ignore_index, float* loss,
+                                                             float* lse, int64_t tokens, int64_t width, int64_t vocab,
+                                                             void* workspace, size_t workspace_bytes, void* stream) {
+    return trop::guarded("tropical_linear_cross_entropy_forward", [&] {
+        return trop::ce_forward({dtype, x, w, target, ldx, ldw, target_bytes, ignore_index, tokens, width, vocab,
+                                 workspace, workspace_bytes, stream},
+                                loss, lse);
+    });
+}
+
+extern "C" trop_status tropical_linear_cross_entropy_workspace_size(trop_dtype dtype, int64_t tokens, int64_t width,
+                                                                    int64_t vocab, int backward, size_t* bytes) {
+    using namespace trop;
+    return guarded("tropical_linear_cross_entropy_workspace_size", [&]() -> trop_status {
+        if (!bytes) return fail(TROP_ERR_INVALID_ARGUMENT, "bytes is NULL");
+        *bytes = 0;
+        const trop_status st = check_sizes(dtype, tokens, width, vocab);
+        if (st != TROP_OK) return st;
+        if (width == 0 || vocab == 0 || (tokens == 0 && !backward)) return ok();
+        CePlan packed, plain;
+        if (!plan(dtype, tokens, width, vocab, backward != 0, true, &packed) ||
+            !plan(dtype, tokens, width, vocab, backward != 0, dtype == TROP_F32, &plain))
+            return fail(TROP_ERR_UNSUPPORTED, "workspace size overflows");
+        *bytes = packed.bytes > plain.bytes ? packed.bytes : plain.bytes;
+        return ok();
+    });
+}
+
+extern "C" trop_status tropical_linear_cross_entropy_backward(
+    trop_dtype dtype, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* target, int target_bytes,
+    int64_t ignore_index, const float* lse, const float* grad_loss, int64_t grad_loss_stride, void* grad_x,
+    int64_t ldgx, void* grad_w, int64_t ldgw, int64_t tokens, int64_t width, int64_t vocab, void* workspace,
+    size_t workspace_bytes, void* stream) {
+    return trop::guarded("tropical_linear_cross_entropy_backward", [&] {
+        return trop::ce_backward({dtype, x, w, target, ldx, ldw, target_bytes, ignore_index, tokens, width, vocab,
+                                  workspace, workspace_bytes, stream},
+                                 lse, grad_loss, grad_loss_stride, grad_x, ldgx, grad_w, ldgw);
+    });
+}

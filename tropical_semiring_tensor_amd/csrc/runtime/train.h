@@ -24,7 +24,18 @@ enum TrainKernelId : int {
     TK_ADAMW = TK_LN_MERGE + 2,  // + 2 (bf16) + (master ? 1 : 0)
     TK_ADAMW8 = TK_ADAMW + 4,
     TK_ADAMW8_UNPACK = TK_ADAMW8 + 4,
-    TK_COUNT
+    TK_CE_KEEP,
+    TK_CE_MAGNITUDE,
+    TK_CE_MERGE,
+    TK_CE_PACK_X,  // every family from here on: + (bf16 ? 1 : 0)
+    TK_CE_PACK_W = TK_CE_PACK_X + 2,
+    TK_CE_FINISH = TK_CE_PACK_W + 2,
+    TK_CE_STATS = TK_CE_FINISH + 2,  // + 2 tile (256, 128)
+    TK_CE_GRAD = TK_CE_STATS + 4,    // + 2 tile (256, 128, 64 tokens)
+    TK_CE_GX = TK_CE_GRAD + 6,       // + 2 tile (256, 128, 64 tokens)
+    TK_CE_GW = TK_CE_GX + 6,         // + 2 tile (256, 128)
+    TK_CE_FEW = TK_CE_GW + 4,        // + 2 (3 (label blocks - 1) + token blocks 1, 2, 4)
+    TK_COUNT = TK_CE_FEW + 12
 };
 
 // Current device with the training code object loaded on it.

@@ -87,4 +87,57 @@ struct TropAdamw8Params {
     TropAdamw8Entry t[TROP_ADAMW8_TENSORS];
 };
 
+// ---- linear cross entropy --------------------------------------------------
+// Tokens up to this many are scored by the streaming kernel (no packing).
+#define TROP_CE_FEW 64
+// Workgroups of the magnitude pass, each leaving two partial maxima.
+#define TROP_CE_MAX_PARTS 512
+
+// Scalars that the first kernels of a call leave for the later ones.
+struct TropCeControl {
+    int32_t kept;      // tokens that count
+    float grad_max;    // largest |grad_loss| of a kept token (1 when that is 0)
+    int32_t x_exp;     // float32 operands: x 2^x_exp and w 2^w_exp are split
+    int32_t w_exp;     // into float16 planes
+};
+
+struct TropCeParams {
+    const void* x;
+    const void* w;
+    const void* target;
+    const float* lse_in;      // backward
+    const float* grad_loss;   // backward
+    float* loss;              // forward
+    float* lse;               // forward
+    void* grad_x;
+    void* grad_w;
+    int64_t ldx, ldw, ldgx, ldgw, grad_loss_stride, ignore_index;
+    int64_t tokens, width, vocab;
+    // workspace
+    TropCeControl* control;
+    int32_t* rows;            // kept index -> token
+    int32_t* slot;            // token -> kept index or -1
+    int32_t* kept_target;     // per kept token
+    float* kept_lse;
+    float* kept_grad;         // grad_loss / grad_max
+    float* magnitude;         // [2][TROP_CE_MAX_PARTS]
+    float* stats;             // forward: [token][tiles][2] maximum and sum of exponentials
+    float* target_logit;      // per kept token (per token in the streaming kernel)
+    void* xp;                 // packed x: [planes][padded][width_p]
+    void* wp;                 // packed piece of w: [planes][piece][width_p]
+    void* g;                  // piece of the logits' gradient: [planes][piece / 4][padded][4]
+    float* gx_part;           // [splits][padded][width_p]
+    int64_t padded, width_p;
+    int64_t v0, piece;        // this launch's labels: [v0, v0 + piece), piece a multiple of the tile
+    int64_t tile0;            // first statistics tile of this launch
+    int64_t tiles;            // statistics tiles in all
+    int32_t target_bytes;
+    int32_t w_packed;         // the piece is read from wp (else from w itself)
+    int32_t splits, split_tiles;  // gx: parts along the labels and k tiles of each
+    int32_t accumulate;       // gx: add to what the piece before left
+    int32_t max_parts;        // workgroups of the magnitude pass
+    int32_t identity;         // merge: kept index = token (streaming kernel)
+    int32_t backward;
+};
+
 static_assert(sizeof(TropAdamwParams) <= 4096 && sizeof(TropAdamw8Params) <= 4096, "kernel argument block");
