@@ -117,6 +117,8 @@ def test_small(tb, tokens, width, vocab, dtype, pad):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("tokens,width,vocab", [
     (300, 64, 24581),     # logits in 256 x 256 tiles
+    (300, 72, 24581),     # the same, the width ending in the first half of 64 columns
+    (300, 8, 24581),
     (700, 1096, 8300),    # grad_x in 256 x 256 tiles, split along the labels
     (200, 1000, 12345),   # grad_w in 256 x 256 tiles
     (60, 256, 66000),     # few tokens, two blocks of labels a wave

@@ -36,8 +36,6 @@
 
 namespace trop {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
 constexpr float CE_LOG2E = 1.44269504088896340736f;
 
 // exp of a difference of logits.  bfloat16 operands: the exponent's rounding
@@ -253,11 +251,11 @@ __device__ __forceinline__ bool ce_tile(int64_t id, int64_t tm, int64_t tn, int6
 }
 
 // The label matrix's rows from piece row r0 on as a KM operand (along the width).
-template <int PLANES>
+template <typename C>
 __device__ __forceinline__ MgOperand ce_w_rows(const TropCeParams& p, int64_t r0) {
     MgOperand o;
-    o.k_bytes = MG_BK * 2;
-    if (PLANES == 2 || p.w_packed) {
+    o.k_bytes = C::BK * 2;
+    if (C::PLANES == 2 || p.w_packed) {
         o.base = static_cast<const char*>(p.wp) + r0 * p.width_p * 2;
         o.ld = p.width_p;
         o.plane_bytes = p.piece * p.width_p * 2;
@@ -285,10 +283,12 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
     b.base = static_cast<const char*>(p.xp) + ni * C::BN * p.width_p * 2;
     b.ld = p.width_p;
     b.plane_bytes = p.padded * p.width_p * 2;
-    b.k_bytes = MG_BK * 2;
+    b.k_bytes = C::BK * 2;
     b.last_row = b.last_k = 0x7fffffff;
-    f32x16 acc[C::FM][C::FN];
-    mg_walk<C>(acc, ce_w_rows<C::PLANES>(p, mi * C::BM), b, (int)(p.width_p / MG_BK), lds);
+    f32x4 acc[C::FM][C::FN];
+    // (only tiles that hold a column: the loads clamp to a row's last chunk
+    // within a tile, not from a tile past it)
+    mg_walk<C>(acc, ce_w_rows<C>(p, mi * C::BM), b, (int)((p.width + C::BK - 1) / C::BK), lds);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
     const int64_t v_wave = p.v0 + mi * C::BM + (wave / C::WN) * (C::BM / C::WM);  // label of the wave's row 0
@@ -300,7 +300,7 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
 #pragma unroll
             for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][j][r] = ldexpf(acc[i][j][r], e);
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = ldexpf(acc[i][j][r], e);
     }
     // labels past the vocabulary (the last tile only)
     const bool ragged = v_wave + C::BM / C::WM > p.vocab;
@@ -308,21 +308,21 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t v = v_wave + 32 * i + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
+            for (int r = 0; r < 4; ++r) {
+                const int64_t v = v_wave + 16 * i + 4 * (lane / 16) + r;
 #pragma unroll
                 for (int j = 0; j < C::FN; ++j) acc[i][j][r] = v < p.vocab ? acc[i][j][r] : -INFINITY;
             }
     }
-    // rows of the targets within this lane's block column j: register r of
-    // block i where 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4 is the target's row
+    // the target's row of the wave's part, where this lane holds it
+    // (register r of block i: row 16 i + 4 (lane / 16) + r), else -1
     int64_t n[C::FN];
     int32_t trow[C::FN];
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
-        n[j] = ni * C::BN + n_wave + 32 * j + (lane & 31);
+        n[j] = ni * C::BN + n_wave + 16 * j + (lane & 15);
         const int64_t d = n[j] < kept ? p.kept_target[n[j]] - v_wave : -1;
-        trow[j] = d >= 0 && d < C::BM / C::WM && ((d >> 2) & 1) == lane / 32 ? (int32_t)d : -1;
+        trow[j] = d >= 0 && d < C::BM / C::WM && ((d >> 2) & 3) == lane / 16 ? (int32_t)d : -1;
     }
     if constexpr (EPI == CE_STATS) {
         float2* part = reinterpret_cast<float2*>(lds);  // [WM][BN]
@@ -332,15 +332,15 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
 #pragma unroll
                 for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (trow[j] == 32 * i + 8 * (r / 4) + 4 * (lane / 32) + r % 4)
-                            p.target_logit[n[j]] = acc[i][j][r];
+                    for (int r = 0; r < 4; ++r)
+                        if (trow[j] == 16 * i + 4 * (lane / 16) + r) p.target_logit[n[j]] = acc[i][j][r];
             }
             float m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) m = nan_max(m, acc[i][j][r]);
+                for (int r = 0; r < 4; ++r) m = nan_max(m, acc[i][j][r]);
+            m = nan_max(m, __shfl_xor(m, 16, 64));
             m = nan_max(m, __shfl_xor(m, 32, 64));
             // (a block of -inf has nothing to sum; its logits minus 0 stay -inf)
             const float base = m == -INFINITY ? 0.f : m;
@@ -348,9 +348,10 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
 #pragma unroll
             for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s += ce_exp<C::PLANES>(acc[i][j][r] - base);
+                for (int r = 0; r < 4; ++r) s += ce_exp<C::PLANES>(acc[i][j][r] - base);
+            s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
-            if (lane < 32) part[(wave / C::WN) * C::BN + n_wave + 32 * j + lane] = make_float2(m, s);
+            if (lane < 16) part[(wave / C::WN) * C::BN + n_wave + 16 * j + lane] = make_float2(m, s);
         }
         __syncthreads();
         if (threadIdx.x < C::BN) {
@@ -372,129 +373,131 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
             const bool on = n[j] < kept;
             const float lse = on ? p.kept_lse[n[j]] : 0.f, weight = on ? p.kept_grad[n[j]] : 0.f;
             const bool hit = __any(trow[j] >= 0);
-            char* out = static_cast<char*>(p.g) +
-                        (((v_wave - p.v0) / 4 + lane / 32) * p.padded + n[j]) * 8;
+            char* out = static_cast<char*>(p.g) + (((v_wave - p.v0) / 4 + lane / 16) * p.padded + n[j]) * 8;
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i)
+            for (int i = 0; i < C::FM; ++i) {
+                FloatVec<4> g;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float g[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        g[e] = ce_exp<C::PLANES>(acc[i][j][4 * q + e] - lse);
-                        if (hit && trow[j] == 32 * i + 8 * q + 4 * (lane / 32) + e) g[e] -= 1.f;
-                        g[e] = on ? g[e] * weight : 0.f;
-                    }
-                    char* o = out + (int64_t)(8 * i + 2 * q) * p.padded * 8;
-                    if constexpr (C::PLANES == 1) {
-                        FloatVec<4> f = {g[0], g[1], g[2], g[3]};
-                        *reinterpret_cast<VecOf<bf16, 4>::raw*>(o) = from_float<bf16, 4>(f);
-                    } else {
-                        _Float16 __attribute__((ext_vector_type(4))) h, l;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            _Float16 a, b;
-                            ce_split(g[e] * 32768.f, a, b);
-                            h[e] = a;
-                            l[e] = b;
-                        }
-                        *reinterpret_cast<decltype(h)*>(o) = h;
-                        *reinterpret_cast<decltype(l)*>(o + plane) = l;
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    float v = ce_exp<C::PLANES>(acc[i][j][r] - lse);
+                    if (hit && trow[j] == 16 * i + 4 * (lane / 16) + r) v -= 1.f;
+                    g[r] = on ? v * weight : 0.f;
                 }
+                char* o = out + (int64_t)(4 * i) * p.padded * 8;
+                if constexpr (C::PLANES == 1) {
+                    *reinterpret_cast<VecOf<bf16, 4>::raw*>(o) = from_float<bf16, 4>(g);
+                } else {
+                    _Float16 __attribute__((ext_vector_type(4))) h, l;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        _Float16 a, b;
+                        ce_split(g[r] * 32768.f, a, b);
+                        h[r] = a;
+                        l[r] = b;
+                    }
+                    *reinterpret_cast<decltype(h)*>(o) = h;
+                    *reinterpret_cast<decltype(l)*>(o + plane) = l;
+                }
+            }
         }
     }
 }
 
-// grad_x of a BM-token x BN-column tile over part `split` of the piece's
-// labels, into (or added to) the part's float32 sums.
+// grad_x of a BM-column x BN-token tile over part `split` of the piece's
+// labels, into (or added to) the part's float32 sums.  The columns are the
+// product's rows, so a lane holds four consecutive ones of a token.
 template <typename C>
 __device__ __forceinline__ void ce_grad_x_body(const TropCeParams& p, char* lds) {
     const int64_t kept = p.control->kept;
-    const int64_t tm = (kept + C::BM - 1) / C::BM, tn = (p.width + C::BN - 1) / C::BN;
+    const int64_t tm = (kept + C::BN - 1) / C::BN, tn = (p.width + C::BM - 1) / C::BM;
     int64_t mi, q;
     if (!ce_tile(blockIdx.x, tm, tn * p.splits, mi, q)) return;
     const int64_t ni = q % tn, split = q / tn;
     // (k tiles that hold a label: a part past them is empty, its sums zero)
-    const int64_t ktiles = (min(p.piece, p.vocab - p.v0) + MG_BK - 1) / MG_BK;
+    const int64_t ktiles = (min(p.piece, p.vocab - p.v0) + C::BK - 1) / C::BK;
     const int64_t kt0 = min(split * p.split_tiles, ktiles), kt1 = min(kt0 + p.split_tiles, ktiles);
-    const int64_t k0 = kt0 * MG_BK;
+    const int64_t k0 = kt0 * C::BK;
     MgOperand a, b;
-    a.base = static_cast<const char*>(p.g) + (k0 / 4 * p.padded + mi * C::BM) * 8;
-    a.ld = p.padded;
-    a.plane_bytes = p.piece * p.padded * 2;
-    a.k_bytes = (MG_BK / 4) * p.padded * 8;
-    a.last_row = a.last_k = 0;
     if (C::PLANES == 2 || p.w_packed) {
-        b.base = static_cast<const char*>(p.wp) + (k0 * p.width_p + ni * C::BN) * 2;
-        b.ld = p.width_p;
-        b.plane_bytes = p.piece * p.width_p * 2;
-        b.last_row = (int32_t)((p.width_p - ni * C::BN) / 8 - 1);
-        b.last_k = 0x7fffffff;
+        a.base = static_cast<const char*>(p.wp) + (k0 * p.width_p + ni * C::BM) * 2;
+        a.ld = p.width_p;
+        a.plane_bytes = p.piece * p.width_p * 2;
+        a.last_row = (int32_t)((p.width_p - ni * C::BM) / 8 - 1);
+        a.last_k = 0x7fffffff;
     } else {
-        b.base = static_cast<const char*>(p.w) + ((p.v0 + k0) * p.ldw + ni * C::BN) * 2;
-        b.ld = p.ldw;
-        b.plane_bytes = 0;
-        b.last_row = (int32_t)((p.width - ni * C::BN) / 8 - 1);
-        b.last_k = (int32_t)min(p.vocab - 1 - (p.v0 + k0), (int64_t)0x7fffffff);
+        a.base = static_cast<const char*>(p.w) + ((p.v0 + k0) * p.ldw + ni * C::BM) * 2;
+        a.ld = p.ldw;
+        a.plane_bytes = 0;
+        a.last_row = (int32_t)((p.width - ni * C::BM) / 8 - 1);
+        a.last_k = (int32_t)min(p.vocab - 1 - (p.v0 + k0), (int64_t)0x7fffffff);
     }
-    b.k_bytes = MG_BK * b.ld * 2;
-    f32x16 acc[C::FM][C::FN];
+    a.k_bytes = C::BK * a.ld * 2;
+    b.base = static_cast<const char*>(p.g) + (k0 / 4 * p.padded + mi * C::BN) * 8;
+    b.ld = p.padded;
+    b.plane_bytes = p.piece * p.padded * 2;
+    b.k_bytes = (C::BK / 4) * p.padded * 8;
+    b.last_row = b.last_k = 0;
+    f32x4 acc[C::FM][C::FN];
     mg_walk<C>(acc, a, b, (int)(kt1 - kt0), lds);
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-    const int64_t r0 = mi * C::BM + (wave / C::WN) * (C::BM / C::WM) + 4 * (lane / 32);
-    const int64_t c0 = ni * C::BN + (wave % C::WN) * (C::BN / C::WN) + (lane & 31);
-    float* out = p.gx_part + (split * p.padded + r0) * p.width_p + c0;
+    const int64_t c0 = ni * C::BM + (wave / C::WN) * (C::BM / C::WM) + 4 * (lane / 16);
+    const int64_t n0 = mi * C::BN + (wave % C::WN) * (C::BN / C::WN) + (lane & 15);
+    float* out = p.gx_part + (split * p.padded + n0) * p.width_p + c0;
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
-        if (c0 + 32 * j >= p.width_p) continue;
+    for (int i = 0; i < C::FM; ++i) {
+        if (c0 + 16 * i >= p.width_p) continue;
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
+        for (int j = 0; j < C::FN; ++j) {
+            f32x4* o = reinterpret_cast<f32x4*>(out + (int64_t)(16 * j) * p.width_p + 16 * i);
+            f32x4 v = acc[i][j];
+            if (p.accumulate) {
+                const f32x4 before = *o;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float* o = out + (int64_t)(32 * i + 8 * (r / 4) + r % 4) * p.width_p + 32 * j;
-                *o = p.accumulate ? *o + acc[i][j][r] : acc[i][j][r];
+                for (int r = 0; r < 4; ++r) v[r] += before[r];
             }
+            *o = v;
+        }
     }
 }
 
-// grad_w of a BM-label x BN-column tile: the whole sum over the kept tokens.
+// grad_w of a BM-column x BN-label tile: the whole sum over the kept tokens.
 template <typename C, typename T>
 __device__ __forceinline__ void ce_grad_w_body(const TropCeParams& p, char* lds) {
     const int64_t kept = p.control->kept;
     int64_t mi, ni;
-    if (!ce_tile(blockIdx.x, (min(p.piece, p.vocab - p.v0) + C::BM - 1) / C::BM, (p.width + C::BN - 1) / C::BN, mi, ni))
+    if (!ce_tile(blockIdx.x, (min(p.piece, p.vocab - p.v0) + C::BN - 1) / C::BN, (p.width + C::BM - 1) / C::BM, mi, ni))
         return;
     MgOperand a, b;
-    a.base = static_cast<const char*>(p.g) + mi * (C::BM / 4) * p.padded * 8;
-    a.ld = p.padded;
-    a.plane_bytes = p.piece * p.padded * 2;
-    a.k_bytes = MG_BK * 8;
-    a.last_row = a.last_k = 0;
-    b.base = static_cast<const char*>(p.xp) + ni * C::BN * 2;
-    b.ld = p.width_p;
-    b.plane_bytes = p.padded * p.width_p * 2;
-    b.k_bytes = MG_BK * p.width_p * 2;
-    b.last_row = (int32_t)((p.width_p - ni * C::BN) / 8 - 1);
-    b.last_k = 0x7fffffff;
-    f32x16 acc[C::FM][C::FN];
-    mg_walk<C>(acc, a, b, (int)((kept + MG_BK - 1) / MG_BK), lds);
+    a.base = static_cast<const char*>(p.xp) + ni * C::BM * 2;
+    a.ld = p.width_p;
+    a.plane_bytes = p.padded * p.width_p * 2;
+    a.k_bytes = C::BK * p.width_p * 2;
+    a.last_row = (int32_t)((p.width_p - ni * C::BM) / 8 - 1);
+    a.last_k = 0x7fffffff;
+    b.base = static_cast<const char*>(p.g) + mi * (C::BN / 4) * p.padded * 8;
+    b.ld = p.padded;
+    b.plane_bytes = p.piece * p.padded * 2;
+    b.k_bytes = C::BK * 8;
+    b.last_row = b.last_k = 0;
+    f32x4 acc[C::FM][C::FN];
+    mg_walk<C>(acc, a, b, (int)((kept + C::BK - 1) / C::BK), lds);
     float scale = p.control->grad_max;
     if constexpr (C::PLANES == 2) scale = ldexpf(scale, -15 - p.control->x_exp);
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-    const int64_t v0 = p.v0 + mi * C::BM + (wave / C::WN) * (C::BM / C::WM) + 4 * (lane / 32);
-    const int64_t c0 = ni * C::BN + (wave % C::WN) * (C::BN / C::WN) + (lane & 31);
-    T* out = static_cast<T*>(p.grad_w) + v0 * p.ldgw + c0;
+    const int64_t c0 = ni * C::BM + (wave / C::WN) * (C::BM / C::WM) + 4 * (lane / 16);
+    const int64_t v0 = p.v0 + mi * C::BN + (wave % C::WN) * (C::BN / C::WN) + (lane & 15);
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
-        if (c0 + 32 * j >= p.width) continue;
+        const int64_t v = v0 + 16 * j;
+        if (v >= p.vocab) continue;
+        T* out = static_cast<T*>(p.grad_w) + v * p.ldgw;
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
+        for (int i = 0; i < C::FM; ++i) {
+            FloatVec<4> g;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = 32 * i + 8 * (r / 4) + r % 4;
-                if (v0 + row < p.vocab) out[(int64_t)row * p.ldgw + 32 * j] = (T)(acc[i][j][r] * scale);
-            }
+            for (int r = 0; r < 4; ++r) g[r] = acc[i][j][r] * scale;
+            if (c0 + 16 * i < p.width) store_row<T, 4>(out, c0 + 16 * i, p.width, from_float<T, 4>(g));
+        }
     }
 }
 

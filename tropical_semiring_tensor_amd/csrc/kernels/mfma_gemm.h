@@ -3,21 +3,22 @@
 // entropy's kernels.
 //
 // A workgroup of WM x WN waves computes a BM x BN tile; a wave computes
-// (BM / WM) x (BN / WN) of it in 32 x 32 blocks (v_mfma_f32_32x32x16).  K is
-// walked in tiles of 64.  A tile goes from global memory to LDS directly
-// (16 bytes per lane, no registers in between) into one of two buffers while
-// the other is multiplied.  Operands are read as they lie in memory, so
-// nothing is transposed beforehand:
+// (BM / WM) x (BN / WN) of it in 16 x 16 blocks (v_mfma_f32_16x16x32).  K is
+// walked in tiles of BK.  A tile goes from global memory to LDS directly
+// (16 bytes per lane, no registers in between) into one of STAGES buffers
+// while earlier ones are multiplied.  Operands are read as they lie in
+// memory, so nothing is transposed beforehand:
 //   KM  element (i, k) at i ld + k           (rows along k)
 //   MM  element (i, k) at k ld + i           (rows along i)
 //   QK  element (i, k) at (k / 4) 4 ld + 4 i + k % 4    (quads along k)
 //   QM  element (i, k) at (i / 4) 4 ld + 4 k + i % 4    (quads along i)
-// A lane of the 32x32x16 instruction takes 8 consecutive k of one i: one
+// A lane of the 16x16x32 instruction takes 8 consecutive k of one i: one
 // 16-byte LDS read for KM, two 8-byte reads for QK, two transposing reads
 // (ds_read_b64_tr_b16: 16 lanes exchange a 4 x 16 block) for MM and QM.  The
 // LDS copies are swizzled in 16-byte chunks so that the lanes of a read
-// meet distinct banks; since a direct load fills LDS in lane order, it is
-// the lanes' global addresses that are permuted.
+// meet distinct banks (no conflicts by the counters); since a direct load
+// fills LDS in lane order, it is the lanes' global addresses that are
+// permuted.
 //
 // PLANES = 1: bfloat16 values.  PLANES = 2: a float32 value scaled by a
 // power of two, as the sum of two float16 values h + l (22 bits); the
@@ -29,9 +30,7 @@ namespace trop {
 
 enum OperandKind { KM, MM, QK, QM };
 
-constexpr int MG_BK = 64;  // k of one LDS tile
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -62,21 +61,33 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, const char* base, uint
                  : "memory");
 }
 
-// Every load to LDS of this wave has landed, every LDS read has returned,
-// and so it is for all waves of the workgroup.
-__device__ __forceinline__ void mg_sync() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// All but this wave's newest PENDING loads to LDS have landed, every LDS
+// read has returned, and so it is for all waves of the workgroup.
+template <int PENDING>
+__device__ __forceinline__ void mg_sync() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PENDING) : "memory");
+}
+__device__ __forceinline__ void mg_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
-template <OperandKind KIND, int ROWS, int WAVES>
+template <OperandKind KIND, int ROWS, int BK, int WAVES>
 struct MgTile {
-    static constexpr int BYTES = ROWS * MG_BK * 2;
-    static constexpr int LOADS = ROWS / 8 / WAVES;  // per wave
-    static_assert(LOADS >= 1 && ROWS % (8 * WAVES) == 0, "tile rows per wave");
-    static constexpr int ROW_CHUNKS = KIND == KM ? 8 : KIND == MM ? ROWS / 8 : KIND == QK ? ROWS / 2 : 32;
+    static constexpr int BYTES = ROWS * BK * 2;
+    static constexpr int LOADS = BYTES / 1024 / WAVES;  // per wave
+    static_assert(LOADS >= 1 && BYTES % (1024 * WAVES) == 0, "tile rows per wave");
+    // 16-byte chunks of a line of the LDS copy
+    static constexpr int ROW_CHUNKS = KIND == KM ? BK / 8 : KIND == MM ? ROWS / 8 : KIND == QK ? ROWS / 2 : BK / 2;
 
+    // Chunk c of a line lies at c ^ swizzle(line).  LDS serves 256 bytes, 16
+    // chunks, at a time, so the lanes of a read that are served together
+    // must differ in their chunk modulo 16:
+    //   KM  16 rows, one chunk each       MM, QM  4 lines x 2 chunks x 2 k groups
+    //   QK  16 rows of 8 bytes in 2 lines
     static __device__ __forceinline__ int swizzle(int line) {
-        if constexpr (KIND == KM) return (line >> 1) & 7;
-        if constexpr (KIND == MM) return ROWS >= 128 ? (line & 3) * 4 : ((line >> 1) & 1) * 4;
-        if constexpr (KIND == QM) return (line & 7) * 2;
+        if constexpr (KIND == KM) return BK == 64 ? (line >> 1) & 7 : (0 - (line >> 2)) & 3;
+        if constexpr (KIND == MM)
+            return (ROWS >= 128 ? (line & 3) * 4 : ((line >> 1) & 1) * 4) + ((line >> 3) & 1) * 2;
+        if constexpr (KIND == QK) return ((line >> 1) & 1) * 8;
+        if constexpr (KIND == QM) return (line & 1) * 2 + ((line >> 1) & 1) * 8;
         return 0;
     }
 
@@ -98,48 +109,52 @@ struct MgTile {
     // Loads of k tile kt of a plane (base: that tile's) into `lds`.
     static __device__ __forceinline__ void load(const MgOperand& o, const char* base, int kt, uint32_t lds, int wave,
                                                 int lane, const uint32_t (&off)[LOADS]) {
+        bool tail = false;  // the operand ends inside this tile
+        if constexpr (KIND == KM) tail = (kt + 1) * (BK / 8) - 1 > o.last_k;
+        if constexpr (KIND == MM) tail = (kt + 1) * BK - 1 > o.last_k;
+        if (__builtin_expect(tail, 0)) {
 #pragma unroll
-        for (int s = 0; s < LOADS; ++s) {
-            uint32_t v = off[s];
-            if constexpr (KIND == KM) {
-                if ((kt + 1) * 8 - 1 > o.last_k) {  // the row ends inside this tile: its last chunk again
-                    const int c = (wave + WAVES * s) * 64 + lane, col = (c % 8) ^ swizzle(c / 8);
-                    v -= (uint32_t)max(0, kt * 8 + col - o.last_k) * 16;
+            for (int s = 0; s < LOADS; ++s) {
+                const int c = (wave + WAVES * s) * 64 + lane, line = c / ROW_CHUNKS;
+                uint32_t v = off[s];
+                if constexpr (KIND == KM) {  // its last chunk again: x is zero there
+                    const int col = (c % ROW_CHUNKS) ^ swizzle(line);
+                    v -= (uint32_t)max(0, kt * (BK / 8) + col - o.last_k) * 16;
+                } else {  // its last row again: G is zero there
+                    v -= (uint32_t)((int64_t)max(0, kt * BK + line - o.last_k) * o.ld * 2);
                 }
+                load_to_lds(lds + (wave + WAVES * s) * 1024, base, v);
             }
-            if constexpr (KIND == MM) {
-                if ((kt + 1) * MG_BK - 1 > o.last_k) {
-                    const int line = ((wave + WAVES * s) * 64 + lane) / ROW_CHUNKS;
-                    v -= (uint32_t)((int64_t)max(0, kt * MG_BK + line - o.last_k) * o.ld * 2);
-                }
-            }
-            load_to_lds(lds + (wave + WAVES * s) * 1024, base, v);
+        } else {
+#pragma unroll
+            for (int s = 0; s < LOADS; ++s) load_to_lds(lds + (wave + WAVES * s) * 1024, base, off[s]);
         }
     }
 
-    // Fragment of rows [row, row + 32) and k [16 kk, 16 kk + 16) of a tile.
+    // Fragment of rows [row, row + 16) and k [32 kk, 32 kk + 32) of a tile.
     static __device__ __forceinline__ s16x8 fragment(const char* tile, int row, int kk, int lane) {
+        const int g = lane / 16, i = lane & 15;
         if constexpr (KIND == KM) {
-            const int r = row + (lane & 31);
-            return *reinterpret_cast<const s16x8*>(tile + r * 128 + (((kk * 2 + lane / 32) ^ swizzle(lane & 31)) * 16));
+            return *reinterpret_cast<const s16x8*>(tile + (row + i) * (BK * 2) + (((kk * 4 + g) ^ swizzle(i)) * 16));
         } else if constexpr (KIND == QK) {
-            const char* p = tile + (kk * 4 + (lane / 32) * 2) * (ROWS * 8) + (row + (lane & 31)) * 8;
+            // (row is a multiple of 16 tokens, 8 chunks; i / 2 < 8)
+            const int quad = kk * 8 + g * 2;
+            const char* p = tile + quad * (ROWS * 8) + (((row + i) / 2) ^ swizzle(quad)) * 16 + (i & 1) * 8;
             const s16x4 a = *reinterpret_cast<const s16x4*>(p);
             const s16x4 b = *reinterpret_cast<const s16x4*>(p + ROWS * 8);
             return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         } else {
-            const int g = lane / 16, i = lane & 15;
             s16x4 v[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const int k = kk * 16 + (g / 2) * 8 + t * 4 + i / 4;
+                const int k = kk * 32 + g * 8 + t * 4 + i / 4;
                 const char* p;
                 if constexpr (KIND == MM) {
-                    const int chunk = row / 8 + (g & 1) * 2 + (i & 3) / 2;
+                    const int chunk = row / 8 + (i & 3) / 2;
                     p = tile + k * (ROWS * 2) + (chunk ^ swizzle(k)) * 16 + (i & 1) * 8;
                 } else {
-                    const int quad = row / 4 + (g & 1) * 4 + (i & 3);
-                    p = tile + quad * 512 + ((k / 2) ^ swizzle(quad)) * 16 + (k & 1) * 8;
+                    const int quad = row / 4 + (i & 3);
+                    p = tile + quad * (BK * 8) + ((k / 2) ^ swizzle(quad)) * 16 + (k & 1) * 8;
                 }
                 v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MG_LDS s16x4*)p);
             }
@@ -149,32 +164,50 @@ struct MgTile {
 };
 
 template <int PLANES>
-__device__ __forceinline__ f32x16 mg_mfma(s16x8 a, s16x8 b, f32x16 c) {
+__device__ __forceinline__ f32x4 mg_mfma(s16x8 a, s16x8 b, f32x4 c) {
     if constexpr (PLANES == 1)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
                                                        0, 0, 0);
     else
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                       0, 0);
 }
 
+// A tile of eight waves with both operands along k alternates its waves in
+// two groups (see mg_walk); the others read and multiply in turn, each
+// wave's reads under its neighbours' products.  Measured at 256 x 256 (one
+// MI355X, 8192 x 8192 x 4096 and 8192 x 4096 x 8192, float32 stored): in two
+// groups KM KM 1181-1210 TFLOP/s, MM QK 1168-1201, MM QM 1224-1254; in turn
+// 1132-1151, 1242-1245, 1253-1257.  32 x 32 x 16 instructions, four waves of
+// 128 x 128, more stages or loads spread between products all stay within
+// 1080-1290: with the matrix units busy 60-65% of the cycles the clock
+// settles at 1.85-2.05 GHz, lower where they are busier.
 template <int BM_, int BN_, int WM_, int WN_, OperandKind KA_, OperandKind KB_, int PLANES_>
 struct MgConfig {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PLANES = PLANES_;
     static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
-    static constexpr int FM = BM / WM / 32, FN = BN / WN / 32;  // 32 x 32 blocks of a wave
+    static constexpr bool PINGPONG = WAVES == 8 && KA_ == KM && KB_ == KM;
+    static constexpr int BK = PINGPONG ? 32 : 64, STAGES = PINGPONG ? 4 : 2;
+    static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16 x 16 blocks of a wave
     static constexpr int PASSES = PLANES == 1 ? 1 : 3;
-    using TA = MgTile<KA_, BM, WAVES>;
-    using TB = MgTile<KB_, BN, WAVES>;
+    using TA = MgTile<KA_, BM, BK, WAVES>;
+    using TB = MgTile<KB_, BN, BK, WAVES>;
     static constexpr int STAGE = TA::BYTES + TB::BYTES;
-    static constexpr int LDS_BYTES = 2 * STAGE;
+    static constexpr int LDS_BYTES = STAGES * STAGE;
 };
 
-// Walks k tiles [0, ktiles) of both operands.  The sums of row
-// 32 fi + 8 (r / 4) + 4 (lane / 32) + r % 4 and column 32 fj + lane % 32 of
-// the wave's part are acc[fi][fj][r].  `lds`: LDS_BYTES.
+// Walks the first `ktiles` k tiles of both operands, each of which starts
+// at or before an operand's last_k.  The sum of row
+// 16 fi + 4 (lane / 16) + r and column 16 fj + lane % 16 of the wave's part
+// is acc[fi][fj][r].  `lds`: LDS_BYTES.
+//
+// Eight waves: the second four (one more wave on each SIMD) run half a turn
+// behind the first, held by one extra barrier.  A turn is: read a tile's
+// fragments and start the loads of the tile STAGES - 1 further; barrier;
+// multiply; barrier.  So on each SIMD one wave multiplies while the other
+// reads, and the loads have two to three turns to land.
 template <typename C>
-__device__ __forceinline__ void mg_walk(f32x16 (&acc)[C::FM][C::FN], const MgOperand& a, const MgOperand& b,
+__device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOperand& a, const MgOperand& b,
                                         int ktiles, char* lds) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -185,11 +218,13 @@ __device__ __forceinline__ void mg_walk(f32x16 (&acc)[C::FM][C::FN], const MgOpe
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const uint32_t lds0 = lds_offset(lds);
     const int total = ktiles * C::PASSES;
+    if (total <= 0) {
+        mg_sync<0>();
+        return;
+    }
     // the next tile to load: its pass and its k tile
     int pass = 0, kt = 0;
     const char *pa = a.base, *pb = b.base;
@@ -206,26 +241,68 @@ __device__ __forceinline__ void mg_walk(f32x16 (&acc)[C::FM][C::FN], const MgOpe
             pb = b.base + (C::PASSES == 3 && pass == 1 ? b.plane_bytes : 0);
         }
     };
-    if (total > 0) load_next(0);
-    mg_sync();
-    for (int t = 0; t < total; ++t) {
-        const int buf = t & 1;
-        if (t + 1 < total) load_next(buf ^ 1);
+    s16x8 fa[C::FM], fb[C::FN];
+    auto read = [&](int buf, int kk) {
         const char* ta = lds + buf * C::STAGE;
         const char* tb = ta + C::TA::BYTES;
 #pragma unroll
-        for (int kk = 0; kk < MG_BK / 16; ++kk) {
-            s16x8 fa[C::FM], fb[C::FN];
+        for (int j = 0; j < C::FN; ++j) fb[j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j) fb[j] = C::TB::fragment(tb, brow + 32 * j, kk, lane);
+        for (int i = 0; i < C::FM; ++i) fa[i] = C::TA::fragment(ta, arow + 16 * i, kk, lane);
+    };
+    auto multiply = [&]() {
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i) fa[i] = C::TA::fragment(ta, arow + 32 * i, kk, lane);
+        for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-                for (int j = 0; j < C::FN; ++j) acc[i][j] = mg_mfma<C::PLANES>(fa[i], fb[j], acc[i][j]);
+            for (int j = 0; j < C::FN; ++j) acc[i][j] = mg_mfma<C::PLANES>(fa[i], fb[j], acc[i][j]);
+    };
+    if constexpr (C::PINGPONG) {
+        constexpr int S = C::STAGES, PENDING = (S - 2) * (C::TA::LOADS + C::TB::LOADS);
+        for (int q = 0; q < S - 1 && q < total; ++q) load_next(q);
+        // tile 0 is in LDS
+        if (S - 1 <= total)
+            mg_sync<PENDING>();
+        else
+            mg_sync<0>();
+        const bool second = wave >= C::WAVES / 2;
+        if (second) mg_barrier();
+        int buf = 0, lbuf = S - 1;
+        for (int t = 0; t < total; ++t) {
+            // into tile t - 1's buffer: the other group read it before the
+            // barrier that started this turn
+            const bool more = t + S - 1 < total;
+            if (more) load_next(lbuf);
+            read(buf, 0);
+            // this wave's share of tile t + 1 has landed
+            if (more)
+                mg_sync<PENDING>();
+            else
+                mg_sync<0>();
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);
+            multiply();
+            __builtin_amdgcn_s_setprio(0);
+            __builtin_amdgcn_sched_barrier(0);
+            mg_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            lbuf = buf;
+            buf = buf + 1 == S ? 0 : buf + 1;
         }
-        mg_sync();
+        if (!second) mg_barrier();
+        mg_sync<0>();
+    } else {
+        load_next(0);
+        mg_sync<0>();
+        for (int t = 0; t < total; ++t) {
+            const int buf = t & 1;
+            if (t + 1 < total) load_next(buf ^ 1);
+#pragma unroll
+            for (int kk = 0; kk < C::BK / 32; ++kk) {
+                read(buf, kk);
+                multiply();
+            }
+            mg_sync<0>();
+        }
     }
 }
 

@@ -84,11 +84,11 @@ extern "C" __global__ __launch_bounds__(256) void trop_ce_merge(TropCeParams p) 
     using Logits256_##NAME = MgConfig<256, 256, 2, 4, KM, KM, PLANES>;                                  \
     using Logits128_##NAME = MgConfig<128, 128, 2, 2, KM, KM, PLANES>;                                  \
     using Logits64_##NAME = MgConfig<128, 64, 4, 1, KM, KM, PLANES>;                                    \
-    using GradX256_##NAME = MgConfig<256, 256, 2, 4, QK, MM, PLANES>;                                   \
-    using GradX128_##NAME = MgConfig<128, 128, 2, 2, QK, MM, PLANES>;                                   \
-    using GradX64_##NAME = MgConfig<64, 128, 1, 4, QK, MM, PLANES>;                                     \
-    using GradW256_##NAME = MgConfig<256, 256, 2, 4, QM, MM, PLANES>;                                   \
-    using GradW128_##NAME = MgConfig<128, 128, 2, 2, QM, MM, PLANES>;                                   \
+    using GradX256_##NAME = MgConfig<256, 256, 2, 4, MM, QK, PLANES>;                                   \
+    using GradX128_##NAME = MgConfig<128, 128, 2, 2, MM, QK, PLANES>;                                   \
+    using GradX64_##NAME = MgConfig<128, 64, 4, 1, MM, QK, PLANES>;                                     \
+    using GradW256_##NAME = MgConfig<256, 256, 2, 4, MM, QM, PLANES>;                                   \
+    using GradW128_##NAME = MgConfig<128, 128, 2, 2, MM, QM, PLANES>;                                   \
     TROP_CE_TILE(stats256_##NAME, Logits256_##NAME, (ce_logits_body<Logits256_##NAME, CE_STATS>))       \
     TROP_CE_TILE(stats128_##NAME, Logits128_##NAME, (ce_logits_body<Logits128_##NAME, CE_STATS>))       \
     TROP_CE_TILE(grad256_##NAME, Logits256_##NAME, (ce_logits_body<Logits256_##NAME, CE_GRAD>))         \
