@@ -579,8 +579,8 @@ TROP_API trop_status tropical_linear_cross_entropy_forward(trop_dtype dtype, con
 /*
  * Workspace (bytes) of the linear cross entropy calls for this shape:
  * backward == 0 for the forward, else for the backward.  It holds packed
- * operands, per-tile softmax statistics and, for the backward, one piece of
- * the label set's gradients of the logits; never tokens x vocab values.
+ * operands, per-tile softmax statistics and, for the backward, the logits'
+ * gradient of one piece of the label set (256 MiB at most, or 256 labels).
  * The size serves every row stride and alignment.  Host-only.
  * Errors: TROP_ERR_INVALID_ARGUMENT (bad dtype, negative size, NULL bytes).
  */

@@ -57,57 +57,62 @@ __device__ __forceinline__ bool ce_counts(const TropCeParams& p, int64_t t) {
 }
 
 // ---- which tokens count ----------------------------------------------------
-// One workgroup of 1024: each thread takes a run of consecutive tokens, a
-// scan over the runs' counts gives their places.
+// One workgroup of 1024: each wave takes a run of consecutive tokens, 64 at a
+// time, and counts by ballot; the waves' counts give each its first place.
 __device__ __forceinline__ void ce_keep_body(const TropCeParams& p) {
     __shared__ int32_t wave_count[16];
     __shared__ float wave_max[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-    const int64_t run = (p.tokens + 1023) / 1024;
-    const int64_t n0 = min((int64_t)threadIdx.x * run, p.tokens), n1 = min(n0 + run, p.tokens);
+    const int64_t run = (p.tokens + 1023) / 1024 * 64;
+    const int64_t n0 = min(wave * run, p.tokens), n1 = min(n0 + run, p.tokens);
     int32_t count = 0;
     float gmax = 0.f;
-    for (int64_t n = n0; n < n1; ++n) {
-        if (!ce_counts(p, ce_target(p, n))) continue;
-        ++count;
-        if (p.backward) gmax = fmaxf(gmax, fabsf(p.grad_loss[n * p.grad_loss_stride]));
-    }
-    int32_t before = count;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int32_t v = __shfl_up(before, o, 64);
-        if (lane >= o) before += v;
+#pragma unroll 4
+    for (int64_t b = n0; b < n1; b += 64) {
+        const int64_t n = b + lane;
+        const bool keep = n < n1 && ce_counts(p, ce_target(p, n));
+        count += __popcll(__ballot(keep));
+        if (p.backward && keep) gmax = fmaxf(gmax, fabsf(p.grad_loss[n * p.grad_loss_stride]));
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) gmax = fmaxf(gmax, __shfl_xor(gmax, o, 64));
-    if (lane == 63) wave_count[wave] = before;
-    if (lane == 0) wave_max[wave] = gmax;
+    if (lane == 0) {
+        wave_count[wave] = count;
+        wave_max[wave] = gmax;
+    }
     __syncthreads();
-    int32_t base = 0, total = 0;
+    int32_t at = 0, total = 0;
     gmax = 0.f;
+#pragma unroll
     for (int w = 0; w < 16; ++w) {
-        if (w < wave) base += wave_count[w];
+        if (w < wave) at += wave_count[w];
         total += wave_count[w];
         gmax = fmaxf(gmax, wave_max[w]);
     }
     if (!(gmax > 0.f) || gmax > 3.0e38f) gmax = 1.f;  // nothing to scale, or an infinite weight
-    int32_t at = base + before - count;
-    for (int64_t n = n0; n < n1; ++n) {
-        const int64_t t = ce_target(p, n);
-        const bool keep = ce_counts(p, t);
-        p.slot[n] = keep ? at : -1;
+#pragma unroll 4
+    for (int64_t b = n0; b < n1; b += 64) {
+        const int64_t n = b + lane;
+        const int64_t t = n < n1 ? ce_target(p, n) : -1;
+        const bool keep = n < n1 && ce_counts(p, t);
+        const uint64_t mask = __ballot(keep);
         if (keep) {
-            p.rows[at] = (int32_t)n;
-            p.kept_target[at] = (int32_t)t;
+            const int32_t i = at + __popcll(mask & (((uint64_t)1 << lane) - 1));
+            p.slot[n] = i;
+            p.rows[i] = (int32_t)n;
+            p.kept_target[i] = (int32_t)t;
             if (p.backward) {
-                p.kept_lse[at] = p.lse_in[n];
-                p.kept_grad[at] = p.grad_loss[n * p.grad_loss_stride] / gmax;
+                p.kept_lse[i] = p.lse_in[n];
+                p.kept_grad[i] = p.grad_loss[n * p.grad_loss_stride] / gmax;
             }
-            ++at;
-        } else if (!p.backward) {
-            p.loss[n] = 0.f;
-            p.lse[n] = 0.f;
+        } else if (n < n1) {
+            p.slot[n] = -1;
+            if (!p.backward) {
+                p.loss[n] = 0.f;
+                p.lse[n] = 0.f;
+            }
         }
+        at += __popcll(mask);
     }
     if (threadIdx.x == 0) {
         p.control->kept = total;
@@ -128,8 +133,9 @@ __device__ __forceinline__ void ce_magnitude_body(const TropCeParams& p) {
         // a wave to a row
         for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < rows; r += (int64_t)p.max_parts * 4) {
             const float* row = m + (which ? r : (int64_t)p.rows[r]) * ld;
+#pragma unroll 4
             for (int64_t c = lane * 4; c < p.width; c += 256) {
-                const FloatVec<4> v = load_row<float, 4>(row, c, p.width);
+                const FloatVec<4> v = load_row_stream<float, 4>(row, c, p.width);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float a = fabsf(v[e]);
@@ -184,21 +190,20 @@ __device__ __forceinline__ void ce_pack8(const void* row, int64_t c, int64_t wid
     }
 }
 
-// Kept rows of x, in order, and zero rows up to a whole tile.  A workgroup
-// takes a row; for float32 each reduces the partial maxima, and the first
-// leaves the exponents for the kernels after it.
+// Kept rows of x, in order, and zero rows up to a whole tile.  A wave takes
+// a row; for float32 each workgroup reduces the partial maxima, and the
+// first leaves the exponents for the kernels after it.
 template <int PLANES>
 __device__ __forceinline__ void ce_pack_x_body(const TropCeParams& p) {
-    const int64_t kept = p.control->kept, i = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t kept = p.control->kept, i = (int64_t)blockIdx.x * 4 + wave;
     __shared__ float lds[2][4];
     int32_t e = 0;
     if constexpr (PLANES == 2) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
         float best[2];
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-            float b = 0.f;
-            for (int q = threadIdx.x; q < p.max_parts; q += 256) b = fmaxf(b, p.magnitude[which * TROP_CE_MAX_PARTS + q]);
+            float b = (int)threadIdx.x < p.max_parts ? p.magnitude[which * TROP_CE_MAX_PARTS + threadIdx.x] : 0.f;
 #pragma unroll
             for (int o = 32; o > 0; o >>= 1) b = fmaxf(b, __shfl_xor(b, o, 64));
             if (lane == 0) lds[which][wave] = b;
@@ -208,7 +213,7 @@ __device__ __forceinline__ void ce_pack_x_body(const TropCeParams& p) {
         for (int which = 0; which < 2; ++which)
             best[which] = fmaxf(fmaxf(lds[which][0], lds[which][1]), fmaxf(lds[which][2], lds[which][3]));
         e = ce_scale_exp(best[0]);
-        if (i == 0 && threadIdx.x == 0) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
             p.control->x_exp = e;
             p.control->w_exp = ce_scale_exp(best[1]);
         }
@@ -217,7 +222,8 @@ __device__ __forceinline__ void ce_pack_x_body(const TropCeParams& p) {
     const size_t eb = PLANES == 1 ? 2 : 4;
     const char* row = i < kept ? static_cast<const char*>(p.x) + (int64_t)p.rows[i] * p.ldx * eb : nullptr;
     char* out = static_cast<char*>(p.xp) + i * p.width_p * 2;
-    for (int64_t c = threadIdx.x * 8; c < p.width_p; c += 256 * 8)
+#pragma unroll 2
+    for (int64_t c = lane * 8; c < p.width_p; c += 64 * 8)
         ce_pack8<PLANES>(row, c, row ? p.width : 0, e, out + c * 2, p.padded * p.width_p * 2);
 }
 
@@ -460,29 +466,40 @@ __device__ __forceinline__ void ce_grad_x_body(const TropCeParams& p, char* lds)
     }
 }
 
-// grad_w of a BM-column x BN-label tile: the whole sum over the kept tokens.
+// What the float32 sums of grad_w have to be multiplied by.
+template <int PLANES>
+__device__ __forceinline__ float ce_grad_w_scale(const TropCeParams& p) {
+    const float scale = p.control->grad_max;
+    if constexpr (PLANES == 2) return ldexpf(scale, -15 - p.control->x_exp);
+    return scale;
+}
+
+// grad_w of a BM-column x BN-label tile: the sum over the kept tokens, or
+// over part `split` of them into the part's float32 sums (few tiles).
 template <typename C, typename T>
 __device__ __forceinline__ void ce_grad_w_body(const TropCeParams& p, char* lds) {
     const int64_t kept = p.control->kept;
-    int64_t mi, ni;
-    if (!ce_tile(blockIdx.x, (min(p.piece, p.vocab - p.v0) + C::BN - 1) / C::BN, (p.width + C::BM - 1) / C::BM, mi, ni))
-        return;
+    const int64_t tn = (p.width + C::BM - 1) / C::BM;
+    int64_t mi, q;
+    if (!ce_tile(blockIdx.x, (min(p.piece, p.vocab - p.v0) + C::BN - 1) / C::BN, tn * p.gw_splits, mi, q)) return;
+    const int64_t ni = q % tn, split = q / tn;
+    const int64_t ktiles = (kept + C::BK - 1) / C::BK, per = (ktiles + p.gw_splits - 1) / p.gw_splits;
+    const int64_t kt0 = min(split * per, ktiles), kt1 = min(kt0 + per, ktiles), k0 = kt0 * C::BK;
     MgOperand a, b;
-    a.base = static_cast<const char*>(p.xp) + ni * C::BM * 2;
+    a.base = static_cast<const char*>(p.xp) + (k0 * p.width_p + ni * C::BM) * 2;
     a.ld = p.width_p;
     a.plane_bytes = p.padded * p.width_p * 2;
     a.k_bytes = C::BK * p.width_p * 2;
     a.last_row = (int32_t)((p.width_p - ni * C::BM) / 8 - 1);
     a.last_k = 0x7fffffff;
-    b.base = static_cast<const char*>(p.g) + mi * (C::BN / 4) * p.padded * 8;
+    b.base = static_cast<const char*>(p.g) + (mi * (C::BN / 4) * p.padded + k0) * 8;
     b.ld = p.padded;
     b.plane_bytes = p.piece * p.padded * 2;
     b.k_bytes = C::BK * 8;
     b.last_row = b.last_k = 0;
     f32x4 acc[C::FM][C::FN];
-    mg_walk<C>(acc, a, b, (int)((kept + C::BK - 1) / C::BK), lds);
-    float scale = p.control->grad_max;
-    if constexpr (C::PLANES == 2) scale = ldexpf(scale, -15 - p.control->x_exp);
+    mg_walk<C>(acc, a, b, (int)(kt1 - kt0), lds);
+    const float scale = p.gw_splits > 1 ? 1.f : ce_grad_w_scale<C::PLANES>(p);
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
     const int64_t c0 = ni * C::BM + (wave / C::WN) * (C::BM / C::WM) + 4 * (lane / 16);
     const int64_t v0 = p.v0 + mi * C::BN + (wave % C::WN) * (C::BN / C::WN) + (lane & 15);
@@ -491,62 +508,91 @@ __device__ __forceinline__ void ce_grad_w_body(const TropCeParams& p, char* lds)
         const int64_t v = v0 + 16 * j;
         if (v >= p.vocab) continue;
         T* out = static_cast<T*>(p.grad_w) + v * p.ldgw;
+        float* part = p.gw_part + (split * p.piece + (v - p.v0)) * p.width_p;
 #pragma unroll
         for (int i = 0; i < C::FM; ++i) {
             FloatVec<4> g;
 #pragma unroll
             for (int r = 0; r < 4; ++r) g[r] = acc[i][j][r] * scale;
-            if (c0 + 16 * i < p.width) store_row<T, 4>(out, c0 + 16 * i, p.width, from_float<T, 4>(g));
+            if (c0 + 16 * i >= p.width) continue;
+            if (p.gw_splits > 1)
+                *reinterpret_cast<f32x4*>(part + c0 + 16 * i) = g;
+            else
+                store_row<T, 4>(out, c0 + 16 * i, p.width, from_float<T, 4>(g));
         }
     }
 }
 
-// grad_x rows: the parts' sums in order, scaled; zeros for tokens that do
-// not count.  A workgroup takes a row.
+// Columns [c, c + 4) of a row summed over `splits` parts, `step` floats apart.
+__device__ __forceinline__ FloatVec<4> ce_sum_parts(const float* q, int splits, int64_t step, float scale) {
+    FloatVec<4> s = load_vec<float, 4>(q);
+#pragma unroll 8
+    for (int k = 1; k < splits; ++k) {
+        const FloatVec<4> o = load_vec<float, 4>(q + k * step);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += o[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] *= scale;
+    return s;
+}
+
+// grad_x: the parts' sums in order, scaled; zeros for tokens that do not
+// count.  A workgroup takes 1024 columns of a row (blockIdx.x = row blocks + block).
 template <typename T, int PLANES>
 __device__ __forceinline__ void ce_finish_body(const TropCeParams& p) {
-    const int64_t n = blockIdx.x;
-    const int32_t i = p.slot[n];
-    float scale = p.control->grad_max;
-    if constexpr (PLANES == 2) scale = ldexpf(scale, -15 - p.control->w_exp);
-    T* out = static_cast<T*>(p.grad_x) + n * p.ldgx;
-    for (int64_t c = threadIdx.x * 4; c < p.width; c += 256 * 4) {
-        FloatVec<4> s = {0.f, 0.f, 0.f, 0.f};
-        if (i >= 0) {
-            const float* q = p.gx_part + (int64_t)i * p.width_p + c;
-            s = load_vec<float, 4>(q);  // width_p is a multiple of 64
-            for (int k = 1; k < p.splits; ++k) {
-                q += p.padded * p.width_p;
-                const FloatVec<4> o = load_vec<float, 4>(q);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] += o[e];
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] *= scale;
-        }
-        store_row<T, 4>(out, c, p.width, from_float<T, 4>(s));
+    const int64_t blocks = (p.width + 1023) / 1024;
+    const int64_t n = blockIdx.x / blocks, c = (blockIdx.x % blocks) * 1024 + threadIdx.x * 4;
+    if (c >= p.width) return;
+    int64_t i = n;
+    float scale = 1.f;
+    if (p.identity) {
+        if (!ce_counts(p, ce_target(p, n))) i = -1;
+    } else {
+        i = p.slot[n];
+        scale = p.control->grad_max;
+        if constexpr (PLANES == 2) scale = ldexpf(scale, -15 - p.control->w_exp);
     }
+    FloatVec<4> s = {0.f, 0.f, 0.f, 0.f};
+    if (i >= 0) s = ce_sum_parts(p.gx_part + i * p.width_p + c, p.splits, p.padded * p.width_p, scale);
+    store_row<T, 4>(static_cast<T*>(p.grad_x) + n * p.ldgx, c, p.width, from_float<T, 4>(s));
+}
+
+// grad_w of a piece from its parts, likewise.
+template <typename T, int PLANES>
+__device__ __forceinline__ void ce_finish_w_body(const TropCeParams& p) {
+    const int64_t blocks = (p.width + 1023) / 1024;
+    const int64_t r = blockIdx.x / blocks, c = (blockIdx.x % blocks) * 1024 + threadIdx.x * 4;
+    if (c >= p.width) return;
+    const FloatVec<4> s = ce_sum_parts(p.gw_part + r * p.width_p + c, p.gw_splits, p.piece * p.width_p,
+                                       ce_grad_w_scale<PLANES>(p));
+    store_row<T, 4>(static_cast<T*>(p.grad_w) + (p.v0 + r) * p.ldgw, c, p.width, from_float<T, 4>(s));
 }
 
 // ---- few tokens ------------------------------------------------------------
-// Up to 64 tokens: w is streamed once from HBM into the 16 x 16 matrix
-// instructions' registers, no LDS, no packing: a wave takes 16 RF labels and
-// all tokens (16 per block column).  A lane reads 16 bytes of row lane % 16
-// at k chunk lane / 16, so a row's four lanes read 64 consecutive bytes.
-// float32 stays float32 (four 16x16x4 instructions per 16 k; the order of k
-// within them is the same for both operands and otherwise free).
-template <typename T, int RF, int NB>
+// Up to 64 tokens: w is streamed from HBM straight into the matrix
+// instructions' registers, with no LDS copy and no packing.  The logits' pass
+// reads it once; the backward reads it once more for grad_x and writes
+// grad_w.  All three are bound by those bytes, so they want many loads in
+// flight: the four waves of a workgroup share its rows and split the sum.
+//
+// Logits: a workgroup takes 16 RF labels and all tokens (16 to a block
+// column).  A lane reads 16 bytes of row lane % 16 at k chunk lane / 16, so
+// a row's four lanes read 64 consecutive bytes.  float32 stays float32 (four
+// 16x16x4 instructions per 16 k; the order of k within them is the same for
+// both operands and otherwise free).  G is kept in float32, [label][16 NB].
+template <typename T, int RF, int NB, CeEpilogue EPI>
 __device__ __forceinline__ void ce_few_body(const TropCeParams& p) {
     constexpr int VEC = 16 / sizeof(T), KSTEP = 4 * VEC, U = 4;
     using V = typename VecOf<T, VEC>::raw;
-    __shared__ float2 part[4][NB * 16];
+    __shared__ f32x4 sums[3][RF * NB][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-    const int64_t v_wave = ((int64_t)blockIdx.x * 4 + wave) * 16 * RF;
+    const int64_t v0 = p.v0 + (int64_t)blockIdx.x * 16 * RF;
     const T* wr[RF];
     const T* xr[NB];
 #pragma unroll
     for (int i = 0; i < RF; ++i)
-        wr[i] = static_cast<const T*>(p.w) + min(v_wave + 16 * i + (lane & 15), p.vocab - 1) * p.ldw;
+        wr[i] = static_cast<const T*>(p.w) + min(v0 + 16 * i + (lane & 15), p.vocab - 1) * p.ldw;
 #pragma unroll
     for (int j = 0; j < NB; ++j)
         xr[j] = static_cast<const T*>(p.x) + min((int64_t)(16 * j + (lane & 15)), p.tokens - 1) * p.ldx;
@@ -566,20 +612,26 @@ __device__ __forceinline__ void ce_few_body(const TropCeParams& p) {
             }
     };
     const int kl = (lane / 16) * VEC;
-    int64_t k = 0;
-    for (; k + U * KSTEP <= p.width; k += U * KSTEP) {
+    // Each workgroup starts its walk along the rows one unit (256 bytes)
+    // after the one before it: rows are often a multiple of 8 KiB apart, and
+    // workgroups in step would ask the same few memory channels (512 MiB of
+    // 8 KiB rows: 93 us against 127).
+    const int64_t units = p.width / (U * KSTEP), first = units ? blockIdx.x % units : 0;
+    for (int64_t u4 = wave; u4 < units; u4 += 4) {
+        const int64_t at = u4 + first < units ? u4 + first : u4 + first - units;
+        const int64_t k = at * U * KSTEP + kl;
         V a[U][RF], b[U][NB];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int i = 0; i < RF; ++i) a[u][i] = load_vec<T, VEC>(wr[i] + k + kl + u * KSTEP);
+            for (int i = 0; i < RF; ++i) a[u][i] = load_vec<T, VEC>(wr[i] + k + u * KSTEP);
 #pragma unroll
-            for (int j = 0; j < NB; ++j) b[u][j] = load_vec<T, VEC>(xr[j] + k + kl + u * KSTEP);
+            for (int j = 0; j < NB; ++j) b[u][j] = load_vec<T, VEC>(xr[j] + k + u * KSTEP);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) step(a[u], b[u]);
     }
-    for (; k < p.width; k += KSTEP) {
+    for (int64_t k = units * U * KSTEP + wave * KSTEP; k < p.width; k += 4 * KSTEP) {
         V a[RF], b[NB];
 #pragma unroll
         for (int i = 0; i < RF; ++i) a[i] = load_row<T, VEC>(wr[i], k + kl, p.width);
@@ -587,71 +639,250 @@ __device__ __forceinline__ void ce_few_body(const TropCeParams& p) {
         for (int j = 0; j < NB; ++j) b[j] = load_row<T, VEC>(xr[j], k + kl, p.width);
         step(a, b);
     }
+    // the waves' sums, added in wave order by the first
+    if (wave > 0) {
+#pragma unroll
+        for (int i = 0; i < RF; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) sums[wave - 1][i * NB + j][lane] = acc[i][j];
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int i = 0; i < RF; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const f32x4 o = sums[q][i * NB + j][lane];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][j][r] += o[r];
+            }
     // row 16 i + 4 (lane / 16) + r, column 16 j + lane % 16
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
         const int64_t n = 16 * j + (lane & 15);
         const int64_t t = n < p.tokens ? ce_target(p, n) : -1;
-        float m = -INFINITY;
+        if constexpr (EPI == CE_STATS) {
+            float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < RF; ++i)
+            for (int i = 0; i < RF; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t v = v_wave + 16 * i + 4 * (lane / 16) + r;
-                if (v == t && v < p.vocab) p.target_logit[n] = acc[i][j][r];
-                if (v >= p.vocab) acc[i][j][r] = -INFINITY;
-                m = nan_max(m, acc[i][j][r]);
-            }
-        m = nan_max(m, __shfl_xor(m, 16, 64));
-        m = nan_max(m, __shfl_xor(m, 32, 64));
-        const float base = m == -INFINITY ? 0.f : m;
-        float s = 0.f;
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t v = v0 + 16 * i + 4 * (lane / 16) + r;
+                    if (v == t && v < p.vocab) p.target_logit[n] = acc[i][j][r];
+                    if (v >= p.vocab) acc[i][j][r] = -INFINITY;
+                    m = nan_max(m, acc[i][j][r]);
+                }
+            m = nan_max(m, __shfl_xor(m, 16, 64));
+            m = nan_max(m, __shfl_xor(m, 32, 64));
+            const float base = m == -INFINITY ? 0.f : m;
+            float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < RF; ++i)
+            for (int i = 0; i < RF; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s += expf(acc[i][j][r] - base);
-        s += __shfl_xor(s, 16, 64);
-        s += __shfl_xor(s, 32, 64);
-        if (lane < 16) part[wave][16 * j + lane] = make_float2(m, s);
-    }
-    __syncthreads();
-    if (threadIdx.x < NB * 16 && threadIdx.x < p.tokens) {
-        float2 a = part[0][threadIdx.x];
+                for (int r = 0; r < 4; ++r) s += expf(acc[i][j][r] - base);
+            s += __shfl_xor(s, 16, 64);
+            s += __shfl_xor(s, 32, 64);
+            if (lane < 16 && n < p.tokens)
+                reinterpret_cast<float2*>(p.stats)[n * p.tiles + blockIdx.x] = make_float2(m, s);
+        } else {
+            const bool on = n < p.tokens && ce_counts(p, t);
+            const float lse = on ? p.lse_in[n] : 0.f;
+            const float weight = on ? p.grad_loss[n * p.grad_loss_stride] : 0.f;
+            float* out = static_cast<float*>(p.g) + (v0 - p.v0) * (16 * NB) + n;
 #pragma unroll
-        for (int q = 1; q < 4; ++q) {
-            const float2 o = part[q][threadIdx.x];
-            const float m = nan_max(a.x, o.x), base = m == -INFINITY ? 0.f : m;
-            a.y = a.y * expf(a.x - base) + o.y * expf(o.x - base);
-            a.x = m;
+            for (int i = 0; i < RF; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * i + 4 * (lane / 16) + r;
+                    const float g = expf(acc[i][j][r] - lse) - (v0 + row == t ? 1.f : 0.f);
+                    out[(int64_t)row * (16 * NB)] = on && v0 + row < p.vocab ? g * weight : 0.f;
+                }
         }
-        reinterpret_cast<float2*>(p.stats)[threadIdx.x * p.tiles + blockIdx.x] = a;
+    }
+}
+
+// grad_x of all tokens, 16 DV columns to a workgroup, over part
+// blockIdx.x / column blocks of the piece's labels: 16x16x4 float32
+// instructions with k = label, so that a lane reads DV consecutive columns
+// (16 bytes) of label lane / 16 and instruction j takes columns DV m + j as
+// its rows m.  bfloat16 w is widened: the product is exact.  The four waves
+// take 4 U labels in turn; their sums are added in wave order.
+template <typename T, int NB>
+__device__ __forceinline__ void ce_few_grad_x_body(const TropCeParams& p) {
+    constexpr int DV = 16 / sizeof(T), U = NB < 4 && sizeof(T) == 4 ? 8 : 4, NP = 16 * NB;
+    __shared__ f32x4 sums[DV * NB][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t blocks = (p.width + 16 * DV - 1) / (16 * DV);
+    const int64_t split = blockIdx.x / blocks;
+    const int64_t c = (blockIdx.x % blocks) * 16 * DV + (lane & 15) * DV;
+    const int64_t labels = min(p.piece, p.vocab - p.v0), per = (int64_t)p.split_tiles * 4 * U * 4;
+    const int64_t r0 = split * per, r1 = min(r0 + per, labels);
+    const float* g = static_cast<const float*>(p.g) + (lane & 15);
+    f32x4 acc[DV][NB] = {};
+    for (int64_t r = r0 + wave * 4 * U; r < r1; r += 4 * 4 * U) {
+        typename VecOf<T, DV>::raw w[U];
+        float b[U][NB];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = r + 4 * u + lane / 16;  // a label past the part's end: its G taken as 0
+            w[u] = load_row<T, DV>(static_cast<const T*>(p.w) + (p.v0 + min(row, labels - 1)) * p.ldw, c, p.width);
+#pragma unroll
+            for (int j = 0; j < NB; ++j) b[u][j] = row < r1 ? g[row * NP + 16 * j] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const FloatVec<DV> f = to_float<T, DV>(w[u]);
+#pragma unroll
+            for (int d = 0; d < DV; ++d)
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    acc[d][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[d], b[u][j], acc[d][j], 0, 0, 0);
+        }
+    }
+    for (int q = 1; q < 4; ++q) {
+        __syncthreads();
+        if (wave == q) {
+#pragma unroll
+            for (int d = 0; d < DV; ++d)
+#pragma unroll
+                for (int j = 0; j < NB; ++j) sums[d * NB + j][lane] = acc[d][j];
+        }
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int d = 0; d < DV; ++d)
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const f32x4 o = sums[d * NB + j][lane];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[d][j][e] += o[e];
+                }
+        }
+    }
+    if (wave > 0) return;
+    // instruction d, row 4 (lane / 16) + e, column lane % 16: columns
+    // DV (4 (lane / 16) + e) + d of token 16 j + lane % 16
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        const int64_t n = 16 * j + (lane & 15);
+        if (n >= p.tokens) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t col = (blockIdx.x % blocks) * 16 * DV + DV * (4 * (lane / 16) + e);
+            if (col >= p.width_p) continue;
+#pragma unroll
+            for (int h = 0; h < DV; h += 4) {
+                f32x4 v = {acc[h][j][e], acc[h + 1][j][e], acc[h + 2][j][e], acc[h + 3][j][e]};
+                f32x4* o = reinterpret_cast<f32x4*>(p.gx_part + (split * p.padded + n) * p.width_p + col + h);
+                if (p.accumulate) {
+                    const f32x4 before = *o;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] += before[q];
+                }
+                *o = v;
+            }
+        }
+    }
+}
+
+// grad_w: a wave takes 16 VB labels and every (column parts)-th block of
+// 16 DV columns; k = token, G stays in registers, x comes from the caches.
+// Instruction d takes column d of chunk (m % 4) 4 + m / 4 (of DV columns) as
+// its row m: a lane ends with chunk 4 e + lane / 16 in register e, so that a
+// label's four lanes store 64 consecutive bytes.
+template <typename T, int NB>
+__device__ __forceinline__ void ce_few_grad_w_body(const TropCeParams& p) {
+    constexpr int DV = 16 / sizeof(T), VB = 2, NP = 16 * NB;
+    using V = typename VecOf<T, DV>::raw;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t labels = min(p.piece, p.vocab - p.v0);
+    const int64_t groups = (labels + 64 * VB - 1) / (64 * VB);
+    const int64_t part = blockIdx.x / groups, parts = gridDim.x / groups;
+    const int64_t r0 = ((blockIdx.x % groups) * 4 + wave) * 16 * VB;
+    if (r0 >= labels) return;
+    const float* g = static_cast<const float*>(p.g);
+    float b[VB][4 * NB];
+    bool on[4 * NB];  // token lane / 16 + 4 s counts
+    const int chunk = (lane & 3) * 4 + (lane & 15) / 4;
+#pragma unroll
+    for (int s = 0; s < 4 * NB; ++s) {
+        const int64_t n = 4 * s + lane / 16;
+        on[s] = n < p.tokens && ce_counts(p, ce_target(p, n));
+#pragma unroll
+        for (int i = 0; i < VB; ++i) {
+            const int64_t row = r0 + 16 * i + (lane & 15);
+            b[i][s] = row < labels ? g[row * NP + n] : 0.f;
+        }
+    }
+    // (workgroups start at different columns, as in the logits' pass)
+    const int64_t blocks = (p.width + 16 * DV - 1) / (16 * DV), mine = (blocks - part + parts - 1) / parts;
+    for (int64_t k = 0; k < mine; ++k) {
+        const int64_t c0 = (part + (k + blockIdx.x % groups) % mine * parts) * 16 * DV;
+        f32x4 acc[DV][VB] = {};
+#pragma unroll
+        for (int s = 0; s < 4 * NB; ++s) {
+            V x = {};
+            if (on[s])
+                x = load_row<T, DV>(static_cast<const T*>(p.x) + (4 * s + lane / 16) * p.ldx, c0 + chunk * DV, p.width);
+            const FloatVec<DV> f = to_float<T, DV>(x);
+#pragma unroll
+            for (int d = 0; d < DV; ++d)
+#pragma unroll
+                for (int i = 0; i < VB; ++i)
+                    acc[d][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[d], b[i][s], acc[d][i], 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < VB; ++i) {
+            const int64_t row = r0 + 16 * i + (lane & 15);
+            if (row >= labels) continue;
+            T* out = static_cast<T*>(p.grad_w) + (p.v0 + row) * p.ldgw;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t col = c0 + DV * (4 * e + lane / 16);
+                FloatVec<DV> v;
+#pragma unroll
+                for (int d = 0; d < DV; ++d) v[d] = acc[d][i][e];
+                if (col < p.width) store_row<T, DV>(out, col, p.width, from_float<T, DV>(v));
+            }
+        }
     }
 }
 
 // ---- statistics joined -----------------------------------------------------
-// A wave takes a token: its tiles' maxima and sums, then loss and lse.
+// A workgroup takes a token: its tiles' maxima and sums, then loss and lse.
 __device__ __forceinline__ void ce_merge_body(const TropCeParams& p) {
-    const int lane = threadIdx.x & 63;
-    const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    __shared__ float2 lds[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t i = blockIdx.x;
     const int64_t kept = p.identity ? p.tokens : (int64_t)p.control->kept;
     if (i >= kept) return;
     const int64_t n = p.identity ? i : (int64_t)p.rows[i];
     if (p.identity && !ce_counts(p, ce_target(p, n))) {
-        if (lane == 0) p.loss[n] = p.lse[n] = 0.f;
+        if (threadIdx.x == 0) p.loss[n] = p.lse[n] = 0.f;
         return;
     }
     const float2* q = reinterpret_cast<const float2*>(p.stats) + i * p.tiles;
     float m = -INFINITY, s = 0.f;
-    for (int64_t t = lane; t < p.tiles; t += 64) {
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < p.tiles; t += 256) {
         const float2 a = q[t];
         const float top = nan_max(m, a.x), base = top == -INFINITY ? 0.f : top;
         s = s * expf(m - base) + a.y * expf(a.x - base);
         m = top;
     }
-    const float top = wave_nan_max(m), base = top == -INFINITY ? 0.f : top;
+    float top = wave_nan_max(m), base = top == -INFINITY ? 0.f : top;
     s = wave_sum(s * expf(m - base));
-    if (lane == 0) {
-        const float lse = top + logf(s);
+    if (lane == 0) lds[wave] = make_float2(top, s);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        m = nan_max(nan_max(lds[0].x, lds[1].x), nan_max(lds[2].x, lds[3].x));
+        base = m == -INFINITY ? 0.f : m;
+        s = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) s += lds[w].y * expf(lds[w].x - base);
+        const float lse = m + logf(s);
         p.lse[n] = lse;
         p.loss[n] = lse - p.target_logit[i];
     }

@@ -81,30 +81,49 @@ extern "C" __global__ __launch_bounds__(256) void trop_ce_merge(TropCeParams p) 
     extern "C" __global__ __launch_bounds__(256) void trop_ce_finish_##NAME(TropCeParams p) {           \
         ce_finish_body<T, PLANES>(p);                                                                   \
     }                                                                                                   \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_finish_w_##NAME(TropCeParams p) {         \
+        ce_finish_w_body<T, PLANES>(p);                                                                 \
+    }                                                                                                   \
     using Logits256_##NAME = MgConfig<256, 256, 2, 4, KM, KM, PLANES>;                                  \
     using Logits128_##NAME = MgConfig<128, 128, 2, 2, KM, KM, PLANES>;                                  \
-    using Logits64_##NAME = MgConfig<128, 64, 4, 1, KM, KM, PLANES>;                                    \
     using GradX256_##NAME = MgConfig<256, 256, 2, 4, MM, QK, PLANES>;                                   \
     using GradX128_##NAME = MgConfig<128, 128, 2, 2, MM, QK, PLANES>;                                   \
-    using GradX64_##NAME = MgConfig<128, 64, 4, 1, MM, QK, PLANES>;                                     \
     using GradW256_##NAME = MgConfig<256, 256, 2, 4, MM, QM, PLANES>;                                   \
     using GradW128_##NAME = MgConfig<128, 128, 2, 2, MM, QM, PLANES>;                                   \
     TROP_CE_TILE(stats256_##NAME, Logits256_##NAME, (ce_logits_body<Logits256_##NAME, CE_STATS>))       \
     TROP_CE_TILE(stats128_##NAME, Logits128_##NAME, (ce_logits_body<Logits128_##NAME, CE_STATS>))       \
     TROP_CE_TILE(grad256_##NAME, Logits256_##NAME, (ce_logits_body<Logits256_##NAME, CE_GRAD>))         \
     TROP_CE_TILE(grad128_##NAME, Logits128_##NAME, (ce_logits_body<Logits128_##NAME, CE_GRAD>))         \
-    TROP_CE_TILE(grad64_##NAME, Logits64_##NAME, (ce_logits_body<Logits64_##NAME, CE_GRAD>))            \
     TROP_CE_TILE(gx256_##NAME, GradX256_##NAME, ce_grad_x_body<GradX256_##NAME>)                        \
     TROP_CE_TILE(gx128_##NAME, GradX128_##NAME, ce_grad_x_body<GradX128_##NAME>)                        \
-    TROP_CE_TILE(gx64_##NAME, GradX64_##NAME, ce_grad_x_body<GradX64_##NAME>)                           \
     TROP_CE_TILE(gw256_##NAME, GradW256_##NAME, (ce_grad_w_body<GradW256_##NAME, T>))                   \
     TROP_CE_TILE(gw128_##NAME, GradW128_##NAME, (ce_grad_w_body<GradW128_##NAME, T>))                   \
-    TROP_CE_FEW(NAME, T, 1, 1) TROP_CE_FEW(NAME, T, 1, 2) TROP_CE_FEW(NAME, T, 1, 4)                    \
-    TROP_CE_FEW(NAME, T, 2, 1) TROP_CE_FEW(NAME, T, 2, 2) TROP_CE_FEW(NAME, T, 2, 4)
-// few tokens: blocks of 16 labels a wave, of 16 tokens
-#define TROP_CE_FEW(NAME, T, RF, NB)                                                                          \
-    extern "C" __global__ __launch_bounds__(256) void trop_ce_few_r##RF##_n##NB##_##NAME(TropCeParams p) {     \
-        ce_few_body<T, RF, NB>(p);                                                                             \
+    TROP_CE_FEW(NAME, T, 1)                                                                             \
+    TROP_CE_FEW(NAME, T, 2)                                                                             \
+    TROP_CE_FEW(NAME, T, 4)                                                                             \
+    TROP_CE_FEW_GRAD(NAME, T, 1)                                                                        \
+    TROP_CE_FEW_GRAD(NAME, T, 2)
+// few tokens: NB blocks of 16; one or two blocks of 16 labels a workgroup
+#define TROP_CE_FEW(NAME, T, NB)                                                                          \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_few1_n##NB##_##NAME(TropCeParams p) {        \
+        ce_few_body<T, 1, NB, CE_STATS>(p);                                                                \
+    }                                                                                                      \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_few2_n##NB##_##NAME(TropCeParams p) {        \
+        ce_few_body<T, 2, NB, CE_STATS>(p);                                                                \
+    }
+#define TROP_CE_FEW_GRAD(NAME, T, NB)                                                                     \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_few_grad1_n##NB##_##NAME(TropCeParams p) {   \
+        ce_few_body<T, 1, NB, CE_GRAD>(p);                                                                 \
+    }                                                                                                      \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_few_grad2_n##NB##_##NAME(TropCeParams p) {   \
+        ce_few_body<T, 2, NB, CE_GRAD>(p);                                                                 \
+    }                                                                                                      \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_few_gx_n##NB##_##NAME(TropCeParams p) {      \
+        ce_few_grad_x_body<T, NB>(p);                                                                      \
+    }                                                                                                      \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_few_gw_n##NB##_##NAME(TropCeParams p) {      \
+        ce_few_grad_w_body<T, NB>(p);                                                                      \
     }
 TROP_CE_ENTRIES(f32, float, 2)
 TROP_CE_ENTRIES(bf16, bf16, 1)
+TROP_CE_FEW_GRAD(f32, float, 4)

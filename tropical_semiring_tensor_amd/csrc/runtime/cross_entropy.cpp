@@ -12,8 +12,6 @@ constexpr int64_t kBK = 64;               // k of a product's tile
 constexpr int64_t kPieceBytes = 256 << 20;  // of a piece of G, and of packed w
 constexpr int64_t kMaxTokens = 1 << 22, kMaxWidth = 1 << 22;  // 32-bit offsets within a tile
 constexpr int64_t kMaxVocab = ((int64_t)1 << 31) - 512;       // label indices are 32-bit
-constexpr int kFill = 192;  // workgroups that count as filling the device with 256 x 256 tiles
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
@@ -25,23 +23,57 @@ int64_t piece_labels(int64_t vocab, int64_t bytes) {
     return round_up(ceil_div(vocab, ceil_div(vocab, most)), 256);
 }
 
+// Time (us) of a product in `tiles` tiles of `kind` (0: 256 x 256, 1: 128 x
+// 128), each walking `ktiles` k tiles of 64 in one pass.  Measured on one
+// MI355X: a 256 x 256 workgroup has a CU to itself and takes 1.75 us a k
+// tile; a 128 x 128 one takes 0.85 us alone on a CU and 1.15 beside another;
+// a tile costs 6 us or 4 besides (first loads, epilogue).
+double tile_time(int kind, int64_t tiles, int64_t ktiles) {
+    if (kind == 0) return (double)ceil_div(tiles, 256) * ((double)ktiles * 1.75 + 6.0);
+    if (tiles <= 256) return (double)ktiles * 0.85 + 4.0;
+    return (double)ceil_div(tiles, 512) * ((double)ktiles * 1.15 + 4.0);
+}
+
+// The tile and the number of parts along k for a rows x cols product over
+// `ktiles` (all passes) whose parts are `bytes` each and are written and
+// read again when there are several: the pair with the least time.
+void choose_tile(int64_t rows, int64_t cols, int64_t ktiles, int64_t bytes, int* tile, int64_t* splits) {
+    double best = 0;
+    *tile = 1;
+    *splits = 1;
+    for (int kind = 0; kind < 2; ++kind) {
+        const int64_t edge = kind == 0 ? 256 : 128, tiles = ceil_div(rows, edge) * ceil_div(cols, edge);
+        for (int64_t n = 1; n <= 16 && (n == 1 || ktiles / n >= 8); ++n) {
+            double t = tile_time(kind, tiles * n, ceil_div(ktiles, n));
+            if (n > 1) t += 4.0 + (double)(2 * n * bytes) / 4e6;  // one more launch, 4 TB/s
+            if ((kind == 0 && n == 1) || t < best) {
+                best = t;
+                *tile = kind;
+                *splits = n;
+            }
+        }
+    }
+}
+
 struct CePlan {
     int64_t planes, padded, width_p;
-    bool few;           // forward of few tokens: no packing
+    bool few;           // few tokens: streaming kernels, no packing
     bool packed;        // w is read from packed pieces
     int64_t piece;      // labels of a piece (a multiple of 256; forward unpacked: all)
-    int logits_tile, gx_tile, gw_tile;  // 0: 256, 1: 128, 2: 64 tokens
-    int few_rows, few_tokens;           // the streaming kernel's blocks (16 each)
+    int logits_tile, gx_tile, gw_tile;  // 0: 256, 1: 128
+    int few_blocks;     // streaming kernels: log2 of the blocks of 16 tokens
+    int few_rows;       // and blocks of 16 labels of a logits workgroup
     int64_t tiles;      // statistics per token
-    int64_t splits;
+    int64_t splits, gw_splits;
+    int64_t split_tiles;  // streaming grad_x: rounds of a part
     int64_t max_parts;
     // workspace offsets
-    size_t control, rows, slot, kept_target, kept_lse, kept_grad, magnitude, stats, target_logit, xp, wp, g, gx_part;
+    size_t control, rows, slot, kept_target, kept_lse, kept_grad, magnitude, stats, target_logit, xp, wp, g, gx_part,
+        gw_part;
     size_t bytes;
 };
 
-int64_t logits_bm(const CePlan& c) { return c.logits_tile == 0 ? 256 : 128; }
-int64_t logits_bn(const CePlan& c) { return c.logits_tile == 0 ? 256 : c.logits_tile == 1 ? 128 : 64; }
+int64_t tile_edge(int tile) { return tile == 0 ? 256 : 128; }
 
 bool take(CePlan* c, size_t* at, int64_t bytes) {
     *at = c->bytes;
@@ -51,27 +83,56 @@ bool take(CePlan* c, size_t* at, int64_t bytes) {
     return true;
 }
 
-// tokens, width, vocab in range (check_sizes), vocab and width >= 1.
-bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool backward, bool packed, CePlan* c) {
-    *c = CePlan();
-    c->planes = dt == TROP_BF16 ? 1 : 2;
-    c->padded = round_up(tokens > 0 ? tokens : 1, 256);
-    c->width_p = round_up(width, kBK);
-    c->packed = packed;
-    c->bytes = 256;  // room to align the caller's pointer
-    c->few = !backward && tokens <= TROP_CE_FEW;
+// Streaming kernels (at most TROP_CE_FEW tokens).
+bool plan_few(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool backward, CePlan* c) {
+    c->few = true;
+    c->few_blocks = tokens <= 16 ? 0 : tokens <= 32 ? 1 : 2;
+    const int64_t np = (int64_t)16 << c->few_blocks;
+    // two blocks of labels a workgroup share its token registers; one where
+    // two would leave fewer than four workgroups for each CU
+    c->few_rows = vocab >= 1024 * 32 ? 2 : 1;
     bool ok = true;
-    if (c->few) {
-        c->few_tokens = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
-        // two blocks of labels a wave reuse its token registers; one where
-        // there would be fewer than two workgroups for each CU
-        c->few_rows = vocab >= 512 * 128 ? 2 : 1;
-        c->tiles = ceil_div(vocab, 64 * c->few_rows);
+    if (!backward) {
+        c->piece = vocab;
+        c->tiles = ceil_div(vocab, 16 * c->few_rows);
         ok &= take(c, &c->stats, tokens * c->tiles * 8);
         ok &= take(c, &c->target_logit, tokens * 4);
         return ok;
     }
+    c->piece = piece_labels(vocab, np * 4);
+    ok &= take(c, &c->g, (c->piece + 32) * np * 4);
+    // grad_x: about 1024 workgroups (four a CU), each of at least two rounds
+    // of the labels that its four waves take at a time
+    const int64_t round = dt == TROP_BF16 || c->few_blocks == 2 ? 64 : 128;
+    const int64_t blocks = ceil_div(width, dt == TROP_BF16 ? 128 : 64), rounds = ceil_div(c->piece, round);
+    int64_t n = ceil_div(1024, blocks);
+    if (n > ceil_div(rounds, 2)) n = ceil_div(rounds, 2);
+    if (n > 64) n = 64;
+    c->split_tiles = ceil_div(rounds, n);
+    c->splits = ceil_div(rounds, c->split_tiles);
+    ok &= take(c, &c->gx_part, c->splits * c->padded * c->width_p * 4);
+    return ok;
+}
+
+// tokens, width, vocab in range (check_sizes), vocab and width >= 1.
+bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool backward, bool packed, CePlan* c) {
+    *c = CePlan();
+    c->planes = dt == TROP_BF16 ? 1 : 2;
+    c->width_p = round_up(width, kBK);
+    c->bytes = 256;  // room to align the caller's pointer
+    c->splits = c->gw_splits = 1;
+    // (the backward's float32 sums of widened bfloat16 cost more than the
+    // tiles' packing from 33 tokens on: 32768 x 4096, 60 tokens 541 us, 65 in
+    // tiles 303; 30 tokens 308)
+    if (tokens > 0 && tokens <= (backward && dt == TROP_BF16 ? TROP_CE_FEW / 2 : TROP_CE_FEW)) {
+        c->padded = TROP_CE_FEW;
+        return plan_few(dt, tokens, width, vocab, backward, c);
+    }
+    c->padded = round_up(tokens > 0 ? tokens : 1, 256);
+    c->packed = packed;
+    bool ok = true;
     const int64_t w_row = c->width_p * 2 * c->planes, g_label = c->padded * 2 * c->planes;
+    const int64_t passes = c->planes == 1 ? 1 : 3, count = tokens > 0 ? tokens : 1;
     const bool whole = !backward && !packed;  // one launch over all labels
     c->piece = round_up(vocab, 256);
     if (!whole) {
@@ -80,9 +141,11 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
         c->piece = piece_labels(vocab, bytes);
     }
     const int64_t labels = c->piece < vocab ? c->piece : vocab;
-    // 256 x 256 tiles have the best rate; smaller ones where they would
-    // leave CUs without a tile
-    c->logits_tile = ceil_div(labels, 256) * ceil_div(tokens, 256) >= kFill ? 0 : tokens > 64 || !backward ? 1 : 2;
+    const int64_t wtiles = ceil_div(width, kBK) * passes;
+    c->logits_tile = tile_time(0, ceil_div(labels, 256) * ceil_div(count, 256), wtiles) <=
+                             tile_time(1, ceil_div(labels, 128) * ceil_div(count, 128), wtiles)
+                         ? 0
+                         : 1;
     ok &= take(c, &c->control, sizeof(TropCeControl));
     ok &= take(c, &c->rows, c->padded * 4);
     ok &= take(c, &c->slot, c->padded * 4);
@@ -94,7 +157,7 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     ok &= take(c, &c->xp, c->padded * c->width_p * 2 * c->planes);
     if (packed) ok &= take(c, &c->wp, c->piece * w_row);
     if (!backward) {
-        c->tiles = ceil_div(vocab, logits_bm(*c));
+        c->tiles = ceil_div(vocab, tile_edge(c->logits_tile));
         ok &= take(c, &c->stats, tokens * c->tiles * 8);
         ok &= take(c, &c->target_logit, c->padded * 4);
         return ok;
@@ -103,23 +166,11 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     ok &= take(c, &c->kept_grad, c->padded * 4);
     // (the weight's 256-label tiles may read past a piece that ends at 128)
     ok &= take(c, &c->g, (c->piece + 256) * g_label);
-    const int64_t ktiles = ceil_div(labels, kBK);
-    // grad_x: parts along the labels until the device is full, each of 8 k
-    // tiles at least; 256 tiles where that fills it
-    int64_t tiles = ceil_div(tokens > 0 ? tokens : 1, 256) * ceil_div(width, 256);
-    const int64_t most = ktiles / 8 > 1 ? ktiles / 8 : 1;
-    c->gx_tile = tiles * (most < 16 ? most : 16) >= kFill && tokens > 128 ? 0 : tokens > 64 ? 1 : 2;
-    int64_t want = 256;
-    if (c->gx_tile) {
-        tiles = ceil_div(tokens > 0 ? tokens : 1, c->gx_tile == 1 ? 128 : 64) * ceil_div(width, 128);
-        want = 512;
-    }
-    c->splits = want / tiles;
-    if (c->splits > most) c->splits = most;
-    if (c->splits > 16) c->splits = 16;
-    if (c->splits < 1) c->splits = 1;
-    ok &= take(c, &c->gx_part, c->splits * c->padded * c->width_p * 4);
-    c->gw_tile = ceil_div(labels, 256) * ceil_div(width, 256) >= kFill ? 0 : 1;
+    const int64_t part = c->padded * c->width_p * 4;
+    choose_tile(count, width, ceil_div(labels, kBK) * passes, part, &c->gx_tile, &c->splits);
+    ok &= take(c, &c->gx_part, c->splits * part);
+    choose_tile(labels, width, ceil_div(count, kBK) * passes, labels * c->width_p * 4, &c->gw_tile, &c->gw_splits);
+    if (c->gw_splits > 1) ok &= take(c, &c->gw_part, c->gw_splits * c->piece * c->width_p * 4);
     return ok;
 }
 
@@ -200,11 +251,14 @@ TropCeParams params(const CeCall& a, const CePlan& c, char* ws) {
     p.wp = ws + c.wp;
     p.g = ws + c.g;
     p.gx_part = reinterpret_cast<float*>(ws + c.gx_part);
+    p.gw_part = reinterpret_cast<float*>(ws + c.gw_part);
     p.padded = c.padded;
     p.width_p = c.width_p;
     p.tiles = c.tiles;
     p.w_packed = c.packed;
     p.splits = (int32_t)c.splits;
+    p.gw_splits = (int32_t)c.gw_splits;
+    p.identity = c.few;
     p.max_parts = (int32_t)c.max_parts;
     return p;
 }
@@ -216,7 +270,7 @@ trop_status prepare_tokens(int dev, const CeCall& a, const CePlan& c, const Trop
     trop_status st = train_launch(dev, TK_CE_KEEP, TROP_T_CE_PACK, 1, 1024, &p, s);
     if (st == TROP_OK && c.planes == 2)
         st = train_launch(dev, TK_CE_MAGNITUDE, TROP_T_CE_PACK, c.max_parts, 256, &p, s);
-    if (st == TROP_OK) st = train_launch(dev, typed(TK_CE_PACK_X, a.dt), TROP_T_CE_PACK, c.padded, 256, &p, s);
+    if (st == TROP_OK) st = train_launch(dev, typed(TK_CE_PACK_X, a.dt), TROP_T_CE_PACK, c.padded / 4, 256, &p, s);
     return st;
 }
 
@@ -224,10 +278,76 @@ trop_status prepare_tokens(int dev, const CeCall& a, const CePlan& c, const Trop
 trop_status prepare_piece(int dev, const CeCall& a, const CePlan& c, int64_t v0, TropCeParams& p, hipStream_t s) {
     const int64_t labels = a.vocab - v0 < c.piece ? a.vocab - v0 : c.piece;
     p.v0 = v0;
-    p.piece = round_up(labels, logits_bm(c));
-    p.tile0 = v0 / logits_bm(c);
+    p.piece = round_up(labels, tile_edge(c.logits_tile));
+    p.tile0 = v0 / tile_edge(c.logits_tile);
     if (!c.packed) return TROP_OK;
     return train_launch(dev, typed(TK_CE_PACK_W, a.dt), TROP_T_CE_PACK, p.piece < 4096 ? p.piece : 4096, 256, &p, s);
+}
+
+// A streaming kernel of the family at `id` (`per`: its kernels for one label block).
+TrainKernelId few_kernel(int id, int per, const CePlan& c, trop_dtype dt) {
+    return typed(id + per * (c.few_rows - 1) + 2 * c.few_blocks, dt);
+}
+
+// The backward's pieces with the streaming kernels.
+trop_status few_pieces(int dev, const CeCall& a, const CePlan& c, TropCeParams& p, hipStream_t s) {
+    trop_status st = TROP_OK;
+    const bool bf = a.dt == TROP_BF16;
+    for (int64_t v0 = 0; st == TROP_OK && v0 < a.vocab; v0 += c.piece) {
+        const int64_t labels = a.vocab - v0 < c.piece ? a.vocab - v0 : c.piece;
+        p.v0 = v0;
+        p.piece = labels;
+        p.accumulate = v0 > 0;
+        p.split_tiles = (int32_t)c.split_tiles;
+        st = train_launch(dev, few_kernel(TK_CE_FEW_GRAD, 5, c, a.dt), TROP_T_CE_LOGITS,
+                          ceil_div(labels, 16 * c.few_rows), 256, &p, s);
+        if (st == TROP_OK && p.grad_x)
+            st = train_launch(dev, few_kernel(TK_CE_FEW_GX, 0, c, a.dt), TROP_T_CE_GRAD,
+                              ceil_div(a.width, bf ? 128 : 64) * c.splits, 256, &p, s);
+        if (st == TROP_OK && p.grad_w) {
+            // a workgroup's labels; the columns are shared out until there
+            // are four workgroups for each CU
+            const int64_t groups = ceil_div(labels, 128);
+            int64_t parts = ceil_div(1024, groups);
+            const int64_t blocks = ceil_div(a.width, bf ? 128 : 64);
+            if (parts > blocks) parts = blocks;
+            st = train_launch(dev, few_kernel(TK_CE_FEW_GW, 0, c, a.dt), TROP_T_CE_GRAD, groups * parts, 256, &p, s);
+        }
+    }
+    return st;
+}
+
+// The backward's pieces with the products' tiles.
+trop_status tile_pieces(int dev, const CeCall& a, const CePlan& c, TropCeParams& p, hipStream_t s) {
+    const int64_t tokens = a.tokens > 0 ? a.tokens : 1;
+    trop_status st = prepare_tokens(dev, a, c, p, s);
+    for (int64_t v0 = 0; st == TROP_OK && v0 < a.vocab; v0 += c.piece) {
+        const int64_t labels = a.vocab - v0 < c.piece ? a.vocab - v0 : c.piece;
+        st = prepare_piece(dev, a, c, v0, p, s);
+        if (st == TROP_OK && a.tokens > 0) {
+            const int64_t edge = tile_edge(c.logits_tile);
+            st = train_launch(dev, typed(TK_CE_GRAD + 2 * c.logits_tile, a.dt), TROP_T_CE_LOGITS,
+                              p.piece / edge * ceil_div(tokens, edge), c.logits_tile == 0 ? 512 : 256, &p, s);
+        }
+        if (st == TROP_OK && p.grad_x) {
+            const int64_t edge = tile_edge(c.gx_tile);
+            p.split_tiles = (int32_t)ceil_div(ceil_div(labels, kBK), c.splits);
+            p.accumulate = v0 > 0;
+            st = train_launch(dev, typed(TK_CE_GX + 2 * c.gx_tile, a.dt), TROP_T_CE_GRAD,
+                              ceil_div(tokens, edge) * ceil_div(a.width, edge) * c.splits, c.gx_tile == 0 ? 512 : 256,
+                              &p, s);
+        }
+        if (st == TROP_OK && p.grad_w) {
+            const int64_t edge = tile_edge(c.gw_tile);
+            st = train_launch(dev, typed(TK_CE_GW + 2 * c.gw_tile, a.dt), TROP_T_CE_GRAD,
+                              ceil_div(labels, edge) * ceil_div(a.width, edge) * c.gw_splits,
+                              c.gw_tile == 0 ? 512 : 256, &p, s);
+            if (st == TROP_OK && c.gw_splits > 1)
+                st = train_launch(dev, typed(TK_CE_FINISH_W, a.dt), TROP_T_CE_MERGE,
+                                  labels * ceil_div(a.width, 1024), 256, &p, s);
+        }
+    }
+    return st;
 }
 
 trop_status ce_forward(const CeCall& a, float* loss, float* lse) {
@@ -251,20 +371,19 @@ trop_status ce_forward(const CeCall& a, float* loss, float* lse) {
     p.lse = lse;
     const hipStream_t s = static_cast<hipStream_t>(a.stream);
     if (c.few) {
-        p.identity = 1;
-        const int id = TK_CE_FEW + 2 * (3 * (c.few_rows - 1) + (c.few_tokens == 4 ? 2 : c.few_tokens - 1));
-        st = train_launch(dev, typed(id, a.dt), TROP_T_CE_LOGITS, c.tiles, 256, &p, s);
+        st = train_launch(dev, few_kernel(TK_CE_FEW, 6, c, a.dt), TROP_T_CE_LOGITS,
+                          c.tiles, 256, &p, s);
     } else {
         st = prepare_tokens(dev, a, c, p, s);
         for (int64_t v0 = 0; st == TROP_OK && v0 < a.vocab; v0 += c.piece) {
             st = prepare_piece(dev, a, c, v0, p, s);
+            const int64_t edge = tile_edge(c.logits_tile);
             if (st == TROP_OK)
                 st = train_launch(dev, typed(TK_CE_STATS + 2 * c.logits_tile, a.dt), TROP_T_CE_LOGITS,
-                                  p.piece / logits_bm(c) * ceil_div(a.tokens, logits_bn(c)),
-                                  c.logits_tile == 0 ? 512 : 256, &p, s);
+                                  p.piece / edge * ceil_div(a.tokens, edge), c.logits_tile == 0 ? 512 : 256, &p, s);
         }
     }
-    if (st == TROP_OK) st = train_launch(dev, TK_CE_MERGE, TROP_T_CE_MERGE, ceil_div(a.tokens, 4), 256, &p, s);
+    if (st == TROP_OK) st = train_launch(dev, TK_CE_MERGE, TROP_T_CE_MERGE, a.tokens, 256, &p, s);
     return st == TROP_OK ? ok() : st;
 }
 
@@ -306,31 +425,10 @@ trop_status ce_backward(const CeCall& a, const float* lse, const float* grad_los
     p.ldgx = ldgx;
     p.ldgw = ldgw;
     const hipStream_t s = static_cast<hipStream_t>(a.stream);
-    const int64_t tokens = a.tokens > 0 ? a.tokens : 1;
-    st = prepare_tokens(dev, a, c, p, s);
-    for (int64_t v0 = 0; st == TROP_OK && v0 < a.vocab; v0 += c.piece) {
-        st = prepare_piece(dev, a, c, v0, p, s);
-        if (st == TROP_OK && a.tokens > 0)
-            st = train_launch(dev, typed(TK_CE_GRAD + 2 * c.logits_tile, a.dt), TROP_T_CE_LOGITS,
-                              p.piece / logits_bm(c) * ceil_div(tokens, logits_bn(c)),
-                              c.logits_tile == 0 ? 512 : 256, &p, s);
-        if (st == TROP_OK && grad_x) {
-            const int64_t bm = c.gx_tile == 0 ? 256 : c.gx_tile == 1 ? 128 : 64, bn = c.gx_tile == 0 ? 256 : 128;
-            const int64_t labels = a.vocab - v0 < c.piece ? a.vocab - v0 : c.piece;
-            p.split_tiles = (int32_t)ceil_div(ceil_div(labels, kBK), c.splits);
-            p.accumulate = v0 > 0;
-            st = train_launch(dev, typed(TK_CE_GX + 2 * c.gx_tile, a.dt), TROP_T_CE_GRAD,
-                              ceil_div(tokens, bm) * ceil_div(a.width, bn) * c.splits, c.gx_tile == 0 ? 512 : 256, &p,
-                              s);
-        }
-        if (st == TROP_OK && grad_w) {
-            const int64_t b = c.gw_tile == 0 ? 256 : 128;
-            st = train_launch(dev, typed(TK_CE_GW + 2 * c.gw_tile, a.dt), TROP_T_CE_GRAD,
-                              ceil_div(p.piece, b) * ceil_div(a.width, b), c.gw_tile == 0 ? 512 : 256, &p, s);
-        }
-    }
+    st = c.few ? few_pieces(dev, a, c, p, s) : tile_pieces(dev, a, c, p, s);
     if (st == TROP_OK && grad_x)
-        st = train_launch(dev, typed(TK_CE_FINISH, a.dt), TROP_T_CE_MERGE, a.tokens, 256, &p, s);
+        st = train_launch(dev, typed(TK_CE_FINISH, a.dt), TROP_T_CE_MERGE, a.tokens * ceil_div(a.width, 1024), 256, &p,
+                          s);
     return st == TROP_OK ? ok() : st;
 }
 

@@ -30,12 +30,17 @@ enum TrainKernelId : int {
     TK_CE_PACK_X,  // every family from here on: + (bf16 ? 1 : 0)
     TK_CE_PACK_W = TK_CE_PACK_X + 2,
     TK_CE_FINISH = TK_CE_PACK_W + 2,
-    TK_CE_STATS = TK_CE_FINISH + 2,  // + 2 tile (256, 128)
-    TK_CE_GRAD = TK_CE_STATS + 4,    // + 2 tile (256, 128, 64 tokens)
-    TK_CE_GX = TK_CE_GRAD + 6,       // + 2 tile (256, 128, 64 tokens)
-    TK_CE_GW = TK_CE_GX + 6,         // + 2 tile (256, 128)
-    TK_CE_FEW = TK_CE_GW + 4,        // + 2 (3 (label blocks - 1) + token blocks 1, 2, 4)
-    TK_COUNT = TK_CE_FEW + 12
+    TK_CE_FINISH_W = TK_CE_FINISH + 2,
+    TK_CE_STATS = TK_CE_FINISH_W + 2,  // + 2 tile (256, 128)
+    TK_CE_GRAD = TK_CE_STATS + 4,
+    TK_CE_GX = TK_CE_GRAD + 4,
+    TK_CE_GW = TK_CE_GX + 4,
+    // few tokens: + (bf16 ? 1 : 0) + 2 log2(blocks of 16 tokens: 1, 2, 4) + 6 (5) (label blocks - 1)
+    TK_CE_FEW = TK_CE_GW + 4,          // statistics
+    TK_CE_FEW_GRAD = TK_CE_FEW + 12,   // G; likewise, without bf16 for 4 blocks
+    TK_CE_FEW_GX = TK_CE_FEW_GRAD + 10,  // the gradients: without label blocks
+    TK_CE_FEW_GW = TK_CE_FEW_GX + 5,
+    TK_COUNT = TK_CE_FEW_GW + 5
 };
 
 // Current device with the training code object loaded on it.

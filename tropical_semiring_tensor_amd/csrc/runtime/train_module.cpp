@@ -36,22 +36,29 @@ const char* const kNames[] = {
     "trop_ce_pack_x_f32",         "trop_ce_pack_x_bf16",
     "trop_ce_pack_w_f32",         "trop_ce_pack_w_bf16",
     "trop_ce_finish_f32",         "trop_ce_finish_bf16",
+    "trop_ce_finish_w_f32",       "trop_ce_finish_w_bf16",
     "trop_ce_stats256_f32",       "trop_ce_stats256_bf16",
     "trop_ce_stats128_f32",       "trop_ce_stats128_bf16",
     "trop_ce_grad256_f32",        "trop_ce_grad256_bf16",
     "trop_ce_grad128_f32",        "trop_ce_grad128_bf16",
-    "trop_ce_grad64_f32",         "trop_ce_grad64_bf16",
     "trop_ce_gx256_f32",          "trop_ce_gx256_bf16",
     "trop_ce_gx128_f32",          "trop_ce_gx128_bf16",
-    "trop_ce_gx64_f32",           "trop_ce_gx64_bf16",
     "trop_ce_gw256_f32",          "trop_ce_gw256_bf16",
     "trop_ce_gw128_f32",          "trop_ce_gw128_bf16",
-    "trop_ce_few_r1_n1_f32",      "trop_ce_few_r1_n1_bf16",
-    "trop_ce_few_r1_n2_f32",      "trop_ce_few_r1_n2_bf16",
-    "trop_ce_few_r1_n4_f32",      "trop_ce_few_r1_n4_bf16",
-    "trop_ce_few_r2_n1_f32",      "trop_ce_few_r2_n1_bf16",
-    "trop_ce_few_r2_n2_f32",      "trop_ce_few_r2_n2_bf16",
-    "trop_ce_few_r2_n4_f32",      "trop_ce_few_r2_n4_bf16",
+    "trop_ce_few1_n1_f32", "trop_ce_few1_n1_bf16",
+    "trop_ce_few1_n2_f32", "trop_ce_few1_n2_bf16",
+    "trop_ce_few1_n4_f32", "trop_ce_few1_n4_bf16",
+    "trop_ce_few2_n1_f32", "trop_ce_few2_n1_bf16",
+    "trop_ce_few2_n2_f32", "trop_ce_few2_n2_bf16",
+    "trop_ce_few2_n4_f32", "trop_ce_few2_n4_bf16",
+    "trop_ce_few_grad1_n1_f32", "trop_ce_few_grad1_n1_bf16", "trop_ce_few_grad1_n2_f32",
+    "trop_ce_few_grad1_n2_bf16", "trop_ce_few_grad1_n4_f32",
+    "trop_ce_few_grad2_n1_f32", "trop_ce_few_grad2_n1_bf16", "trop_ce_few_grad2_n2_f32",
+    "trop_ce_few_grad2_n2_bf16", "trop_ce_few_grad2_n4_f32",
+    "trop_ce_few_gx_n1_f32", "trop_ce_few_gx_n1_bf16", "trop_ce_few_gx_n2_f32",
+    "trop_ce_few_gx_n2_bf16", "trop_ce_few_gx_n4_f32",
+    "trop_ce_few_gw_n1_f32", "trop_ce_few_gw_n1_bf16", "trop_ce_few_gw_n2_f32",
+    "trop_ce_few_gw_n2_bf16", "trop_ce_few_gw_n4_f32",
 };
 static_assert(sizeof(kNames) / sizeof(kNames[0]) == TK_COUNT, "training kernels");
 

@@ -91,7 +91,7 @@ struct TropAdamw8Params {
 // Tokens up to this many are scored by the streaming kernel (no packing).
 #define TROP_CE_FEW 64
 // Workgroups of the magnitude pass, each leaving two partial maxima.
-#define TROP_CE_MAX_PARTS 512
+#define TROP_CE_MAX_PARTS 256
 
 // Scalars that the first kernels of a call leave for the later ones.
 struct TropCeControl {
@@ -127,6 +127,7 @@ struct TropCeParams {
     void* wp;                 // packed piece of w: [planes][piece][width_p]
     void* g;                  // piece of the logits' gradient: [planes][piece / 4][padded][4]
     float* gx_part;           // [splits][padded][width_p]
+    float* gw_part;           // [gw_splits][piece][width_p], when gw_splits > 1
     int64_t padded, width_p;
     int64_t v0, piece;        // this launch's labels: [v0, v0 + piece), piece a multiple of the tile
     int64_t tile0;            // first statistics tile of this launch
@@ -134,6 +135,7 @@ struct TropCeParams {
     int32_t target_bytes;
     int32_t w_packed;         // the piece is read from wp (else from w itself)
     int32_t splits, split_tiles;  // gx: parts along the labels and k tiles of each
+    int32_t gw_splits;        // gw: parts along the tokens
     int32_t accumulate;       // gx: add to what the piece before left
     int32_t max_parts;        // workgroups of the magnitude pass
     int32_t identity;         // merge: kept index = token (streaming kernel)
