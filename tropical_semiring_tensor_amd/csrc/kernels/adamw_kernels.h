@@ -8,6 +8,8 @@
 // device together.  All arithmetic is one IEEE float32 operation at a time,
 // in the order the header states.
 #pragma once
+#include <type_traits>
+
 #include "train_common.h"
 
 namespace trop {
@@ -43,13 +45,13 @@ __device__ __forceinline__ void adamw_body(const TropAdamwParams& p) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t c = base + (u * 256 + threadIdx.x) * 4;
-        g[u] = load_row<T, 4>(static_cast<const T*>(e.grad), c, e.n);
-        m[u] = load_row<float, 4>(e.m, c, e.n);
-        v[u] = load_row<float, 4>(e.v, c, e.n);
+        g[u] = load_row_stream<T, 4>(static_cast<const T*>(e.grad), c, e.n);
+        m[u] = load_row_stream<float, 4>(e.m, c, e.n);
+        v[u] = load_row_stream<float, 4>(e.v, c, e.n);
         if constexpr (MASTER)
-            q[u] = load_row<float, 4>(e.master, c, e.n);
+            q[u] = load_row_stream<float, 4>(e.master, c, e.n);
         else
-            q[u] = to_float<T, 4>(load_row<T, 4>(static_cast<const T*>(e.param), c, e.n));
+            q[u] = to_float<T, 4>(load_row_stream<T, 4>(static_cast<const T*>(e.param), c, e.n));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -64,10 +66,10 @@ __device__ __forceinline__ void adamw_body(const TropAdamwParams& p) {
             q[u][i] = qq;
         }
         if (c < e.n) {
-            store_row<float, 4>(e.m, c, e.n, m[u]);
-            store_row<float, 4>(e.v, c, e.n, v[u]);
-            if constexpr (MASTER) store_row<float, 4>(e.master, c, e.n, q[u]);
-            store_row<T, 4>(static_cast<T*>(e.param), c, e.n, from_float<T, 4>(q[u]));
+            store_row_stream<float, 4>(e.m, c, e.n, m[u]);
+            store_row_stream<float, 4>(e.v, c, e.n, v[u]);
+            if constexpr (MASTER) store_row_stream<float, 4>(e.master, c, e.n, q[u]);
+            store_row_stream<T, 4>(static_cast<T*>(e.param), c, e.n, from_float<T, 4>(q[u]));
         }
     }
 }
@@ -83,21 +85,35 @@ __device__ __forceinline__ float adamw8_v(float code, float a) {
 }
 // Codes of m and v in a block of scale a (0: every element is zero).  A NaN
 // ratio takes code 0: the block's scale is NaN then, and so are its values.
-__device__ __forceinline__ int adamw8_code_m(float m, float a) {
-    const float r = fabsf(m) / (a > 0.f ? a : 1.f);
-    const float c = rintf(sqrtf(r) * 127.0f);
+__device__ __forceinline__ float adamw8_round_m(float m, float a) {
+    return rintf(sqrtf(fabsf(m) / a) * 127.0f);
+}
+__device__ __forceinline__ float adamw8_round_v(float v, float a) {
+    return rintf(sqrtf(sqrtf(v / a)) * 255.0f);
+}
+// The same through the reciprocal of a and the hardware root (1 ulp): the
+// number that is rounded is off by 8 2^-24 of itself at most, below 1.3e-4.
+// `sure` is cleared where a rounding boundary is within 2e-4, or nothing can
+// be said (infinities, NaN).
+__device__ __forceinline__ float adamw8_guess(float x, bool& sure) {
+    const float c = rintf(x);
+    sure &= fabsf(x - c) < 0.4998f;
+    return c;
+}
+__device__ __forceinline__ int adamw8_code_m(float c, float m) {
     const int k = c <= 127.f ? (int)c : 0;
     return m < 0.f ? -k : k;
 }
-__device__ __forceinline__ int adamw8_code_v(float v, float a) {
-    const float r = v / (a > 0.f ? a : 1.f);
-    const float c = rintf(sqrtf(sqrtf(r)) * 255.0f);
+__device__ __forceinline__ int adamw8_code_v(float c, float v) {
     const int k = c <= 255.f ? (int)c : 0;
     return v > 0.f ? (k > 1 ? k : 1) : 0;
 }
 
 // One wave per block of 256 elements, four a lane: the block's scale is a
-// wave reduction, no LDS.
+// wave reduction, no LDS.  Bound by the vector units before HBM when every
+// code took its own division and roots (some 150 operations an element, 1.41
+// ms for 316 million float32 elements); the guess leaves them to the one
+// wave in twenty that holds an element next to a rounding boundary.
 template <typename T, bool MASTER>
 __device__ __forceinline__ void adamw8_body(const TropAdamw8Params& p) {
     const int ti = find_tensor(p, blockIdx.x);
@@ -112,22 +128,22 @@ __device__ __forceinline__ void adamw8_body(const TropAdamw8Params& p) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t c = base + (u * 256 + threadIdx.x) * 4;
-        g[u] = load_row<T, 4>(static_cast<const T*>(e.grad), c, e.n);
-        mc[u] = load_row<int8_t, 4>(e.m, c, e.n);
-        vc[u] = load_row<uint8_t, 4>(e.v, c, e.n);
+        g[u] = load_row_stream<T, 4>(static_cast<const T*>(e.grad), c, e.n);
+        mc[u] = load_row_stream<int8_t, 4>(e.m, c, e.n);
+        vc[u] = load_row_stream<uint8_t, 4>(e.v, c, e.n);
         ma[u] = c < e.n ? e.m_scale[c / TROP_ADAMW_BLOCK_ELEMS] : 0.f;
         va[u] = c < e.n ? e.v_scale[c / TROP_ADAMW_BLOCK_ELEMS] : 0.f;
         if constexpr (MASTER)
-            q[u] = load_row<float, 4>(e.master, c, e.n);
+            q[u] = load_row_stream<float, 4>(e.master, c, e.n);
         else
-            q[u] = to_float<T, 4>(load_row<T, 4>(static_cast<const T*>(e.param), c, e.n));
+            q[u] = to_float<T, 4>(load_row_stream<T, 4>(static_cast<const T*>(e.param), c, e.n));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t c = base + (u * 256 + threadIdx.x) * 4;
         const FloatVec<4> gf = to_float<T, 4>(g[u]);
         float m[4], v[4];
-        float am = 0.f, av = 0.f;
+        uint32_t am_bits = 0, av_bits = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             m[i] = adamw8_m((float)mc[u][i], ma[u]);
@@ -136,25 +152,41 @@ __device__ __forceinline__ void adamw8_body(const TropAdamw8Params& p) {
             adamw_element(p.s, gf[i], m[i], v[i], qq);
             q[u][i] = qq;
             if (c + i >= e.n) m[i] = v[i] = 0.f;
-            am = nan_max(am, fabsf(m[i]));
-            av = nan_max(av, v[i]);
+            am_bits = max(am_bits, __builtin_bit_cast(uint32_t, m[i]) & 0x7fffffffu);
+            av_bits = max(av_bits, __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
         }
-        am = wave_nan_max(am);
-        av = wave_nan_max(av);
+        const float am = __builtin_bit_cast(float, wave_umax(am_bits));
+        const float av = __builtin_bit_cast(float, wave_umax(av_bits));
+        const float dm = am > 0.f ? am : 1.f, dv = av > 0.f ? av : 1.f;
+        const float rm = 1.0f / dm, rv = 1.0f / dv;
+        float cm[4], cv[4];
+        bool sure = true;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            mc[u][i] = (int8_t)adamw8_code_m(m[i], am);
-            vc[u][i] = (uint8_t)adamw8_code_v(v[i], av);
+            cm[i] = adamw8_guess(__builtin_amdgcn_sqrtf(fabsf(m[i]) * rm) * 127.0f, sure);
+            cv[i] = adamw8_guess(__builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(v[i] * rv)) * 255.0f, sure);
+        }
+        if (__any(!sure)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                cm[i] = adamw8_round_m(m[i], dm);
+                cv[i] = adamw8_round_v(v[i], dv);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mc[u][i] = (int8_t)adamw8_code_m(cm[i], m[i]);
+            vc[u][i] = (uint8_t)adamw8_code_v(cv[i], v[i]);
         }
         if (c < e.n) {
-            store_row<int8_t, 4>(e.m, c, e.n, mc[u]);
-            store_row<uint8_t, 4>(e.v, c, e.n, vc[u]);
+            store_row_stream<int8_t, 4>(e.m, c, e.n, mc[u]);
+            store_row_stream<uint8_t, 4>(e.v, c, e.n, vc[u]);
             if ((threadIdx.x & 63) == 0) {
                 e.m_scale[c / TROP_ADAMW_BLOCK_ELEMS] = am;
                 e.v_scale[c / TROP_ADAMW_BLOCK_ELEMS] = av;
             }
-            if constexpr (MASTER) store_row<float, 4>(e.master, c, e.n, q[u]);
-            store_row<T, 4>(static_cast<T*>(e.param), c, e.n, from_float<T, 4>(q[u]));
+            if constexpr (MASTER) store_row_stream<float, 4>(e.master, c, e.n, q[u]);
+            store_row_stream<T, 4>(static_cast<T*>(e.param), c, e.n, from_float<T, 4>(q[u]));
         }
     }
 }
@@ -165,26 +197,28 @@ __device__ __forceinline__ void adamw8_unpack_body(const TropAdamw8Params& p) {
     const TropAdamw8Entry& e = p.t[ti];
     const int64_t base = (int64_t)(blockIdx.x - (ti ? p.chunk_end[ti - 1] : 0u)) * TROP_ADAMW_CHUNK;
     constexpr int U = TROP_ADAMW_CHUNK / (256 * 4);
+    auto unpack = [&](const auto* codes, const float* scales, float* out, auto value) {
+        using K = std::remove_cv_t<std::remove_pointer_t<decltype(codes)>>;
+        typename VecOf<K, 4>::raw k[U];
+        float a[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t c = base + (u * 256 + threadIdx.x) * 4;
-        if (c >= e.n) return;
-        FloatVec<4> o;
-        if (e.param) {
-            const auto k = load_row<int8_t, 4>(e.m, c, e.n);
-            const float a = e.m_scale[c / TROP_ADAMW_BLOCK_ELEMS];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = adamw8_m((float)k[i], a);
-            store_row<float, 4>(static_cast<float*>(e.param), c, e.n, o);
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = base + (u * 256 + threadIdx.x) * 4;
+            k[u] = load_row_stream<K, 4>(codes, c, e.n);
+            a[u] = c < e.n ? scales[c / TROP_ADAMW_BLOCK_ELEMS] : 0.f;
         }
-        if (e.master) {
-            const auto k = load_row<uint8_t, 4>(e.v, c, e.n);
-            const float a = e.v_scale[c / TROP_ADAMW_BLOCK_ELEMS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = adamw8_v((float)k[i], a);
-            store_row<float, 4>(e.master, c, e.n, o);
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = base + (u * 256 + threadIdx.x) * 4;
+            FloatVec<4> o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = value((float)k[u][i], a[u]);
+            if (c < e.n) store_row_stream<float, 4>(out, c, e.n, o);
         }
-    }
+    };
+    if (e.param)
+        unpack(e.m, e.m_scale, static_cast<float*>(e.param), [](float k, float a) { return adamw8_m(k, a); });
+    if (e.master) unpack(e.v, e.v_scale, e.master, [](float k, float a) { return adamw8_v(k, a); });
 }
 
 }  // namespace trop

@@ -79,6 +79,24 @@ __device__ __forceinline__ void store_row_stream(T* row, int64_t c, int64_t n, t
         store_row<T, N>(row, c, n, v);
 }
 
+// Maximum of the wave's 32-bit patterns as unsigned integers: for magnitudes
+// (sign bit clear) the largest float, a NaN above infinity.  Six DPP steps
+// (rows of 16 by shifts, then across rows); lane 63 ends with the result.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_umax(uint32_t x) {
+    const uint32_t o = __builtin_amdgcn_update_dpp(0, x, CTRL, 0xf, 0xf, true);
+    return o > x ? o : x;
+}
+__device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
+    x = dpp_umax<0x111>(x);  // row_shr:1
+    x = dpp_umax<0x112>(x);  // row_shr:2
+    x = dpp_umax<0x114>(x);  // row_shr:4
+    x = dpp_umax<0x118>(x);  // row_shr:8
+    x = dpp_umax<0x142>(x);  // row_bcast:15
+    x = dpp_umax<0x143>(x);  // row_bcast:31
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
 // Butterfly reductions: every lane ends with the wave's result, the same
 // order of operations in every lane pair, so all lanes hold the same bits.
 __device__ __forceinline__ float wave_sum(float x) {
