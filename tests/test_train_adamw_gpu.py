@@ -25,7 +25,12 @@ BLOCK = 256
 def tb():
     from tropical_semiring_tensor_amd import binding
     binding.tropical_train_init(0)
-    return binding
+    yield binding
+    # give the memory back: torch keeps its matrix products' workspace inside
+    # whatever cached block it came from
+    torch.cuda.synchronize()
+    torch._C._cuda_clearCublasWorkspaces()
+    torch.cuda.empty_cache()
 
 
 def tensors(sizes, dtype, seed, odd_offsets=False):

@@ -27,7 +27,12 @@ F32, BF16 = torch.float32, torch.bfloat16
 def tb():
     from tropical_semiring_tensor_amd import binding
     binding.tropical_train_init(0)
-    return binding
+    yield binding
+    # give the memory back: torch keeps its matrix products' workspace inside
+    # whatever cached block it came from
+    torch.cuda.synchronize()
+    torch._C._cuda_clearCublasWorkspaces()
+    torch.cuda.empty_cache()
 
 
 def case(tokens, width, vocab, dtype, seed=0, ignored=0.3, pad=(0, 0), scale=2.0, tdtype=torch.int64):

@@ -23,7 +23,12 @@ F32, BF16 = torch.float32, torch.bfloat16
 def tb():
     from tropical_semiring_tensor_amd import binding
     binding.tropical_train_init(0)
-    return binding
+    yield binding
+    # give the memory back: torch keeps its matrix products' workspace inside
+    # whatever cached block it came from
+    torch.cuda.synchronize()
+    torch._C._cuda_clearCublasWorkspaces()
+    torch.cuda.empty_cache()
 
 
 def half(dtype):

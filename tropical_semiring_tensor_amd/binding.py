@@ -578,13 +578,23 @@ def _flat(t, what, n, dtype):
     return t.data_ptr()
 
 
-def _out_like(t, shape, dtype, device, what):
-    """The caller's output tensor, checked, or a new one for True / None."""
+def _out_matrix(t, rows, cols, dtype, device, what):
+    """(tensor, pointer, row stride) of the caller's output matrix, checked,
+    or of a new one for True / None."""
     if t is None or t is True:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}")
-    return t
+        t = torch.empty((rows, cols), dtype=dtype, device=device)
+        return t, t.data_ptr(), cols
+    if tuple(t.shape) != (rows, cols) or t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} of shape {(rows, cols)}")
+    return t, t.data_ptr(), _row_stride(t, what)
+
+
+def _out_flat(t, n, dtype, device, what):
+    """(tensor, pointer) of a 1-d output, likewise."""
+    if t is None or t is True:
+        t = torch.empty(n, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _flat(t, what, n, dtype)
 
 
 def _workspace(workspace, nbytes, device):
@@ -630,12 +640,11 @@ def tropical_layer_norm_forward(x, gamma=None, beta=None, eps=1e-5, y=None, mean
     pdt = _tdt(par, "gamma and beta") if par is not None else F32
     pg = _flat(gamma, "gamma", cols, par.dtype) if gamma is not None else None
     pb = _flat(beta, "beta", cols, par.dtype) if beta is not None else None
-    y = _out_like(y, (rows, cols), x.dtype, x.device, "y")
-    mean = _out_like(mean, (rows,), torch.float32, x.device, "mean")
-    rstd = _out_like(rstd, (rows,), torch.float32, x.device, "rstd")
-    st = lib().tropical_layer_norm_forward(dt, pdt, x.data_ptr(), ldx, pg, pb, eps, y.data_ptr(),
-                                           _row_stride(y, "y"), _flat(mean, "mean", rows, torch.float32),
-                                           _flat(rstd, "rstd", rows, torch.float32), rows, cols,
+    dev = x.device
+    y, py, ldy = _out_matrix(y, rows, cols, x.dtype, dev, "y")
+    mean, pm = _out_flat(mean, rows, torch.float32, dev, "mean")
+    rstd, pr = _out_flat(rstd, rows, torch.float32, dev, "rstd")
+    st = lib().tropical_layer_norm_forward(dt, pdt, x.data_ptr(), ldx, pg, pb, eps, py, ldy, pm, pr, rows, cols,
                                            _stream_ptr(None, x))
     if st != OK:
         _check(st, "tropical_layer_norm_forward")
@@ -667,20 +676,21 @@ def tropical_layer_norm_backward(dy, x, mean, rstd, gamma=None, dx=True, dgamma=
     pdt = _tdt(gamma, "gamma") if gamma is not None else F32
     pg = _flat(gamma, "gamma", cols, ptype) if gamma is not None else None
     dev = x.device
-    dx = _out_like(dx, (rows, cols), x.dtype, dev, "dx") if dx is not None else None
-    dgamma = _out_like(dgamma, (cols,), ptype, dev, "dgamma") if dgamma is not None else None
-    dbeta = _out_like(dbeta, (cols,), ptype, dev, "dbeta") if dbeta is not None else None
+    px, ldx, pdg, pdb = None, 0, None, None
+    if dx is not None:
+        dx, px, ldx = _out_matrix(dx, rows, cols, x.dtype, dev, "dx")
+    if dgamma is not None:
+        dgamma, pdg = _out_flat(dgamma, cols, ptype, dev, "dgamma")
+    if dbeta is not None:
+        dbeta, pdb = _out_flat(dbeta, cols, ptype, dev, "dbeta")
     need = 0
     if workspace is None and (dgamma is not None or dbeta is not None):
         need = tropical_layer_norm_backward_workspace_size(rows, cols)
     workspace, wp, wn = _workspace(workspace, need, dev)
     st = lib().tropical_layer_norm_backward(
         dt, pdt, dy.data_ptr(), _row_stride(dy, "dy"), x.data_ptr(), _row_stride(x, "x"),
-        _flat(mean, "mean", rows, torch.float32), _flat(rstd, "rstd", rows, torch.float32), pg,
-        dx.data_ptr() if dx is not None else None, _row_stride(dx, "dx") if dx is not None else 0,
-        _flat(dgamma, "dgamma", cols, ptype) if dgamma is not None else None,
-        _flat(dbeta, "dbeta", cols, ptype) if dbeta is not None else None, rows, cols, wp, wn,
-        _stream_ptr(None, x))
+        _flat(mean, "mean", rows, torch.float32), _flat(rstd, "rstd", rows, torch.float32), pg, px, ldx, pdg, pdb,
+        rows, cols, wp, wn, _stream_ptr(None, x))
     if st != OK:
         _check(st, "tropical_layer_norm_backward")
     return dx, dgamma, dbeta
@@ -724,16 +734,15 @@ def tropical_linear_cross_entropy_forward(x, w, target, ignore_index=-100, loss=
     """
     dt, ldx, ldw, tokens, width, vocab, pt, tbytes = _ce_operands(x, w, target)
     dev = x.device
-    loss = _out_like(loss, (tokens,), torch.float32, dev, "loss")
-    lse = _out_like(lse, (tokens,), torch.float32, dev, "lse")
+    loss, pl = _out_flat(loss, tokens, torch.float32, dev, "loss")
+    lse, ps = _out_flat(lse, tokens, torch.float32, dev, "lse")
     need = 0
     if workspace is None:
         need = tropical_linear_cross_entropy_workspace_size(x.dtype, tokens, width, vocab)
     workspace, wp, wn = _workspace(workspace, need, dev)
-    st = lib().tropical_linear_cross_entropy_forward(
-        dt, x.data_ptr(), ldx, w.data_ptr(), ldw, pt, tbytes, ignore_index,
-        _flat(loss, "loss", tokens, torch.float32), _flat(lse, "lse", tokens, torch.float32), tokens, width, vocab,
-        wp, wn, _stream_ptr(None, x))
+    st = lib().tropical_linear_cross_entropy_forward(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, pt, tbytes,
+                                                     ignore_index, pl, ps, tokens, width, vocab, wp, wn,
+                                                     _stream_ptr(None, x))
     if st != OK:
         _check(st, "tropical_linear_cross_entropy_forward")
     return loss, lse
@@ -754,19 +763,18 @@ def tropical_linear_cross_entropy_backward(x, w, target, lse, grad_loss, ignore_
                                                                    grad_loss.shape[0] != tokens):
         raise ValueError(f"grad_loss must be float32, 0-d or of {tokens} elements")
     gstride = grad_loss.stride(0) if grad_loss.dim() == 1 and tokens > 1 else 0
-    grad_x = _out_like(grad_x, (tokens, width), x.dtype, dev, "grad_x") if grad_x is not None else None
-    grad_w = _out_like(grad_w, (vocab, width), x.dtype, dev, "grad_w") if grad_w is not None else None
+    px, ldgx, pw, ldgw = None, 0, None, 0
+    if grad_x is not None:
+        grad_x, px, ldgx = _out_matrix(grad_x, tokens, width, x.dtype, dev, "grad_x")
+    if grad_w is not None:
+        grad_w, pw, ldgw = _out_matrix(grad_w, vocab, width, x.dtype, dev, "grad_w")
     need = 0
     if workspace is None:
         need = tropical_linear_cross_entropy_workspace_size(x.dtype, tokens, width, vocab, backward=True)
     workspace, wp, wn = _workspace(workspace, need, dev)
     st = lib().tropical_linear_cross_entropy_backward(
         dt, x.data_ptr(), ldx, w.data_ptr(), ldw, pt, tbytes, ignore_index, _flat(lse, "lse", tokens, torch.float32),
-        grad_loss.data_ptr(), gstride, grad_x.data_ptr() if grad_x is not None else None,
-        _row_stride(grad_x, "grad_x") if grad_x is not None else 0,
-        grad_w.data_ptr() if grad_w is not None else None,
-        _row_stride(grad_w, "grad_w") if grad_w is not None else 0, tokens, width, vocab, wp, wn,
-        _stream_ptr(None, x))
+        grad_loss.data_ptr(), gstride, px, ldgx, pw, ldgw, tokens, width, vocab, wp, wn, _stream_ptr(None, x))
     if st != OK:
         _check(st, "tropical_linear_cross_entropy_backward")
     return grad_x, grad_w
@@ -777,7 +785,7 @@ def _adamw_table(kind, columns, params, grads, masters):
     tensors, type, elements per scale or 0)."""
     n = len(params)
     if not n:
-        return (kind * 1)(), F32
+        return None, F32
     dtype = params[0].dtype
     dt = _tdt(params[0], "params")
     columns = [("param", params, dtype, 0), ("grad", grads, dtype, 0)] + columns
@@ -786,21 +794,18 @@ def _adamw_table(kind, columns, params, grads, masters):
     for name, ts, ty, block in columns:
         if len(ts) != n:
             raise ValueError(f"{name}: {len(ts)} tensors for {n} parameters")
-    rows = []
-    ptrs = {}
     counts = [p.numel() for p in params]
+    ptrs = {}
     for name, ts, ty, block in columns:
-        col = []
-        for t, e in zip(ts, counts):
-            want = (e + block - 1) // block if block else e
-            if t.dtype != ty or t.numel() != want or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous {ty} tensors of the parameters' sizes")
-            col.append(t.data_ptr())
-        ptrs[name] = col
-    names = [f[0] for f in kind._fields_[:-1]]
-    cols = [ptrs.get(name, [None] * n) for name in names]
-    rows = list(zip(*cols, counts))
-    return (kind * n)(*rows), dt
+        want = [(e + block - 1) // block for e in counts] if block else counts
+        if not all([t.dtype is ty and t.numel() == e and t.is_contiguous() for t, e in zip(ts, want)]):
+            raise ValueError(f"{name} must be contiguous {ty} tensors of the parameters' sizes")
+        ptrs[name] = [t.data_ptr() for t in ts]
+    none = [0] * n
+    # (every field is 8 bytes: the table as one flat array)
+    rows = zip(*(ptrs.get(f[0], none) for f in kind._fields_[:-1]), counts)
+    flat = [x for row in rows for x in row]
+    return ctypes.cast((ctypes.c_uint64 * len(flat))(*flat), ctypes.POINTER(kind)), dt
 
 
 def _adamw_hyper(lr, beta1, beta2, eps, weight_decay, step):
@@ -863,8 +868,8 @@ def tropical_adamw8_unpack(exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_sca
     table, _ = _adamw_table(trop_adamw8_tensor, _adamw8_columns(exp_avgs, exp_avg_scales, exp_avg_sqs,
                                                                 exp_avg_sq_scales), exp_avg_values,
                             exp_avg_sq_values, None)
-    mv = (ctypes.c_void_p * n)(*[r.param for r in table])
-    vv = (ctypes.c_void_p * n)(*[r.grad for r in table])
+    mv = (ctypes.c_void_p * n)(*[t.data_ptr() for t in exp_avg_values])
+    vv = (ctypes.c_void_p * n)(*[t.data_ptr() for t in exp_avg_sq_values])
     st = lib().tropical_adamw8_unpack(table, n, mv, vv, _stream_ptr(None, exp_avgs[0]))
     if st != OK:
         _check(st, "tropical_adamw8_unpack")

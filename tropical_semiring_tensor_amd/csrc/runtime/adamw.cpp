@@ -83,19 +83,19 @@ trop_status step32(trop_dtype dt, const trop_adamw_tensor* t, int64_t count, con
     if (!any) return ok();
     int dev = -1;
     if ((st = train_device(&dev)) != TROP_OK) return st;
-    SpanChecker param(dev), grad(dev), m(dev), v(dev), master(dev);
+    SpanChecker checker(dev);
     int masters = 0, with = 0;
     for (int64_t i = 0; i < count; ++i) {
         const int64_t n = t[i].elements;
         if (n == 0) continue;
         ++with;
-        if ((st = param.check(t[i].param, n, elem_size(dt), "param", i)) != TROP_OK) return st;
-        if ((st = grad.check(t[i].grad, n, elem_size(dt), "grad", i)) != TROP_OK) return st;
-        if ((st = m.check(t[i].exp_avg, n, 4, "exp_avg", i)) != TROP_OK) return st;
-        if ((st = v.check(t[i].exp_avg_sq, n, 4, "exp_avg_sq", i)) != TROP_OK) return st;
+        if ((st = checker.span(t[i].param, n, elem_size(dt), "param", i)) != TROP_OK) return st;
+        if ((st = checker.span(t[i].grad, n, elem_size(dt), "grad", i)) != TROP_OK) return st;
+        if ((st = checker.span(t[i].exp_avg, n, 4, "exp_avg", i)) != TROP_OK) return st;
+        if ((st = checker.span(t[i].exp_avg_sq, n, 4, "exp_avg_sq", i)) != TROP_OK) return st;
         if (t[i].master) {
             ++masters;
-            if ((st = master.check(t[i].master, n, 4, "master", i)) != TROP_OK) return st;
+            if ((st = checker.span(t[i].master, n, 4, "master", i)) != TROP_OK) return st;
         }
     }
     if (masters && masters != with)
@@ -125,21 +125,21 @@ trop_status step8(trop_dtype dt, const trop_adamw8_tensor* t, int64_t count, con
     if (!any) return ok();
     int dev = -1;
     if ((st = train_device(&dev)) != TROP_OK) return st;
-    SpanChecker param(dev), grad(dev), m(dev), ms(dev), v(dev), vs(dev), master(dev);
+    SpanChecker checker(dev);
     int masters = 0, with = 0;
     for (int64_t i = 0; i < count; ++i) {
         const int64_t n = t[i].elements, nb = (n + TROP_ADAMW_BLOCK - 1) / TROP_ADAMW_BLOCK;
         if (n == 0) continue;
         ++with;
-        if ((st = param.check(t[i].param, n, elem_size(dt), "param", i)) != TROP_OK) return st;
-        if ((st = grad.check(t[i].grad, n, elem_size(dt), "grad", i)) != TROP_OK) return st;
-        if ((st = m.check(t[i].exp_avg, n, 1, "exp_avg", i)) != TROP_OK) return st;
-        if ((st = ms.check(t[i].exp_avg_scale, nb, 4, "exp_avg_scale", i)) != TROP_OK) return st;
-        if ((st = v.check(t[i].exp_avg_sq, n, 1, "exp_avg_sq", i)) != TROP_OK) return st;
-        if ((st = vs.check(t[i].exp_avg_sq_scale, nb, 4, "exp_avg_sq_scale", i)) != TROP_OK) return st;
+        if ((st = checker.span(t[i].param, n, elem_size(dt), "param", i)) != TROP_OK) return st;
+        if ((st = checker.span(t[i].grad, n, elem_size(dt), "grad", i)) != TROP_OK) return st;
+        if ((st = checker.span(t[i].exp_avg, n, 1, "exp_avg", i)) != TROP_OK) return st;
+        if ((st = checker.span(t[i].exp_avg_scale, nb, 4, "exp_avg_scale", i)) != TROP_OK) return st;
+        if ((st = checker.span(t[i].exp_avg_sq, n, 1, "exp_avg_sq", i)) != TROP_OK) return st;
+        if ((st = checker.span(t[i].exp_avg_sq_scale, nb, 4, "exp_avg_sq_scale", i)) != TROP_OK) return st;
         if (t[i].master) {
             ++masters;
-            if ((st = master.check(t[i].master, n, 4, "master", i)) != TROP_OK) return st;
+            if ((st = checker.span(t[i].master, n, 4, "master", i)) != TROP_OK) return st;
         }
     }
     if (masters && masters != with)
@@ -165,19 +165,19 @@ trop_status unpack8(const trop_adamw8_tensor* t, int64_t count, float* const* mv
     if (!any || (!mv && !vv)) return ok();
     int dev = -1;
     if ((st = train_device(&dev)) != TROP_OK) return st;
-    SpanChecker m(dev), ms(dev), v(dev), vs(dev), mo(dev), vo(dev);
+    SpanChecker checker(dev);
     for (int64_t i = 0; i < count; ++i) {
         const int64_t n = t[i].elements, nb = (n + TROP_ADAMW_BLOCK - 1) / TROP_ADAMW_BLOCK;
         if (n == 0) continue;
         if (mv && mv[i]) {
-            if ((st = m.check(t[i].exp_avg, n, 1, "exp_avg", i)) != TROP_OK) return st;
-            if ((st = ms.check(t[i].exp_avg_scale, nb, 4, "exp_avg_scale", i)) != TROP_OK) return st;
-            if ((st = mo.check(mv[i], n, 4, "exp_avg_values", i)) != TROP_OK) return st;
+            if ((st = checker.span(t[i].exp_avg, n, 1, "exp_avg", i)) != TROP_OK) return st;
+            if ((st = checker.span(t[i].exp_avg_scale, nb, 4, "exp_avg_scale", i)) != TROP_OK) return st;
+            if ((st = checker.span(mv[i], n, 4, "exp_avg_values", i)) != TROP_OK) return st;
         }
         if (vv && vv[i]) {
-            if ((st = v.check(t[i].exp_avg_sq, n, 1, "exp_avg_sq", i)) != TROP_OK) return st;
-            if ((st = vs.check(t[i].exp_avg_sq_scale, nb, 4, "exp_avg_sq_scale", i)) != TROP_OK) return st;
-            if ((st = vo.check(vv[i], n, 4, "exp_avg_sq_values", i)) != TROP_OK) return st;
+            if ((st = checker.span(t[i].exp_avg_sq, n, 1, "exp_avg_sq", i)) != TROP_OK) return st;
+            if ((st = checker.span(t[i].exp_avg_sq_scale, nb, 4, "exp_avg_sq_scale", i)) != TROP_OK) return st;
+            if ((st = checker.span(vv[i], n, 4, "exp_avg_sq_values", i)) != TROP_OK) return st;
         }
     }
     TropAdamw8Params p = {};

@@ -205,22 +205,22 @@ struct CeCall {
     void* stream;
 };
 
-trop_status check_inputs(const CeCall& a, int dev) {
+trop_status check_inputs(const CeCall& a, SpanChecker& checker) {
     const size_t eb = elem_size(a.dt);
     trop_status st;
     if (a.tokens > 0) {
-        if ((st = check_matrix(a.x, dev, a.tokens, a.width, a.ldx, eb, "x")) != TROP_OK) return st;
-        if ((st = check_matrix(a.target, dev, 1, a.tokens, a.tokens, a.target_bytes, "target")) != TROP_OK) return st;
+        if ((st = checker.matrix(a.x, a.tokens, a.width, a.ldx, eb, "x")) != TROP_OK) return st;
+        if ((st = checker.span(a.target, a.tokens, a.target_bytes, "target")) != TROP_OK) return st;
     }
-    return check_matrix(a.w, dev, a.vocab, a.width, a.ldw, eb, "w");
+    return checker.matrix(a.w, a.vocab, a.width, a.ldw, eb, "w");
 }
 
-trop_status check_workspace(const CeCall& a, const CePlan& c, int dev, char** base) {
+trop_status check_workspace(const CeCall& a, const CePlan& c, SpanChecker& checker, char** base) {
     if (!a.workspace || a.workspace_bytes < c.bytes)
         return fail(TROP_ERR_WORKSPACE_TOO_SMALL,
                     "linear cross entropy needs " + std::to_string(c.bytes) + " workspace bytes, got " +
                         std::to_string(a.workspace ? a.workspace_bytes : 0));
-    const trop_status st = check_device_span(a.workspace, dev, (int64_t)c.bytes, 1, "workspace");
+    const trop_status st = checker.span(a.workspace, (int64_t)c.bytes, 1, "workspace");
     *base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(a.workspace) + 255) / 256 * 256);
     return st;
 }
@@ -358,14 +358,15 @@ trop_status ce_forward(const CeCall& a, float* loss, float* lse) {
     if (a.tokens == 0) return ok();
     int dev = -1;
     if ((st = train_device(&dev)) != TROP_OK) return st;
-    if ((st = check_inputs(a, dev)) != TROP_OK) return st;
-    if ((st = check_matrix(loss, dev, 1, a.tokens, a.tokens, 4, "loss")) != TROP_OK) return st;
-    if ((st = check_matrix(lse, dev, 1, a.tokens, a.tokens, 4, "lse")) != TROP_OK) return st;
+    SpanChecker checker(dev);
+    if ((st = check_inputs(a, checker)) != TROP_OK) return st;
+    if ((st = checker.span(loss, a.tokens, 4, "loss")) != TROP_OK) return st;
+    if ((st = checker.span(lse, a.tokens, 4, "lse")) != TROP_OK) return st;
     CePlan c;
     if (!plan(a.dt, a.tokens, a.width, a.vocab, false, !direct_w(a.dt, a.w, a.ldw, a.width), &c))
         return fail(TROP_ERR_UNSUPPORTED, "workspace size overflows");
     char* ws = nullptr;
-    if ((st = check_workspace(a, c, dev, &ws)) != TROP_OK) return st;
+    if ((st = check_workspace(a, c, checker, &ws)) != TROP_OK) return st;
     TropCeParams p = params(a, c, ws);
     p.loss = loss;
     p.lse = lse;
@@ -399,22 +400,23 @@ trop_status ce_backward(const CeCall& a, const float* lse, const float* grad_los
     int dev = -1;
     if ((st = train_device(&dev)) != TROP_OK) return st;
     const size_t eb = elem_size(a.dt);
-    if ((st = check_inputs(a, dev)) != TROP_OK) return st;
+    SpanChecker checker(dev);
+    if ((st = check_inputs(a, checker)) != TROP_OK) return st;
     if (a.tokens > 0) {
-        if ((st = check_matrix(lse, dev, 1, a.tokens, a.tokens, 4, "lse")) != TROP_OK) return st;
+        if ((st = checker.span(lse, a.tokens, 4, "lse")) != TROP_OK) return st;
         // one element every grad_loss_stride
-        if ((st = check_matrix(grad_loss, dev, a.tokens, grad_loss_stride ? 1 : 0, grad_loss_stride, 4,
-                               "grad_loss")) != TROP_OK)
-            return st;
-        if (!grad_loss_stride && (st = check_matrix(grad_loss, dev, 1, 1, 1, 4, "grad_loss")) != TROP_OK) return st;
+        int64_t reach = 0;
+        if (__builtin_mul_overflow(a.tokens - 1, grad_loss_stride, &reach))
+            return fail(TROP_ERR_INVALID_ARGUMENT, "grad_loss extent overflows");
+        if ((st = checker.span(grad_loss, reach + 1, 4, "grad_loss")) != TROP_OK) return st;
     }
-    if (grad_x && (st = check_matrix(grad_x, dev, a.tokens, a.width, ldgx, eb, "grad_x")) != TROP_OK) return st;
-    if (grad_w && (st = check_matrix(grad_w, dev, a.vocab, a.width, ldgw, eb, "grad_w")) != TROP_OK) return st;
+    if (grad_x && (st = checker.matrix(grad_x, a.tokens, a.width, ldgx, eb, "grad_x")) != TROP_OK) return st;
+    if (grad_w && (st = checker.matrix(grad_w, a.vocab, a.width, ldgw, eb, "grad_w")) != TROP_OK) return st;
     CePlan c;
     if (!plan(a.dt, a.tokens, a.width, a.vocab, true, !direct_w(a.dt, a.w, a.ldw, a.width), &c))
         return fail(TROP_ERR_UNSUPPORTED, "workspace size overflows");
     char* ws = nullptr;
-    if ((st = check_workspace(a, c, dev, &ws)) != TROP_OK) return st;
+    if ((st = check_workspace(a, c, checker, &ws)) != TROP_OK) return st;
     TropCeParams p = params(a, c, ws);
     p.backward = 1;
     p.lse_in = lse;

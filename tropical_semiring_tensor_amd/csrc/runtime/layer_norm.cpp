@@ -56,13 +56,14 @@ trop_status forward(trop_dtype dt, trop_dtype pdt, const void* x, int64_t ldx, c
     int dev = -1;
     if ((st = train_device(&dev)) != TROP_OK) return st;
     const size_t eb = elem_size(dt), pb = elem_size(pdt);
-    if ((st = check_matrix(x, dev, rows, cols, ldx, eb, "x")) != TROP_OK) return st;
-    if ((st = check_matrix(y, dev, rows, cols, ldy, eb, "y")) != TROP_OK) return st;
+    SpanChecker checker(dev);
+    if ((st = checker.matrix(x, rows, cols, ldx, eb, "x")) != TROP_OK) return st;
+    if ((st = checker.matrix(y, rows, cols, ldy, eb, "y")) != TROP_OK) return st;
     if (x == y && ldx != ldy) return fail(TROP_ERR_INVALID_ARGUMENT, "y is x but its row stride is another");
-    if (gamma && (st = check_matrix(gamma, dev, 1, cols, cols, pb, "gamma")) != TROP_OK) return st;
-    if (beta && (st = check_matrix(beta, dev, 1, cols, cols, pb, "beta")) != TROP_OK) return st;
-    if (mean && (st = check_matrix(mean, dev, 1, rows, rows, 4, "mean")) != TROP_OK) return st;
-    if (rstd && (st = check_matrix(rstd, dev, 1, rows, rows, 4, "rstd")) != TROP_OK) return st;
+    if (gamma && (st = checker.span(gamma, cols, pb, "gamma")) != TROP_OK) return st;
+    if (beta && (st = checker.span(beta, cols, pb, "beta")) != TROP_OK) return st;
+    if (mean && (st = checker.span(mean, rows, 4, "mean")) != TROP_OK) return st;
+    if (rstd && (st = checker.span(rstd, rows, 4, "rstd")) != TROP_OK) return st;
     TropLayerNormParams p = {};
     p.x = x;
     p.gamma = gamma;
@@ -92,18 +93,19 @@ trop_status backward(trop_dtype dt, trop_dtype pdt, const void* dy, int64_t lddy
     int dev = -1;
     if ((st = train_device(&dev)) != TROP_OK) return st;
     const size_t eb = elem_size(dt), pb = elem_size(pdt);
+    SpanChecker checker(dev);
     if (rows > 0) {
-        if ((st = check_matrix(dy, dev, rows, cols, lddy, eb, "dy")) != TROP_OK) return st;
-        if ((st = check_matrix(x, dev, rows, cols, ldx, eb, "x")) != TROP_OK) return st;
-        if ((st = check_matrix(mean, dev, 1, rows, rows, 4, "mean")) != TROP_OK) return st;
-        if ((st = check_matrix(rstd, dev, 1, rows, rows, 4, "rstd")) != TROP_OK) return st;
-        if (dx && (st = check_matrix(dx, dev, rows, cols, lddx, eb, "dx")) != TROP_OK) return st;
+        if ((st = checker.matrix(dy, rows, cols, lddy, eb, "dy")) != TROP_OK) return st;
+        if ((st = checker.matrix(x, rows, cols, ldx, eb, "x")) != TROP_OK) return st;
+        if ((st = checker.span(mean, rows, 4, "mean")) != TROP_OK) return st;
+        if ((st = checker.span(rstd, rows, 4, "rstd")) != TROP_OK) return st;
+        if (dx && (st = checker.matrix(dx, rows, cols, lddx, eb, "dx")) != TROP_OK) return st;
         if (dx && dx == dy && lddx != lddy)
             return fail(TROP_ERR_INVALID_ARGUMENT, "dx is dy but its row stride is another");
     }
-    if (gamma && (st = check_matrix(gamma, dev, 1, cols, cols, pb, "gamma")) != TROP_OK) return st;
-    if (dgamma && (st = check_matrix(dgamma, dev, 1, cols, cols, pb, "dgamma")) != TROP_OK) return st;
-    if (dbeta && (st = check_matrix(dbeta, dev, 1, cols, cols, pb, "dbeta")) != TROP_OK) return st;
+    if (gamma && (st = checker.span(gamma, cols, pb, "gamma")) != TROP_OK) return st;
+    if (dgamma && (st = checker.span(dgamma, cols, pb, "dgamma")) != TROP_OK) return st;
+    if (dbeta && (st = checker.span(dbeta, cols, pb, "dbeta")) != TROP_OK) return st;
     const bool params = dgamma || dbeta;
     size_t need = 0;
     if (params && (st = part_bytes(rows, cols, &need)) != TROP_OK) return st;
@@ -112,7 +114,7 @@ trop_status backward(trop_dtype dt, trop_dtype pdt, const void* dy, int64_t lddy
             return fail(TROP_ERR_WORKSPACE_TOO_SMALL, "layer norm backward needs " + std::to_string(need) +
                                                           " workspace bytes, got " +
                                                           std::to_string(workspace ? workspace_bytes : 0));
-        if ((st = check_matrix(workspace, dev, 1, (int64_t)(need / 4), (int64_t)(need / 4), 4, "workspace")) != TROP_OK)
+        if ((st = checker.span(workspace, (int64_t)(need / 4), 4, "workspace")) != TROP_OK)
             return st;
     }
     const hipStream_t s = static_cast<hipStream_t>(stream);

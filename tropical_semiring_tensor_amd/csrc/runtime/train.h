@@ -52,17 +52,16 @@ void reset_train_launches();
 
 inline size_t elem_size(trop_dtype dt) { return dt == TROP_BF16 ? 2 : 4; }
 
-// `p` must hold a row-major rows x cols matrix of row stride ld (all >= 1,
-// ld >= cols) in device memory of `dev`, aligned to its elements.
-trop_status check_matrix(const void* p, int dev, int64_t rows, int64_t cols, int64_t ld, size_t elem_bytes,
-                         const char* what);
-
-// Extents and allocations of one call: a pointer inside the range that the
-// call checked last needs no further query (many tensors share a segment).
+// Extents and allocations of one call's pointers.  One inside the allocation
+// that the call checked last needs no further query (small tensors share the
+// allocator's segments, a call's own are often neighbours).
 class SpanChecker {
    public:
     explicit SpanChecker(int dev) : dev_(dev) {}
-    trop_status check(const void* p, int64_t elems, size_t elem_bytes, const char* what, int64_t index);
+    // `elems` elements from p on, aligned to their size
+    trop_status span(const void* p, int64_t elems, size_t elem_bytes, const char* what, int64_t index = -1);
+    // a row-major rows x cols matrix of row stride ld (rows, cols >= 1)
+    trop_status matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t elem_bytes, const char* what);
 
    private:
     int dev_;

@@ -134,26 +134,12 @@ void reset_train_launches() {
     for (auto& n : g_launches) n.store(0);
 }
 
-trop_status check_matrix(const void* p, int dev, int64_t rows, int64_t cols, int64_t ld, size_t elem_bytes,
-                         const char* what) {
-    if (ld < cols) return fail(TROP_ERR_INVALID_ARGUMENT, std::string(what) + ": row stride below the row's length");
-    int64_t span = 0;
-    if (__builtin_mul_overflow(rows - 1, ld, &span) || __builtin_add_overflow(span, cols, &span))
-        return fail(TROP_ERR_INVALID_ARGUMENT, std::string(what) + " extent overflows");
-    if (reinterpret_cast<uintptr_t>(p) % elem_bytes)
-        return fail(TROP_ERR_INVALID_ARGUMENT, std::string(what) + " is not aligned to its elements");
-    return check_device_span(p, dev, span, elem_bytes, what);
-}
-
-trop_status SpanChecker::check(const void* p, int64_t elems, size_t elem_bytes, const char* what, int64_t index) {
+trop_status SpanChecker::span(const void* p, int64_t elems, size_t elem_bytes, const char* what, int64_t index) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    if (a % elem_bytes)
-        return fail(TROP_ERR_INVALID_ARGUMENT,
-                    std::string(what) + " of tensor " + std::to_string(index) + " is not aligned to its elements");
-    if (a >= lo_ && a < hi_ && (unsigned __int128)elems * elem_bytes <= hi_ - a) return TROP_OK;
-    const trop_status st =
-        check_device_span(p, dev_, elems, elem_bytes,
-                          (std::string(what) + " of tensor " + std::to_string(index)).c_str());
+    if (a >= lo_ && a < hi_ && a % elem_bytes == 0 && (unsigned __int128)elems * elem_bytes <= hi_ - a) return TROP_OK;
+    const std::string name = index < 0 ? what : std::string(what) + " of tensor " + std::to_string(index);
+    if (a % elem_bytes) return fail(TROP_ERR_INVALID_ARGUMENT, name + " is not aligned to its elements");
+    const trop_status st = check_device_span(p, dev_, elems, elem_bytes, name.c_str());
     if (st != TROP_OK) return st;
     hipDeviceptr_t base = nullptr;
     size_t size = 0;
@@ -164,6 +150,15 @@ trop_status SpanChecker::check(const void* p, int64_t elems, size_t elem_bytes, 
         (void)hipGetLastError();
     }
     return TROP_OK;
+}
+
+trop_status SpanChecker::matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t elem_bytes,
+                                const char* what) {
+    if (ld < cols) return fail(TROP_ERR_INVALID_ARGUMENT, std::string(what) + ": row stride below the row's length");
+    int64_t elems = 0;
+    if (__builtin_mul_overflow(rows - 1, ld, &elems) || __builtin_add_overflow(elems, cols, &elems))
+        return fail(TROP_ERR_INVALID_ARGUMENT, std::string(what) + " extent overflows");
+    return span(p, elems, elem_bytes, what);
 }
 
 }  // namespace trop
