@@ -117,22 +117,24 @@ __device__ __forceinline__ void ce_keep_body(const TropCeParams& p) {
     if (threadIdx.x == 0) {
         p.control->kept = total;
         p.control->grad_max = gmax;
-        p.control->x_exp = p.control->w_exp = 0;
     }
 }
 
 // ---- float32: the matrices' largest magnitudes -----------------------------
-// Partial maxima over the finite elements of the kept rows of x and of w.
+// Partial maxima over the finite elements of the rows of x that count and of
+// w: workgroups 1 ... max_parts of the launch that lists the tokens.
 __device__ __forceinline__ void ce_magnitude_body(const TropCeParams& p) {
-    __shared__ float lds[4];
+    __shared__ float lds[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t part = blockIdx.x - 1;
     for (int which = 0; which < 2; ++which) {
         const float* m = static_cast<const float*>(which ? p.w : p.x);
-        const int64_t ld = which ? p.ldw : p.ldx, rows = which ? p.vocab : p.control->kept;
+        const int64_t ld = which ? p.ldw : p.ldx, rows = which ? p.vocab : p.tokens;
         float best = 0.f;
         // a wave to a row
-        for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < rows; r += (int64_t)p.max_parts * 4) {
-            const float* row = m + (which ? r : (int64_t)p.rows[r]) * ld;
+        for (int64_t r = part * 16 + wave; r < rows; r += (int64_t)p.max_parts * 16) {
+            if (!which && !ce_counts(p, ce_target(p, r))) continue;
+            const float* row = m + r * ld;
 #pragma unroll 4
             for (int64_t c = lane * 4; c < p.width; c += 256) {
                 const FloatVec<4> v = load_row_stream<float, 4>(row, c, p.width);
@@ -147,8 +149,10 @@ __device__ __forceinline__ void ce_magnitude_body(const TropCeParams& p) {
         for (int o = 32; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor(best, o, 64));
         if (lane == 0) lds[wave] = best;
         __syncthreads();
-        if (threadIdx.x == 0)
-            p.magnitude[which * TROP_CE_MAX_PARTS + blockIdx.x] = fmaxf(fmaxf(lds[0], lds[1]), fmaxf(lds[2], lds[3]));
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 16; ++w) best = fmaxf(best, lds[w]);
+            p.magnitude[which * TROP_CE_MAX_PARTS + part] = best;
+        }
         __syncthreads();
     }
 }
@@ -190,17 +194,19 @@ __device__ __forceinline__ void ce_pack8(const void* row, int64_t c, int64_t wid
     }
 }
 
-// Kept rows of x, in order, and zero rows up to a whole tile.  A wave takes
-// a row; for float32 each workgroup reduces the partial maxima, and the
-// first leaves the exponents for the kernels after it.
+// Kept rows of x, in order, and zero rows up to a whole tile (the first
+// pack_x workgroups), then rows [v0, v0 + piece) of w (its last row again past
+// the vocabulary).  A wave takes a row; for float32 each workgroup reduces
+// the partial maxima, and the first leaves the exponents for the kernels after.
 template <int PLANES>
-__device__ __forceinline__ void ce_pack_x_body(const TropCeParams& p) {
+__device__ __forceinline__ void ce_pack_body(const TropCeParams& p) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-    const int64_t kept = p.control->kept, i = (int64_t)blockIdx.x * 4 + wave;
+    const bool is_w = blockIdx.x >= p.pack_x;
+    const int64_t i = ((int64_t)blockIdx.x - (is_w ? p.pack_x : 0)) * 4 + wave;
     __shared__ float lds[2][4];
     int32_t e = 0;
     if constexpr (PLANES == 2) {
-        float best[2];
+        int32_t exps[2];
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             float b = (int)threadIdx.x < p.max_parts ? p.magnitude[which * TROP_CE_MAX_PARTS + threadIdx.x] : 0.f;
@@ -211,33 +217,32 @@ __device__ __forceinline__ void ce_pack_x_body(const TropCeParams& p) {
         __syncthreads();
 #pragma unroll
         for (int which = 0; which < 2; ++which)
-            best[which] = fmaxf(fmaxf(lds[which][0], lds[which][1]), fmaxf(lds[which][2], lds[which][3]));
-        e = ce_scale_exp(best[0]);
-        if (blockIdx.x == 0 && threadIdx.x == 0) {
-            p.control->x_exp = e;
-            p.control->w_exp = ce_scale_exp(best[1]);
+            exps[which] = ce_scale_exp(fmaxf(fmaxf(lds[which][0], lds[which][1]), fmaxf(lds[which][2], lds[which][3])));
+        e = is_w ? exps[1] : exps[0];
+        if (!is_w && blockIdx.x == 0 && threadIdx.x == 0) {
+            p.control->x_exp = exps[0];
+            p.control->w_exp = exps[1];
         }
     }
-    if (i >= (kept + 255) / 256 * 256) return;
     const size_t eb = PLANES == 1 ? 2 : 4;
-    const char* row = i < kept ? static_cast<const char*>(p.x) + (int64_t)p.rows[i] * p.ldx * eb : nullptr;
-    char* out = static_cast<char*>(p.xp) + i * p.width_p * 2;
+    const char* row;
+    char* out;
+    int64_t plane;
+    if (is_w) {
+        if (i >= p.piece) return;
+        row = static_cast<const char*>(p.w) + min(p.v0 + i, p.vocab - 1) * p.ldw * eb;
+        out = static_cast<char*>(p.wp) + i * p.width_p * 2;
+        plane = p.piece * p.width_p * 2;
+    } else {
+        const int64_t kept = p.control->kept;
+        if (i >= (kept + 255) / 256 * 256) return;
+        row = i < kept ? static_cast<const char*>(p.x) + (int64_t)p.rows[i] * p.ldx * eb : nullptr;
+        out = static_cast<char*>(p.xp) + i * p.width_p * 2;
+        plane = p.padded * p.width_p * 2;
+    }
 #pragma unroll 2
     for (int64_t c = lane * 8; c < p.width_p; c += 64 * 8)
-        ce_pack8<PLANES>(row, c, row ? p.width : 0, e, out + c * 2, p.padded * p.width_p * 2);
-}
-
-// Rows [v0, v0 + piece) of w (its last row again past the vocabulary).
-template <int PLANES>
-__device__ __forceinline__ void ce_pack_w_body(const TropCeParams& p) {
-    const size_t eb = PLANES == 1 ? 2 : 4;
-    const int32_t e = p.control->w_exp;
-    for (int64_t r = blockIdx.x; r < p.piece; r += gridDim.x) {
-        const char* row = static_cast<const char*>(p.w) + min(p.v0 + r, p.vocab - 1) * p.ldw * eb;
-        char* out = static_cast<char*>(p.wp) + r * p.width_p * 2;
-        for (int64_t c = threadIdx.x * 8; c < p.width_p; c += 256 * 8)
-            ce_pack8<PLANES>(row, c, p.width, e, out + c * 2, p.piece * p.width_p * 2);
-    }
+        ce_pack8<PLANES>(row, c, row ? p.width : 0, e, out + c * 2, plane);
 }
 
 // ---- tiles -----------------------------------------------------------------

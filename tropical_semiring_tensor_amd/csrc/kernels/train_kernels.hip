@@ -61,8 +61,12 @@ TROP_ADAMW_ENTRIES(bf16_master, bf16, true)
 
 extern "C" __global__ __launch_bounds__(256) void trop_adamw8_unpack(TropAdamw8Params p) { adamw8_unpack_body(p); }
 
-extern "C" __global__ __launch_bounds__(1024) void trop_ce_keep(TropCeParams p) { ce_keep_body(p); }
-extern "C" __global__ __launch_bounds__(256) void trop_ce_magnitude(TropCeParams p) { ce_magnitude_body(p); }
+extern "C" __global__ __launch_bounds__(1024) void trop_ce_keep(TropCeParams p) {
+    if (blockIdx.x == 0)
+        ce_keep_body(p);
+    else
+        ce_magnitude_body(p);
+}
 extern "C" __global__ __launch_bounds__(256) void trop_ce_merge(TropCeParams p) { ce_merge_body(p); }
 
 // one product tile: its LDS and the body's workgroup
@@ -72,11 +76,8 @@ extern "C" __global__ __launch_bounds__(256) void trop_ce_merge(TropCeParams p) 
         BODY(p, lds);                                                                              \
     }
 #define TROP_CE_ENTRIES(NAME, T, PLANES)                                                               \
-    extern "C" __global__ __launch_bounds__(256) void trop_ce_pack_x_##NAME(TropCeParams p) {           \
-        ce_pack_x_body<PLANES>(p);                                                                      \
-    }                                                                                                   \
-    extern "C" __global__ __launch_bounds__(256) void trop_ce_pack_w_##NAME(TropCeParams p) {           \
-        ce_pack_w_body<PLANES>(p);                                                                      \
+    extern "C" __global__ __launch_bounds__(256) void trop_ce_pack_##NAME(TropCeParams p) {             \
+        ce_pack_body<PLANES>(p);                                                                        \
     }                                                                                                   \
     extern "C" __global__ __launch_bounds__(256) void trop_ce_finish_##NAME(TropCeParams p) {           \
         ce_finish_body<T, PLANES>(p);                                                                   \
@@ -86,12 +87,19 @@ extern "C" __global__ __launch_bounds__(256) void trop_ce_merge(TropCeParams p) 
     }                                                                                                   \
     using Logits256_##NAME = MgConfig<256, 256, 2, 4, KM, KM, PLANES>;                                  \
     using Logits128_##NAME = MgConfig<128, 128, 2, 2, KM, KM, PLANES>;                                  \
+    using Logits64_##NAME = MgConfig<64, 64, 2, 2, KM, KM, PLANES>;                                     \
+    using GradX64_##NAME = MgConfig<64, 64, 2, 2, MM, QK, PLANES>;                                      \
+    using GradW64_##NAME = MgConfig<64, 64, 2, 2, MM, QM, PLANES>;                                      \
     using GradX256_##NAME = MgConfig<256, 256, 2, 4, MM, QK, PLANES>;                                   \
     using GradX128_##NAME = MgConfig<128, 128, 2, 2, MM, QK, PLANES>;                                   \
     using GradW256_##NAME = MgConfig<256, 256, 2, 4, MM, QM, PLANES>;                                   \
     using GradW128_##NAME = MgConfig<128, 128, 2, 2, MM, QM, PLANES>;                                   \
     TROP_CE_TILE(stats256_##NAME, Logits256_##NAME, (ce_logits_body<Logits256_##NAME, CE_STATS>))       \
     TROP_CE_TILE(stats128_##NAME, Logits128_##NAME, (ce_logits_body<Logits128_##NAME, CE_STATS>))       \
+    TROP_CE_TILE(stats64_##NAME, Logits64_##NAME, (ce_logits_body<Logits64_##NAME, CE_STATS>))          \
+    TROP_CE_TILE(grad64_##NAME, Logits64_##NAME, (ce_logits_body<Logits64_##NAME, CE_GRAD>))            \
+    TROP_CE_TILE(gx64_##NAME, GradX64_##NAME, ce_grad_x_body<GradX64_##NAME>)                           \
+    TROP_CE_TILE(gw64_##NAME, GradW64_##NAME, (ce_grad_w_body<GradW64_##NAME, T>))                      \
     TROP_CE_TILE(grad256_##NAME, Logits256_##NAME, (ce_logits_body<Logits256_##NAME, CE_GRAD>))         \
     TROP_CE_TILE(grad128_##NAME, Logits128_##NAME, (ce_logits_body<Logits128_##NAME, CE_GRAD>))         \
     TROP_CE_TILE(gx256_##NAME, GradX256_##NAME, ce_grad_x_body<GradX256_##NAME>)                        \

@@ -24,25 +24,31 @@ int64_t piece_labels(int64_t vocab, int64_t bytes) {
 }
 
 // Time (us) of a product in `tiles` tiles of `kind` (0: 256 x 256, 1: 128 x
-// 128), each walking `ktiles` k tiles of 64 in one pass.  Measured on one
-// MI355X: a 256 x 256 workgroup has a CU to itself and takes 1.75 us a k
-// tile; a 128 x 128 one takes 0.85 us alone on a CU and 1.15 beside another;
-// a tile costs 6 us or 4 besides (first loads, epilogue).
+// 128, 2: 64 x 64), each walking `ktiles` k tiles of 64 in one pass.
+// Measured on one MI355X (256 CUs): a 256 x 256 workgroup has a CU to itself
+// and takes 1.75 us a k tile; a 128 x 128 one 0.7 us alone on a CU, 1.15
+// beside another; a 64 x 64 one 0.3 us alone, 0.5 with two and 0.85 with
+// four on a CU; a tile costs 6, 5 or 4 us besides (first loads, epilogue).
 double tile_time(int kind, int64_t tiles, int64_t ktiles) {
-    if (kind == 0) return (double)ceil_div(tiles, 256) * ((double)ktiles * 1.75 + 6.0);
-    if (tiles <= 256) return (double)ktiles * 0.85 + 4.0;
-    return (double)ceil_div(tiles, 512) * ((double)ktiles * 1.15 + 4.0);
+    const double k = (double)ktiles;
+    if (kind == 0) return (double)ceil_div(tiles, 256) * (k * 1.75 + 6.0);
+    if (kind == 1) return tiles <= 256 ? k * 0.7 + 5.0 : (double)ceil_div(tiles, 512) * (k * 1.15 + 5.0);
+    return tiles <= 256 ? k * 0.3 + 4.0
+                        : tiles <= 512 ? k * 0.5 + 4.0 : (double)ceil_div(tiles, 1024) * (k * 0.85 + 4.0);
 }
+
+int64_t tile_edge(int tile) { return 256 >> tile; }
+uint32_t tile_threads(int tile) { return tile == 0 ? 512 : 256; }
 
 // The tile and the number of parts along k for a rows x cols product over
 // `ktiles` (all passes) whose parts are `bytes` each and are written and
 // read again when there are several: the pair with the least time.
 void choose_tile(int64_t rows, int64_t cols, int64_t ktiles, int64_t bytes, int* tile, int64_t* splits) {
     double best = 0;
-    *tile = 1;
+    *tile = 0;
     *splits = 1;
-    for (int kind = 0; kind < 2; ++kind) {
-        const int64_t edge = kind == 0 ? 256 : 128, tiles = ceil_div(rows, edge) * ceil_div(cols, edge);
+    for (int kind = 0; kind < 3; ++kind) {
+        const int64_t edge = tile_edge(kind), tiles = ceil_div(rows, edge) * ceil_div(cols, edge);
         for (int64_t n = 1; n <= 16 && (n == 1 || ktiles / n >= 8); ++n) {
             double t = tile_time(kind, tiles * n, ceil_div(ktiles, n));
             if (n > 1) t += 4.0 + (double)(2 * n * bytes) / 4e6;  // one more launch, 4 TB/s
@@ -60,7 +66,7 @@ struct CePlan {
     bool few;           // few tokens: streaming kernels, no packing
     bool packed;        // w is read from packed pieces
     int64_t piece;      // labels of a piece (a multiple of 256; forward unpacked: all)
-    int logits_tile, gx_tile, gw_tile;  // 0: 256, 1: 128
+    int logits_tile, gx_tile, gw_tile;  // 0: 256, 1: 128, 2: 64
     int few_blocks;     // streaming kernels: log2 of the blocks of 16 tokens
     int few_rows;       // and blocks of 16 labels of a logits workgroup
     int64_t tiles;      // statistics per token
@@ -72,8 +78,6 @@ struct CePlan {
         gw_part;
     size_t bytes;
 };
-
-int64_t tile_edge(int tile) { return tile == 0 ? 256 : 128; }
 
 bool take(CePlan* c, size_t* at, int64_t bytes) {
     *at = c->bytes;
@@ -142,10 +146,15 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     }
     const int64_t labels = c->piece < vocab ? c->piece : vocab;
     const int64_t wtiles = ceil_div(width, kBK) * passes;
-    c->logits_tile = tile_time(0, ceil_div(labels, 256) * ceil_div(count, 256), wtiles) <=
-                             tile_time(1, ceil_div(labels, 128) * ceil_div(count, 128), wtiles)
-                         ? 0
-                         : 1;
+    double best = 0;
+    for (int kind = 0; kind < 3; ++kind) {
+        const int64_t edge = tile_edge(kind);
+        const double t = tile_time(kind, ceil_div(labels, edge) * ceil_div(count, edge), wtiles);
+        if (kind == 0 || t < best) {
+            best = t;
+            c->logits_tile = kind;
+        }
+    }
     ok &= take(c, &c->control, sizeof(TropCeControl));
     ok &= take(c, &c->rows, c->padded * 4);
     ok &= take(c, &c->slot, c->padded * 4);
@@ -265,23 +274,20 @@ TropCeParams params(const CeCall& a, const CePlan& c, char* ws) {
 
 TrainKernelId typed(int id, trop_dtype dt) { return (TrainKernelId)(id + (dt == TROP_BF16 ? 1 : 0)); }
 
-// List the kept tokens and pack them.
-trop_status prepare_tokens(int dev, const CeCall& a, const CePlan& c, const TropCeParams& p, hipStream_t s) {
-    trop_status st = train_launch(dev, TK_CE_KEEP, TROP_T_CE_PACK, 1, 1024, &p, s);
-    if (st == TROP_OK && c.planes == 2)
-        st = train_launch(dev, TK_CE_MAGNITUDE, TROP_T_CE_PACK, c.max_parts, 256, &p, s);
-    if (st == TROP_OK) st = train_launch(dev, typed(TK_CE_PACK_X, a.dt), TROP_T_CE_PACK, c.padded / 4, 256, &p, s);
-    return st;
+// List the kept tokens (and, for float32, look for the largest magnitudes).
+trop_status list_tokens(int dev, const CePlan& c, const TropCeParams& p, hipStream_t s) {
+    return train_launch(dev, TK_CE_KEEP, TROP_T_CE_PACK, 1 + c.max_parts, 1024, &p, s);
 }
 
-// This piece's labels into p, and w packed if it has to be.
+// This piece's labels into p; x packed with the first, and w if it has to be.
 trop_status prepare_piece(int dev, const CeCall& a, const CePlan& c, int64_t v0, TropCeParams& p, hipStream_t s) {
     const int64_t labels = a.vocab - v0 < c.piece ? a.vocab - v0 : c.piece;
     p.v0 = v0;
     p.piece = round_up(labels, tile_edge(c.logits_tile));
     p.tile0 = v0 / tile_edge(c.logits_tile);
-    if (!c.packed) return TROP_OK;
-    return train_launch(dev, typed(TK_CE_PACK_W, a.dt), TROP_T_CE_PACK, p.piece < 4096 ? p.piece : 4096, 256, &p, s);
+    p.pack_x = v0 == 0 ? (int32_t)(c.padded / 4) : 0;
+    const int64_t groups = p.pack_x + (c.packed ? ceil_div(p.piece, 4) : 0);
+    return train_launch(dev, typed(TK_CE_PACK, a.dt), TROP_T_CE_PACK, groups, 256, &p, s);
 }
 
 // A streaming kernel of the family at `id` (`per`: its kernels for one label block).
@@ -320,28 +326,28 @@ trop_status few_pieces(int dev, const CeCall& a, const CePlan& c, TropCeParams& 
 // The backward's pieces with the products' tiles.
 trop_status tile_pieces(int dev, const CeCall& a, const CePlan& c, TropCeParams& p, hipStream_t s) {
     const int64_t tokens = a.tokens > 0 ? a.tokens : 1;
-    trop_status st = prepare_tokens(dev, a, c, p, s);
+    trop_status st = list_tokens(dev, c, p, s);
     for (int64_t v0 = 0; st == TROP_OK && v0 < a.vocab; v0 += c.piece) {
         const int64_t labels = a.vocab - v0 < c.piece ? a.vocab - v0 : c.piece;
         st = prepare_piece(dev, a, c, v0, p, s);
         if (st == TROP_OK && a.tokens > 0) {
             const int64_t edge = tile_edge(c.logits_tile);
             st = train_launch(dev, typed(TK_CE_GRAD + 2 * c.logits_tile, a.dt), TROP_T_CE_LOGITS,
-                              p.piece / edge * ceil_div(tokens, edge), c.logits_tile == 0 ? 512 : 256, &p, s);
+                              p.piece / edge * ceil_div(tokens, edge), tile_threads(c.logits_tile), &p, s);
         }
         if (st == TROP_OK && p.grad_x) {
             const int64_t edge = tile_edge(c.gx_tile);
             p.split_tiles = (int32_t)ceil_div(ceil_div(labels, kBK), c.splits);
             p.accumulate = v0 > 0;
             st = train_launch(dev, typed(TK_CE_GX + 2 * c.gx_tile, a.dt), TROP_T_CE_GRAD,
-                              ceil_div(tokens, edge) * ceil_div(a.width, edge) * c.splits, c.gx_tile == 0 ? 512 : 256,
+                              ceil_div(tokens, edge) * ceil_div(a.width, edge) * c.splits, tile_threads(c.gx_tile),
                               &p, s);
         }
         if (st == TROP_OK && p.grad_w) {
             const int64_t edge = tile_edge(c.gw_tile);
             st = train_launch(dev, typed(TK_CE_GW + 2 * c.gw_tile, a.dt), TROP_T_CE_GRAD,
                               ceil_div(labels, edge) * ceil_div(a.width, edge) * c.gw_splits,
-                              c.gw_tile == 0 ? 512 : 256, &p, s);
+                              tile_threads(c.gw_tile), &p, s);
             if (st == TROP_OK && c.gw_splits > 1)
                 st = train_launch(dev, typed(TK_CE_FINISH_W, a.dt), TROP_T_CE_MERGE,
                                   labels * ceil_div(a.width, 1024), 256, &p, s);
@@ -375,13 +381,13 @@ trop_status ce_forward(const CeCall& a, float* loss, float* lse) {
         st = train_launch(dev, few_kernel(TK_CE_FEW, 6, c, a.dt), TROP_T_CE_LOGITS,
                           c.tiles, 256, &p, s);
     } else {
-        st = prepare_tokens(dev, a, c, p, s);
+        st = list_tokens(dev, c, p, s);
         for (int64_t v0 = 0; st == TROP_OK && v0 < a.vocab; v0 += c.piece) {
             st = prepare_piece(dev, a, c, v0, p, s);
             const int64_t edge = tile_edge(c.logits_tile);
             if (st == TROP_OK)
                 st = train_launch(dev, typed(TK_CE_STATS + 2 * c.logits_tile, a.dt), TROP_T_CE_LOGITS,
-                                  p.piece / edge * ceil_div(a.tokens, edge), c.logits_tile == 0 ? 512 : 256, &p, s);
+                                  p.piece / edge * ceil_div(a.tokens, edge), tile_threads(c.logits_tile), &p, s);
         }
     }
     if (st == TROP_OK) st = train_launch(dev, TK_CE_MERGE, TROP_T_CE_MERGE, a.tokens, 256, &p, s);

@@ -32,19 +32,22 @@ const char* const kNames[] = {
     "trop_adamw8_f32",            "trop_adamw8_f32_master",
     "trop_adamw8_bf16",           "trop_adamw8_bf16_master",
     "trop_adamw8_unpack",
-    "trop_ce_keep", "trop_ce_magnitude", "trop_ce_merge",
-    "trop_ce_pack_x_f32",         "trop_ce_pack_x_bf16",
-    "trop_ce_pack_w_f32",         "trop_ce_pack_w_bf16",
-    "trop_ce_finish_f32",         "trop_ce_finish_bf16",
-    "trop_ce_finish_w_f32",       "trop_ce_finish_w_bf16",
-    "trop_ce_stats256_f32",       "trop_ce_stats256_bf16",
-    "trop_ce_stats128_f32",       "trop_ce_stats128_bf16",
-    "trop_ce_grad256_f32",        "trop_ce_grad256_bf16",
-    "trop_ce_grad128_f32",        "trop_ce_grad128_bf16",
-    "trop_ce_gx256_f32",          "trop_ce_gx256_bf16",
-    "trop_ce_gx128_f32",          "trop_ce_gx128_bf16",
-    "trop_ce_gw256_f32",          "trop_ce_gw256_bf16",
-    "trop_ce_gw128_f32",          "trop_ce_gw128_bf16",
+    "trop_ce_keep",               "trop_ce_merge",
+    "trop_ce_pack_f32", "trop_ce_pack_bf16",
+    "trop_ce_finish_f32", "trop_ce_finish_bf16",
+    "trop_ce_finish_w_f32", "trop_ce_finish_w_bf16",
+    "trop_ce_stats256_f32", "trop_ce_stats256_bf16",
+    "trop_ce_stats128_f32", "trop_ce_stats128_bf16",
+    "trop_ce_stats64_f32", "trop_ce_stats64_bf16",
+    "trop_ce_grad256_f32", "trop_ce_grad256_bf16",
+    "trop_ce_grad128_f32", "trop_ce_grad128_bf16",
+    "trop_ce_grad64_f32", "trop_ce_grad64_bf16",
+    "trop_ce_gx256_f32", "trop_ce_gx256_bf16",
+    "trop_ce_gx128_f32", "trop_ce_gx128_bf16",
+    "trop_ce_gx64_f32", "trop_ce_gx64_bf16",
+    "trop_ce_gw256_f32", "trop_ce_gw256_bf16",
+    "trop_ce_gw128_f32", "trop_ce_gw128_bf16",
+    "trop_ce_gw64_f32", "trop_ce_gw64_bf16",
     "trop_ce_few1_n1_f32", "trop_ce_few1_n1_bf16",
     "trop_ce_few1_n2_f32", "trop_ce_few1_n2_bf16",
     "trop_ce_few1_n4_f32", "trop_ce_few1_n4_bf16",

@@ -138,6 +138,7 @@ struct TropCeParams {
     int32_t gw_splits;        // gw: parts along the tokens
     int32_t accumulate;       // gx: add to what the piece before left
     int32_t max_parts;        // workgroups of the magnitude pass
+    int32_t pack_x;           // packing: workgroups that take rows of x
     int32_t identity;         // merge: kept index = token (streaming kernel)
     int32_t backward;
 };
