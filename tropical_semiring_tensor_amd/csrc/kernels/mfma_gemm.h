@@ -4,9 +4,9 @@
 //
 // A workgroup of WM x WN waves computes a BM x BN tile; a wave computes
 // (BM / WM) x (BN / WN) of it in 16 x 16 blocks (v_mfma_f32_16x16x32).  K is
-// walked in tiles of BK.  A tile goes from global memory to LDS directly
-// (16 bytes per lane, no registers in between) into one of STAGES buffers
-// while earlier ones are multiplied.  Operands are read as they lie in
+// walked in tiles of 64.  A tile goes from global memory to LDS directly
+// (16 bytes per lane, no registers in between) into one of two buffers while
+// the other is multiplied.  Operands are read as they lie in
 // memory, so nothing is transposed beforehand:
 //   KM  element (i, k) at i ld + k           (rows along k)
 //   MM  element (i, k) at k ld + i           (rows along i)
@@ -61,16 +61,20 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, const char* base, uint
                  : "memory");
 }
 
-// All but this wave's newest PENDING loads to LDS have landed, every LDS
-// read has returned, and so it is for all waves of the workgroup.
-template <int PENDING>
+// This wave's LDS reads have returned (and, with LOADS, its loads to LDS have
+// landed), and so it is for all waves of the workgroup.
+template <bool LOADS>
 __device__ __forceinline__ void mg_sync() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PENDING) : "memory");
+    if constexpr (LOADS)
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 __device__ __forceinline__ void mg_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
 template <OperandKind KIND, int ROWS, int BK, int WAVES>
 struct MgTile {
+    static_assert(BK == 64, "the swizzles");
     static constexpr int BYTES = ROWS * BK * 2;
     static constexpr int LOADS = BYTES / 1024 / WAVES;  // per wave
     static_assert(LOADS >= 1 && BYTES % (1024 * WAVES) == 0, "tile rows per wave");
@@ -83,7 +87,7 @@ struct MgTile {
     //   KM  16 rows, one chunk each       MM, QM  4 lines x 2 chunks x 2 k groups
     //   QK  16 rows of 8 bytes in 2 lines
     static __device__ __forceinline__ int swizzle(int line) {
-        if constexpr (KIND == KM) return BK == 64 ? (line >> 1) & 7 : (0 - (line >> 2)) & 3;
+        if constexpr (KIND == KM) return (line >> 1) & 7;
         if constexpr (KIND == MM)
             return (ROWS >= 128 ? (line & 3) * 4 : ((line >> 1) & 1) * 4) + ((line >> 3) & 1) * 2;
         if constexpr (KIND == QK) return ((line >> 1) & 1) * 8;
@@ -91,10 +95,19 @@ struct MgTile {
         return 0;
     }
 
+    // A wave's loads are STEP lines apart.  Where no line is clamped (all but
+    // KM) they then differ by a constant, kept out of the vector registers:
+    // one offset serves all.  (Of two spilled registers, one was an offset,
+    // whose reload waited for the loads before it: grad_w 970 against 830 us.)
+    static constexpr int STEP = WAVES * 64 / ROW_CHUNKS;
+    static constexpr int OFFSETS = KIND == KM ? LOADS : 1;
+    static_assert(KIND == KM || LOADS == 1 || (WAVES * 64 % ROW_CHUNKS == 0 && STEP % (KIND == MM ? 16 : 4) == 0),
+                  "equal swizzles STEP lines apart");
+
     // This lane's byte offsets of its loads, from the tile's base.
-    static __device__ __forceinline__ void offsets(const MgOperand& o, int wave, int lane, uint32_t (&off)[LOADS]) {
+    static __device__ __forceinline__ void offsets(const MgOperand& o, int wave, int lane, uint32_t (&off)[OFFSETS]) {
 #pragma unroll
-        for (int s = 0; s < LOADS; ++s) {
+        for (int s = 0; s < OFFSETS; ++s) {
             const int c = (wave + WAVES * s) * 64 + lane;  // chunk of the tile
             const int line = c / ROW_CHUNKS, col = (c % ROW_CHUNKS) ^ swizzle(line);
             if constexpr (KIND == KM)
@@ -108,7 +121,8 @@ struct MgTile {
 
     // Loads of k tile kt of a plane (base: that tile's) into `lds`.
     static __device__ __forceinline__ void load(const MgOperand& o, const char* base, int kt, uint32_t lds, int wave,
-                                                int lane, const uint32_t (&off)[LOADS]) {
+                                                int lane, const uint32_t (&off)[OFFSETS]) {
+        const int64_t step = STEP * o.ld * (KIND == MM ? 2 : 8);
         bool tail = false;  // the operand ends inside this tile
         if constexpr (KIND == KM) tail = (kt + 1) * (BK / 8) - 1 > o.last_k;
         if constexpr (KIND == MM) tail = (kt + 1) * BK - 1 > o.last_k;
@@ -116,18 +130,23 @@ struct MgTile {
 #pragma unroll
             for (int s = 0; s < LOADS; ++s) {
                 const int c = (wave + WAVES * s) * 64 + lane, line = c / ROW_CHUNKS;
-                uint32_t v = off[s];
+                uint32_t v;
                 if constexpr (KIND == KM) {  // its last chunk again: x is zero there
                     const int col = (c % ROW_CHUNKS) ^ swizzle(line);
-                    v -= (uint32_t)max(0, kt * (BK / 8) + col - o.last_k) * 16;
+                    v = off[s] - (uint32_t)max(0, kt * (BK / 8) + col - o.last_k) * 16;
                 } else {  // its last row again: G is zero there
-                    v -= (uint32_t)((int64_t)max(0, kt * BK + line - o.last_k) * o.ld * 2);
+                    v = off[0] + (uint32_t)(s * step) - (uint32_t)((int64_t)max(0, kt * BK + line - o.last_k) * o.ld * 2);
                 }
                 load_to_lds(lds + (wave + WAVES * s) * 1024, base, v);
             }
         } else {
 #pragma unroll
-            for (int s = 0; s < LOADS; ++s) load_to_lds(lds + (wave + WAVES * s) * 1024, base, off[s]);
+            for (int s = 0; s < LOADS; ++s) {
+                if constexpr (KIND == KM)
+                    load_to_lds(lds + (wave + WAVES * s) * 1024, base, off[s]);
+                else
+                    load_to_lds(lds + (wave + WAVES * s) * 1024, base + s * step, off[0]);
+            }
         }
     }
 
@@ -173,21 +192,23 @@ __device__ __forceinline__ f32x4 mg_mfma(s16x8 a, s16x8 b, f32x4 c) {
                                                       0, 0);
 }
 
-// A tile of eight waves with both operands along k alternates its waves in
-// two groups (see mg_walk); the others read and multiply in turn, each
-// wave's reads under its neighbours' products.  Measured at 256 x 256 (one
-// MI355X, 8192 x 8192 x 4096 and 8192 x 4096 x 8192, float32 stored): in two
-// groups KM KM 1181-1210 TFLOP/s, MM QK 1168-1201, MM QM 1224-1254; in turn
-// 1132-1151, 1242-1245, 1253-1257.  32 x 32 x 16 instructions, four waves of
-// 128 x 128, more stages or loads spread between products all stay within
-// 1080-1290: with the matrix units busy 60-65% of the cycles the clock
-// settles at 1.85-2.05 GHz, lower where they are busier.
+// A tile of eight waves alternates them in two groups (see mg_walk); four
+// waves read and multiply in turn, with other workgroups' waves between.
+// Measured at 256 x 256 (one MI355X, 8192 x 8192 x 4096 and 8192 x 4096 x
+// 8192, float32 stored): KM KM 1241-1255 TFLOP/s, MM QK 1262-1288, MM QM
+// 1260-1294; all eight waves in turn 1132-1151, 1242-1245, 1253-1257; in two
+// groups with k tiles of 32 in four buffers 1199-1225, 1168-1201, 1224-1254
+// (half-line requests for KM).  32 x 32 x 16 instructions, four waves of 128 x
+// 128, more buffers, loads spread between the products: 1080-1290.  With the
+// matrix units busy 60-65% of the cycles the clock settles at 1.85-2.05 GHz,
+// lower where they are busier; with every load hitting the L1 (a timing copy)
+// KM KM reaches 1500.  In 128 x 128, k tiles of 32 or three buffers are slower
+// by up to a fifth.
 template <int BM_, int BN_, int WM_, int WN_, OperandKind KA_, OperandKind KB_, int PLANES_>
 struct MgConfig {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PLANES = PLANES_;
     static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
-    static constexpr bool PINGPONG = WAVES == 8 && KA_ == KM && KB_ == KM;
-    static constexpr int BK = PINGPONG ? 32 : 64, STAGES = PINGPONG ? 4 : 2;
+    static constexpr int BK = 64, STAGES = 2;
     static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16 x 16 blocks of a wave
     static constexpr int PASSES = PLANES == 1 ? 1 : 3;
     using TA = MgTile<KA_, BM, BK, WAVES>;
@@ -202,17 +223,20 @@ struct MgConfig {
 // is acc[fi][fj][r].  `lds`: LDS_BYTES.
 //
 // Eight waves: the second four (one more wave on each SIMD) run half a turn
-// behind the first, held by one extra barrier.  A turn is: read a tile's
-// fragments and start the loads of the tile STAGES - 1 further; barrier;
-// multiply; barrier.  So on each SIMD one wave multiplies while the other
-// reads, and the loads have two to three turns to land.
+// behind the first, held by one extra barrier.  A turn is: read the tile's
+// fragments; barrier; multiply; barrier.  So on each SIMD one wave
+// multiplies while the other reads.  In the half turn in which the first
+// group reads tile t and the second multiplies tile t - 1, both start their
+// loads of tile t + 1 into the buffer that tile t - 1 left (the second group
+// read it in the half turn before), and have until the end of the next half
+// turn: the first group's multiplying, the second's reading.
 template <typename C>
 __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOperand& a, const MgOperand& b,
                                         int ktiles, char* lds) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int arow = (wave / C::WN) * (C::BM / C::WM), brow = (wave % C::WN) * (C::BN / C::WN);
-    uint32_t aoff[C::TA::LOADS], boff[C::TB::LOADS];
+    uint32_t aoff[C::TA::OFFSETS], boff[C::TB::OFFSETS];
     C::TA::offsets(a, wave, lane, aoff);
     C::TB::offsets(b, wave, lane, boff);
 #pragma unroll
@@ -222,7 +246,7 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
     const uint32_t lds0 = lds_offset(lds);
     const int total = ktiles * C::PASSES;
     if (total <= 0) {
-        mg_sync<0>();
+        mg_sync<true>();
         return;
     }
     // the next tile to load: its pass and its k tile
@@ -241,76 +265,82 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
             pb = b.base + (C::PASSES == 3 && pass == 1 ? b.plane_bytes : 0);
         }
     };
-    s16x8 fa[C::FM], fb[C::FN];
-    auto read = [&](int buf, int kk) {
-        const char* ta = lds + buf * C::STAGE;
-        const char* tb = ta + C::TA::BYTES;
+    if constexpr (C::WAVES == 8) {
+        constexpr int NK = C::BK / 32;
+        s16x8 fa[NK][C::FM], fb[NK][C::FN];
+        auto read = [&](int buf) {
+            const char* ta = lds + buf * C::STAGE;
+            const char* tb = ta + C::TA::BYTES;
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) fb[j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
+            for (int kk = 0; kk < NK; ++kk) {
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) fa[i] = C::TA::fragment(ta, arow + 16 * i, kk, lane);
-    };
-    auto multiply = [&]() {
+                for (int j = 0; j < C::FN; ++j) fb[kk][j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
+                for (int i = 0; i < C::FM; ++i) fa[kk][i] = C::TA::fragment(ta, arow + 16 * i, kk, lane);
+            }
+        };
+        auto multiply = [&]() {
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j) acc[i][j] = mg_mfma<C::PLANES>(fa[i], fb[j], acc[i][j]);
-    };
-    if constexpr (C::PINGPONG) {
-        constexpr int S = C::STAGES, PENDING = (S - 2) * (C::TA::LOADS + C::TB::LOADS);
-        for (int q = 0; q < S - 1 && q < total; ++q) load_next(q);
-        // tile 0 is in LDS
-        if (S - 1 <= total)
-            mg_sync<PENDING>();
-        else
-            mg_sync<0>();
-        const bool second = wave >= C::WAVES / 2;
-        if (second) mg_barrier();
-        int buf = 0, lbuf = S - 1;
-        for (int t = 0; t < total; ++t) {
-            // into tile t - 1's buffer: the other group read it before the
-            // barrier that started this turn
-            const bool more = t + S - 1 < total;
-            if (more) load_next(lbuf);
-            read(buf, 0);
-            // this wave's share of tile t + 1 has landed
-            if (more)
-                mg_sync<PENDING>();
-            else
-                mg_sync<0>();
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_setprio(1);
-            multiply();
-            __builtin_amdgcn_s_setprio(0);
-            __builtin_amdgcn_sched_barrier(0);
-            mg_barrier();
-            __builtin_amdgcn_sched_barrier(0);
-            lbuf = buf;
-            buf = buf + 1 == S ? 0 : buf + 1;
-        }
-        if (!second) mg_barrier();
-        mg_sync<0>();
-    } else {
-        // One barrier a tile.  Four waves (two workgroups to a CU) start the
-        // next tile's loads behind it, eight before the last products of
-        // the turn are issued: measured 1165 and 1029 TFLOP/s for MM QK in
-        // 128 x 128, 1170 and 1245 in 256 x 256.
-        constexpr bool BEHIND = C::WAVES == 4;
+            for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < C::FN; ++j) acc[i][j] = mg_mfma<C::PLANES>(fa[kk][i], fb[kk][j], acc[i][j]);
+        };
         load_next(0);
-        if constexpr (!BEHIND) mg_sync<0>();
+        mg_sync<true>();
+        if (wave >= 4) {
+            if (1 < total) load_next(1);
+            mg_barrier();
+            for (int t = 0; t < total; ++t) {
+                read(t & 1);
+                mg_sync<true>();
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_setprio(1);
+                if (t + 2 < total) load_next(t & 1);
+                multiply();
+                __builtin_amdgcn_s_setprio(0);
+                __builtin_amdgcn_sched_barrier(0);
+                mg_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            for (int t = 0; t < total; ++t) {
+                if (t + 1 < total) load_next((t + 1) & 1);
+                read(t & 1);
+                mg_sync<false>();
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_setprio(1);
+                multiply();
+                __builtin_amdgcn_s_setprio(0);
+                __builtin_amdgcn_sched_barrier(0);
+                mg_sync<true>();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            mg_barrier();
+        }
+    } else {
+        load_next(0);
         for (int t = 0; t < total; ++t) {
-            const int buf = t & 1;
-            if constexpr (BEHIND) mg_sync<0>();  // tile t has landed; tile t - 1 has been read
-            if (t + 1 < total) load_next(buf ^ 1);
+            mg_sync<true>();  // tile t has landed; tile t - 1 has been read
+            if (t + 1 < total) load_next((t + 1) & 1);
+            const char* ta = lds + (t & 1) * C::STAGE;
+            const char* tb = ta + C::TA::BYTES;
 #pragma unroll
             for (int kk = 0; kk < C::BK / 32; ++kk) {
-                read(buf, kk);
-                multiply();
+                s16x8 fa[C::FM], fb[C::FN];
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j) fb[j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i) fa[i] = C::TA::fragment(ta, arow + 16 * i, kk, lane);
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < C::FN; ++j) acc[i][j] = mg_mfma<C::PLANES>(fa[i], fb[j], acc[i][j]);
             }
-            if constexpr (!BEHIND) mg_sync<0>();
         }
-        if constexpr (BEHIND) mg_sync<0>();
     }
+    mg_sync<true>();
 }
 
 }  // namespace trop
