@@ -38,15 +38,10 @@ namespace trop {
 
 constexpr float CE_LOG2E = 1.44269504088896340736f;
 
-// exp of a difference of logits.  bfloat16 operands: the exponent's rounding
-// (2^-24 of it) is far below the products' own error.  float32: expf.
-template <int PLANES>
-__device__ __forceinline__ float ce_exp(float x) {
-    if constexpr (PLANES == 1)
-        return __builtin_amdgcn_exp2f(x * CE_LOG2E);
-    else
-        return expf(x);
-}
+// exp of a logit less the maximum or lse.  The exponent's rounding makes it
+// |x| 2^-24 of itself wrong, no more than the rounding of lse does.  (expf is
+// a dozen operations more in the tiles' epilogues.)
+__device__ __forceinline__ float ce_exp(float x) { return __builtin_amdgcn_exp2f(x * CE_LOG2E); }
 
 __device__ __forceinline__ int64_t ce_target(const TropCeParams& p, int64_t n) {
     return p.target_bytes == 8 ? static_cast<const int64_t*>(p.target)[n]
@@ -170,12 +165,12 @@ __device__ __forceinline__ void ce_split(float scaled, _Float16& h, _Float16& l)
 }
 
 // ---- packing ---------------------------------------------------------------
-// 8 elements of a row [c, c + 8), zeros past its end, into the planes.
+// 8 elements of a row [c, c + 8), zeros past its end, into the packed row
+// (float32: 32 elements' h, then their l).
 template <int PLANES>
-__device__ __forceinline__ void ce_pack8(const void* row, int64_t c, int64_t width, int32_t e, char* out,
-                                         int64_t plane_bytes) {
+__device__ __forceinline__ void ce_pack8(const void* row, int64_t c, int64_t width, int32_t e, char* out) {
     if constexpr (PLANES == 1) {
-        *reinterpret_cast<VecOf<bf16, 8>::raw*>(out) = load_row<bf16, 8>(static_cast<const bf16*>(row), c, width);
+        *reinterpret_cast<VecOf<bf16, 8>::raw*>(out + c * 2) = load_row<bf16, 8>(static_cast<const bf16*>(row), c, width);
     } else {
         f16x8 h, l;
 #pragma unroll
@@ -189,8 +184,9 @@ __device__ __forceinline__ void ce_pack8(const void* row, int64_t c, int64_t wid
                 l[q * 4 + i] = b;
             }
         }
+        out += c / 32 * 128 + c % 32 * 2;
         *reinterpret_cast<f16x8*>(out) = h;
-        *reinterpret_cast<f16x8*>(out + plane_bytes) = l;
+        *reinterpret_cast<f16x8*>(out + 64) = l;
     }
 }
 
@@ -227,22 +223,19 @@ __device__ __forceinline__ void ce_pack_body(const TropCeParams& p) {
     const size_t eb = PLANES == 1 ? 2 : 4;
     const char* row;
     char* out;
-    int64_t plane;
     if (is_w) {
         if (i >= p.piece) return;
         row = static_cast<const char*>(p.w) + min(p.v0 + i, p.vocab - 1) * p.ldw * eb;
-        out = static_cast<char*>(p.wp) + i * p.width_p * 2;
-        plane = p.piece * p.width_p * 2;
+        out = static_cast<char*>(p.wp) + i * p.width_p * 2 * PLANES;
     } else {
         const int64_t kept = p.control->kept;
         if (i >= (kept + 255) / 256 * 256) return;
         row = i < kept ? static_cast<const char*>(p.x) + (int64_t)p.rows[i] * p.ldx * eb : nullptr;
-        out = static_cast<char*>(p.xp) + i * p.width_p * 2;
-        plane = p.padded * p.width_p * 2;
+        out = static_cast<char*>(p.xp) + i * p.width_p * 2 * PLANES;
     }
 #pragma unroll 2
     for (int64_t c = lane * 8; c < p.width_p; c += 64 * 8)
-        ce_pack8<PLANES>(row, c, row ? p.width : 0, e, out + c * 2, plane);
+        ce_pack8<PLANES>(row, c, row ? p.width : 0, e, out);
 }
 
 // ---- tiles -----------------------------------------------------------------
@@ -265,17 +258,16 @@ __device__ __forceinline__ bool ce_tile(int64_t id, int64_t tm, int64_t tn, int6
 template <typename C>
 __device__ __forceinline__ MgOperand ce_w_rows(const TropCeParams& p, int64_t r0) {
     MgOperand o;
-    o.k_bytes = C::BK * 2;
+    o.k_bytes = 128;
+    o.plane_bytes = 0;
     if (C::PLANES == 2 || p.w_packed) {
-        o.base = static_cast<const char*>(p.wp) + r0 * p.width_p * 2;
-        o.ld = p.width_p;
-        o.plane_bytes = p.piece * p.width_p * 2;
+        o.ld = p.width_p * C::PLANES;
+        o.base = static_cast<const char*>(p.wp) + r0 * o.ld * 2;
         o.last_row = 0x7fffffff;
         o.last_k = 0x7fffffff;
     } else {
         o.base = static_cast<const char*>(p.w) + (p.v0 + r0) * p.ldw * 2;
         o.ld = p.ldw;
-        o.plane_bytes = 0;
         o.last_row = (int32_t)min(p.vocab - 1 - (p.v0 + r0), (int64_t)0x7fffffff);
         o.last_k = (int32_t)(p.width / 8 - 1);
     }
@@ -291,15 +283,15 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
     int64_t mi, ni;
     if (!ce_tile(blockIdx.x, p.piece / C::BM, (kept + C::BN - 1) / C::BN, mi, ni)) return;
     MgOperand b;
-    b.base = static_cast<const char*>(p.xp) + ni * C::BN * p.width_p * 2;
-    b.ld = p.width_p;
-    b.plane_bytes = p.padded * p.width_p * 2;
-    b.k_bytes = C::BK * 2;
+    b.ld = p.width_p * C::PLANES;
+    b.base = static_cast<const char*>(p.xp) + ni * C::BN * b.ld * 2;
+    b.plane_bytes = 0;
+    b.k_bytes = 128;
     b.last_row = b.last_k = 0x7fffffff;
     f32x4 acc[C::FM][C::FN];
     // (only tiles that hold a column: the loads clamp to a row's last chunk
     // within a tile, not from a tile past it)
-    mg_walk<C>(acc, ce_w_rows<C>(p, mi * C::BM), b, (int)((p.width + C::BK - 1) / C::BK), lds);
+    mg_walk<C>(acc, ce_w_rows<C>(p, mi * C::BM), b, (int)((p.width + C::KT - 1) / C::KT), lds);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
     const int64_t v_wave = p.v0 + mi * C::BM + (wave / C::WN) * (C::BM / C::WM);  // label of the wave's row 0
@@ -340,11 +332,12 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
             if (__any(trow[j] >= 0)) {
+                float l = 0.f;
 #pragma unroll
                 for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (trow[j] == 16 * i + 4 * (lane / 16) + r) p.target_logit[n[j]] = acc[i][j][r];
+                    for (int r = 0; r < 4; ++r) l = trow[j] == 16 * i + 4 * (lane / 16) + r ? acc[i][j][r] : l;
+                if (trow[j] >= 0) p.target_logit[n[j]] = l;
             }
             float m = -INFINITY;
 #pragma unroll
@@ -359,7 +352,7 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
 #pragma unroll
             for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s += ce_exp<C::PLANES>(acc[i][j][r] - base);
+                for (int r = 0; r < 4; ++r) s += ce_exp(acc[i][j][r] - base);
             s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
             if (lane < 16) part[(wave / C::WN) * C::BN + n_wave + 16 * j + lane] = make_float2(m, s);
@@ -372,7 +365,7 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
             for (int q = 1; q < C::WM; ++q) {
                 const float2 o = part[q * C::BN + threadIdx.x];
                 const float m = nan_max(a.x, o.x), base = m == -INFINITY ? 0.f : m;
-                a.y = a.y * ce_exp<C::PLANES>(a.x - base) + o.y * ce_exp<C::PLANES>(o.x - base);
+                a.y = a.y * ce_exp(a.x - base) + o.y * ce_exp(o.x - base);
                 a.x = m;
             }
             if (tok < kept) reinterpret_cast<float2*>(p.stats)[tok * p.tiles + p.tile0 + mi] = a;
@@ -383,17 +376,23 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
         for (int j = 0; j < C::FN; ++j) {
             const bool on = n[j] < kept;
             const float lse = on ? p.kept_lse[n[j]] : 0.f, weight = on ? p.kept_grad[n[j]] : 0.f;
-            const bool hit = __any(trow[j] >= 0);
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = ce_exp(acc[i][j][r] - lse);
+            if (__any(trow[j] >= 0)) {
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][j][r] -= trow[j] == 16 * i + 4 * (lane / 16) + r ? 1.f : 0.f;
+            }
             char* out = static_cast<char*>(p.g) + (((v_wave - p.v0) / 4 + lane / 16) * p.padded + n[j]) * 8;
 #pragma unroll
             for (int i = 0; i < C::FM; ++i) {
                 FloatVec<4> g;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float v = ce_exp<C::PLANES>(acc[i][j][r] - lse);
-                    if (hit && trow[j] == 16 * i + 4 * (lane / 16) + r) v -= 1.f;
-                    g[r] = on ? v * weight : 0.f;
-                }
+                for (int r = 0; r < 4; ++r) g[r] = on ? acc[i][j][r] * weight : 0.f;
                 char* o = out + (int64_t)(4 * i) * p.padded * 8;
                 if constexpr (C::PLANES == 1) {
                     *reinterpret_cast<VecOf<bf16, 4>::raw*>(o) = from_float<bf16, 4>(g);
@@ -425,28 +424,27 @@ __device__ __forceinline__ void ce_grad_x_body(const TropCeParams& p, char* lds)
     if (!ce_tile(blockIdx.x, tm, tn * p.splits, mi, q)) return;
     const int64_t ni = q % tn, split = q / tn;
     // (k tiles that hold a label: a part past them is empty, its sums zero)
-    const int64_t ktiles = (min(p.piece, p.vocab - p.v0) + C::BK - 1) / C::BK;
+    const int64_t ktiles = (min(p.piece, p.vocab - p.v0) + C::KT - 1) / C::KT;
     const int64_t kt0 = min(split * p.split_tiles, ktiles), kt1 = min(kt0 + p.split_tiles, ktiles);
-    const int64_t k0 = kt0 * C::BK;
+    const int64_t k0 = kt0 * C::KT;
     MgOperand a, b;
+    a.plane_bytes = 0;
     if (C::PLANES == 2 || p.w_packed) {
-        a.base = static_cast<const char*>(p.wp) + (k0 * p.width_p + ni * C::BM) * 2;
-        a.ld = p.width_p;
-        a.plane_bytes = p.piece * p.width_p * 2;
-        a.last_row = (int32_t)((p.width_p - ni * C::BM) / 8 - 1);
+        a.ld = p.width_p * C::PLANES;
+        a.base = static_cast<const char*>(p.wp) + (k0 * a.ld + ni * C::BM * C::PLANES) * 2;
+        a.last_row = (int32_t)((p.width_p - ni * C::BM) * C::PLANES / 8 - 1);
         a.last_k = 0x7fffffff;
     } else {
         a.base = static_cast<const char*>(p.w) + ((p.v0 + k0) * p.ldw + ni * C::BM) * 2;
         a.ld = p.ldw;
-        a.plane_bytes = 0;
         a.last_row = (int32_t)((p.width - ni * C::BM) / 8 - 1);
         a.last_k = (int32_t)min(p.vocab - 1 - (p.v0 + k0), (int64_t)0x7fffffff);
     }
-    a.k_bytes = C::BK * a.ld * 2;
+    a.k_bytes = C::KT * a.ld * 2;
     b.base = static_cast<const char*>(p.g) + (k0 / 4 * p.padded + mi * C::BN) * 8;
     b.ld = p.padded;
     b.plane_bytes = p.piece * p.padded * 2;
-    b.k_bytes = (C::BK / 4) * p.padded * 8;
+    b.k_bytes = (C::KT / 4) * p.padded * 8;
     b.last_row = b.last_k = 0;
     f32x4 acc[C::FM][C::FN];
     mg_walk<C>(acc, a, b, (int)(kt1 - kt0), lds);
@@ -488,19 +486,19 @@ __device__ __forceinline__ void ce_grad_w_body(const TropCeParams& p, char* lds)
     int64_t mi, q;
     if (!ce_tile(blockIdx.x, (min(p.piece, p.vocab - p.v0) + C::BN - 1) / C::BN, tn * p.gw_splits, mi, q)) return;
     const int64_t ni = q % tn, split = q / tn;
-    const int64_t ktiles = (kept + C::BK - 1) / C::BK, per = (ktiles + p.gw_splits - 1) / p.gw_splits;
-    const int64_t kt0 = min(split * per, ktiles), kt1 = min(kt0 + per, ktiles), k0 = kt0 * C::BK;
+    const int64_t ktiles = (kept + C::KT - 1) / C::KT, per = (ktiles + p.gw_splits - 1) / p.gw_splits;
+    const int64_t kt0 = min(split * per, ktiles), kt1 = min(kt0 + per, ktiles), k0 = kt0 * C::KT;
     MgOperand a, b;
-    a.base = static_cast<const char*>(p.xp) + (k0 * p.width_p + ni * C::BM) * 2;
-    a.ld = p.width_p;
-    a.plane_bytes = p.padded * p.width_p * 2;
-    a.k_bytes = C::BK * p.width_p * 2;
-    a.last_row = (int32_t)((p.width_p - ni * C::BM) / 8 - 1);
+    a.ld = p.width_p * C::PLANES;
+    a.base = static_cast<const char*>(p.xp) + (k0 * a.ld + ni * C::BM * C::PLANES) * 2;
+    a.plane_bytes = 0;
+    a.k_bytes = C::KT * a.ld * 2;
+    a.last_row = (int32_t)((p.width_p - ni * C::BM) * C::PLANES / 8 - 1);
     a.last_k = 0x7fffffff;
     b.base = static_cast<const char*>(p.g) + (mi * (C::BN / 4) * p.padded + k0) * 8;
     b.ld = p.padded;
     b.plane_bytes = p.piece * p.padded * 2;
-    b.k_bytes = C::BK * 8;
+    b.k_bytes = C::KT * 8;
     b.last_row = b.last_k = 0;
     f32x4 acc[C::FM][C::FN];
     mg_walk<C>(acc, a, b, (int)(kt1 - kt0), lds);
@@ -686,7 +684,7 @@ __device__ __forceinline__ void ce_few_body(const TropCeParams& p) {
 #pragma unroll
             for (int i = 0; i < RF; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s += expf(acc[i][j][r] - base);
+                for (int r = 0; r < 4; ++r) s += ce_exp(acc[i][j][r] - base);
             s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
             if (lane < 16 && n < p.tokens)
@@ -701,7 +699,7 @@ __device__ __forceinline__ void ce_few_body(const TropCeParams& p) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = 16 * i + 4 * (lane / 16) + r;
-                    const float g = expf(acc[i][j][r] - lse) - (v0 + row == t ? 1.f : 0.f);
+                    const float g = ce_exp(acc[i][j][r] - lse) - (v0 + row == t ? 1.f : 0.f);
                     out[(int64_t)row * (16 * NB)] = on && v0 + row < p.vocab ? g * weight : 0.f;
                 }
         }
@@ -874,11 +872,11 @@ __device__ __forceinline__ void ce_merge_body(const TropCeParams& p) {
     for (int64_t t = threadIdx.x; t < p.tiles; t += 256) {
         const float2 a = q[t];
         const float top = nan_max(m, a.x), base = top == -INFINITY ? 0.f : top;
-        s = s * expf(m - base) + a.y * expf(a.x - base);
+        s = s * ce_exp(m - base) + a.y * ce_exp(a.x - base);
         m = top;
     }
     float top = wave_nan_max(m), base = top == -INFINITY ? 0.f : top;
-    s = wave_sum(s * expf(m - base));
+    s = wave_sum(s * ce_exp(m - base));
     if (lane == 0) lds[wave] = make_float2(top, s);
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -886,7 +884,7 @@ __device__ __forceinline__ void ce_merge_body(const TropCeParams& p) {
         base = m == -INFINITY ? 0.f : m;
         s = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) s += lds[w].y * expf(lds[w].x - base);
+        for (int w = 0; w < 4; ++w) s += lds[w].y * ce_exp(lds[w].x - base);
         const float lse = m + logf(s);
         p.lse[n] = lse;
         p.loss[n] = lse - p.target_logit[i];

@@ -20,9 +20,12 @@
 // fills LDS in lane order, it is the lanes' global addresses that are
 // permuted.
 //
-// PLANES = 1: bfloat16 values.  PLANES = 2: a float32 value scaled by a
-// power of two, as the sum of two float16 values h + l (22 bits); the
-// product is l h' + h l' + h h', three walks over K, smallest terms first.
+// PLANES = 1: bfloat16 values, k tiles of 64.  PLANES = 2: a float32 value
+// scaled by a power of two, as the sum of two float16 values h + l (22
+// bits); the product is l h' + h l' + h h'.  A k tile is 32 of both planes,
+// as many bytes, so that every value is loaded and read once for its three
+// products.  KM and MM have 32 consecutive elements' h, then their l (`ld`
+// counts both); QK and QM have the planes apart.
 #pragma once
 #include "train_common.h"
 
@@ -40,7 +43,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 struct MgOperand {
     const char* base;     // tile row 0 at k = 0, plane 0
     int64_t ld;           // elements
-    int64_t plane_bytes;  // from plane 0 to plane 1
+    int64_t plane_bytes;  // QK, QM: from plane 0 to plane 1
     int64_t k_bytes;      // from one k tile to the next
     int32_t last_row;     // KM: last readable tile row; MM: last readable 8-element chunk of a row
     int32_t last_k;       // KM: last readable chunk of a row (counted from k = 0); MM: last readable k
@@ -72,14 +75,18 @@ __device__ __forceinline__ void mg_sync() {
 }
 __device__ __forceinline__ void mg_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
-template <OperandKind KIND, int ROWS, int BK, int WAVES>
+template <OperandKind KIND, int ROWS, int PLANES, int WAVES>
 struct MgTile {
-    static_assert(BK == 64, "the swizzles");
+    static constexpr int BK = 64;       // elements of a tile row, of both planes
+    static constexpr int KT = BK / PLANES;  // its k
     static constexpr int BYTES = ROWS * BK * 2;
     static constexpr int LOADS = BYTES / 1024 / WAVES;  // per wave
     static_assert(LOADS >= 1 && BYTES % (1024 * WAVES) == 0, "tile rows per wave");
     // 16-byte chunks of a line of the LDS copy
-    static constexpr int ROW_CHUNKS = KIND == KM ? BK / 8 : KIND == MM ? ROWS / 8 : KIND == QK ? ROWS / 2 : BK / 2;
+    // (two planes: a line of MM holds both, as memory does; QK has the second
+    // plane's lines after the first's, QM its chunks after the first's)
+    static constexpr int ROW_CHUNKS =
+        KIND == KM ? BK / 8 : KIND == MM ? PLANES * ROWS / 8 : KIND == QK ? ROWS / 2 : BK / 2;
 
     // Chunk c of a line lies at c ^ swizzle(line).  LDS serves 256 bytes, 16
     // chunks, at a time, so the lanes of a read that are served together
@@ -89,20 +96,24 @@ struct MgTile {
     static __device__ __forceinline__ int swizzle(int line) {
         if constexpr (KIND == KM) return (line >> 1) & 7;
         if constexpr (KIND == MM)
-            return (ROWS >= 128 ? (line & 3) * 4 : ((line >> 1) & 1) * 4) + ((line >> 3) & 1) * 2;
+            return (PLANES * ROWS >= 128 ? (line & 3) * 4 : ((line >> 1) & 1) * 4) + ((line >> 3) & 1) * 2;
         if constexpr (KIND == QK) return ((line >> 1) & 1) * 8;
         if constexpr (KIND == QM) return (line & 1) * 2 + ((line >> 1) & 1) * 8;
         return 0;
     }
 
     // A wave's loads are STEP lines apart.  Where no line is clamped (all but
-    // KM) they then differ by a constant, kept out of the vector registers:
-    // one offset serves all.  (Of two spilled registers, one was an offset,
-    // whose reload waited for the loads before it: grad_w 970 against 830 us.)
+    // KM) those of equal swizzle then differ by a constant, kept out of the
+    // vector registers: one offset serves all (two where MM's steps of 8
+    // lines alternate in swizzle).  (Of two spilled registers, one was an
+    // offset, whose reload waited for the loads before it: grad_w 970
+    // against 830 us.)
     static constexpr int STEP = WAVES * 64 / ROW_CHUNKS;
-    static constexpr int OFFSETS = KIND == KM ? LOADS : 1;
-    static_assert(KIND == KM || LOADS == 1 || (WAVES * 64 % ROW_CHUNKS == 0 && STEP % (KIND == MM ? 16 : 4) == 0),
-                  "equal swizzles STEP lines apart");
+    static constexpr int OFFSETS = KIND == KM ? LOADS : KIND == MM && STEP % 16 == 8 && LOADS > 1 ? 2 : 1;
+    static_assert(KIND == KM || LOADS == 1 ||
+                      (WAVES * 64 % ROW_CHUNKS == 0 && STEP % (KIND == MM ? 16 / OFFSETS : 4) == 0),
+                  "equal swizzles OFFSETS STEP lines apart");
+    static_assert(KIND != QK || PLANES == 1 || 8 % STEP == 0, "a load of QK within a plane");
 
     // This lane's byte offsets of its loads, from the tile's base.
     static __device__ __forceinline__ void offsets(const MgOperand& o, int wave, int lane, uint32_t (&off)[OFFSETS]) {
@@ -114,18 +125,20 @@ struct MgTile {
                 off[s] = (uint32_t)((int64_t)min(line, o.last_row) * o.ld * 2 + col * 16);
             else if constexpr (KIND == MM)
                 off[s] = (uint32_t)((int64_t)line * o.ld * 2 + min(col, o.last_row) * 16);
+            else if constexpr (KIND == QM && PLANES == 2)
+                off[s] = (uint32_t)((int64_t)line * o.ld * 8 + (col & 15) * 16 + (col >> 4) * o.plane_bytes);
             else
                 off[s] = (uint32_t)((int64_t)line * o.ld * 8 + col * 16);
         }
     }
 
-    // Loads of k tile kt of a plane (base: that tile's) into `lds`.
+    // Loads of k tile kt (base: that tile's) into `lds`.
     static __device__ __forceinline__ void load(const MgOperand& o, const char* base, int kt, uint32_t lds, int wave,
                                                 int lane, const uint32_t (&off)[OFFSETS]) {
         const int64_t step = STEP * o.ld * (KIND == MM ? 2 : 8);
         bool tail = false;  // the operand ends inside this tile
-        if constexpr (KIND == KM) tail = (kt + 1) * (BK / 8) - 1 > o.last_k;
-        if constexpr (KIND == MM) tail = (kt + 1) * BK - 1 > o.last_k;
+        if constexpr (KIND == KM && PLANES == 1) tail = (kt + 1) * (BK / 8) - 1 > o.last_k;
+        if constexpr (KIND == MM && PLANES == 1) tail = (kt + 1) * BK - 1 > o.last_k;
         if (__builtin_expect(tail, 0)) {
 #pragma unroll
             for (int s = 0; s < LOADS; ++s) {
@@ -144,13 +157,18 @@ struct MgTile {
             for (int s = 0; s < LOADS; ++s) {
                 if constexpr (KIND == KM)
                     load_to_lds(lds + (wave + WAVES * s) * 1024, base, off[s]);
+                else if constexpr (KIND == QK && PLANES == 2)
+                    load_to_lds(lds + (wave + WAVES * s) * 1024,
+                                base + s * STEP / 8 * o.plane_bytes + s % (8 / STEP) * step, off[0]);
                 else
-                    load_to_lds(lds + (wave + WAVES * s) * 1024, base + s * step, off[0]);
+                    load_to_lds(lds + (wave + WAVES * s) * 1024, base + s / OFFSETS * OFFSETS * step,
+                                off[s % OFFSETS]);
             }
         }
     }
 
-    // Fragment of rows [row, row + 16) and k [32 kk, 32 kk + 32) of a tile.
+    // Fragment of rows [row, row + 16) of a tile: k [32 kk, 32 kk + 32), or
+    // all 32 k of plane kk.
     static __device__ __forceinline__ s16x8 fragment(const char* tile, int row, int kk, int lane) {
         const int g = lane / 16, i = lane & 15;
         if constexpr (KIND == KM) {
@@ -168,7 +186,10 @@ struct MgTile {
             for (int t = 0; t < 2; ++t) {
                 const int k = kk * 32 + g * 8 + t * 4 + i / 4;
                 const char* p;
-                if constexpr (KIND == MM) {
+                if constexpr (KIND == MM && PLANES == 2) {
+                    const int chunk = row / 32 * 8 + kk * 4 + row % 32 / 8 + (i & 3) / 2, line = k - kk * 32;
+                    p = tile + line * (ROWS * 4) + (chunk ^ swizzle(line)) * 16 + (i & 1) * 8;
+                } else if constexpr (KIND == MM) {
                     const int chunk = row / 8 + (i & 3) / 2;
                     p = tile + k * (ROWS * 2) + (chunk ^ swizzle(k)) * 16 + (i & 1) * 8;
                 } else {
@@ -208,14 +229,23 @@ template <int BM_, int BN_, int WM_, int WN_, OperandKind KA_, OperandKind KB_, 
 struct MgConfig {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PLANES = PLANES_;
     static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
-    static constexpr int BK = 64, STAGES = 2;
+    static constexpr int STAGES = 2;
     static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16 x 16 blocks of a wave
-    static constexpr int PASSES = PLANES == 1 ? 1 : 3;
-    using TA = MgTile<KA_, BM, BK, WAVES>;
-    using TB = MgTile<KB_, BN, BK, WAVES>;
+    using TA = MgTile<KA_, BM, PLANES, WAVES>;
+    using TB = MgTile<KB_, BN, PLANES, WAVES>;
+    static constexpr int KT = TA::KT;  // k of a tile
     static constexpr int STAGE = TA::BYTES + TB::BYTES;
     static constexpr int LDS_BYTES = STAGES * STAGE;
 };
+
+template <typename C>
+__device__ __forceinline__ void mg_multiply(f32x4 (&acc)[C::FM][C::FN], const s16x8 (&a)[C::FM],
+                                            const s16x8 (&b)[C::FN]) {
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = mg_mfma<C::PLANES>(a[i], b[j], acc[i][j]);
+}
 
 // Walks the first `ktiles` k tiles of both operands, each of which starts
 // at or before an operand's last_k.  The sum of row
@@ -244,35 +274,26 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const uint32_t lds0 = lds_offset(lds);
-    const int total = ktiles * C::PASSES;
-    if (total <= 0) {
+    if (ktiles <= 0) {
         mg_sync<true>();
         return;
     }
-    // the next tile to load: its pass and its k tile
-    int pass = 0, kt = 0;
+    int kt = 0;  // the next tile to load
     const char *pa = a.base, *pb = b.base;
-    if constexpr (C::PASSES == 3) pa += a.plane_bytes;
     auto load_next = [&](int buf) {
         C::TA::load(a, pa, kt, lds0 + buf * C::STAGE, wave, lane, aoff);
         C::TB::load(b, pb, kt, lds0 + buf * C::STAGE + C::TA::BYTES, wave, lane, boff);
         pa += a.k_bytes;
         pb += b.k_bytes;
-        if (++kt == ktiles) {
-            kt = 0;
-            ++pass;
-            pa = a.base;
-            pb = b.base + (C::PASSES == 3 && pass == 1 ? b.plane_bytes : 0);
-        }
+        ++kt;
     };
     if constexpr (C::WAVES == 8) {
-        constexpr int NK = C::BK / 32;
-        s16x8 fa[NK][C::FM], fb[NK][C::FN];
+        s16x8 fa[2][C::FM], fb[2][C::FN];
         auto read = [&](int buf) {
             const char* ta = lds + buf * C::STAGE;
             const char* tb = ta + C::TA::BYTES;
 #pragma unroll
-            for (int kk = 0; kk < NK; ++kk) {
+            for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
                 for (int j = 0; j < C::FN; ++j) fb[kk][j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
 #pragma unroll
@@ -280,24 +301,26 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
             }
         };
         auto multiply = [&]() {
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk)
-#pragma unroll
-                for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-                    for (int j = 0; j < C::FN; ++j) acc[i][j] = mg_mfma<C::PLANES>(fa[kk][i], fb[kk][j], acc[i][j]);
+            if constexpr (C::PLANES == 1) {
+                mg_multiply<C>(acc, fa[0], fb[0]);
+                mg_multiply<C>(acc, fa[1], fb[1]);
+            } else {
+                mg_multiply<C>(acc, fa[1], fb[0]);
+                mg_multiply<C>(acc, fa[0], fb[1]);
+                mg_multiply<C>(acc, fa[0], fb[0]);
+            }
         };
         load_next(0);
         mg_sync<true>();
         if (wave >= 4) {
-            if (1 < total) load_next(1);
+            if (1 < ktiles) load_next(1);
             mg_barrier();
-            for (int t = 0; t < total; ++t) {
+            for (int t = 0; t < ktiles; ++t) {
                 read(t & 1);
                 mg_sync<true>();
                 __builtin_amdgcn_sched_barrier(0);
                 __builtin_amdgcn_s_setprio(1);
-                if (t + 2 < total) load_next(t & 1);
+                if (t + 2 < ktiles) load_next(t & 1);
                 multiply();
                 __builtin_amdgcn_s_setprio(0);
                 __builtin_amdgcn_sched_barrier(0);
@@ -305,8 +328,8 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
-            for (int t = 0; t < total; ++t) {
-                if (t + 1 < total) load_next((t + 1) & 1);
+            for (int t = 0; t < ktiles; ++t) {
+                if (t + 1 < ktiles) load_next((t + 1) & 1);
                 read(t & 1);
                 mg_sync<false>();
                 __builtin_amdgcn_sched_barrier(0);
@@ -321,22 +344,24 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
         }
     } else {
         load_next(0);
-        for (int t = 0; t < total; ++t) {
+        for (int t = 0; t < ktiles; ++t) {
             mg_sync<true>();  // tile t has landed; tile t - 1 has been read
-            if (t + 1 < total) load_next((t + 1) & 1);
+            if (t + 1 < ktiles) load_next((t + 1) & 1);
             const char* ta = lds + (t & 1) * C::STAGE;
             const char* tb = ta + C::TA::BYTES;
+            s16x8 fa[2][C::FM], fb[2][C::FN];
 #pragma unroll
-            for (int kk = 0; kk < C::BK / 32; ++kk) {
-                s16x8 fa[C::FM], fb[C::FN];
+            for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-                for (int j = 0; j < C::FN; ++j) fb[j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
+                for (int j = 0; j < C::FN; ++j) fb[kk][j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
 #pragma unroll
-                for (int i = 0; i < C::FM; ++i) fa[i] = C::TA::fragment(ta, arow + 16 * i, kk, lane);
-#pragma unroll
-                for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-                    for (int j = 0; j < C::FN; ++j) acc[i][j] = mg_mfma<C::PLANES>(fa[i], fb[j], acc[i][j]);
+                for (int i = 0; i < C::FM; ++i) fa[kk][i] = C::TA::fragment(ta, arow + 16 * i, kk, lane);
+                if constexpr (C::PLANES == 1) mg_multiply<C>(acc, fa[kk], fb[kk]);
+            }
+            if constexpr (C::PLANES == 2) {
+                mg_multiply<C>(acc, fa[1], fb[0]);
+                mg_multiply<C>(acc, fa[0], fb[1]);
+                mg_multiply<C>(acc, fa[0], fb[0]);
             }
         }
     }

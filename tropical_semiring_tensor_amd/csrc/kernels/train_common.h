@@ -105,7 +105,7 @@ __device__ __forceinline__ float wave_sum(float x) {
     return x;
 }
 // Maximum that keeps a NaN (fmaxf would drop it).
-__device__ __forceinline__ float nan_max(float a, float b) { return (a > b || a != a) ? a : b; }
+__device__ __forceinline__ float nan_max(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float wave_nan_max(float x) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) x = nan_max(x, __shfl_xor(x, o, 64));

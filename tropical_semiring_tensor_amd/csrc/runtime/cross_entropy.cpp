@@ -337,7 +337,7 @@ trop_status tile_pieces(int dev, const CeCall& a, const CePlan& c, TropCeParams&
         }
         if (st == TROP_OK && p.grad_x) {
             const int64_t edge = tile_edge(c.gx_tile);
-            p.split_tiles = (int32_t)ceil_div(ceil_div(labels, kBK), c.splits);
+            p.split_tiles = (int32_t)ceil_div(ceil_div(labels, kBK / c.planes), c.splits);
             p.accumulate = v0 > 0;
             st = train_launch(dev, typed(TK_CE_GX + 2 * c.gx_tile, a.dt), TROP_T_CE_GRAD,
                               ceil_div(tokens, edge) * ceil_div(a.width, edge) * c.splits, tile_threads(c.gx_tile),
