@@ -98,14 +98,14 @@ extern "C" __global__ __launch_bounds__(256) void trop_ce_merge(TropCeParams p) 
     TROP_CE_TILE(stats128_##NAME, Logits128_##NAME, (ce_logits_body<Logits128_##NAME, CE_STATS>))       \
     TROP_CE_TILE(stats64_##NAME, Logits64_##NAME, (ce_logits_body<Logits64_##NAME, CE_STATS>))          \
     TROP_CE_TILE(grad64_##NAME, Logits64_##NAME, (ce_logits_body<Logits64_##NAME, CE_GRAD>))            \
-    TROP_CE_TILE(gx64_##NAME, GradX64_##NAME, ce_grad_x_body<GradX64_##NAME>)                           \
-    TROP_CE_TILE(gw64_##NAME, GradW64_##NAME, (ce_grad_w_body<GradW64_##NAME, T>))                      \
+    TROP_CE_TILE(gradients64_##NAME, GradX64_##NAME,                                              \
+                 (ce_gradients_body<GradX64_##NAME, GradW64_##NAME, T>))                               \
     TROP_CE_TILE(grad256_##NAME, Logits256_##NAME, (ce_logits_body<Logits256_##NAME, CE_GRAD>))         \
     TROP_CE_TILE(grad128_##NAME, Logits128_##NAME, (ce_logits_body<Logits128_##NAME, CE_GRAD>))         \
-    TROP_CE_TILE(gx256_##NAME, GradX256_##NAME, ce_grad_x_body<GradX256_##NAME>)                        \
-    TROP_CE_TILE(gx128_##NAME, GradX128_##NAME, ce_grad_x_body<GradX128_##NAME>)                        \
-    TROP_CE_TILE(gw256_##NAME, GradW256_##NAME, (ce_grad_w_body<GradW256_##NAME, T>))                   \
-    TROP_CE_TILE(gw128_##NAME, GradW128_##NAME, (ce_grad_w_body<GradW128_##NAME, T>))                   \
+    TROP_CE_TILE(gradients256_##NAME, GradX256_##NAME,                                            \
+                 (ce_gradients_body<GradX256_##NAME, GradW256_##NAME, T>))                             \
+    TROP_CE_TILE(gradients128_##NAME, GradX128_##NAME,                                            \
+                 (ce_gradients_body<GradX128_##NAME, GradW128_##NAME, T>))                             \
     TROP_CE_FEW(NAME, T, 1)                                                                             \
     TROP_CE_FEW(NAME, T, 2)                                                                             \
     TROP_CE_FEW(NAME, T, 4)                                                                             \

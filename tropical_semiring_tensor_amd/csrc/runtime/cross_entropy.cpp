@@ -1,6 +1,7 @@
 // Linear cross entropy: argument checks, the plan of a call (tiles, pieces
 // of the label set, workspace layout) and its launches (see
 // cross_entropy_kernels.h).
+#include <algorithm>
 #include <string>
 
 #include "train.h"
@@ -23,42 +24,90 @@ int64_t piece_labels(int64_t vocab, int64_t bytes) {
     return round_up(ceil_div(vocab, ceil_div(vocab, most)), 256);
 }
 
-// Time (us) of a product in `tiles` tiles of `kind` (0: 256 x 256, 1: 128 x
-// 128, 2: 64 x 64), each walking `ktiles` k tiles of 64 in one pass.
+// A tile's time (us) over `k` tiles of 64 along k, and how many run at once,
+// in a launch of `tiles` (kind 0: 256 x 256, 1: 128 x 128, 2: 64 x 64).
 // Measured on one MI355X (256 CUs): a 256 x 256 workgroup has a CU to itself
 // and takes 1.75 us a k tile; a 128 x 128 one 0.7 us alone on a CU, 1.15
 // beside another; a 64 x 64 one 0.3 us alone, 0.5 with two and 0.85 with
 // four on a CU; a tile costs 6, 5 or 4 us besides (first loads, epilogue).
-double tile_time(int kind, int64_t tiles, int64_t ktiles) {
-    const double k = (double)ktiles;
-    if (kind == 0) return (double)ceil_div(tiles, 256) * (k * 1.75 + 6.0);
-    if (kind == 1) return tiles <= 256 ? k * 0.7 + 5.0 : (double)ceil_div(tiles, 512) * (k * 1.15 + 5.0);
-    return tiles <= 256 ? k * 0.3 + 4.0
-                        : tiles <= 512 ? k * 0.5 + 4.0 : (double)ceil_div(tiles, 1024) * (k * 0.85 + 4.0);
+// A k tile of 32 of float32's two planes takes 1.25 of these.
+struct TileRate {
+    double us;
+    int64_t slots;
+};
+TileRate tile_rate(int kind, int64_t tiles, double k) {
+    if (kind == 0) return {k * 1.75 + 6.0, 256};
+    if (kind == 1) return tiles <= 256 ? TileRate{k * 0.7 + 5.0, 256} : TileRate{k * 1.15 + 5.0, 512};
+    return tiles <= 256   ? TileRate{k * 0.3 + 4.0, 256}
+           : tiles <= 512 ? TileRate{k * 0.5 + 4.0, 512}
+                          : TileRate{k * 0.85 + 4.0, 1024};
+}
+double tile_time(int kind, int64_t tiles, double k) {
+    const TileRate r = tile_rate(kind, tiles, k);
+    return (double)ceil_div(tiles, r.slots) * r.us;
+}
+
+// Time of `tx` tiles over kx, then `tw` over kw in one launch: a slot that
+// the first leave takes the second's.
+double pair_time(int kind, int64_t tx, double kx, int64_t tw, double kw) {
+    const TileRate x = tile_rate(kind, tx + tw, kx), w = tile_rate(kind, tx + tw, kw);
+    // after `full` rounds of the first, `late` slots have one more of them
+    const int64_t full = tx / x.slots, late = tx % x.slots, free = x.slots - late;
+    const double lag = x.us / w.us;
+    // rounds of the second when it ends in the free slots, or in the late ones
+    const int64_t whole = (int64_t)lag;
+    int64_t i = std::min(ceil_div(tw, free), (tw + late * whole) / x.slots);
+    int64_t j = std::max<int64_t>(0, (tw - free * (whole + 1)) / x.slots);
+    while (free * i + late * std::max<int64_t>(0, (int64_t)((double)i - lag)) < tw) ++i;
+    while (free * (int64_t)((double)j + lag) + late * j < tw) ++j;
+    return full * x.us + std::max(late ? x.us : 0.0, std::min(i * w.us, x.us + j * w.us));
 }
 
 int64_t tile_edge(int tile) { return 256 >> tile; }
 uint32_t tile_threads(int tile) { return tile == 0 ? 512 : 256; }
 
-// The tile and the number of parts along k for a rows x cols product over
-// `ktiles` (all passes) whose parts are `bytes` each and are written and
-// read again when there are several: the pair with the least time.
-void choose_tile(int64_t rows, int64_t cols, int64_t ktiles, int64_t bytes, int* tile, int64_t* splits) {
-    double best = 0;
-    *tile = 0;
-    *splits = 1;
+// The gradients of `tokens` x `labels` of G: tile and parts along k with the
+// least time.  kx, kw: k tiles (`unit` of a tile_rate's each).  A part's sums
+// are written and read again at 4 TB/s; grad_w's parts take one more launch.
+// How many tokens count is not known here, and a part of grad_x that is right
+// for all of them can outlast the rest when some are left out (1000 x 1000 x
+// 50001, bfloat16, a third ignored: 197 us in 7 parts, 164 in 10): the time
+// is the mean over all and half of them.
+struct GradTiles {
+    int tile;
+    int64_t splits, gw_splits;
+};
+GradTiles choose_grad_tiles(int64_t tokens, int64_t labels, int64_t width, int64_t kx, int64_t kw, double unit,
+                            int64_t gx_bytes, int64_t gw_bytes) {
+    GradTiles best = {0, 1, 1};
+    double least = -1;
     for (int kind = 0; kind < 3; ++kind) {
-        const int64_t edge = tile_edge(kind), tiles = ceil_div(rows, edge) * ceil_div(cols, edge);
-        for (int64_t n = 1; n <= 16 && (n == 1 || ktiles / n >= 8); ++n) {
-            double t = tile_time(kind, tiles * n, ceil_div(ktiles, n));
-            if (n > 1) t += 4.0 + (double)(2 * n * bytes) / 4e6;  // one more launch, 4 TB/s
-            if ((kind == 0 && n == 1) || t < best) {
-                best = t;
-                *tile = kind;
-                *splits = n;
+        const int64_t edge = tile_edge(kind), columns = ceil_div(width, edge);
+        const int64_t tx = ceil_div(tokens, edge) * columns, tw = ceil_div(labels, edge) * columns;
+        const int64_t tx_half = ceil_div((tokens + 1) / 2, edge) * columns;
+        int64_t m = 1;
+        double wtime = tile_time(kind, tw, (double)kw * unit), wextra = 0;
+        for (int64_t n = 2; n <= 16 && kw / n >= 8 && tw * n <= 1024; ++n) {
+            const double extra = 4.0 + (double)(2 * n * gw_bytes) / 4e6;
+            const double t = tile_time(kind, tw * n, (double)ceil_div(kw, n) * unit) + extra;
+            if (t < wtime) {
+                wtime = t;
+                wextra = extra;
+                m = n;
+            }
+        }
+        const double ww = (double)ceil_div(kw, m) * unit, ww_half = (double)ceil_div((kw + 1) / 2, m) * unit;
+        for (int64_t n = 1; n <= 32 && (n == 1 || kx / n >= 8); n += 1 + n / 8) {
+            const double wx = (double)ceil_div(kx, n) * unit;
+            const double t = wextra + (double)(2 * n * gx_bytes) / 4e6 +
+                             (pair_time(kind, tx * n, wx, tw * m, ww) + pair_time(kind, tx_half * n, wx, tw * m, ww_half)) / 2;
+            if (least < 0 || t < least) {
+                least = t;
+                best = {kind, n, m};
             }
         }
     }
+    return best;
 }
 
 struct CePlan {
@@ -66,7 +115,7 @@ struct CePlan {
     bool few;           // few tokens: streaming kernels, no packing
     bool packed;        // w is read from packed pieces
     int64_t piece;      // labels of a piece (a multiple of 256; forward unpacked: all)
-    int logits_tile, gx_tile, gw_tile;  // 0: 256, 1: 128, 2: 64
+    int logits_tile, grad_tile;  // 0: 256, 1: 128, 2: 64
     int few_blocks;     // streaming kernels: log2 of the blocks of 16 tokens
     int few_rows;       // and blocks of 16 labels of a logits workgroup
     int64_t tiles;      // statistics per token
@@ -136,7 +185,8 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     c->packed = packed;
     bool ok = true;
     const int64_t w_row = c->width_p * 2 * c->planes, g_label = c->padded * 2 * c->planes;
-    const int64_t passes = c->planes == 1 ? 1 : 3, count = tokens > 0 ? tokens : 1;
+    const int64_t count = tokens > 0 ? tokens : 1, kt = kBK / c->planes;
+    const double unit = c->planes == 1 ? 1.0 : 1.25;
     const bool whole = !backward && !packed;  // one launch over all labels
     c->piece = round_up(vocab, 256);
     if (!whole) {
@@ -145,7 +195,7 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
         c->piece = piece_labels(vocab, bytes);
     }
     const int64_t labels = c->piece < vocab ? c->piece : vocab;
-    const int64_t wtiles = ceil_div(width, kBK) * passes;
+    const double wtiles = (double)ceil_div(width, kt) * unit;
     double best = 0;
     for (int kind = 0; kind < 3; ++kind) {
         const int64_t edge = tile_edge(kind);
@@ -176,9 +226,12 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     // (the weight's 256-label tiles may read past a piece that ends at 128)
     ok &= take(c, &c->g, (c->piece + 256) * g_label);
     const int64_t part = c->padded * c->width_p * 4;
-    choose_tile(count, width, ceil_div(labels, kBK) * passes, part, &c->gx_tile, &c->splits);
+    const GradTiles t = choose_grad_tiles(count, labels, width, ceil_div(labels, kt), ceil_div(count, kt), unit, part,
+                                          labels * c->width_p * 4);
+    c->grad_tile = t.tile;
+    c->splits = t.splits;
+    c->gw_splits = t.gw_splits;
     ok &= take(c, &c->gx_part, c->splits * part);
-    choose_tile(labels, width, ceil_div(count, kBK) * passes, labels * c->width_p * 4, &c->gw_tile, &c->gw_splits);
     if (c->gw_splits > 1) ok &= take(c, &c->gw_part, c->gw_splits * c->piece * c->width_p * 4);
     return ok;
 }
@@ -335,20 +388,16 @@ trop_status tile_pieces(int dev, const CeCall& a, const CePlan& c, TropCeParams&
             st = train_launch(dev, typed(TK_CE_GRAD + 2 * c.logits_tile, a.dt), TROP_T_CE_LOGITS,
                               p.piece / edge * ceil_div(tokens, edge), tile_threads(c.logits_tile), &p, s);
         }
-        if (st == TROP_OK && p.grad_x) {
-            const int64_t edge = tile_edge(c.gx_tile);
+        if (st == TROP_OK) {
+            const int64_t edge = tile_edge(c.grad_tile), columns = ceil_div(a.width, edge);
+            const int64_t gx = p.grad_x ? round_up(ceil_div(tokens, edge) * columns * c.splits, 8) : 0;
+            const int64_t gw = p.grad_w ? ceil_div(labels, edge) * columns * c.gw_splits : 0;
             p.split_tiles = (int32_t)ceil_div(ceil_div(labels, kBK / c.planes), c.splits);
             p.accumulate = v0 > 0;
-            st = train_launch(dev, typed(TK_CE_GX + 2 * c.gx_tile, a.dt), TROP_T_CE_GRAD,
-                              ceil_div(tokens, edge) * ceil_div(a.width, edge) * c.splits, tile_threads(c.gx_tile),
-                              &p, s);
-        }
-        if (st == TROP_OK && p.grad_w) {
-            const int64_t edge = tile_edge(c.gw_tile);
-            st = train_launch(dev, typed(TK_CE_GW + 2 * c.gw_tile, a.dt), TROP_T_CE_GRAD,
-                              ceil_div(labels, edge) * ceil_div(a.width, edge) * c.gw_splits,
-                              tile_threads(c.gw_tile), &p, s);
-            if (st == TROP_OK && c.gw_splits > 1)
+            p.gx_groups = (uint32_t)gx;
+            st = train_launch(dev, typed(TK_CE_GRADIENTS + 2 * c.grad_tile, a.dt), TROP_T_CE_GRAD, gx + gw,
+                              tile_threads(c.grad_tile), &p, s);
+            if (st == TROP_OK && p.grad_w && c.gw_splits > 1)
                 st = train_launch(dev, typed(TK_CE_FINISH_W, a.dt), TROP_T_CE_MERGE,
                                   labels * ceil_div(a.width, 1024), 256, &p, s);
         }
@@ -464,11 +513,13 @@ extern "C" trop_status tropical_linear_cross_entropy_workspace_size(trop_dtype d
         const trop_status st = check_sizes(dtype, tokens, width, vocab);
         if (st != TROP_OK) return st;
         if (width == 0 || vocab == 0 || (tokens == 0 && !backward)) return ok();
-        CePlan packed, plain;
-        if (!plan(dtype, tokens, width, vocab, backward != 0, true, &packed) ||
-            !plan(dtype, tokens, width, vocab, backward != 0, dtype == TROP_F32, &plain))
-            return fail(TROP_ERR_UNSUPPORTED, "workspace size overflows");
-        *bytes = packed.bytes > plain.bytes ? packed.bytes : plain.bytes;
+        for (const bool packed : {true, false}) {
+            CePlan c;
+            if (!packed && dtype == TROP_F32) break;  // always packed
+            if (!plan(dtype, tokens, width, vocab, backward != 0, packed, &c))
+                return fail(TROP_ERR_UNSUPPORTED, "workspace size overflows");
+            if (c.bytes > *bytes) *bytes = c.bytes;
+        }
         return ok();
     });
 }

@@ -29,12 +29,11 @@ enum TrainKernelId : int {
     TK_CE_PACK,  // every family from here on: + (bf16 ? 1 : 0)
     TK_CE_FINISH = TK_CE_PACK + 2,
     TK_CE_FINISH_W = TK_CE_FINISH + 2,
-    TK_CE_STATS = TK_CE_FINISH_W + 2,  // + 2 tile (256, 128, 64), likewise the next three
+    TK_CE_STATS = TK_CE_FINISH_W + 2,  // + 2 tile (256, 128, 64), likewise the next two
     TK_CE_GRAD = TK_CE_STATS + 6,
-    TK_CE_GX = TK_CE_GRAD + 6,
-    TK_CE_GW = TK_CE_GX + 6,
+    TK_CE_GRADIENTS = TK_CE_GRAD + 6,
     // few tokens: + (bf16 ? 1 : 0) + 2 log2(blocks of 16 tokens: 1, 2, 4) + 6 (5) (label blocks - 1)
-    TK_CE_FEW = TK_CE_GW + 6,          // statistics
+    TK_CE_FEW = TK_CE_GRADIENTS + 6,   // statistics
     TK_CE_FEW_GRAD = TK_CE_FEW + 12,   // G; likewise, without bf16 for 4 blocks
     TK_CE_FEW_GX = TK_CE_FEW_GRAD + 10,  // the gradients: without label blocks
     TK_CE_FEW_GW = TK_CE_FEW_GX + 5,

@@ -42,12 +42,9 @@ const char* const kNames[] = {
     "trop_ce_grad256_f32", "trop_ce_grad256_bf16",
     "trop_ce_grad128_f32", "trop_ce_grad128_bf16",
     "trop_ce_grad64_f32", "trop_ce_grad64_bf16",
-    "trop_ce_gx256_f32", "trop_ce_gx256_bf16",
-    "trop_ce_gx128_f32", "trop_ce_gx128_bf16",
-    "trop_ce_gx64_f32", "trop_ce_gx64_bf16",
-    "trop_ce_gw256_f32", "trop_ce_gw256_bf16",
-    "trop_ce_gw128_f32", "trop_ce_gw128_bf16",
-    "trop_ce_gw64_f32", "trop_ce_gw64_bf16",
+    "trop_ce_gradients256_f32", "trop_ce_gradients256_bf16",
+    "trop_ce_gradients128_f32", "trop_ce_gradients128_bf16",
+    "trop_ce_gradients64_f32", "trop_ce_gradients64_bf16",
     "trop_ce_few1_n1_f32", "trop_ce_few1_n1_bf16",
     "trop_ce_few1_n2_f32", "trop_ce_few1_n2_bf16",
     "trop_ce_few1_n4_f32", "trop_ce_few1_n4_bf16",

@@ -136,6 +136,7 @@ struct TropCeParams {
     int32_t w_packed;         // the piece is read from wp (else from w itself)
     int32_t splits, split_tiles;  // gx: parts along the labels and k tiles of each
     int32_t gw_splits;        // gw: parts along the tokens
+    uint32_t gx_groups;       // workgroups of grad_x, before grad_w's (a multiple of 8)
     int32_t accumulate;       // gx: add to what the piece before left
     int32_t max_parts;        // workgroups of the magnitude pass
     int32_t pack_x;           // packing: workgroups that take rows of x
