@@ -111,20 +111,20 @@ extern "C" __global__ __launch_bounds__(256) void trop_ce_merge(TropCeParams p) 
     TROP_CE_FEW(NAME, T, 4)                                                                             \
     TROP_CE_FEW_GRAD(NAME, T, 1)                                                                        \
     TROP_CE_FEW_GRAD(NAME, T, 2)
-// few tokens: NB blocks of 16; one or two blocks of 16 labels a workgroup
+// few tokens: NB blocks of 16; one or several blocks of 16 labels a workgroup
 #define TROP_CE_FEW(NAME, T, NB)                                                                          \
     extern "C" __global__ __launch_bounds__(256) void trop_ce_few1_n##NB##_##NAME(TropCeParams p) {        \
         ce_few_body<T, 1, NB, CE_STATS>(p);                                                                \
     }                                                                                                      \
-    extern "C" __global__ __launch_bounds__(256) void trop_ce_few2_n##NB##_##NAME(TropCeParams p) {        \
-        ce_few_body<T, 2, NB, CE_STATS>(p);                                                                \
+    extern "C" __global__ __launch_bounds__(256, 2) void trop_ce_few2_n##NB##_##NAME(TropCeParams p) {        \
+        ce_few_body<T, trop_ce_few_rows(NB, sizeof(T)), NB, CE_STATS>(p);                                                                \
     }
 #define TROP_CE_FEW_GRAD(NAME, T, NB)                                                                     \
     extern "C" __global__ __launch_bounds__(256) void trop_ce_few_grad1_n##NB##_##NAME(TropCeParams p) {   \
         ce_few_body<T, 1, NB, CE_GRAD>(p);                                                                 \
     }                                                                                                      \
     extern "C" __global__ __launch_bounds__(256) void trop_ce_few_grad2_n##NB##_##NAME(TropCeParams p) {   \
-        ce_few_body<T, 2, NB, CE_GRAD>(p);                                                                 \
+        ce_few_body<T, trop_ce_few_rows(NB, sizeof(T)), NB, CE_GRAD>(p);                                                                 \
     }                                                                                                      \
     extern "C" __global__ __launch_bounds__(256) void trop_ce_few_gx_n##NB##_##NAME(TropCeParams p) {      \
         ce_few_grad_x_body<T, NB>(p);                                                                      \

@@ -136,14 +136,22 @@ bool take(CePlan* c, size_t* at, int64_t bytes) {
     return true;
 }
 
+// Workgroups of the streaming gradients that run at once on 256 CUs, by their
+// registers (for 1, 2, 4 blocks of tokens: grad_x 112, 152, 232 in float32,
+// 152, 220 in bfloat16; grad_w 100, 112, 144 and 152, 168).
+int64_t few_slots(trop_dtype dt, int few_blocks, bool grad_x) {
+    static constexpr int x[2][3] = {{4, 3, 2}, {3, 2, 2}}, w[2][3] = {{4, 4, 3}, {3, 3, 3}};
+    return 256 * (grad_x ? x : w)[dt == TROP_BF16][few_blocks];
+}
+
 // Streaming kernels (at most TROP_CE_FEW tokens).
 bool plan_few(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool backward, CePlan* c) {
     c->few = true;
     c->few_blocks = tokens <= 16 ? 0 : tokens <= 32 ? 1 : 2;
     const int64_t np = (int64_t)16 << c->few_blocks;
-    // two blocks of labels a workgroup share its token registers; one where
-    // two would leave fewer than four workgroups for each CU
-    c->few_rows = vocab >= 1024 * 32 ? 2 : 1;
+    // (one block of labels where more would leave fewer than four workgroups
+    // of two for each CU)
+    c->few_rows = vocab >= 1024 * 32 ? trop_ce_few_rows(1 << c->few_blocks, (int)elem_size(dt)) : 1;
     bool ok = true;
     if (!backward) {
         c->piece = vocab;
@@ -153,14 +161,15 @@ bool plan_few(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool 
         return ok;
     }
     c->piece = piece_labels(vocab, np * 4);
-    ok &= take(c, &c->g, (c->piece + 32) * np * 4);
-    // grad_x: about 1024 workgroups (four a CU), each of at least two rounds
-    // of the labels that its four waves take at a time
-    const int64_t round = dt == TROP_BF16 || c->few_blocks == 2 ? 64 : 128;
+    ok &= take(c, &c->g, (c->piece + 64) * np * 4);
+    // grad_x: parts along the labels that the device holds at once, each of
+    // at least two rounds of the labels that its four waves take at a time
+    const int64_t round = 64;
     const int64_t blocks = ceil_div(width, dt == TROP_BF16 ? 128 : 64), rounds = ceil_div(c->piece, round);
-    int64_t n = ceil_div(1024, blocks);
+    int64_t n = few_slots(dt, c->few_blocks, true) / blocks;
     if (n > ceil_div(rounds, 2)) n = ceil_div(rounds, 2);
     if (n > 64) n = 64;
+    if (n < 1) n = 1;
     c->split_tiles = ceil_div(rounds, n);
     c->splits = ceil_div(rounds, c->split_tiles);
     ok &= take(c, &c->gx_part, c->splits * c->padded * c->width_p * 4);
@@ -345,7 +354,7 @@ trop_status prepare_piece(int dev, const CeCall& a, const CePlan& c, int64_t v0,
 
 // A streaming kernel of the family at `id` (`per`: its kernels for one label block).
 TrainKernelId few_kernel(int id, int per, const CePlan& c, trop_dtype dt) {
-    return typed(id + per * (c.few_rows - 1) + 2 * c.few_blocks, dt);
+    return typed(id + per * (c.few_rows > 1) + 2 * c.few_blocks, dt);
 }
 
 // The backward's pieces with the streaming kernels.
@@ -364,12 +373,13 @@ trop_status few_pieces(int dev, const CeCall& a, const CePlan& c, TropCeParams& 
             st = train_launch(dev, few_kernel(TK_CE_FEW_GX, 0, c, a.dt), TROP_T_CE_GRAD,
                               ceil_div(a.width, bf ? 128 : 64) * c.splits, 256, &p, s);
         if (st == TROP_OK && p.grad_w) {
-            // a workgroup's labels; the columns are shared out until there
-            // are four workgroups for each CU
-            const int64_t groups = ceil_div(labels, 128);
-            int64_t parts = ceil_div(1024, groups);
-            const int64_t blocks = ceil_div(a.width, bf ? 128 : 64);
-            if (parts > blocks) parts = blocks;
+            // a workgroup's labels; the columns in as many parts as make the
+            // rounds of workgroups shortest
+            const int64_t groups = ceil_div(labels, 128), slots = few_slots(a.dt, c.few_blocks, false);
+            const int64_t most = std::min(ceil_div(a.width, bf ? 128 : 64), std::max<int64_t>(4, slots / groups));
+            int64_t parts = 1;
+            for (int64_t n = 2; n <= most; ++n)
+                if (ceil_div(groups * n, slots) * parts < ceil_div(groups * parts, slots) * n) parts = n;
             st = train_launch(dev, few_kernel(TK_CE_FEW_GW, 0, c, a.dt), TROP_T_CE_GRAD, groups * parts, 256, &p, s);
         }
     }
