@@ -564,11 +564,17 @@ TROP_API trop_status tropical_layer_norm_backward(trop_dtype dtype, trop_dtype p
  *   accuracy; sums are float32 for both.
  * target: target_bytes 4 (int32) or 8 (int64), tokens elements.
  * loss, lse: float32, tokens elements each.
+ * The rows of x that count and w are meant to be finite: where one of their
+ *   elements is not, what depends on it may be NaN even where the formula
+ *   gives an infinity or, of a label at -inf, a number.  With more than 64
+ *   tokens, float32 elements below 2^-18 of their matrix's largest keep an
+ *   absolute precision of 2^-39 of that largest.
  * workspace: at least tropical_linear_cross_entropy_workspace_size bytes of
  *   device memory, used only by work on `stream`.
  * tokens, width, vocab >= 0 (vocab >= 1 and width >= 1 when tokens > 0).
  * Errors: TROP_ERR_INVALID_ARGUMENT, TROP_ERR_NOT_DEVICE_MEMORY,
- *   TROP_ERR_WORKSPACE_TOO_SMALL, TROP_ERR_HIP.
+ *   TROP_ERR_WORKSPACE_TOO_SMALL, TROP_ERR_UNSUPPORTED (more than 2^22 tokens,
+ *   a width above 2^22 or about 2^31 labels), TROP_ERR_HIP.
  */
 TROP_API trop_status tropical_linear_cross_entropy_forward(trop_dtype dtype, const void* x, int64_t ldx,
                                                   const void* w, int64_t ldw, const void* target,

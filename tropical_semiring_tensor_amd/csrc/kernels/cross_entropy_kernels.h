@@ -11,6 +11,12 @@
 // end as G in 16 bits, which two more products consume.  8 N V D operations
 // in all, 2 more than with kept logits; the 4 N V bytes of logits are never
 // written.  For many tokens the matrix cores bound it, for few the read of w.
+// Measured, forward and backward: 8192 x 4096 x 65536 bfloat16 (7780 tokens
+// count) 13.1 ms, 1.27 PFLOP/s (logits 3.0 ms, their gradient 3.3, both
+// products of it 6.6); 4096 x 1024 x 32768 float32 2.47 ms, 430 TFLOP/s (0.62,
+// 0.66, 1.16); 1000 x 1000 x 50001 bfloat16, a third ignored, 0.37 ms, bound
+// by whole rounds of tiles; 256 x 512 x 8000 float32 87 us, by nine short
+// launches.
 //
 // Tokens that do not count are left out: the kept ones are listed first
 // (ordered, by one workgroup), and x is packed in that order, so masked
@@ -586,11 +592,14 @@ __device__ __forceinline__ void ce_finish_w_body(const TropCeParams& p) {
 }
 
 // ---- few tokens ------------------------------------------------------------
-// Up to 64 tokens: w is streamed from HBM straight into the matrix
-// instructions' registers, with no LDS copy and no packing.  The logits' pass
-// reads it once; the backward reads it once more for grad_x and writes
-// grad_w.  All three are bound by those bytes, so they want many loads in
-// flight: the four waves of a workgroup share its rows and split the sum.
+// Up to 64 tokens (32 in the backward of bfloat16): w is streamed from HBM
+// straight into the matrix instructions' registers, with no LDS copy and no
+// packing.  The logits' pass reads it once; the backward reads it twice and
+// writes grad_w.  All are bound by those bytes up to 16 tokens (1 token x
+// 4096 x 65536 bfloat16: 96 us, 5.6 TB/s), so they want many loads in flight:
+// the four waves of a workgroup share its rows and split the sum.  Beyond, by
+// the float32 matrix instructions too (60 tokens x 2560 x 58817 float32:
+// logits 300 us, grad_x 206, grad_w 281, where w's bytes take 125).
 //
 // Logits: a workgroup takes 16 RF labels and all tokens (16 to a block
 // column).  A lane reads 16 bytes of row lane % 16 at k chunk lane / 16, so

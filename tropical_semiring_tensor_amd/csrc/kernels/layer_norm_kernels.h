@@ -19,8 +19,11 @@
 // in its registers; the workgroups' partial sums ([2][parts][cols]) are
 // added in order by a second kernel: no atomics, the same bits every time.
 // The backward streams x, dy and dx past the caches (forward and backward of
-// 16384 x 4096 bfloat16 in turn: 48 + 71 us against 51 + 78); the forward
-// does not gain from it, and its y is read next.
+// 16384 x 4096 bfloat16 in turn: 48 + 72 us against 51 + 78); the forward
+// does not gain from it, and its y is read next.  Those 48 and 72 us move 268
+// and 403 MB at 5.6 TB/s, the partial sums' merge takes 4.5 us more; a large
+// copy reaches 4.7 TB/s, a read 6.  1537 x 1001 float32 (a wave to a row): 5.7,
+// 8.8 and 4.0 us; one row of 4096 bfloat16 3.2 us, all of it latency.
 #pragma once
 #include "train_common.h"
 

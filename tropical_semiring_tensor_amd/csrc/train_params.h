@@ -130,8 +130,8 @@ struct TropCeParams {
     float* magnitude;         // [2][TROP_CE_MAX_PARTS]
     float* stats;             // forward: [token][tiles][2] maximum and sum of exponentials
     float* target_logit;      // per kept token (per token in the streaming kernel)
-    void* xp;                 // packed x: [planes][padded][width_p]
-    void* wp;                 // packed piece of w: [planes][piece][width_p]
+    void* xp;                 // packed x: [padded][width_p], float32 [padded][width_p / 32][2][32]
+    void* wp;                 // packed piece of w: [piece] rows likewise
     void* g;                  // piece of the logits' gradient: [planes][piece / 4][padded][4]
     float* gx_part;           // [splits][padded][width_p]
     float* gw_part;           // [gw_splits][piece][width_p], when gw_splits > 1
