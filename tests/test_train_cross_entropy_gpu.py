@@ -127,6 +127,11 @@ def test_small(tb, tokens, width, vocab, dtype, pad):
     (700, 1096, 8300),    # grad_x in 256 x 256 tiles, split along the labels
     (200, 1000, 12345),   # grad_w in 256 x 256 tiles
     (60, 256, 66000),     # few tokens, two blocks of labels a wave
+    (30, 1300, 33001),    # few tokens, four blocks of labels; odd column blocks
+    (9, 2604, 1501),      # few tokens, several units of columns to a wave
+    (16, 1030, 32777),
+    (50, 130, 5000),      # grad_w's columns in parts
+    (700, 264, 700),      # grad_w split along the tokens beside grad_x
     (40, 256, 9000)])
 def test_tiles(tb, tokens, width, vocab, dtype):
     check(tb, *case(tokens, width, vocab, dtype, seed=1))
