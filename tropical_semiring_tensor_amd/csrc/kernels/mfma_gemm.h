@@ -5,8 +5,8 @@
 // A workgroup of WM x WN waves computes a BM x BN tile; a wave computes
 // (BM / WM) x (BN / WN) of it in 16 x 16 blocks (v_mfma_f32_16x16x32).  K is
 // walked in tiles of 64.  A tile goes from global memory to LDS directly
-// (16 bytes per lane, no registers in between) into one of two buffers while
-// the other is multiplied.  Operands are read as they lie in
+// (16 bytes per lane, no registers in between) into one of two buffers (or
+// four, three tiles ahead) while another is multiplied.  Operands are read as they lie in
 // memory, so nothing is transposed beforehand:
 //   KM  element (i, k) at i ld + k           (rows along k)
 //   MM  element (i, k) at k ld + i           (rows along i)
@@ -229,15 +229,17 @@ __device__ __forceinline__ f32x4 mg_mfma(s16x8 a, s16x8 b, f32x4 c) {
 // of 16-bit products against 1140 to 1250 in three walks, a plane pair each.
 // (A large library product on the same card: 1430-1470 in bfloat16, 153 in
 // float32.)
-template <int BM_, int BN_, int WM_, int WN_, OperandKind KA_, OperandKind KB_, int PLANES_>
+template <int BM_, int BN_, int WM_, int WN_, OperandKind KA_, OperandKind KB_, int PLANES_, int STAGES_ = 2>
 struct MgConfig {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PLANES = PLANES_;
     static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
-    static constexpr int STAGES = 2;
+    static constexpr int STAGES = STAGES_;  // buffers
     static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16 x 16 blocks of a wave
     using TA = MgTile<KA_, BM, PLANES, WAVES>;
     using TB = MgTile<KB_, BN, PLANES, WAVES>;
     static constexpr int KT = TA::KT;  // k of a tile
+    static constexpr int LOADS = TA::LOADS + TB::LOADS;  // of a wave for a tile
+    static_assert(STAGES == 2 || (WAVES == 4 && (STAGES & (STAGES - 1)) == 0 && LOADS * (STAGES - 2) < 64), "the waits");
     static constexpr int STAGE = TA::BYTES + TB::BYTES;
     static constexpr int LDS_BYTES = STAGES * STAGE;
 };
@@ -347,11 +349,17 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
             mg_barrier();
         }
     } else {
-        load_next(0);
+        constexpr int S = C::STAGES;
+        for (int t = 0; t < min(S - 1, ktiles); ++t) load_next(t);
         for (int t = 0; t < ktiles; ++t) {
-            mg_sync<true>();  // tile t has landed; tile t - 1 has been read
-            if (t + 1 < ktiles) load_next((t + 1) & 1);
-            const char* ta = lds + (t & 1) * C::STAGE;
+            // tile t has landed (the S - 2 after it may be on their way);
+            // tile t - 1 has been read
+            if (S > 2 && t + S - 1 <= ktiles)
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * C::LOADS) : "memory");
+            else
+                mg_sync<true>();
+            if (t + S - 1 < ktiles) load_next((t + S - 1) & (S - 1));
+            const char* ta = lds + (t & (S - 1)) * C::STAGE;
             const char* tb = ta + C::TA::BYTES;
             s16x8 fa[2][C::FM], fb[2][C::FN];
 #pragma unroll

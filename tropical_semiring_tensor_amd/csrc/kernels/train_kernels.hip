@@ -87,7 +87,8 @@ extern "C" __global__ __launch_bounds__(256) void trop_ce_merge(TropCeParams p) 
     }                                                                                                   \
     using Logits256_##NAME = MgConfig<256, 256, 2, 4, KM, KM, PLANES>;                                  \
     using Logits128_##NAME = MgConfig<128, 128, 2, 2, KM, KM, PLANES>;                                  \
-    using Logits64_##NAME = MgConfig<64, 64, 2, 2, KM, KM, PLANES>;                                     \
+    using Logits128d_##NAME = MgConfig<128, 128, 2, 2, KM, KM, PLANES, 4>;                              \
+    using Logits64_##NAME = MgConfig<64, 64, 2, 2, KM, KM, PLANES, 4>;                                  \
     using GradX64_##NAME = MgConfig<64, 64, 2, 2, MM, QK, PLANES>;                                      \
     using GradW64_##NAME = MgConfig<64, 64, 2, 2, MM, QM, PLANES>;                                      \
     using GradX256_##NAME = MgConfig<256, 256, 2, 4, MM, QK, PLANES>;                                   \
@@ -96,6 +97,8 @@ extern "C" __global__ __launch_bounds__(256) void trop_ce_merge(TropCeParams p) 
     using GradW128_##NAME = MgConfig<128, 128, 2, 2, MM, QM, PLANES>;                                   \
     TROP_CE_TILE(stats256_##NAME, Logits256_##NAME, (ce_logits_body<Logits256_##NAME, CE_STATS>))       \
     TROP_CE_TILE(stats128_##NAME, Logits128_##NAME, (ce_logits_body<Logits128_##NAME, CE_STATS>))       \
+    TROP_CE_TILE(stats128d_##NAME, Logits128d_##NAME, (ce_logits_body<Logits128d_##NAME, CE_STATS>))    \
+    TROP_CE_TILE(grad128d_##NAME, Logits128d_##NAME, (ce_logits_body<Logits128d_##NAME, CE_GRAD>))      \
     TROP_CE_TILE(stats64_##NAME, Logits64_##NAME, (ce_logits_body<Logits64_##NAME, CE_STATS>))          \
     TROP_CE_TILE(grad64_##NAME, Logits64_##NAME, (ce_logits_body<Logits64_##NAME, CE_GRAD>))            \
     TROP_CE_TILE(gradients64_##NAME, GradX64_##NAME,                                              \

@@ -63,7 +63,20 @@ double pair_time(int kind, int64_t tx, double kx, int64_t tw, double kw) {
     return full * x.us + std::max(late ? x.us : 0.0, std::min(i * w.us, x.us + j * w.us));
 }
 
-int64_t tile_edge(int tile) { return 256 >> tile; }
+// The logits' product: the 64 x 64 tiles have four buffers, and so do the 128 x
+// 128 (kind 3) where a CU has no more than one of them: with no other workgroup
+// beside it a tile waits for its loads (66 tokens x 1856 x 25495 float32, 200
+// tiles of 128: 77 us with two buffers, 61 with four; 110 x 3392 x 7405, 232
+// tiles of 64: 63 and 41; but 303 x 1856 x 16810, 396 of 128: 84 and 106).  A 64
+// x 64 one takes 0.27 us a k tile alone on a CU, 0.41 beside another.
+double logits_time(int kind, int64_t tiles, double k) {
+    if (kind == 2) return tiles <= 256 ? k * 0.27 + 4.0 : (double)ceil_div(tiles, 512) * (k * 0.41 + 4.0);
+    if (kind == 3) return (double)ceil_div(tiles, 256) * (k * 0.77 + 5.0);
+    if (kind == 1) return (double)ceil_div(tiles, 512) * (k * 1.15 + 5.0);
+    return tile_time(kind, tiles, k);
+}
+
+int64_t tile_edge(int tile) { return tile == 3 ? 128 : 256 >> tile; }
 uint32_t tile_threads(int tile) { return tile == 0 ? 512 : 256; }
 
 // The gradients of `tokens` x `labels` of G: tile and parts along k with the
@@ -115,7 +128,7 @@ struct CePlan {
     bool few;           // few tokens: streaming kernels, no packing
     bool packed;        // w is read from packed pieces
     int64_t piece;      // labels of a piece (a multiple of 256; forward unpacked: all)
-    int logits_tile, grad_tile;  // 0: 256, 1: 128, 2: 64
+    int logits_tile, grad_tile;  // 0: 256, 1: 128, 2: 64, 3: 128 with four buffers
     int few_blocks;     // streaming kernels: log2 of the blocks of 16 tokens
     int few_rows;       // and blocks of 16 labels of a logits workgroup
     int64_t tiles;      // statistics per token
@@ -206,9 +219,9 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     const int64_t labels = c->piece < vocab ? c->piece : vocab;
     const double wtiles = (double)ceil_div(width, kt) * unit;
     double best = 0;
-    for (int kind = 0; kind < 3; ++kind) {
+    for (int kind = 0; kind < 4; ++kind) {
         const int64_t edge = tile_edge(kind);
-        const double t = tile_time(kind, ceil_div(labels, edge) * ceil_div(count, edge), wtiles);
+        const double t = logits_time(kind, ceil_div(labels, edge) * ceil_div(count, edge), wtiles);
         if (kind == 0 || t < best) {
             best = t;
             c->logits_tile = kind;

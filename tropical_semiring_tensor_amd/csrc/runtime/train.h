@@ -29,9 +29,9 @@ enum TrainKernelId : int {
     TK_CE_PACK,  // every family from here on: + (bf16 ? 1 : 0)
     TK_CE_FINISH = TK_CE_PACK + 2,
     TK_CE_FINISH_W = TK_CE_FINISH + 2,
-    TK_CE_STATS = TK_CE_FINISH_W + 2,  // + 2 tile (256, 128, 64), likewise the next two
-    TK_CE_GRAD = TK_CE_STATS + 6,
-    TK_CE_GRADIENTS = TK_CE_GRAD + 6,
+    TK_CE_STATS = TK_CE_FINISH_W + 2,  // + 2 tile (256, 128, 64, 128 with four buffers)
+    TK_CE_GRAD = TK_CE_STATS + 8,      // likewise
+    TK_CE_GRADIENTS = TK_CE_GRAD + 8,  // + 2 tile (256, 128, 64)
     // few tokens: + (bf16 ? 1 : 0) + 2 log2(blocks of 16 tokens: 1, 2, 4) + 6 (5) (label blocks - 1)
     TK_CE_FEW = TK_CE_GRADIENTS + 6,   // statistics
     TK_CE_FEW_GRAD = TK_CE_FEW + 12,   // G; likewise, without bf16 for 4 blocks

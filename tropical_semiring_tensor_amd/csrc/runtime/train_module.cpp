@@ -39,9 +39,11 @@ const char* const kNames[] = {
     "trop_ce_stats256_f32", "trop_ce_stats256_bf16",
     "trop_ce_stats128_f32", "trop_ce_stats128_bf16",
     "trop_ce_stats64_f32", "trop_ce_stats64_bf16",
+    "trop_ce_stats128d_f32", "trop_ce_stats128d_bf16",
     "trop_ce_grad256_f32", "trop_ce_grad256_bf16",
     "trop_ce_grad128_f32", "trop_ce_grad128_bf16",
     "trop_ce_grad64_f32", "trop_ce_grad64_bf16",
+    "trop_ce_grad128d_f32", "trop_ce_grad128d_bf16",
     "trop_ce_gradients256_f32", "trop_ce_gradients256_bf16",
     "trop_ce_gradients128_f32", "trop_ce_gradients128_bf16",
     "trop_ce_gradients64_f32", "trop_ce_gradients64_bf16",
