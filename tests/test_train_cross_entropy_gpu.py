@@ -131,6 +131,10 @@ def test_small(tb, tokens, width, vocab, dtype, pad):
     (9, 2604, 1501),      # few tokens, several units of columns to a wave
     (16, 1030, 32777),
     (50, 130, 5000),      # grad_w's columns in parts
+    (66, 420, 30001),     # a large label matrix and few tiles of tokens
+    (256, 2604, 4100),
+    (130, 100, 120001),
+    (70, 1000, 11011),
     (700, 264, 700),      # grad_w split along the tokens beside grad_x
     (40, 256, 9000)])
 def test_tiles(tb, tokens, width, vocab, dtype):

@@ -27,7 +27,8 @@
 // value scaled by one power of two per matrix (largest magnitude in [2^14,
 // 2^15)): 22 bits of every element above 2^-18 of its matrix's largest, an
 // absolute 2^-39 of that largest below; three 16-bit products at 1/16 of the
-// float32 units' cost each.  G is split the same way, scaled by 2^15 from
+// float32 units' cost each.  (A large w that few tokens meet is split by the
+// tiles that read it, others beforehand.)  G is split the same way, scaled by 2^15 from
 // [-1, 1]: elements below 2^-30 of the largest token gradient lose digits.
 //
 // G is stored in quads of labels ([label / 4][token][4]): four consecutive
@@ -266,7 +267,14 @@ __device__ __forceinline__ MgOperand ce_w_rows(const TropCeParams& p, int64_t r0
     MgOperand o;
     o.k_bytes = 128;
     o.plane_bytes = 0;
-    if (C::PLANES == 2 || p.w_packed) {
+    o.exp = 0;
+    if constexpr (C::RAW) {
+        o.base = static_cast<const char*>(p.w) + (p.v0 + r0) * p.ldw * 4;
+        o.ld = p.ldw;
+        o.last_row = (int32_t)min(p.vocab - 1 - (p.v0 + r0), (int64_t)0x7fffffff);
+        o.last_k = (int32_t)(p.width / 4 - 1);
+        o.exp = p.control->w_exp;
+    } else if (C::PLANES == 2 || p.w_packed) {
         o.ld = p.width_p * C::PLANES;
         o.base = static_cast<const char*>(p.wp) + r0 * o.ld * 2;
         o.last_row = 0x7fffffff;
@@ -435,7 +443,14 @@ __device__ __forceinline__ void ce_grad_x_body(const TropCeParams& p, int64_t id
     const int64_t k0 = kt0 * C::KT;
     MgOperand a, b;
     a.plane_bytes = 0;
-    if (C::PLANES == 2 || p.w_packed) {
+    a.exp = 0;
+    if constexpr (C::RAW) {
+        a.base = static_cast<const char*>(p.w) + ((p.v0 + k0) * p.ldw + ni * C::BM) * 4;
+        a.ld = p.ldw;
+        a.last_row = (int32_t)((p.width - ni * C::BM) / 4 - 1);
+        a.last_k = (int32_t)min(p.vocab - 1 - (p.v0 + k0), (int64_t)0x7fffffff);
+        a.exp = p.control->w_exp;
+    } else if (C::PLANES == 2 || p.w_packed) {
         a.ld = p.width_p * C::PLANES;
         a.base = static_cast<const char*>(p.wp) + (k0 * a.ld + ni * C::BM * C::PLANES) * 2;
         a.last_row = (int32_t)((p.width_p - ni * C::BM) * C::PLANES / 8 - 1);
@@ -446,7 +461,7 @@ __device__ __forceinline__ void ce_grad_x_body(const TropCeParams& p, int64_t id
         a.last_row = (int32_t)((p.width - ni * C::BM) / 8 - 1);
         a.last_k = (int32_t)min(p.vocab - 1 - (p.v0 + k0), (int64_t)0x7fffffff);
     }
-    a.k_bytes = C::KT * a.ld * 2;
+    a.k_bytes = C::KT * a.ld * (C::RAW ? 4 : 2);
     b.base = static_cast<const char*>(p.g) + (k0 / 4 * p.padded + mi * C::BN) * 8;
     b.ld = p.padded;
     b.plane_bytes = p.piece * p.padded * 2;
@@ -498,6 +513,7 @@ __device__ __forceinline__ void ce_grad_w_body(const TropCeParams& p, int64_t id
     a.ld = p.width_p * C::PLANES;
     a.base = static_cast<const char*>(p.xp) + (k0 * a.ld + ni * C::BM * C::PLANES) * 2;
     a.plane_bytes = 0;
+    a.exp = 0;
     a.k_bytes = C::KT * a.ld * 2;
     a.last_row = (int32_t)((p.width_p - ni * C::BM) * C::PLANES / 8 - 1);
     a.last_k = 0x7fffffff;

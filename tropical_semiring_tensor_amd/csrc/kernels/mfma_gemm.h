@@ -25,13 +25,16 @@
 // bits); the product is l h' + h l' + h h'.  A k tile is 32 of both planes,
 // as many bytes, so that every value is loaded and read once for its three
 // products.  KM and MM have 32 consecutive elements' h, then their l (`ld`
-// counts both); QK and QM have the planes apart.
+// counts both); QK and QM have the planes apart.  RKM and RMM are KM and MM
+// in float32 as it lies in memory, scaled and split by the wave that reads it
+// from LDS (16 bytes and 4 bytes a read): no copy beforehand, for matrices
+// that one or two tiles read.
 #pragma once
 #include "train_common.h"
 
 namespace trop {
 
-enum OperandKind { KM, MM, QK, QM };
+enum OperandKind { KM, MM, QK, QM, RKM, RMM };
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -45,8 +48,9 @@ struct MgOperand {
     int64_t ld;           // elements
     int64_t plane_bytes;  // QK, QM: from plane 0 to plane 1
     int64_t k_bytes;      // from one k tile to the next
-    int32_t last_row;     // KM: last readable tile row; MM: last readable 8-element chunk of a row
+    int32_t last_row;     // KM: last readable tile row; MM: last readable 16-byte chunk of a row
     int32_t last_k;       // KM: last readable chunk of a row (counted from k = 0); MM: last readable k
+    int32_t exp;          // RKM, RMM: the scale's exponent
 };
 
 #define MG_LDS __attribute__((address_space(3)))
@@ -77,7 +81,9 @@ __device__ __forceinline__ void mg_barrier() { asm volatile("s_barrier" ::: "mem
 
 template <OperandKind KIND, int ROWS, int PLANES, int WAVES>
 struct MgTile {
-    static constexpr int BK = 64;       // elements of a tile row, of both planes
+    static constexpr bool RAW = KIND == RKM || KIND == RMM;
+    static constexpr int BK = 64;       // 16-bit elements of a tile row, of both planes
+    static_assert(!RAW || PLANES == 2, "float32");
     static constexpr int KT = BK / PLANES;  // its k
     static constexpr int BYTES = ROWS * BK * 2;
     static constexpr int LOADS = BYTES / 1024 / WAVES;  // per wave
@@ -85,16 +91,19 @@ struct MgTile {
     // 16-byte chunks of a line of the LDS copy
     // (two planes: a line of MM holds both, as memory does; QK has the second
     // plane's lines after the first's, QM its chunks after the first's)
-    static constexpr int ROW_CHUNKS =
-        KIND == KM ? BK / 8 : KIND == MM ? PLANES * ROWS / 8 : KIND == QK ? ROWS / 2 : BK / 2;
+    static constexpr int ROW_CHUNKS = KIND == KM || KIND == RKM   ? BK / 8
+                                      : KIND == MM || KIND == RMM ? PLANES * ROWS / 8
+                                      : KIND == QK                ? ROWS / 2
+                                                                  : BK / 2;
 
     // Chunk c of a line lies at c ^ swizzle(line).  LDS serves 256 bytes, 16
     // chunks, at a time, so the lanes of a read that are served together
     // must differ in their chunk modulo 16:
     //   KM  16 rows, one chunk each       MM, QM  4 lines x 2 chunks x 2 k groups
-    //   QK  16 rows of 8 bytes in 2 lines
+    //   QK  16 rows of 8 bytes in 2 lines    RMM  4 lines, 8 apart, x 4 chunks
     static __device__ __forceinline__ int swizzle(int line) {
-        if constexpr (KIND == KM) return (line >> 1) & 7;
+        if constexpr (KIND == KM || KIND == RKM) return (line >> 1) & 7;
+        if constexpr (KIND == RMM) return ((line >> 3) & 3) * 4;
         if constexpr (KIND == MM)
             return (PLANES * ROWS >= 128 ? (line & 3) * 4 : ((line >> 1) & 1) * 4) + ((line >> 3) & 1) * 2;
         if constexpr (KIND == QK) return ((line >> 1) & 1) * 8;
@@ -109,8 +118,8 @@ struct MgTile {
     // offset, whose reload waited for the loads before it: grad_w 970
     // against 830 us.)
     static constexpr int STEP = WAVES * 64 / ROW_CHUNKS;
-    static constexpr int OFFSETS = KIND == KM ? LOADS : KIND == MM && STEP % 16 == 8 && LOADS > 1 ? 2 : 1;
-    static_assert(KIND == KM || LOADS == 1 ||
+    static constexpr int OFFSETS = KIND == KM || RAW ? LOADS : KIND == MM && STEP % 16 == 8 && LOADS > 1 ? 2 : 1;
+    static_assert(KIND == KM || RAW || LOADS == 1 ||
                       (WAVES * 64 % ROW_CHUNKS == 0 && STEP % (KIND == MM ? 16 / OFFSETS : 4) == 0),
                   "equal swizzles OFFSETS STEP lines apart");
     static_assert(KIND != QK || PLANES == 1 || 8 % STEP == 0, "a load of QK within a plane");
@@ -125,6 +134,10 @@ struct MgTile {
                 off[s] = (uint32_t)((int64_t)min(line, o.last_row) * o.ld * 2 + col * 16);
             else if constexpr (KIND == MM)
                 off[s] = (uint32_t)((int64_t)line * o.ld * 2 + min(col, o.last_row) * 16);
+            else if constexpr (KIND == RKM)
+                off[s] = (uint32_t)((int64_t)min(line, o.last_row) * o.ld * 4 + col * 16);
+            else if constexpr (KIND == RMM)
+                off[s] = (uint32_t)((int64_t)line * o.ld * 4 + min(col, o.last_row) * 16);
             else if constexpr (KIND == QM && PLANES == 2)
                 off[s] = (uint32_t)((int64_t)line * o.ld * 8 + (col & 15) * 16 + (col >> 4) * o.plane_bytes);
             else
@@ -139,15 +152,19 @@ struct MgTile {
         bool tail = false;  // the operand ends inside this tile
         if constexpr (KIND == KM && PLANES == 1) tail = (kt + 1) * (BK / 8) - 1 > o.last_k;
         if constexpr (KIND == MM && PLANES == 1) tail = (kt + 1) * BK - 1 > o.last_k;
+        if constexpr (KIND == RKM) tail = (kt + 1) * (BK / 8) - 1 > o.last_k;
+        if constexpr (KIND == RMM) tail = (kt + 1) * KT - 1 > o.last_k;
         if (__builtin_expect(tail, 0)) {
 #pragma unroll
             for (int s = 0; s < LOADS; ++s) {
                 const int c = (wave + WAVES * s) * 64 + lane, line = c / ROW_CHUNKS;
                 uint32_t v;
-                if constexpr (KIND == KM) {  // its last chunk again: x is zero there
+                if constexpr (KIND == KM || KIND == RKM) {  // its last chunk again: x is zero there
                     const int col = (c % ROW_CHUNKS) ^ swizzle(line);
                     v = off[s] - (uint32_t)max(0, kt * (BK / 8) + col - o.last_k) * 16;
-                } else {  // its last row again: G is zero there
+                } else if constexpr (KIND == RMM) {  // its last row again: G is zero there
+                    v = off[s] - (uint32_t)((int64_t)max(0, kt * KT + line - o.last_k) * o.ld * 4);
+                } else {
                     v = off[0] + (uint32_t)(s * step) - (uint32_t)((int64_t)max(0, kt * BK + line - o.last_k) * o.ld * 2);
                 }
                 load_to_lds(lds + (wave + WAVES * s) * 1024, base, v);
@@ -155,7 +172,7 @@ struct MgTile {
         } else {
 #pragma unroll
             for (int s = 0; s < LOADS; ++s) {
-                if constexpr (KIND == KM)
+                if constexpr (KIND == KM || RAW)
                     load_to_lds(lds + (wave + WAVES * s) * 1024, base, off[s]);
                 else if constexpr (KIND == QK && PLANES == 2)
                     load_to_lds(lds + (wave + WAVES * s) * 1024,
@@ -201,6 +218,41 @@ struct MgTile {
             return __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
+
+    // Both fragments of rows [row, row + 16).
+    static __device__ __forceinline__ void fragments(const char* tile, int row, int lane, int32_t exp, s16x8& h,
+                                                     s16x8& l) {
+        if constexpr (!RAW) {
+            h = fragment(tile, row, 0, lane);
+            l = fragment(tile, row, 1, lane);
+        } else {
+            const int g = lane / 16, i = lane & 15;
+            float v[8];
+            if constexpr (KIND == RKM) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const f32x4 c = *reinterpret_cast<const f32x4*>(tile + (row + i) * (BK * 2) +
+                                                                    (((2 * g + t) ^ swizzle(i)) * 16));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[4 * t + q] = c[q];
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    v[q] = *reinterpret_cast<const float*>(tile + (g * 8 + q) * (ROWS * 4) +
+                                                           ((((row + i) / 4) ^ (g * 4)) * 16) + (i & 3) * 4);
+            }
+            f16x8 a, b;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float s = ldexpf(v[q], exp);
+                a[q] = (_Float16)s;
+                b[q] = (_Float16)(s - (float)a[q]);
+            }
+            h = __builtin_bit_cast(s16x8, a);
+            l = __builtin_bit_cast(s16x8, b);
+        }
+    }
 };
 
 template <int PLANES>
@@ -238,6 +290,7 @@ struct MgConfig {
     using TA = MgTile<KA_, BM, PLANES, WAVES>;
     using TB = MgTile<KB_, BN, PLANES, WAVES>;
     static constexpr int KT = TA::KT;  // k of a tile
+    static constexpr bool RAW = TA::RAW;
     static constexpr int LOADS = TA::LOADS + TB::LOADS;  // of a wave for a tile
     static_assert(STAGES == 2 || (WAVES == 4 && (STAGES & (STAGES - 1)) == 0 && LOADS * (STAGES - 2) < 64), "the waits");
     static constexpr int STAGE = TA::BYTES + TB::BYTES;
@@ -362,15 +415,20 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
             const char* ta = lds + (t & (S - 1)) * C::STAGE;
             const char* tb = ta + C::TA::BYTES;
             s16x8 fa[2][C::FM], fb[2][C::FN];
+            if constexpr (C::PLANES == 1) {
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
+                for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-                for (int j = 0; j < C::FN; ++j) fb[kk][j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
+                    for (int j = 0; j < C::FN; ++j) fb[kk][j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
 #pragma unroll
-                for (int i = 0; i < C::FM; ++i) fa[kk][i] = C::TA::fragment(ta, arow + 16 * i, kk, lane);
-                if constexpr (C::PLANES == 1) mg_multiply<C>(acc, fa[kk], fb[kk]);
-            }
-            if constexpr (C::PLANES == 2) {
+                    for (int i = 0; i < C::FM; ++i) fa[kk][i] = C::TA::fragment(ta, arow + 16 * i, kk, lane);
+                    mg_multiply<C>(acc, fa[kk], fb[kk]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j) C::TB::fragments(tb, brow + 16 * j, lane, 0, fb[0][j], fb[1][j]);
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i) C::TA::fragments(ta, arow + 16 * i, lane, a.exp, fa[0][i], fa[1][i]);
                 mg_multiply<C>(acc, fa[1], fb[0]);
                 mg_multiply<C>(acc, fa[0], fb[1]);
                 mg_multiply<C>(acc, fa[0], fb[0]);

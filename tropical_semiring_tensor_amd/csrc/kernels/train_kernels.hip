@@ -135,6 +135,20 @@ extern "C" __global__ __launch_bounds__(256) void trop_ce_merge(TropCeParams p) 
     extern "C" __global__ __launch_bounds__(256) void trop_ce_few_gw_n##NB##_##NAME(TropCeParams p) {      \
         ce_few_grad_w_body<T, NB>(p);                                                                      \
     }
+// float32 w read as it lies, for one or two tiles of tokens
+using Raw128 = MgConfig<128, 128, 2, 2, RKM, KM, 2>;
+using Raw128d = MgConfig<128, 128, 2, 2, RKM, KM, 2, 4>;
+using Raw64 = MgConfig<64, 64, 2, 2, RKM, KM, 2, 4>;
+using RawX128 = MgConfig<128, 128, 2, 2, RMM, QK, 2>;
+using RawX64 = MgConfig<64, 64, 2, 2, RMM, QK, 2>;
 TROP_CE_ENTRIES(f32, float, 2)
 TROP_CE_ENTRIES(bf16, bf16, 1)
 TROP_CE_FEW_GRAD(f32, float, 4)
+TROP_CE_TILE(stats128_raw, Raw128, (ce_logits_body<Raw128, CE_STATS>))
+TROP_CE_TILE(stats64_raw, Raw64, (ce_logits_body<Raw64, CE_STATS>))
+TROP_CE_TILE(stats128d_raw, Raw128d, (ce_logits_body<Raw128d, CE_STATS>))
+TROP_CE_TILE(grad128_raw, Raw128, (ce_logits_body<Raw128, CE_GRAD>))
+TROP_CE_TILE(grad64_raw, Raw64, (ce_logits_body<Raw64, CE_GRAD>))
+TROP_CE_TILE(grad128d_raw, Raw128d, (ce_logits_body<Raw128d, CE_GRAD>))
+TROP_CE_TILE(gradients128_raw, RawX128, (ce_gradients_body<RawX128, GradW128_f32, float>))
+TROP_CE_TILE(gradients64_raw, RawX64, (ce_gradients_body<RawX64, GradW64_f32, float>))

@@ -12,6 +12,7 @@ namespace {
 constexpr int64_t kBK = 64;               // k of a product's tile
 constexpr int64_t kPieceBytes = 256 << 20;  // of a piece of G, and of packed w
 constexpr int64_t kMaxTokens = 1 << 22, kMaxWidth = 1 << 22;  // 32-bit offsets within a tile
+constexpr int64_t kRawElements = 10 << 20;  // of a float32 w that is read as it lies
 constexpr int64_t kMaxVocab = ((int64_t)1 << 31) - 512;       // label indices are 32-bit
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -90,11 +91,11 @@ struct GradTiles {
     int tile;
     int64_t splits, gw_splits;
 };
-GradTiles choose_grad_tiles(int64_t tokens, int64_t labels, int64_t width, int64_t kx, int64_t kw, double unit,
+GradTiles choose_grad_tiles(bool raw, int64_t tokens, int64_t labels, int64_t width, int64_t kx, int64_t kw, double unit,
                             int64_t gx_bytes, int64_t gw_bytes) {
     GradTiles best = {0, 1, 1};
     double least = -1;
-    for (int kind = 0; kind < 3; ++kind) {
+    for (int kind = raw ? 1 : 0; kind < 3; ++kind) {
         const int64_t edge = tile_edge(kind), columns = ceil_div(width, edge);
         const int64_t tx = ceil_div(tokens, edge) * columns, tw = ceil_div(labels, edge) * columns;
         const int64_t tx_half = ceil_div((tokens + 1) / 2, edge) * columns;
@@ -127,6 +128,7 @@ struct CePlan {
     int64_t planes, padded, width_p;
     bool few;           // few tokens: streaming kernels, no packing
     bool packed;        // w is read from packed pieces
+    bool raw;           // float32 w is read as it lies
     int64_t piece;      // labels of a piece (a multiple of 256; forward unpacked: all)
     int logits_tile, grad_tile;  // 0: 256, 1: 128, 2: 64, 3: 128 with four buffers
     int few_blocks;     // streaming kernels: log2 of the blocks of 16 tokens
@@ -204,25 +206,32 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
         return plan_few(dt, tokens, width, vocab, backward, c);
     }
     c->padded = round_up(tokens > 0 ? tokens : 1, 256);
-    c->packed = packed;
+    // float32 w as it lies, split by the tiles that read it, saves its packed
+    // copy where two tiles of tokens at most read it, but has them wait for
+    // the split: forward and backward without the magnitudes, packed and as
+    // it lies, 66 tokens x 1856 x 25495: 379 and 293 us; 250 x 1856 x 16810:
+    // 379 and 330; 183 x 320 x 33477 (11 million elements): 134 and 127; 232 x
+    // 2560 x 3457 (9 million): 120 and 130; 150 x 1024 x 259: 44 and 57.
+    c->raw = dt == TROP_F32 && !packed && tokens <= 256 && vocab * width >= kRawElements;
+    c->packed = packed || (dt == TROP_F32 && !c->raw);
     bool ok = true;
     const int64_t w_row = c->width_p * 2 * c->planes, g_label = c->padded * 2 * c->planes;
     const int64_t count = tokens > 0 ? tokens : 1, kt = kBK / c->planes;
     const double unit = c->planes == 1 ? 1.0 : 1.25;
-    const bool whole = !backward && !packed;  // one launch over all labels
+    const bool whole = !backward && !c->packed;  // one launch over all labels
     c->piece = round_up(vocab, 256);
     if (!whole) {
-        int64_t bytes = packed ? w_row : 0;
+        int64_t bytes = c->packed ? w_row : 0;
         if (backward && g_label > bytes) bytes = g_label;
         c->piece = piece_labels(vocab, bytes);
     }
     const int64_t labels = c->piece < vocab ? c->piece : vocab;
     const double wtiles = (double)ceil_div(width, kt) * unit;
-    double best = 0;
-    for (int kind = 0; kind < 4; ++kind) {
+    double best = -1;
+    for (int kind = c->raw ? 1 : 0; kind < 4; ++kind) {
         const int64_t edge = tile_edge(kind);
         const double t = logits_time(kind, ceil_div(labels, edge) * ceil_div(count, edge), wtiles);
-        if (kind == 0 || t < best) {
+        if (best < 0 || t < best) {
             best = t;
             c->logits_tile = kind;
         }
@@ -236,7 +245,7 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
         ok &= take(c, &c->magnitude, 2 * TROP_CE_MAX_PARTS * 4);
     }
     ok &= take(c, &c->xp, c->padded * c->width_p * 2 * c->planes);
-    if (packed) ok &= take(c, &c->wp, c->piece * w_row);
+    if (c->packed) ok &= take(c, &c->wp, c->piece * w_row);
     if (!backward) {
         c->tiles = ceil_div(vocab, tile_edge(c->logits_tile));
         ok &= take(c, &c->stats, tokens * c->tiles * 8);
@@ -248,7 +257,7 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     // (the weight's 256-label tiles may read past a piece that ends at 128)
     ok &= take(c, &c->g, (c->piece + 256) * g_label);
     const int64_t part = c->padded * c->width_p * 4;
-    const GradTiles t = choose_grad_tiles(count, labels, width, ceil_div(labels, kt), ceil_div(count, kt), unit, part,
+    const GradTiles t = choose_grad_tiles(c->raw, count, labels, width, ceil_div(labels, kt), ceil_div(count, kt), unit, part,
                                           labels * c->width_p * 4);
     c->grad_tile = t.tile;
     c->splits = t.splits;
@@ -273,8 +282,8 @@ trop_status check_sizes(trop_dtype dt, int64_t tokens, int64_t width, int64_t vo
 // Can the products read w where it lies?  16-byte rows, and row offsets
 // within a tile that fit 32 bits.
 bool direct_w(trop_dtype dt, const void* w, int64_t ldw, int64_t width) {
-    return dt == TROP_BF16 && width % 8 == 0 && ldw % 8 == 0 && ldw <= kMaxWidth &&
-           reinterpret_cast<uintptr_t>(w) % 16 == 0;
+    const int64_t chunk = dt == TROP_BF16 ? 8 : 4;
+    return width % chunk == 0 && ldw % chunk == 0 && ldw <= kMaxWidth && reinterpret_cast<uintptr_t>(w) % 16 == 0;
 }
 
 struct CeCall {
@@ -365,6 +374,10 @@ trop_status prepare_piece(int dev, const CeCall& a, const CePlan& c, int64_t v0,
     return train_launch(dev, typed(TK_CE_PACK, a.dt), TROP_T_CE_PACK, groups, 256, &p, s);
 }
 
+TrainKernelId logits_kernel(int id, int raw_id, const CePlan& c, trop_dtype dt) {
+    return c.raw ? (TrainKernelId)(raw_id + c.logits_tile - 1) : typed(id + 2 * c.logits_tile, dt);
+}
+
 // A streaming kernel of the family at `id` (`per`: its kernels for one label block).
 TrainKernelId few_kernel(int id, int per, const CePlan& c, trop_dtype dt) {
     return typed(id + per * (c.few_rows > 1) + 2 * c.few_blocks, dt);
@@ -408,7 +421,7 @@ trop_status tile_pieces(int dev, const CeCall& a, const CePlan& c, TropCeParams&
         st = prepare_piece(dev, a, c, v0, p, s);
         if (st == TROP_OK && a.tokens > 0) {
             const int64_t edge = tile_edge(c.logits_tile);
-            st = train_launch(dev, typed(TK_CE_GRAD + 2 * c.logits_tile, a.dt), TROP_T_CE_LOGITS,
+            st = train_launch(dev, logits_kernel(TK_CE_GRAD, TK_CE_GRAD_RAW, c, a.dt), TROP_T_CE_LOGITS,
                               p.piece / edge * ceil_div(tokens, edge), tile_threads(c.logits_tile), &p, s);
         }
         if (st == TROP_OK) {
@@ -418,8 +431,10 @@ trop_status tile_pieces(int dev, const CeCall& a, const CePlan& c, TropCeParams&
             p.split_tiles = (int32_t)ceil_div(ceil_div(labels, kBK / c.planes), c.splits);
             p.accumulate = v0 > 0;
             p.gx_groups = (uint32_t)gx;
-            st = train_launch(dev, typed(TK_CE_GRADIENTS + 2 * c.grad_tile, a.dt), TROP_T_CE_GRAD, gx + gw,
-                              tile_threads(c.grad_tile), &p, s);
+            st = train_launch(dev,
+                              c.raw ? (TrainKernelId)(TK_CE_GRADIENTS_RAW + c.grad_tile - 1)
+                                    : typed(TK_CE_GRADIENTS + 2 * c.grad_tile, a.dt),
+                              TROP_T_CE_GRAD, gx + gw, tile_threads(c.grad_tile), &p, s);
             if (st == TROP_OK && p.grad_w && c.gw_splits > 1)
                 st = train_launch(dev, typed(TK_CE_FINISH_W, a.dt), TROP_T_CE_MERGE,
                                   labels * ceil_div(a.width, 1024), 256, &p, s);
@@ -458,7 +473,7 @@ trop_status ce_forward(const CeCall& a, float* loss, float* lse) {
             st = prepare_piece(dev, a, c, v0, p, s);
             const int64_t edge = tile_edge(c.logits_tile);
             if (st == TROP_OK)
-                st = train_launch(dev, typed(TK_CE_STATS + 2 * c.logits_tile, a.dt), TROP_T_CE_LOGITS,
+                st = train_launch(dev, logits_kernel(TK_CE_STATS, TK_CE_STATS_RAW, c, a.dt), TROP_T_CE_LOGITS,
                                   p.piece / edge * ceil_div(a.tokens, edge), tile_threads(c.logits_tile), &p, s);
         }
     }
@@ -538,7 +553,6 @@ extern "C" trop_status tropical_linear_cross_entropy_workspace_size(trop_dtype d
         if (width == 0 || vocab == 0 || (tokens == 0 && !backward)) return ok();
         for (const bool packed : {true, false}) {
             CePlan c;
-            if (!packed && dtype == TROP_F32) break;  // always packed
             if (!plan(dtype, tokens, width, vocab, backward != 0, packed, &c))
                 return fail(TROP_ERR_UNSUPPORTED, "workspace size overflows");
             if (c.bytes > *bytes) *bytes = c.bytes;

@@ -32,8 +32,12 @@ enum TrainKernelId : int {
     TK_CE_STATS = TK_CE_FINISH_W + 2,  // + 2 tile (256, 128, 64, 128 with four buffers)
     TK_CE_GRAD = TK_CE_STATS + 8,      // likewise
     TK_CE_GRADIENTS = TK_CE_GRAD + 8,  // + 2 tile (256, 128, 64)
+    // float32 w as it lies: tiles 128, 64, 128 with four buffers (gradients: 128, 64)
+    TK_CE_STATS_RAW = TK_CE_GRADIENTS + 6,
+    TK_CE_GRAD_RAW = TK_CE_STATS_RAW + 3,
+    TK_CE_GRADIENTS_RAW = TK_CE_GRAD_RAW + 3,
     // few tokens: + (bf16 ? 1 : 0) + 2 log2(blocks of 16 tokens: 1, 2, 4) + 6 (5) (label blocks - 1)
-    TK_CE_FEW = TK_CE_GRADIENTS + 6,   // statistics
+    TK_CE_FEW = TK_CE_GRADIENTS_RAW + 2,  // statistics
     TK_CE_FEW_GRAD = TK_CE_FEW + 12,   // G; likewise, without bf16 for 4 blocks
     TK_CE_FEW_GX = TK_CE_FEW_GRAD + 10,  // the gradients: without label blocks
     TK_CE_FEW_GW = TK_CE_FEW_GX + 5,

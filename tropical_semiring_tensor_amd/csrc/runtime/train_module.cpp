@@ -47,6 +47,9 @@ const char* const kNames[] = {
     "trop_ce_gradients256_f32", "trop_ce_gradients256_bf16",
     "trop_ce_gradients128_f32", "trop_ce_gradients128_bf16",
     "trop_ce_gradients64_f32", "trop_ce_gradients64_bf16",
+    "trop_ce_stats128_raw", "trop_ce_stats64_raw", "trop_ce_stats128d_raw",
+    "trop_ce_grad128_raw", "trop_ce_grad64_raw", "trop_ce_grad128d_raw",
+    "trop_ce_gradients128_raw", "trop_ce_gradients64_raw",
     "trop_ce_few1_n1_f32", "trop_ce_few1_n1_bf16",
     "trop_ce_few1_n2_f32", "trop_ce_few1_n2_bf16",
     "trop_ce_few1_n4_f32", "trop_ce_few1_n4_bf16",
