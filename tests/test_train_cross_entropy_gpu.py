@@ -130,6 +130,8 @@ def test_small(tb, tokens, width, vocab, dtype, pad):
     (30, 1300, 33001),    # few tokens, four blocks of labels; odd column blocks
     (9, 2604, 1501),      # few tokens, several units of columns to a wave
     (16, 1030, 32777),
+    (60, 130, 40001),
+    (50, 1024, 12000),
     (50, 130, 5000),      # grad_w's columns in parts
     (66, 420, 30001),     # a large label matrix and few tiles of tokens
     (256, 2604, 4100),

@@ -12,10 +12,11 @@
 // in all, 2 more than with kept logits; the 4 N V bytes of logits are never
 // written.  For many tokens the matrix cores bound it, for few the read of w.
 // Measured, forward and backward: 8192 x 4096 x 65536 bfloat16 (7780 tokens
-// count) 13.1 ms, 1.27 PFLOP/s (logits 3.0 ms, their gradient 3.3, both
-// products of it 6.6); 4096 x 1024 x 32768 float32 2.47 ms, 430 TFLOP/s (0.62,
-// 0.66, 1.16); 1000 x 1000 x 50001 bfloat16, a third ignored, 0.37 ms, bound
-// by whole rounds of tiles; 256 x 512 x 8000 float32 87 us, by nine short
+// count) 13.1 to 14.2 ms by the card's power, 1.18 to 1.27 PFLOP/s (logits
+// 3.0, their gradient 3.3, both products of it 6.6 of 13.1 ms); 4096 x 1024 x
+// 32768 float32 2.5 to 2.7 ms, 390 to 420 TFLOP/s (0.62, 0.66, 1.16 of 2.5);
+// 1000 x 1000 x 50001 bfloat16, a third ignored, 0.37 ms, bound by whole
+// rounds of tiles; 256 x 512 x 8000 float32 87 us, by nine short
 // launches.
 //
 // Tokens that do not count are left out: the kept ones are listed first
@@ -608,7 +609,7 @@ __device__ __forceinline__ void ce_finish_w_body(const TropCeParams& p) {
 }
 
 // ---- few tokens ------------------------------------------------------------
-// Up to 64 tokens (32 in the backward of bfloat16): w is streamed from HBM
+// Up to 64 tokens (32 in bfloat16's backward and where w is large): w is streamed from HBM
 // straight into the matrix instructions' registers, with no LDS copy and no
 // packing.  The logits' pass reads it once; the backward reads it twice and
 // writes grad_w.  All are bound by those bytes up to 16 tokens (1 token x

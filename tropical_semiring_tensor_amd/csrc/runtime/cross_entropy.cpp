@@ -12,7 +12,8 @@ namespace {
 constexpr int64_t kBK = 64;               // k of a product's tile
 constexpr int64_t kPieceBytes = 256 << 20;  // of a piece of G, and of packed w
 constexpr int64_t kMaxTokens = 1 << 22, kMaxWidth = 1 << 22;  // 32-bit offsets within a tile
-constexpr int64_t kRawElements = 10 << 20;  // of a float32 w that is read as it lies
+constexpr int64_t kLargeElements = 10 << 20;  // of a w that few tokens' tiles read as it lies
+constexpr int64_t kTileElements = 16 << 20;  // of a bfloat16 w for 33 to 64 tokens' logits in tiles
 constexpr int64_t kMaxVocab = ((int64_t)1 << 31) - 512;       // label indices are 32-bit
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -198,10 +199,15 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     c->width_p = round_up(width, kBK);
     c->bytes = 256;  // room to align the caller's pointer
     c->splits = c->gw_splits = 1;
-    // (the backward's float32 sums of widened bfloat16 cost more than the
-    // tiles' packing from 33 tokens on: 32768 x 4096, 60 tokens 541 us, 65 in
-    // tiles 303; 30 tokens 308)
-    if (tokens > 0 && tokens <= (backward && dt == TROP_BF16 ? TROP_CE_FEW / 2 : TROP_CE_FEW)) {
+    // Few tokens take the streaming kernels.  Beyond 32 the tiles are faster
+    // where they need no packed copy of a large w, and always in bfloat16's
+    // backward, whose streaming form sums widened values (both directions, in
+    // tiles and streaming: 65 and 64 tokens x 2560 x 58817 float32 847 and 1085
+    // us, 4096 x 8000 285 and 278; forward, bfloat16, 60 tokens: 4096 x 16100 36 and
+    // 80, 4096 x 5000 37 and 43, 1024 x 12000 24 and 22, 4096 x 2600 36 and 27).
+    const bool large = !packed && vocab * width >= (backward ? kLargeElements : kTileElements);
+    const bool tiles = backward ? dt == TROP_BF16 || large : dt == TROP_BF16 && large;
+    if (tokens > 0 && tokens <= (tiles ? TROP_CE_FEW / 2 : TROP_CE_FEW)) {
         c->padded = TROP_CE_FEW;
         return plan_few(dt, tokens, width, vocab, backward, c);
     }
@@ -212,7 +218,7 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     // it lies, 66 tokens x 1856 x 25495: 379 and 293 us; 250 x 1856 x 16810:
     // 379 and 330; 183 x 320 x 33477 (11 million elements): 134 and 127; 232 x
     // 2560 x 3457 (9 million): 120 and 130; 150 x 1024 x 259: 44 and 57.
-    c->raw = dt == TROP_F32 && !packed && tokens <= 256 && vocab * width >= kRawElements;
+    c->raw = dt == TROP_F32 && !packed && tokens <= 256 && vocab * width >= kLargeElements;
     c->packed = packed || (dt == TROP_F32 && !c->raw);
     bool ok = true;
     const int64_t w_row = c->width_p * 2 * c->planes, g_label = c->padded * 2 * c->planes;

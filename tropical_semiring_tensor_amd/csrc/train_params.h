@@ -88,12 +88,12 @@ struct TropAdamw8Params {
 };
 
 // ---- linear cross entropy --------------------------------------------------
-// Tokens up to this many are scored by the streaming kernel (no packing).
+// Tokens up to this many may take the streaming kernels (no packing).
 #define TROP_CE_FEW 64
 // Blocks of 16 labels that a workgroup of its logits takes when there are
 // plenty, for nb blocks of 16 tokens: they share the tokens' loads, as far as
-// the registers go.  One block, two and four, 26 x 2560 x 58817: float32 -,
-// 206, 195 us; 60 tokens: bfloat16 -, 137, 97, but float32 -, 300, 326.
+// the registers go.  Two blocks and four, 26 tokens x 2560 x 58817: float32's
+// G 189 and 171 us; 60 tokens: bfloat16 137 and 97, but float32 300 and 326.
 constexpr int trop_ce_few_rows(int nb, int elem_bytes) {
     return nb == 2 || (nb == 4 && elem_bytes == 2) ? 4 : 2;
 }
