@@ -143,6 +143,12 @@ def test_tiles(tb, tokens, width, vocab, dtype):
     check(tb, *case(tokens, width, vocab, dtype, seed=1))
 
 
+@pytest.mark.parametrize("tokens", [40, 70, 300])
+@pytest.mark.parametrize("dtype,pad", [(F32, (3, 4)), (F32, (0, 1)), (BF16, (8, 8))])
+def test_large_matrix_in_a_wider_buffer(tb, tokens, dtype, pad):
+    check(tb, *case(tokens, 1000, 17001, dtype, seed=9, pad=pad))
+
+
 @pytest.mark.parametrize("dtype,pad", [(F32, (0, 0)), (BF16, (0, 0)), (BF16, (1, 1))])
 def test_pieces(tb, dtype, pad):
     """A label set of several pieces (of 256 MiB of its logits' gradient)."""

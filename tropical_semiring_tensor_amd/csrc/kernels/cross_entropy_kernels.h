@@ -609,14 +609,14 @@ __device__ __forceinline__ void ce_finish_w_body(const TropCeParams& p) {
 }
 
 // ---- few tokens ------------------------------------------------------------
-// Up to 64 tokens (32 in bfloat16's backward and where w is large): w is streamed from HBM
-// straight into the matrix instructions' registers, with no LDS copy and no
-// packing.  The logits' pass reads it once; the backward reads it twice and
-// writes grad_w.  All are bound by those bytes up to 16 tokens (1 token x
-// 4096 x 65536 bfloat16: 96 us, 5.6 TB/s), so they want many loads in flight:
-// the four waves of a workgroup share its rows and split the sum.  Beyond, by
-// the float32 matrix instructions too (60 tokens x 2560 x 58817 float32:
-// logits 300 us, grad_x 206, grad_w 281, where w's bytes take 125).
+// Up to 64 tokens (32 in bfloat16's backward and where w is large): w is
+// streamed from HBM straight into the matrix instructions' registers, with no
+// LDS copy and no packing.  The logits' pass reads it once; the backward reads
+// it twice and writes grad_w.  All are bound by those bytes up to 16 tokens (1
+// token x 4096 x 65536 bfloat16: 96 us, 5.6 TB/s), so they want many loads in
+// flight: the four waves of a workgroup share its rows and split the sum.
+// Beyond, by the float32 matrix instructions too (26 tokens x 2560 x 58817
+// float32: logits 206 us, grad_x 135, grad_w 175, where w's bytes take 125).
 //
 // Logits: a workgroup takes 16 RF labels and all tokens (16 to a block
 // column).  A lane reads 16 bytes of row lane % 16 at k chunk lane / 16, so
