@@ -603,6 +603,10 @@ TROP_API trop_status tropical_linear_cross_entropy_workspace_size(trop_dtype dty
  * ldgx) and grad_w (vocab x width, row stride ldgw) have `dtype`; either may
  * be NULL (not computed).  Every element of a requested gradient is written;
  * tokens that do not count add nothing.
+ * With more than 32 tokens G is held in fewer bits for the products: in
+ * bfloat16 it is rounded to bfloat16 (8 significant bits) once; in float32 it
+ * has 22 bits, and an absolute 2^-38 of its own token's |grad_loss| in grad_x,
+ * of its own label's largest |G| in grad_w.
  * Errors: as the forward.
  */
 TROP_API trop_status tropical_linear_cross_entropy_backward(trop_dtype dtype, const void* x, int64_t ldx,

@@ -349,3 +349,68 @@ def test_refusals(tb):
         tb.tropical_linear_cross_entropy_backward(x, w, t, lse, gl[:50])
     with pytest.raises(ValueError):
         tb.tropical_linear_cross_entropy_backward(x, w, t, lse, gl, grad_w=torch.empty(300, 63, device=DEV))
+
+
+def check_float32(tb, x, w, t, gl):
+    """Float32 gradients where magnitudes differ within a matrix.
+
+    As above, but what the planes keep of G is measured where it counts: an
+    element's absolute error is 2^-38 of its own token's weight in grad_x and
+    2^-38 of its own label's largest G in grad_w.  The planes of x and w keep
+    2^-38 of their matrix's largest element (in the logits too)."""
+    n, d = x.shape
+    X, W, g = x.double(), w.double(), gl.double()[:, None]
+    keep = t >= 0
+    g, X = torch.where(keep[:, None], g, 0.0), torch.where(keep[:, None], X, 0.0)
+    floor = 2.0 ** -38
+    l = X @ W.t()
+    dl = (d + 40) * U * (X.abs() @ W.abs().t())
+    dl = dl + floor * (X.abs().max() * W.abs().sum(1) + W.abs().max() * X.abs().sum(1)[:, None])
+    lse = torch.logsumexp(l, 1)
+    dlse = dl.amax(1) + 200 * U + 4 * U * lse.abs()
+    p = (l - lse[:, None]).exp()
+    G = p.scatter_add(1, t.clamp(min=0)[:, None], torch.full_like(g, -1.0)) * g
+    dG = g.abs() * p * (dl + dlse[:, None] + 60 * U) + (2.0 ** -22 * 1.01 + 4 * U) * G.abs() + 2.0 ** -126
+    want = G @ W, G.t() @ X
+    tol = [(dG + floor * g.abs()) @ W.abs() + (w.shape[0] + 40) * U * (G.abs() @ W.abs())
+           + floor * G.abs().sum(1, keepdim=True) * W.abs().max(),
+           (dG + floor * G.abs().amax(0)).t() @ X.abs() + (n + 40) * U * (G.t().abs() @ X.abs())
+           + floor * G.abs().sum(0)[:, None] * X.abs().max()]
+    loss, lse = tb.tropical_linear_cross_entropy_forward(x, w, t)
+    got = tb.tropical_linear_cross_entropy_backward(x, w, t, lse, gl)
+    for a, b, e, what in zip(got, want, tol, ("grad_x", "grad_w")):
+        assert_within(a, b, e + 4 * U * (b.abs() + e), what)
+
+
+# streaming, small tiles, w as it lies, grad_x / grad_w in 256 x 256 tiles, grad_w in parts along the tokens
+F32_SHAPES = [(30, 64, 500), (100, 64, 500), (70, 1000, 11011), (700, 1096, 8300), (2100, 64, 300), (700, 264, 700)]
+
+
+@pytest.mark.parametrize("tokens,width,vocab", F32_SHAPES)
+def test_float32_weights_of_tokens_far_apart(tb, tokens, width, vocab):
+    """A token's gradient keeps its digits beside tokens of 2^30 its weight."""
+    x, w, t, gl = case(tokens, width, vocab, F32, seed=12)
+    g = torch.Generator(device=DEV).manual_seed(tokens)
+    check_float32(tb, x, w, t, torch.exp2(-30 * torch.rand(tokens, generator=g, device=DEV)))
+
+
+@pytest.mark.parametrize("tokens,width,vocab", F32_SHAPES)
+def test_float32_improbable_labels(tb, tokens, width, vocab):
+    """Labels that every token finds improbable (1e-9 and down to 1e-20) keep
+    the digits of their rows of grad_w."""
+    x, w, t, gl = case(tokens, width, vocab, F32, seed=13)
+    x[:, 0] = 4.0
+    rare = torch.arange(vocab, device=DEV) % 7 == 3
+    w[:, 0] = torch.where(rare, -4.0 - 0.05 * (torch.arange(vocab, device=DEV) % 80), 0.0)
+    t[rare[t.clamp(min=0)]] = 0
+    check_float32(tb, x, w, t, gl)
+
+
+@pytest.mark.parametrize("tokens,width,vocab", F32_SHAPES)
+def test_float32_mixed_magnitudes(tb, tokens, width, vocab):
+    """Rows of x and w of 1 down to 2^-20."""
+    x, w, t, gl = case(tokens, width, vocab, F32, seed=14)
+    g = torch.Generator(device=DEV).manual_seed(tokens)
+    for m in (x, w):
+        m *= torch.exp2(-20 * torch.rand(len(m), 1, generator=g, device=DEV))
+    check_float32(tb, x, w, t, gl)

@@ -29,16 +29,23 @@
 // 2^15)): 22 bits of every element above 2^-18 of its matrix's largest, an
 // absolute 2^-39 of that largest below; three 16-bit products at 1/16 of the
 // float32 units' cost each.  (A large w that few tokens meet is split by the
-// tiles that read it, others beforehand.)  G is split the same way, scaled by 2^15 from
-// [-1, 1]: elements below 2^-30 of the largest token gradient lose digits.
+// tiles that read it, others beforehand.)  G is kept in float32 and split by
+// the waves that read its fragments, with a scale of its own for every column of the
+// product: a token's weight in grad_x, a label's largest |G| in grad_w.  So
+// what the planes lose, 2^-39 of those, is nothing beside the column's own
+// sum, whatever the other tokens' weights and the other labels'
+// probabilities.  (With one scale for all of G a label of probability 1e-9
+// had its row of grad_w to 2e-3, one of 1e-11 to a tenth.  The scales cost a
+// backward of 4096 x 1024 x 32768 1.92 ms against 1.74.)
 //
 // G is stored in quads of labels ([label / 4][token][4]): four consecutive
 // labels of a token are what a lane of the logits' product holds, so it
 // stores 8 bytes next to its neighbours' without a transpose, and both
 // products that follow read quads directly (along k, or across it with the
-// transposing LDS read).  It is scaled by grad_loss / max |grad_loss|, a
-// power that the float32 sums get back at the end, so that with equal token
-// weights only exp(l - lse) itself is rounded to 16 bits.
+// transposing LDS read; float32's upper and lower 16 bits lie in two such
+// planes for that).  It is scaled by grad_loss / max
+// |grad_loss|, which the float32 sums get back at the end, so that with equal
+// token weights only exp(l - lse) itself is rounded to bfloat16.
 #pragma once
 #include "mfma_gemm.h"
 
@@ -170,6 +177,31 @@ __device__ __forceinline__ int32_t ce_scale_exp(float largest) {
 __device__ __forceinline__ void ce_split(float scaled, _Float16& h, _Float16& l) {
     h = (_Float16)scaled;
     l = (_Float16)(scaled - (float)h);
+}
+
+// The exponent that a column of float32 G is scaled by: |v| 2^e in [2^14,
+// 2^15) for its largest magnitude v, where 2^e is a float32 (a column below
+// 2^-111 has fewer digits).
+__device__ __forceinline__ int32_t ce_column_exp(float largest) { return min(ce_scale_exp(largest), 126); }
+// The same for a token, from its weight (no G of it is larger, but for a rounding).
+__device__ __forceinline__ int32_t ce_token_exp(float weight) {
+    const float a = fabsf(weight);
+    return ce_column_exp(a < INFINITY ? a : 0.f);
+}
+
+// m 2^e, where 2^e alone may be no float32.
+struct CeScale {
+    float m;
+    int32_t e;
+    __device__ __forceinline__ float operator()(float x) const { return ldexpf(x * m, e); }
+};
+// The sums' factor: max |grad_loss| / (2^own 2^other), own and other the
+// exponents of G's column and of the other matrix (bfloat16: none).
+template <int PLANES>
+__device__ __forceinline__ CeScale ce_sum_scale(const TropCeParams& p, int32_t own, int32_t other) {
+    const float g = p.control->grad_max;
+    if constexpr (PLANES == 1) return {g, 0};
+    return {__builtin_amdgcn_frexp_mantf(g), __builtin_amdgcn_frexp_expf(g) - own - other};
 }
 
 // ---- packing ---------------------------------------------------------------
@@ -306,7 +338,8 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
     f32x4 acc[C::FM][C::FN];
     // (only tiles that hold a column: the loads clamp to a row's last chunk
     // within a tile, not from a tile past it)
-    mg_walk<C>(acc, ce_w_rows<C>(p, mi * C::BM), b, (int)((p.width + C::KT - 1) / C::KT), lds);
+    const float none[C::FN] = {};
+    mg_walk<C>(acc, ce_w_rows<C>(p, mi * C::BM), b, none, (int)((p.width + C::KT - 1) / C::KT), lds);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
     const int64_t v_wave = p.v0 + mi * C::BM + (wave / C::WN) * (C::BM / C::WM);  // label of the wave's row 0
@@ -387,6 +420,7 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
         }
     } else {
         const int64_t plane = p.piece * p.padded * 2;  // bytes
+        uint32_t top[C::FM][4] = {};  // float32: the lane's largest finite |G| of its labels, as bits
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
             const bool on = n[j] < kept;
@@ -412,17 +446,37 @@ __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds)
                 if constexpr (C::PLANES == 1) {
                     *reinterpret_cast<VecOf<bf16, 4>::raw*>(o) = from_float<bf16, 4>(g);
                 } else {
-                    _Float16 __attribute__((ext_vector_type(4))) h, l;
+                    const u32x4 u = __builtin_bit_cast(u32x4, g);
+                    *reinterpret_cast<uint2*>(o) = make_uint2(__builtin_amdgcn_perm(u[1], u[0], 0x07060302u),
+                                                              __builtin_amdgcn_perm(u[3], u[2], 0x07060302u));
+                    *reinterpret_cast<uint2*>(o + plane) = make_uint2(__builtin_amdgcn_perm(u[1], u[0], 0x05040100u),
+                                                                      __builtin_amdgcn_perm(u[3], u[2], 0x05040100u));
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        _Float16 a, b;
-                        ce_split(g[r] * 32768.f, a, b);
-                        h[r] = a;
-                        l[r] = b;
+                        const uint32_t a = u[r] & 0x7fffffffu;
+                        top[i][r] = max(top[i][r], a < 0x7f800000u ? a : 0u);
                     }
-                    *reinterpret_cast<decltype(h)*>(o) = h;
-                    *reinterpret_cast<decltype(l)*>(o + plane) = l;
                 }
+            }
+        }
+        if constexpr (C::PLANES == 2) {
+            // the tile's tokens' largest for each label: 16 lanes, then the waves
+            float* part = reinterpret_cast<float*>(lds);  // [WN][BM]
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) {
+                f32x4 m;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) m[r] = __builtin_bit_cast(float, row_umax(top[i][r]));
+                if ((lane & 15) == 15)
+                    *reinterpret_cast<f32x4*>(part + (wave % C::WN) * C::BM + (wave / C::WN) * (C::BM / C::WM) + 16 * i +
+                                              4 * (lane / 16)) = m;
+            }
+            __syncthreads();
+            if (threadIdx.x < C::BM) {
+                float m = part[threadIdx.x];
+#pragma unroll
+                for (int q = 1; q < C::WN; ++q) m = fmaxf(m, part[q * C::BM + threadIdx.x]);
+                p.label_max[ni * p.piece + mi * C::BM + threadIdx.x] = m;
             }
         }
     }
@@ -468,11 +522,17 @@ __device__ __forceinline__ void ce_grad_x_body(const TropCeParams& p, int64_t id
     b.plane_bytes = p.piece * p.padded * 2;
     b.k_bytes = (C::KT / 4) * p.padded * 8;
     b.last_row = b.last_k = 0;
-    f32x4 acc[C::FM][C::FN];
-    mg_walk<C>(acc, a, b, (int)(kt1 - kt0), lds);
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
     const int64_t c0 = ni * C::BM + (wave / C::WN) * (C::BM / C::WM) + 4 * (lane / 16);
     const int64_t n0 = mi * C::BN + (wave % C::WN) * (C::BN / C::WN) + (lane & 15);
+    float scale[C::FN] = {};
+    if constexpr (C::SCALED) {
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+            scale[j] = n0 + 16 * j < kept ? ldexpf(1.f, ce_token_exp(p.kept_grad[n0 + 16 * j])) : 0.f;
+    }
+    f32x4 acc[C::FM][C::FN];
+    mg_walk<C>(acc, a, b, scale, (int)(kt1 - kt0), lds);
     float* out = p.gx_part + (split * p.padded + n0) * p.width_p + c0;
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
@@ -491,12 +551,32 @@ __device__ __forceinline__ void ce_grad_x_body(const TropCeParams& p, int64_t id
     }
 }
 
-// What the float32 sums of grad_w have to be multiplied by.
-template <int PLANES>
-__device__ __forceinline__ float ce_grad_w_scale(const TropCeParams& p) {
-    const float scale = p.control->grad_max;
-    if constexpr (PLANES == 2) return ldexpf(scale, -15 - p.control->x_exp);
-    return scale;
+// The scales' exponents of a grad_w tile's labels (piece rows r0 + 16 j + lane
+// % 16 of the wave's part): from the largest |G| that the logits' tiles left,
+// by the whole workgroup.
+template <typename C>
+__device__ __forceinline__ void ce_label_exps(const TropCeParams& p, int64_t tile_row, int64_t kept, char* lds,
+                                              int32_t (&e)[C::FN]) {
+    float* part = reinterpret_cast<float*>(lds);  // [THREADS / BN][BN]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t row = tile_row + threadIdx.x % C::BN, tiles = (kept + p.logits_edge - 1) / p.logits_edge;
+    float m = 0.f;
+    if (row < p.piece) {
+#pragma unroll 8
+        for (int64_t t = threadIdx.x / C::BN; t < tiles; t += C::THREADS / C::BN)
+            m = fmaxf(m, p.label_max[t * p.piece + row]);
+    }
+    part[threadIdx.x] = m;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+        const int label = (wave % C::WN) * (C::BN / C::WN) + 16 * j + (lane & 15);
+        m = part[label];
+#pragma unroll
+        for (int q = 1; q < C::THREADS / C::BN; ++q) m = fmaxf(m, part[q * C::BN + label]);
+        e[j] = ce_column_exp(m);
+    }
+    __syncthreads();  // the walk's loads go to the same LDS
 }
 
 // Tile `id` of grad_w: BM columns x BN labels, the sum over the kept tokens, or
@@ -523,9 +603,15 @@ __device__ __forceinline__ void ce_grad_w_body(const TropCeParams& p, int64_t id
     b.plane_bytes = p.piece * p.padded * 2;
     b.k_bytes = C::KT * 8;
     b.last_row = b.last_k = 0;
+    int32_t e[C::FN] = {};
+    float scale[C::FN] = {};
+    if constexpr (C::SCALED) {
+        ce_label_exps<C>(p, mi * C::BN, kept, lds, e);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) scale[j] = ldexpf(1.f, e[j]);
+    }
     f32x4 acc[C::FM][C::FN];
-    mg_walk<C>(acc, a, b, (int)(kt1 - kt0), lds);
-    const float scale = p.gw_splits > 1 ? 1.f : ce_grad_w_scale<C::PLANES>(p);
+    mg_walk<C>(acc, a, b, scale, (int)(kt1 - kt0), lds);
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
     const int64_t c0 = ni * C::BM + (wave / C::WN) * (C::BM / C::WM) + 4 * (lane / 16);
     const int64_t v0 = p.v0 + mi * C::BN + (wave % C::WN) * (C::BN / C::WN) + (lane & 15);
@@ -533,18 +619,22 @@ __device__ __forceinline__ void ce_grad_w_body(const TropCeParams& p, int64_t id
     for (int j = 0; j < C::FN; ++j) {
         const int64_t v = v0 + 16 * j;
         if (v >= p.vocab) continue;
+        const CeScale sum = ce_sum_scale<C::PLANES>(p, e[j], p.control->x_exp);
+        if (C::SCALED && p.gw_splits > 1 && ni == 0 && split == 0 && wave / C::WN == 0 && lane < 16)
+            p.label_exp[v - p.v0] = e[j];
         T* out = static_cast<T*>(p.grad_w) + v * p.ldgw;
         float* part = p.gw_part + (split * p.piece + (v - p.v0)) * p.width_p;
 #pragma unroll
         for (int i = 0; i < C::FM; ++i) {
-            FloatVec<4> g;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) g[r] = acc[i][j][r] * scale;
             if (c0 + 16 * i >= p.width) continue;
-            if (p.gw_splits > 1)
-                *reinterpret_cast<f32x4*>(part + c0 + 16 * i) = g;
-            else
+            if (p.gw_splits > 1) {
+                *reinterpret_cast<f32x4*>(part + c0 + 16 * i) = acc[i][j];
+            } else {
+                FloatVec<4> g;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) g[r] = sum(acc[i][j][r]);
                 store_row<T, 4>(out, c0 + 16 * i, p.width, from_float<T, 4>(g));
+            }
         }
     }
 }
@@ -563,7 +653,7 @@ __device__ __forceinline__ void ce_gradients_body(const TropCeParams& p, char* l
 }
 
 // Columns [c, c + 4) of a row summed over `splits` parts, `step` floats apart.
-__device__ __forceinline__ FloatVec<4> ce_sum_parts(const float* q, int splits, int64_t step, float scale) {
+__device__ __forceinline__ FloatVec<4> ce_sum_parts(const float* q, int splits, int64_t step, CeScale scale) {
     FloatVec<4> s = load_vec<float, 4>(q);
 #pragma unroll 8
     for (int k = 1; k < splits; ++k) {
@@ -572,7 +662,7 @@ __device__ __forceinline__ FloatVec<4> ce_sum_parts(const float* q, int splits, 
         for (int e = 0; e < 4; ++e) s[e] += o[e];
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] *= scale;
+    for (int e = 0; e < 4; ++e) s[e] = scale(s[e]);
     return s;
 }
 
@@ -584,13 +674,13 @@ __device__ __forceinline__ void ce_finish_body(const TropCeParams& p) {
     const int64_t n = blockIdx.x / blocks, c = (blockIdx.x % blocks) * 1024 + threadIdx.x * 4;
     if (c >= p.width) return;
     int64_t i = n;
-    float scale = 1.f;
+    CeScale scale = {1.f, 0};
     if (p.identity) {
         if (!ce_counts(p, ce_target(p, n))) i = -1;
     } else {
         i = p.slot[n];
-        scale = p.control->grad_max;
-        if constexpr (PLANES == 2) scale = ldexpf(scale, -15 - p.control->w_exp);
+        const int32_t e = PLANES == 2 && i >= 0 ? ce_token_exp(p.kept_grad[i]) : 0;
+        scale = ce_sum_scale<PLANES>(p, e, p.control->w_exp);
     }
     FloatVec<4> s = {0.f, 0.f, 0.f, 0.f};
     if (i >= 0) s = ce_sum_parts(p.gx_part + i * p.width_p + c, p.splits, p.padded * p.width_p, scale);
@@ -603,8 +693,8 @@ __device__ __forceinline__ void ce_finish_w_body(const TropCeParams& p) {
     const int64_t blocks = (p.width + 1023) / 1024;
     const int64_t r = blockIdx.x / blocks, c = (blockIdx.x % blocks) * 1024 + threadIdx.x * 4;
     if (c >= p.width) return;
-    const FloatVec<4> s = ce_sum_parts(p.gw_part + r * p.width_p + c, p.gw_splits, p.piece * p.width_p,
-                                       ce_grad_w_scale<PLANES>(p));
+    const CeScale scale = ce_sum_scale<PLANES>(p, PLANES == 2 ? p.label_exp[r] : 0, p.control->x_exp);
+    const FloatVec<4> s = ce_sum_parts(p.gw_part + r * p.width_p + c, p.gw_splits, p.piece * p.width_p, scale);
     store_row<T, 4>(static_cast<T*>(p.grad_w) + (p.v0 + r) * p.ldgw, c, p.width, from_float<T, 4>(s));
 }
 

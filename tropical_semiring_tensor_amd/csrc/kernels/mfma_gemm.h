@@ -25,8 +25,11 @@
 // bits); the product is l h' + h l' + h h'.  A k tile is 32 of both planes,
 // as many bytes, so that every value is loaded and read once for its three
 // products.  KM and MM have 32 consecutive elements' h, then their l (`ld`
-// counts both); QK and QM have the planes apart.  RKM and RMM are KM and MM
-// in float32 as it lies in memory, scaled and split by the wave that reads it
+// counts both).  QK and QM have the planes apart, and these hold the float32
+// value's upper and lower 16 bits: the wave that reads a fragment joins them,
+// scales the values and splits them.  The scale is one for each row of B, a
+// column of the product, so that a column keeps its digits however small it
+// is beside the others.  RKM and RMM are KM and MM in float32 as it lies in memory, scaled and split by the wave that reads it
 // from LDS (16 bytes and 4 bytes a read): no copy beforehand, for matrices
 // that one or two tiles read.
 #pragma once
@@ -37,6 +40,7 @@ namespace trop {
 enum OperandKind { KM, MM, QK, QM, RKM, RMM };
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -82,6 +86,7 @@ __device__ __forceinline__ void mg_barrier() { asm volatile("s_barrier" ::: "mem
 template <OperandKind KIND, int ROWS, int PLANES, int WAVES>
 struct MgTile {
     static constexpr bool RAW = KIND == RKM || KIND == RMM;
+    static constexpr bool HALVES = PLANES == 2 && (KIND == QK || KIND == QM);
     static constexpr int BK = 64;       // 16-bit elements of a tile row, of both planes
     static_assert(!RAW || PLANES == 2, "float32");
     static constexpr int KT = BK / PLANES;  // its k
@@ -203,10 +208,7 @@ struct MgTile {
             for (int t = 0; t < 2; ++t) {
                 const int k = kk * 32 + g * 8 + t * 4 + i / 4;
                 const char* p;
-                if constexpr (KIND == MM && PLANES == 2) {
-                    const int chunk = row / 32 * 8 + kk * 4 + row % 32 / 8 + (i & 3) / 2, line = k - kk * 32;
-                    p = tile + line * (ROWS * 4) + (chunk ^ swizzle(line)) * 16 + (i & 1) * 8;
-                } else if constexpr (KIND == MM) {
+                if constexpr (KIND == MM) {
                     const int chunk = row / 8 + (i & 3) / 2;
                     p = tile + k * (ROWS * 2) + (chunk ^ swizzle(k)) * 16 + (i & 1) * 8;
                 } else {
@@ -219,10 +221,65 @@ struct MgTile {
         }
     }
 
-    // Both fragments of rows [row, row + 16).
-    static __device__ __forceinline__ void fragments(const char* tile, int row, int lane, int32_t exp, s16x8& h,
-                                                     s16x8& l) {
-        if constexpr (!RAW) {
+    // Two planes of MM, QK and QM: all of a lane's reads are at its `base` with
+    // constant bits turned over or a constant added, so one register holds
+    // their addresses (one each took 34 spilled ones in grad_w's 256 x 256
+    // tile, beside HALVES' scales).  base: of the wave's rows from row0 on, a
+    // multiple of their number; r: a multiple of 16 below that.
+    static constexpr bool BASED = PLANES == 2 && (KIND == MM || KIND == QK || KIND == QM);
+    static __device__ __forceinline__ uint32_t base(uint32_t tile, int row0, int lane) {
+        const int g = lane / 16, i = lane & 15;
+        if constexpr (KIND == MM) {
+            const int line = g * 8 + i / 4;
+            return tile + line * (ROWS * 4) + ((row0 / 4 + (i & 3) / 2) ^ swizzle(line)) * 16 + (i & 1) * 8;
+        } else if constexpr (KIND == QK) {
+            return tile + g * 2 * (ROWS * 8) + (((row0 + i) / 2) ^ swizzle(g * 2)) * 16 + (i & 1) * 8;
+        } else {
+            const int k = g * 8 + i / 4, quad = row0 / 4 + (i & 3);
+            return tile + quad * (BK * 8) + ((k / 2) ^ swizzle(quad)) * 16 + (k & 1) * 8;
+        }
+    }
+    static __device__ __forceinline__ s16x8 fragment_at(uint32_t base, int r, int kk) {
+        s16x4 v[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if constexpr (KIND == MM) {
+                const uint32_t p = (base ^ (r / 32 * 8 + kk * 4 + r % 32 / 8) * 16) + t * 4 * (ROWS * 4);
+                v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MG_LDS s16x4*)p);
+            } else if constexpr (KIND == QK) {
+                const uint32_t p = (base ^ r / 2 * 16) + (kk * 8 + t) * (ROWS * 8);
+                v[t] = *(MG_LDS const s16x4*)p;
+            } else {
+                const uint32_t p = (base ^ t * 2 * 16) + r / 4 * (BK * 8) + kk * 16 * 16;
+                v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MG_LDS s16x4*)p);
+            }
+        }
+        return __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+
+    // Both fragments of rows [row0 + r, row0 + r + 16), from `tile` or from
+    // `at`, the base.  RAW: of the values times 2^exp; HALVES: times `scale`, a
+    // power of two.
+    static __device__ __forceinline__ void fragments(const char* tile, uint32_t at, int row0, int r, int lane,
+                                                     int32_t exp, float scale, s16x8& h, s16x8& l) {
+        const int row = row0 + r;
+        if constexpr (HALVES) {
+            const u32x4 u = __builtin_bit_cast(u32x4, fragment_at(at, r, 0));
+            const u32x4 d = __builtin_bit_cast(u32x4, fragment_at(at, r, 1));
+            f16x8 a, b;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t bits = __builtin_amdgcn_perm(u[q / 2], d[q / 2], q & 1 ? 0x07060302u : 0x05040100u);
+                const float v = __builtin_bit_cast(float, bits);
+                a[q] = (_Float16)(v * scale);  // (the product is exact)
+                b[q] = (_Float16)__builtin_fmaf(v, scale, -(float)a[q]);
+            }
+            h = __builtin_bit_cast(s16x8, a);
+            l = __builtin_bit_cast(s16x8, b);
+        } else if constexpr (BASED) {
+            h = fragment_at(at, r, 0);
+            l = fragment_at(at, r, 1);
+        } else if constexpr (!RAW) {
             h = fragment(tile, row, 0, lane);
             l = fragment(tile, row, 1, lane);
         } else {
@@ -291,6 +348,7 @@ struct MgConfig {
     using TB = MgTile<KB_, BN, PLANES, WAVES>;
     static constexpr int KT = TA::KT;  // k of a tile
     static constexpr bool RAW = TA::RAW;
+    static constexpr bool SCALED = TB::HALVES;  // B has a scale for each of its rows
     static constexpr int LOADS = TA::LOADS + TB::LOADS;  // of a wave for a tile
     static_assert(STAGES == 2 || (WAVES == 4 && (STAGES & (STAGES - 1)) == 0 && LOADS * (STAGES - 2) < 64), "the waits");
     static constexpr int STAGE = TA::BYTES + TB::BYTES;
@@ -307,7 +365,8 @@ __device__ __forceinline__ void mg_multiply(f32x4 (&acc)[C::FM][C::FN], const s1
 }
 
 // Walks the first `ktiles` k tiles of both operands, each of which starts
-// at or before an operand's last_k.  The sum of row
+// at or before an operand's last_k.  `scale`: SCALED, of B's row 16 fj + lane %
+// 16 of the wave's part.  The sum of row
 // 16 fi + 4 (lane / 16) + r and column 16 fj + lane % 16 of the wave's part
 // is acc[fi][fj][r].  `lds`: LDS_BYTES.
 //
@@ -321,7 +380,7 @@ __device__ __forceinline__ void mg_multiply(f32x4 (&acc)[C::FM][C::FN], const s1
 // turn: the first group's multiplying, the second's reading.
 template <typename C>
 __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOperand& a, const MgOperand& b,
-                                        int ktiles, char* lds) {
+                                        const float (&scale)[C::FN], int ktiles, char* lds) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int arow = (wave / C::WN) * (C::BM / C::WM), brow = (wave % C::WN) * (C::BN / C::WN);
@@ -333,6 +392,17 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const uint32_t lds0 = lds_offset(lds);
+    uint32_t abase = 0, bbase = 0;
+    if constexpr (C::TA::BASED) abase = C::TA::base(lds0, arow, lane);
+    if constexpr (C::TB::BASED) bbase = C::TB::base(lds0 + C::TA::BYTES, brow, lane);
+    // the bases in a buffer, hidden from the compiler, which would make and
+    // keep every read's address before the loop
+    auto bases = [&](int buf, uint32_t& a_at, uint32_t& b_at) {
+        a_at = abase + buf * C::STAGE;
+        b_at = bbase + buf * C::STAGE;
+        if constexpr (C::TA::BASED) asm volatile("" : "+v"(a_at));
+        if constexpr (C::TB::BASED) asm volatile("" : "+v"(b_at));
+    };
     if (ktiles <= 0) {
         mg_sync<true>();
         return;
@@ -351,12 +421,26 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
         auto read = [&](int buf) {
             const char* ta = lds + buf * C::STAGE;
             const char* tb = ta + C::TA::BYTES;
+            uint32_t a_at, b_at;
+            bases(buf, a_at, b_at);
+            if constexpr (C::SCALED) {
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j)
+                    C::TB::fragments(tb, b_at, brow, 16 * j, lane, 0, scale[j], fb[0][j], fb[1][j]);
+            }
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
+                if constexpr (!C::SCALED) {
 #pragma unroll
-                for (int j = 0; j < C::FN; ++j) fb[kk][j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
+                    for (int j = 0; j < C::FN; ++j) fb[kk][j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
+                }
 #pragma unroll
-                for (int i = 0; i < C::FM; ++i) fa[kk][i] = C::TA::fragment(ta, arow + 16 * i, kk, lane);
+                for (int i = 0; i < C::FM; ++i) {
+                    if constexpr (C::TA::BASED)
+                        fa[kk][i] = C::TA::fragment_at(a_at, 16 * i, kk);
+                    else
+                        fa[kk][i] = C::TA::fragment(ta, arow + 16 * i, kk, lane);
+                }
             }
         };
         auto multiply = [&]() {
@@ -425,10 +509,14 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
                     mg_multiply<C>(acc, fa[kk], fb[kk]);
                 }
             } else {
+                uint32_t a_at, b_at;
+                bases(t & (S - 1), a_at, b_at);
 #pragma unroll
-                for (int j = 0; j < C::FN; ++j) C::TB::fragments(tb, brow + 16 * j, lane, 0, fb[0][j], fb[1][j]);
+                for (int j = 0; j < C::FN; ++j)
+                    C::TB::fragments(tb, b_at, brow, 16 * j, lane, 0, scale[j], fb[0][j], fb[1][j]);
 #pragma unroll
-                for (int i = 0; i < C::FM; ++i) C::TA::fragments(ta, arow + 16 * i, lane, a.exp, fa[0][i], fa[1][i]);
+                for (int i = 0; i < C::FM; ++i)
+                    C::TA::fragments(ta, a_at, arow, 16 * i, lane, a.exp, 1.f, fa[0][i], fa[1][i]);
                 mg_multiply<C>(acc, fa[1], fb[0]);
                 mg_multiply<C>(acc, fa[0], fb[1]);
                 mg_multiply<C>(acc, fa[0], fb[0]);

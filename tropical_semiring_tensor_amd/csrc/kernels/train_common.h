@@ -87,11 +87,15 @@ __device__ __forceinline__ uint32_t dpp_umax(uint32_t x) {
     const uint32_t o = __builtin_amdgcn_update_dpp(0, x, CTRL, 0xf, 0xf, true);
     return o > x ? o : x;
 }
-__device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
+// (lane 15 of each row of 16 ends with its row's)
+__device__ __forceinline__ uint32_t row_umax(uint32_t x) {
     x = dpp_umax<0x111>(x);  // row_shr:1
     x = dpp_umax<0x112>(x);  // row_shr:2
     x = dpp_umax<0x114>(x);  // row_shr:4
-    x = dpp_umax<0x118>(x);  // row_shr:8
+    return dpp_umax<0x118>(x);  // row_shr:8
+}
+__device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
+    x = row_umax(x);
     x = dpp_umax<0x142>(x);  // row_bcast:15
     x = dpp_umax<0x143>(x);  // row_bcast:31
     return __builtin_amdgcn_readlane(x, 63);

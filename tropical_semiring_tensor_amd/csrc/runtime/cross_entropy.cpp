@@ -139,8 +139,8 @@ struct CePlan {
     int64_t split_tiles;  // streaming grad_x: rounds of a part
     int64_t max_parts;
     // workspace offsets
-    size_t control, rows, slot, kept_target, kept_lse, kept_grad, magnitude, stats, target_logit, xp, wp, g, gx_part,
-        gw_part;
+    size_t control, rows, slot, kept_target, kept_lse, kept_grad, magnitude, stats, target_logit, xp, wp, g, label_max,
+        label_exp, gx_part, gw_part;
     size_t bytes;
 };
 
@@ -262,6 +262,10 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     ok &= take(c, &c->kept_grad, c->padded * 4);
     // (the weight's 256-label tiles may read past a piece that ends at 128)
     ok &= take(c, &c->g, (c->piece + 256) * g_label);
+    if (c->planes == 2) {
+        ok &= take(c, &c->label_max, ceil_div(count, tile_edge(c->logits_tile)) * c->piece * 4);
+        ok &= take(c, &c->label_exp, c->piece * 4);
+    }
     const int64_t part = c->padded * c->width_p * 4;
     const GradTiles t = choose_grad_tiles(c->raw, count, labels, width, ceil_div(labels, kt), ceil_div(count, kt), unit, part,
                                           labels * c->width_p * 4);
@@ -349,10 +353,13 @@ TropCeParams params(const CeCall& a, const CePlan& c, char* ws) {
     p.xp = ws + c.xp;
     p.wp = ws + c.wp;
     p.g = ws + c.g;
+    p.label_max = reinterpret_cast<float*>(ws + c.label_max);
+    p.label_exp = reinterpret_cast<int32_t*>(ws + c.label_exp);
     p.gx_part = reinterpret_cast<float*>(ws + c.gx_part);
     p.gw_part = reinterpret_cast<float*>(ws + c.gw_part);
     p.padded = c.padded;
     p.width_p = c.width_p;
+    p.logits_edge = tile_edge(c.logits_tile);
     p.tiles = c.tiles;
     p.w_packed = c.packed;
     p.splits = (int32_t)c.splits;

@@ -132,10 +132,13 @@ struct TropCeParams {
     float* target_logit;      // per kept token (per token in the streaming kernel)
     void* xp;                 // packed x: [padded][width_p], float32 [padded][width_p / 32][2][32]
     void* wp;                 // packed piece of w: [piece] rows likewise
-    void* g;                  // piece of the logits' gradient: [planes][piece / 4][padded][4]
+    void* g;                  // piece of the logits' gradient: [planes][piece / 4][padded][4]; float32: upper, lower 16 bits
+    float* label_max;         // float32: its largest finite magnitudes, [tokens / logits_edge][piece]
+    int32_t* label_exp;       // float32: the exponents of grad_w's scales, when gw_splits > 1
     float* gx_part;           // [splits][padded][width_p]
     float* gw_part;           // [gw_splits][piece][width_p], when gw_splits > 1
     int64_t padded, width_p;
+    int64_t logits_edge;      // tokens of a logits tile
     int64_t v0, piece;        // this launch's labels: [v0, v0 + piece), piece a multiple of the tile
     int64_t tile0;            // first statistics tile of this launch
     int64_t tiles;            // statistics tiles in all
