@@ -282,3 +282,46 @@ def test_refusals(tb):
     st = tb.lib().tropical_layer_norm_forward(0, 0, raw.data_ptr(), 1 << 20, None, None, 1e-5, x.data_ptr(), 1 << 20,
                                               None, None, 4096, 8, None)
     assert st == tb.INVALID_ARGUMENT and "allocation" in tb.tropical_last_error()
+
+
+def test_more_rows_than_a_launch_holds(tb):
+    """2^32 threads are four waves to 2^26 rows, 256 threads to 2^24, 1024 to 2^22."""
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    x = torch.randn((1 << 26) + 5, 2, generator=gen, device=DEV).to(BF16)
+    check_forward(tb, x, None, None)
+    del x
+    for rows, cols in (((1 << 24) + 3, 1025), ((1 << 22) + 3, 4097)):
+        torch.cuda.empty_cache()
+        x = torch.empty(rows, cols, dtype=BF16, device=DEV)  # (what the other rows hold is their own)
+        at = torch.tensor([0, 1, 4097, rows // 2, rows - 5, rows - 4, rows - 3, rows - 2, rows - 1], device=DEV)
+        some = torch.randn(len(at), cols, generator=gen, device=DEV).to(BF16)
+        x[at] = some
+        want = tb.tropical_layer_norm_forward(some)
+        got = tb.tropical_layer_norm_forward(x, y=x)
+        assert all(torch.equal(a, b[at]) for a, b in zip(want, got))
+        del x, got
+    torch.cuda.empty_cache()
+
+
+def test_more_columns_than_a_launch_holds(tb):
+    """The column sums of 512 parts of 2^23 columns, and their sum over 2^27."""
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    rows, cols = 515, (1 << 23) + 300
+    x = torch.zeros(rows, cols, dtype=BF16, device=DEV)
+    at = torch.tensor([0, 255, 4096, cols // 2, cols - 301, cols - 300, cols - 1], device=DEV)
+    x[:, at] = torch.randn(rows, len(at), generator=gen, device=DEV).to(BF16)
+    mean, rstd = torch.zeros(rows, device=DEV), torch.ones(rows, device=DEV)
+    check = x[:, at].contiguous()
+    _, dg, db = tb.tropical_layer_norm_backward(x, x, mean, rstd, dx=None)
+    for got, terms in ((dg, check.double() ** 2), (db, check.double())):
+        assert_within(got[at], terms.sum(0), (rows + 64) * U * terms.abs().sum(0), "column sums")
+        got[at] = 0.0
+        assert not got.any()
+    del x
+    torch.cuda.empty_cache()
+    cols = (1 << 27) + 70
+    x = torch.randn(1, cols, generator=gen, device=DEV).to(BF16)
+    _, dg, db = tb.tropical_layer_norm_backward(x, x, mean[:1], rstd[:1], dx=None)
+    assert torch.equal(db, x[0].float()) and torch.equal(dg, x[0].float() ** 2)
+    del x, dg, db
+    torch.cuda.empty_cache()

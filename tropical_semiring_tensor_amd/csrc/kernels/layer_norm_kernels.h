@@ -301,11 +301,11 @@ __device__ __forceinline__ void layer_norm_backward_loop_body(const TropLayerNor
 }
 
 // ... and the partial column sums by threads that keep a column each:
-// blockIdx.x = part + parts * (256-column block); part q sums rows q,
-// q + parts, ...  Runs before the dx walk, which may overwrite dy.
+// blockIdx.x = part + parts * (256-column block, from col0 on); part q sums
+// rows q, q + parts, ...  Runs before the dx walk, which may overwrite dy.
 template <typename T>
 __device__ __forceinline__ void layer_norm_columns_body(const TropLayerNormParams& p) {
-    const int64_t part = blockIdx.x % p.parts, c = (int64_t)(blockIdx.x / p.parts) * 256 + threadIdx.x;
+    const int64_t part = blockIdx.x % p.parts, c = p.col0 + (int64_t)(blockIdx.x / p.parts) * 256 + threadIdx.x;
     if (c >= p.cols) return;
     float dg = 0.f, db = 0.f;
     for (int64_t r = part; r < p.rows; r += p.parts) {
@@ -319,15 +319,15 @@ __device__ __forceinline__ void layer_norm_columns_body(const TropLayerNormParam
 }
 
 // Sum of the partial column sums.  A workgroup takes 64 columns of dgamma or
-// dbeta, 16 waves the parts wave, wave + 16, ...; the waves' sums are added
+// (the second half of them) dbeta, 16 waves the parts wave, wave + 16, ...; the waves' sums are added
 // in wave order.
 template <typename P>
 __device__ __forceinline__ void layer_norm_merge_body(const TropLayerNormMergeParams& p) {
     __shared__ float lds[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-    const int64_t blocks = (p.cols + 63) / 64;
+    const uint32_t blocks = gridDim.x / 2;
     const bool beta = blockIdx.x >= blocks;
-    const int64_t c = (int64_t)(blockIdx.x - (beta ? blocks : 0)) * 64 + lane;
+    const int64_t c = p.col0 + (int64_t)(blockIdx.x - (beta ? blocks : 0)) * 64 + lane;
     P* out = static_cast<P*>(beta ? p.dbeta : p.dgamma);
     if (!out) return;
     float s = 0.f;

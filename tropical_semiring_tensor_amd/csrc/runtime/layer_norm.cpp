@@ -46,6 +46,24 @@ trop_status part_bytes(int64_t rows, int64_t cols, size_t* bytes) {
     return TROP_OK;
 }
 
+// A kernel with a row group to a row: as many launches as its rows need.
+// `rpg`: rows of a workgroup; eb: bytes of an element.
+trop_status launch_rows(int dev, TrainKernelId id, trop_train_family fam, TropLayerNormParams p, int64_t rpg,
+                        uint32_t block, size_t eb, hipStream_t s) {
+    const int64_t rows = p.rows, most = max_groups(block) * rpg;
+    for (int64_t r0 = 0; r0 < rows; r0 += most) {
+        p.rows = rows - r0 < most ? rows - r0 : most;
+        const trop_status st = train_launch(dev, id, fam, (p.rows + rpg - 1) / rpg, block, &p, s);
+        if (st != TROP_OK) return st;
+        p.x = static_cast<const char*>(p.x) + (size_t)most * p.ldx * eb;
+        if (p.dy) p.dy = static_cast<const char*>(p.dy) + (size_t)most * p.lddy * eb;
+        p.y = static_cast<char*>(p.y) + (size_t)most * p.ldy * eb;
+        if (p.mean) p.mean += most;
+        if (p.rstd) p.rstd += most;
+    }
+    return TROP_OK;
+}
+
 trop_status forward(trop_dtype dt, trop_dtype pdt, const void* x, int64_t ldx, const void* gamma, const void* beta,
                     float eps, void* y, int64_t ldy, float* mean, float* rstd, int64_t rows, int64_t cols,
                     void* stream) {
@@ -79,8 +97,8 @@ trop_status forward(trop_dtype dt, trop_dtype pdt, const void* x, int64_t ldx, c
     p.inv_cols = (float)(1.0 / (double)cols);
     static const TrainKernelId ids[] = {TK_LN_FWD_WAVE, TK_LN_FWD_BLOCK, TK_LN_FWD_WIDE, TK_LN_FWD_LOOP};
     const int g = group_of(cols);
-    st = train_launch(dev, (TrainKernelId)(ids[g] + ln_index(dt, pdt)), TROP_T_LAYER_NORM_FORWARD,
-                      g == 0 ? (rows + 3) / 4 : rows, g < 2 ? 256 : 1024, &p, static_cast<hipStream_t>(stream));
+    st = launch_rows(dev, (TrainKernelId)(ids[g] + ln_index(dt, pdt)), TROP_T_LAYER_NORM_FORWARD, p, g == 0 ? 4 : 1,
+                     g < 2 ? 256 : 1024, eb, static_cast<hipStream_t>(stream));
     return st == TROP_OK ? ok() : st;
 }
 
@@ -144,13 +162,17 @@ trop_status backward(trop_dtype dt, trop_dtype pdt, const void* dy, int64_t lddy
             if (st != TROP_OK) return st;
         } else {
             if (params) {  // before dx, which may be dy's own buffer
-                st = train_launch(dev, (TrainKernelId)(TK_LN_COLUMNS + (dt == TROP_BF16)), TROP_T_LAYER_NORM_BACKWARD,
-                                  parts * ((cols + 255) / 256), 256, &p, s);
-                if (st != TROP_OK) return st;
+                const int64_t most = max_groups(256) / parts * 256;
+                for (; p.col0 < cols; p.col0 += most) {
+                    const int64_t n = cols - p.col0 < most ? cols - p.col0 : most;
+                    st = train_launch(dev, (TrainKernelId)(TK_LN_COLUMNS + (dt == TROP_BF16)),
+                                      TROP_T_LAYER_NORM_BACKWARD, parts * ((n + 255) / 256), 256, &p, s);
+                    if (st != TROP_OK) return st;
+                }
             }
             if (dx) {
-                st = train_launch(dev, (TrainKernelId)(TK_LN_BWD_LOOP + idx), TROP_T_LAYER_NORM_BACKWARD, rows, 1024,
-                                  &p, s);
+                st = launch_rows(dev, (TrainKernelId)(TK_LN_BWD_LOOP + idx), TROP_T_LAYER_NORM_BACKWARD, p, 1, 1024, eb,
+                                 s);
                 if (st != TROP_OK) return st;
             }
         }
@@ -162,9 +184,13 @@ trop_status backward(trop_dtype dt, trop_dtype pdt, const void* dy, int64_t lddy
         q.dbeta = dbeta;
         q.cols = cols;
         q.parts = (int32_t)parts;
-        st = train_launch(dev, (TrainKernelId)(TK_LN_MERGE + (pdt == TROP_BF16)), TROP_T_LAYER_NORM_BACKWARD,
-                          2 * ((cols + 63) / 64), 1024, &q, s);
-        if (st != TROP_OK) return st;
+        const int64_t most = max_groups(1024) / 2 * 64;
+        for (; q.col0 < cols; q.col0 += most) {
+            const int64_t n = cols - q.col0 < most ? cols - q.col0 : most;
+            st = train_launch(dev, (TrainKernelId)(TK_LN_MERGE + (pdt == TROP_BF16)), TROP_T_LAYER_NORM_BACKWARD,
+                              2 * ((n + 63) / 64), 1024, &q, s);
+            if (st != TROP_OK) return st;
+        }
     }
     return ok();
 }

@@ -49,6 +49,8 @@ trop_status train_device(int* dev);
 trop_status train_launch(int dev, TrainKernelId id, trop_train_family fam, int64_t grid, uint32_t block,
                          const void* params, hipStream_t stream);
 int train_cu_count(int dev);
+// Workgroups of `block` threads that one launch may have.
+inline int64_t max_groups(uint32_t block) { return 0xffffffffLL / block; }
 void reset_train_launches();
 
 inline size_t elem_size(trop_dtype dt) { return dt == TROP_BF16 ? 2 : 4; }

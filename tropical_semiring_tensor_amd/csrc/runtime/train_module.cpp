@@ -124,7 +124,7 @@ trop_status train_launch(int dev, TrainKernelId id, trop_train_family fam, int64
     TrainModule* m = g_dev[dev].load(std::memory_order_acquire);
     if (!m) return fail(TROP_ERR_HIP, "training code object not loaded on this device");
     if (grid <= 0) return TROP_OK;
-    if (grid * block > 0xffffffffLL || grid > 0x7fffffffLL)
+    if (grid > max_groups(block))
         return fail(TROP_ERR_INVALID_ARGUMENT, std::string(kNames[id]) + ": too many workgroups");
     void* args[] = {const_cast<void*>(params)};
     hipError_t e = hipModuleLaunchKernel(m->fn[id], (uint32_t)grid, 1, 1, block, 1, 1, 0, stream, args, nullptr);

@@ -23,6 +23,7 @@ struct TropLayerNormParams {
     float* part;        // backward: [2][parts][cols], null without dgamma and dbeta
     int64_t ldx, lddy, ldy;
     int64_t rows, cols;
+    int64_t col0;       // partial column sums of wide rows: the launch's first column
     float eps, inv_cols;
     int32_t parts;      // workgroups of the backward
     int32_t pad_;
@@ -32,7 +33,7 @@ struct TropLayerNormMergeParams {
     const float* part;
     void* dgamma;  // may be null
     void* dbeta;   // may be null
-    int64_t cols;
+    int64_t cols, col0;  // col0: the launch's first column
     int32_t parts;
     int32_t pad_;
 };
