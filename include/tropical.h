@@ -606,7 +606,8 @@ TROP_API trop_status tropical_linear_cross_entropy_workspace_size(trop_dtype dty
  * With more than 32 tokens G is held in fewer bits for the products: in
  * bfloat16 it is rounded to bfloat16 (8 significant bits) once; in float32 it
  * has 22 bits, and an absolute 2^-38 of its own token's |grad_loss| in grad_x,
- * of its own label's largest |G| in grad_w.
+ * of its own label's largest |G| in grad_w.  A non-finite grad_loss of a token
+ * that counts makes its row of grad_x non-finite, and what it adds to grad_w.
  * Errors: as the forward.
  */
 TROP_API trop_status tropical_linear_cross_entropy_backward(trop_dtype dtype, const void* x, int64_t ldx,

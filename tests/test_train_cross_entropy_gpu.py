@@ -414,3 +414,21 @@ def test_float32_mixed_magnitudes(tb, tokens, width, vocab):
     for m in (x, w):
         m *= torch.exp2(-20 * torch.rand(len(m), 1, generator=g, device=DEV))
     check_float32(tb, x, w, t, gl)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens", [20, 90, 300])
+def test_one_infinite_weight(tb, tokens, dtype):
+    """An infinite weight reaches its own token's row of grad_x and no other."""
+    x, w, t, gl = case(tokens, 64, 500, dtype, seed=15, ignored=0.1)
+    gl = gl * 100
+    at = int((t >= 0).nonzero()[3])
+    gl[at] = 0.0
+    want, tol = reference(x, w, t, gl)
+    _, lse = tb.tropical_linear_cross_entropy_forward(x, w, t)
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        gl[at] = bad
+        gx, _ = tb.tropical_linear_cross_entropy_backward(x, w, t, lse, gl)
+        assert not torch.isfinite(gx[at]).any()
+        gx[at] = 0.0
+        assert_within(gx, want[2], tol[2], f"grad_x beside a weight of {bad}")

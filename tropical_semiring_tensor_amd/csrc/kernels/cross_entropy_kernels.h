@@ -82,7 +82,10 @@ __device__ __forceinline__ void ce_keep_body(const TropCeParams& p) {
         const int64_t n = b + lane;
         const bool keep = n < n1 && ce_counts(p, ce_target(p, n));
         count += __popcll(__ballot(keep));
-        if (p.backward && keep) gmax = fmaxf(gmax, fabsf(p.grad_loss[n * p.grad_loss_stride]));
+        if (p.backward && keep) {  // (of the finite ones: an infinite weight spoils its own token only)
+            const float a = fabsf(p.grad_loss[n * p.grad_loss_stride]);
+            gmax = a < INFINITY ? fmaxf(gmax, a) : gmax;
+        }
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) gmax = fmaxf(gmax, __shfl_xor(gmax, o, 64));
@@ -99,7 +102,7 @@ __device__ __forceinline__ void ce_keep_body(const TropCeParams& p) {
         total += wave_count[w];
         gmax = fmaxf(gmax, wave_max[w]);
     }
-    if (!(gmax > 0.f) || gmax > 3.0e38f) gmax = 1.f;  // nothing to scale, or an infinite weight
+    if (gmax == 0.f) gmax = 1.f;  // nothing to scale
 #pragma unroll 4
     for (int64_t b = n0; b < n1; b += 64) {
         const int64_t n = b + lane;

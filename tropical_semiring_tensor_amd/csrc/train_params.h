@@ -104,7 +104,7 @@ constexpr int trop_ce_few_rows(int nb, int elem_bytes) {
 // Scalars that the first kernels of a call leave for the later ones.
 struct TropCeControl {
     int32_t kept;      // tokens that count
-    float grad_max;    // largest |grad_loss| of a kept token (1 when that is 0)
+    float grad_max;    // largest finite |grad_loss| of a kept token (1 when that is 0)
     int32_t x_exp;     // float32 operands: x 2^x_exp and w 2^w_exp are split
     int32_t w_exp;     // into float16 planes
 };
