@@ -432,3 +432,18 @@ def test_one_infinite_weight(tb, tokens, dtype):
         assert not torch.isfinite(gx[at]).any()
         gx[at] = 0.0
         assert_within(gx, want[2], tol[2], f"grad_x beside a weight of {bad}")
+
+
+@pytest.mark.parametrize("tokens", [10, 90])
+def test_float32_largest_numbers(tb, tokens):
+    """Elements of the largest float32 magnitude, logits of ordinary size."""
+    x, w, t, gl = case(tokens, 32, 300, F32, seed=16)
+    big = torch.finfo(F32).max
+    x, w = torch.where(x < 0, -big, big), w * 2.0 ** -125  # (normal numbers but for a few)
+    w[w.abs() < 2.0 ** -126] = 0.0
+    gl = gl * 1e-4
+    want, tol = reference(x, w, t, gl)
+    loss, lse = tb.tropical_linear_cross_entropy_forward(x, w, t)
+    gw = tb.tropical_linear_cross_entropy_backward(x, w, t, lse, gl, grad_x=None)[1]
+    for a, b, e, what in zip((loss, lse, gw), (want[0], want[1], want[3]), (tol[0], tol[1], tol[3]), ("loss", "lse", "grad_w")):
+        assert_within(a, b, e, what)

@@ -154,7 +154,7 @@ __device__ __forceinline__ void ce_magnitude_body(const TropCeParams& p) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float a = fabsf(v[e]);
-                    best = a < 3.4e38f ? fmaxf(best, a) : best;
+                    best = a < INFINITY ? fmaxf(best, a) : best;
                 }
             }
         }
