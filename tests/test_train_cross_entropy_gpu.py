@@ -447,3 +447,64 @@ def test_float32_largest_numbers(tb, tokens):
     gw = tb.tropical_linear_cross_entropy_backward(x, w, t, lse, gl, grad_x=None)[1]
     for a, b, e, what in zip((loss, lse, gw), (want[0], want[1], want[3]), (tol[0], tol[1], tol[3]), ("loss", "lse", "grad_w")):
         assert_within(a, b, e, what)
+
+
+def few_of_many(tokens, width, vocab, dtype, seed):
+    """x, target, weights of `tokens` tokens of which eight count, and those eight."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.empty(tokens, width, dtype=dtype, device=DEV)  # (what the others hold reaches nothing)
+    t = torch.full((tokens,), -100, dtype=torch.int32, device=DEV)
+    at = torch.tensor([0, 1, 300, tokens // 2, tokens - 70, tokens - 3, tokens - 2, tokens - 1], device=DEV)
+    x[at] = torch.randn(8, width, generator=g, device=DEV).to(dtype)
+    t[at] = torch.randint(0, vocab, (8,), generator=g, device=DEV).int()
+    t[at[0]], t[at[1]] = vocab - 1, 0
+    return x, t, torch.rand(tokens, generator=g, device=DEV) + 0.1, at
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_more_logits_than_a_launch_holds(tb, dtype):
+    """2^22 tokens and 131372 labels: more than 2^23 tiles of 256 x 256."""
+    x, t, _, at = few_of_many(1 << 22, 16, 131372, dtype, 17)
+    w = torch.randn(131372, 16, device=DEV, generator=torch.Generator(device=DEV).manual_seed(17)).to(dtype)
+    loss, lse = tb.tropical_linear_cross_entropy_forward(x, w, t)
+    want, tol = reference(x[at], w, t[at])
+    for got, b, e, what in zip((loss, lse), want, tol, ("loss", "lse")):
+        assert_within(got[at], b, e, what)
+        got[at] = 0.0
+        assert not got.any()
+    del x, loss, lse
+    torch.cuda.empty_cache()
+
+
+def test_more_labels_than_a_launch_holds(tb):
+    """More than 2^29 labels with 32 to a workgroup of the streaming form."""
+    vocab = (1 << 29) + 100
+    g = torch.Generator(device=DEV).manual_seed(18)
+    w = torch.randn(vocab, 1, generator=g, device=DEV).to(BF16)
+    x = torch.randn(2, 1, generator=g, device=DEV).to(BF16)
+    t = torch.tensor([vocab - 1, 5], device=DEV)
+    got = tb.tropical_linear_cross_entropy_forward(x, w, t)
+    for i in range(2):
+        want, tol = reference(x[i:i + 1], w, t[i:i + 1])
+        for a, b, e, what in zip(got, want, tol, ("loss", "lse")):
+            assert_within(a[i:i + 1], b, e, what)
+        del want, tol
+    del w
+    torch.cuda.empty_cache()
+
+
+def test_more_rows_of_grad_x_than_a_launch_holds(tb):
+    """2^22 tokens of more than three times 1024 columns."""
+    tokens, width, vocab = 1 << 22, 3100, 16
+    x, t, gl, at = few_of_many(tokens, width, vocab, BF16, 19)
+    w = torch.randn(vocab, width, device=DEV, generator=torch.Generator(device=DEV).manual_seed(19)).to(BF16)
+    _, lse = tb.tropical_linear_cross_entropy_forward(x, w, t)
+    gx, gw = tb.tropical_linear_cross_entropy_backward(x, w, t, lse, gl)
+    want, tol = reference(x[at], w, t[at], gl[at])
+    del x
+    assert_within(gx[at], want[2], tol[2], "grad_x")
+    assert_within(gw, want[3], tol[3], "grad_w")
+    gx[at] = 0.0
+    assert not any(part.any() for part in gx.split(1 << 19))
+    del gx
+    torch.cuda.empty_cache()

@@ -670,11 +670,12 @@ __device__ __forceinline__ FloatVec<4> ce_sum_parts(const float* q, int splits, 
 }
 
 // grad_x: the parts' sums in order, scaled; zeros for tokens that do not
-// count.  A workgroup takes 1024 columns of a row (blockIdx.x = row blocks + block).
+// count.  A workgroup takes 1024 columns of a row (blockIdx.x = (row - row0)
+// blocks + block).
 template <typename T, int PLANES>
 __device__ __forceinline__ void ce_finish_body(const TropCeParams& p) {
     const int64_t blocks = (p.width + 1023) / 1024;
-    const int64_t n = blockIdx.x / blocks, c = (blockIdx.x % blocks) * 1024 + threadIdx.x * 4;
+    const int64_t n = p.row0 + blockIdx.x / blocks, c = (blockIdx.x % blocks) * 1024 + threadIdx.x * 4;
     if (c >= p.width) return;
     int64_t i = n;
     CeScale scale = {1.f, 0};
@@ -852,7 +853,7 @@ __device__ __forceinline__ void ce_few_body(const TropCeParams& p) {
             s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
             if (lane < 16 && n < p.tokens)
-                reinterpret_cast<float2*>(p.stats)[n * p.tiles + blockIdx.x] = make_float2(m, s);
+                reinterpret_cast<float2*>(p.stats)[n * p.tiles + p.tile0 + blockIdx.x] = make_float2(m, s);
         } else {
             const bool on = n < p.tokens && ce_counts(p, t);
             const float lse = on ? p.lse_in[n] : 0.f;

@@ -113,6 +113,7 @@ GradTiles choose_grad_tiles(bool raw, int64_t tokens, int64_t labels, int64_t wi
         }
         const double ww = (double)ceil_div(kw, m) * unit, ww_half = (double)ceil_div((kw + 1) / 2, m) * unit;
         for (int64_t n = 1; n <= 32 && (n == 1 || kx / n >= 8); n += 1 + n / 8) {
+            if (tx * n + tw * m + 8 > max_groups(tile_threads(kind))) break;  // one launch
             const double wx = (double)ceil_div(kx, n) * unit;
             const double t = wextra + (double)(2 * n * gx_bytes) / 4e6 +
                              (pair_time(kind, tx * n, wx, tw * m, ww) + pair_time(kind, tx_half * n, wx, tw * m, ww_half)) / 2;
@@ -130,7 +131,7 @@ struct CePlan {
     bool few;           // few tokens: streaming kernels, no packing
     bool packed;        // w is read from packed pieces
     bool raw;           // float32 w is read as it lies
-    int64_t piece;      // labels of a piece (a multiple of 256; forward unpacked: all)
+    int64_t piece;      // labels of a piece (a multiple of 256; forward unpacked: all, but for a launch's limit)
     int logits_tile, grad_tile;  // 0: 256, 1: 128, 2: 64, 3: 128 with four buffers
     int few_blocks;     // streaming kernels: log2 of the blocks of 16 tokens
     int few_rows;       // and blocks of 16 labels of a logits workgroup
@@ -242,6 +243,10 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
             c->logits_tile = kind;
         }
     }
+    // a piece's logits in one launch
+    const int64_t edge = tile_edge(c->logits_tile);
+    const int64_t most = max_groups(tile_threads(c->logits_tile)) / ceil_div(count, edge) * edge / 256 * 256;
+    if (c->piece > most) c->piece = most;
     ok &= take(c, &c->control, sizeof(TropCeControl));
     ok &= take(c, &c->rows, c->padded * 4);
     ok &= take(c, &c->slot, c->padded * 4);
@@ -478,8 +483,12 @@ trop_status ce_forward(const CeCall& a, float* loss, float* lse) {
     p.lse = lse;
     const hipStream_t s = static_cast<hipStream_t>(a.stream);
     if (c.few) {
-        st = train_launch(dev, few_kernel(TK_CE_FEW, 6, c, a.dt), TROP_T_CE_LOGITS,
-                          c.tiles, 256, &p, s);
+        const int64_t most = max_groups(256);
+        for (; st == TROP_OK && p.tile0 < c.tiles; p.tile0 += most) {
+            p.v0 = p.tile0 * 16 * c.few_rows;
+            st = train_launch(dev, few_kernel(TK_CE_FEW, 6, c, a.dt), TROP_T_CE_LOGITS, std::min(c.tiles - p.tile0, most),
+                              256, &p, s);
+        }
     } else {
         st = list_tokens(dev, c, p, s);
         for (int64_t v0 = 0; st == TROP_OK && v0 < a.vocab; v0 += c.piece) {
@@ -534,9 +543,12 @@ trop_status ce_backward(const CeCall& a, const float* lse, const float* grad_los
     p.ldgw = ldgw;
     const hipStream_t s = static_cast<hipStream_t>(a.stream);
     st = c.few ? few_pieces(dev, a, c, p, s) : tile_pieces(dev, a, c, p, s);
-    if (st == TROP_OK && grad_x)
-        st = train_launch(dev, typed(TK_CE_FINISH, a.dt), TROP_T_CE_MERGE, a.tokens * ceil_div(a.width, 1024), 256, &p,
-                          s);
+    if (grad_x) {
+        const int64_t blocks = ceil_div(a.width, 1024), most = max_groups(256) / blocks;
+        for (; st == TROP_OK && p.row0 < a.tokens; p.row0 += most)
+            st = train_launch(dev, typed(TK_CE_FINISH, a.dt), TROP_T_CE_MERGE, std::min(a.tokens - p.row0, most) * blocks,
+                              256, &p, s);
+    }
     return st == TROP_OK ? ok() : st;
 }
 

@@ -142,6 +142,7 @@ struct TropCeParams {
     int64_t logits_edge;      // tokens of a logits tile
     int64_t v0, piece;        // this launch's labels: [v0, v0 + piece), piece a multiple of the tile
     int64_t tile0;            // first statistics tile of this launch
+    int64_t row0;             // finishing grad_x: the launch's first token
     int64_t tiles;            // statistics tiles in all
     int32_t target_bytes;
     int32_t w_packed;         // the piece is read from wp (else from w itself)
