@@ -646,7 +646,8 @@ typedef struct {
  *     a = max v of the block, c = rint(255 (v / a)^(1/4)), at least 1 for
  *     v > 0 (so that no positive v is taken for zero)
  * A block of zeros has scale 0.  The step uses m and v before they are
- * rounded to codes.  A non-finite gradient makes its block's state NaN.
+ * rounded to codes.  A non-finite gradient makes its block's m and v NaN, and
+ * so does an m or v that overflows its block's m or v.
  */
 #define TROP_ADAMW_BLOCK 256
 typedef struct {

@@ -271,3 +271,26 @@ def test_refusals(tb):
     assert tb.lib().tropical_adamw_step(0, table, 2, ctypes.byref(h), None) == tb.INVALID_ARGUMENT
     torch.cuda.synchronize()
     assert torch.equal(P[0], before)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan"), 1e25])
+def test_8bit_infinite_state(tb, bad):
+    """An infinite gradient spoils its own block's m and v and no other's; one
+    whose square alone overflows spoils v."""
+    n = 1000
+    g = torch.linspace(-1, 1, n, device=DEV)
+    g[400] = 0.0
+    g[300] = bad
+    p = torch.ones(n, device=DEV)
+    m, v = torch.zeros(n, dtype=torch.int8, device=DEV), torch.zeros(n, dtype=torch.uint8, device=DEV)
+    ms, vs = torch.zeros(4, device=DEV), torch.zeros(4, device=DEV)
+    tb.tropical_adamw8_step([p], [g], [m], [ms], [v], [vs], lr=0.1, step=1)
+    mv, vv = tb.tropical_adamw8_unpack([m], [ms], [v], [vs])
+    block = torch.zeros(n, dtype=torch.bool, device=DEV)
+    block[256:512] = True
+    assert torch.equal(vv[0].isnan(), block) and torch.isfinite(vv[0][~block]).all()
+    if bad == 1e25:
+        assert torch.isfinite(mv[0]).all()
+    else:
+        assert torch.equal(mv[0].isnan(), block) and torch.isfinite(mv[0][~block]).all()
+    assert torch.isfinite(p[~block]).all()

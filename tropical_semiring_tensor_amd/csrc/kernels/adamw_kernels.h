@@ -87,8 +87,9 @@ __device__ __forceinline__ float adamw8_v(float code, float a) {
     const float t = code * (1.0f / 255.0f), t2 = t * t;
     return a * (t2 * t2);
 }
-// Codes of m and v in a block of scale a (0: every element is zero).  A NaN
-// ratio takes code 0: the block's scale is NaN then, and so are its values.
+// Codes of m and v in a block of scale a (0: every element is zero).  A block
+// that holds a NaN or an infinity has a NaN scale, whatever its codes: an
+// infinite one would stand for infinities where they are not zero.
 __device__ __forceinline__ float adamw8_round_m(float m, float a) {
     return rintf(sqrtf(fabsf(m) / a) * 127.0f);
 }
@@ -159,8 +160,10 @@ __device__ __forceinline__ void adamw8_body(const TropAdamw8Params& p) {
             am_bits = max(am_bits, __builtin_bit_cast(uint32_t, m[i]) & 0x7fffffffu);
             av_bits = max(av_bits, __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
         }
-        const float am = __builtin_bit_cast(float, wave_umax(am_bits));
-        const float av = __builtin_bit_cast(float, wave_umax(av_bits));
+        float am = __builtin_bit_cast(float, wave_umax(am_bits));
+        float av = __builtin_bit_cast(float, wave_umax(av_bits));
+        am = am < INFINITY ? am : NAN;
+        av = av < INFINITY ? av : NAN;
         const float dm = am > 0.f ? am : 1.f, dv = av > 0.f ? av : 1.f;
         const float rm = 1.0f / dm, rv = 1.0f / dv;
         float cm[4], cv[4];
