@@ -69,7 +69,7 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, const char* base, uint
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(voff), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // This wave's LDS reads have returned (and, with LOADS, its loads to LDS have
