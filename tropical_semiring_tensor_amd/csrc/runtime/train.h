@@ -36,7 +36,8 @@ enum TrainKernelId : int {
     TK_CE_STATS_RAW = TK_CE_GRADIENTS + 6,
     TK_CE_GRAD_RAW = TK_CE_STATS_RAW + 3,
     TK_CE_GRADIENTS_RAW = TK_CE_GRAD_RAW + 3,
-    // few tokens: + (bf16 ? 1 : 0) + 2 log2(blocks of 16 tokens: 1, 2, 4) + 6 (5) (label blocks - 1)
+    // few tokens: + (bf16 ? 1 : 0) + 2 log2(blocks of 16 tokens: 1, 2, 4) + 6 (5) where a
+    // workgroup takes several blocks of labels (trop_ce_few_rows)
     TK_CE_FEW = TK_CE_GRADIENTS_RAW + 2,  // statistics
     TK_CE_FEW_GRAD = TK_CE_FEW + 12,   // G; likewise, without bf16 for 4 blocks
     TK_CE_FEW_GX = TK_CE_FEW_GRAD + 10,  // the gradients: without label blocks
@@ -48,7 +49,6 @@ enum TrainKernelId : int {
 trop_status train_device(int* dev);
 trop_status train_launch(int dev, TrainKernelId id, trop_train_family fam, int64_t grid, uint32_t block,
                          const void* params, hipStream_t stream);
-int train_cu_count(int dev);
 // Workgroups of `block` threads that one launch may have.
 inline int64_t max_groups(uint32_t block) { return 0xffffffffLL / block; }
 void reset_train_launches();

@@ -70,7 +70,6 @@ static_assert(sizeof(kNames) / sizeof(kNames[0]) == TK_COUNT, "training kernels"
 struct TrainModule {
     hipModule_t module = nullptr;
     hipFunction_t fn[TK_COUNT] = {};
-    int cu_count = 0;
 };
 
 std::mutex g_mu;
@@ -92,10 +91,6 @@ trop_status load(int dev) {
             e = hipModuleGetFunction(&m->fn[i], m->module, kNames[i]);
             if (e != hipSuccess) st = hip_fail(e, kNames[i]);
         }
-        if (st == TROP_OK) {
-            e = hipDeviceGetAttribute(&m->cu_count, hipDeviceAttributeMultiprocessorCount, dev);
-            if (e != hipSuccess) st = hip_fail(e, "hipDeviceGetAttribute(multiprocessor count)");
-        }
         if (st != TROP_OK) (void)hipModuleUnload(m->module);
     }
     if (st != TROP_OK) {
@@ -112,11 +107,6 @@ trop_status train_device(int* dev) {
     hipError_t e = hipGetDevice(dev);
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
     return load(*dev);
-}
-
-int train_cu_count(int dev) {
-    TrainModule* m = g_dev[dev].load(std::memory_order_acquire);
-    return m ? m->cu_count : 0;
 }
 
 trop_status train_launch(int dev, TrainKernelId id, trop_train_family fam, int64_t grid, uint32_t block,
