@@ -257,28 +257,31 @@ struct MgTile {
         return __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
     }
 
+    // HALVES: the two fragments h and l hold become those of the float32 values
+    // times `scale`, a power of two.
+    static __device__ __forceinline__ void split(float scale, s16x8& h, s16x8& l) {
+        const u32x4 u = __builtin_bit_cast(u32x4, h), d = __builtin_bit_cast(u32x4, l);
+        f16x8 a, b;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const uint32_t bits = __builtin_amdgcn_perm(u[q / 2], d[q / 2], q & 1 ? 0x07060302u : 0x05040100u);
+            const float v = __builtin_bit_cast(float, bits);
+            a[q] = (_Float16)(v * scale);  // (the product is exact)
+            b[q] = (_Float16)__builtin_fmaf(v, scale, -(float)a[q]);
+        }
+        h = __builtin_bit_cast(s16x8, a);
+        l = __builtin_bit_cast(s16x8, b);
+    }
+
     // Both fragments of rows [row0 + r, row0 + r + 16), from `tile` or from
-    // `at`, the base.  RAW: of the values times 2^exp; HALVES: times `scale`, a
-    // power of two.
+    // `at`, the base.  RAW: of the values times 2^exp; HALVES: times `scale`.
     static __device__ __forceinline__ void fragments(const char* tile, uint32_t at, int row0, int r, int lane,
                                                      int32_t exp, float scale, s16x8& h, s16x8& l) {
         const int row = row0 + r;
-        if constexpr (HALVES) {
-            const u32x4 u = __builtin_bit_cast(u32x4, fragment_at(at, r, 0));
-            const u32x4 d = __builtin_bit_cast(u32x4, fragment_at(at, r, 1));
-            f16x8 a, b;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const uint32_t bits = __builtin_amdgcn_perm(u[q / 2], d[q / 2], q & 1 ? 0x07060302u : 0x05040100u);
-                const float v = __builtin_bit_cast(float, bits);
-                a[q] = (_Float16)(v * scale);  // (the product is exact)
-                b[q] = (_Float16)__builtin_fmaf(v, scale, -(float)a[q]);
-            }
-            h = __builtin_bit_cast(s16x8, a);
-            l = __builtin_bit_cast(s16x8, b);
-        } else if constexpr (BASED) {
+        if constexpr (BASED) {
             h = fragment_at(at, r, 0);
             l = fragment_at(at, r, 1);
+            if constexpr (HALVES) split(scale, h, l);
         } else if constexpr (!RAW) {
             h = fragment(tile, row, 0, lane);
             l = fragment(tile, row, 1, lane);
@@ -423,16 +426,14 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
             const char* tb = ta + C::TA::BYTES;
             uint32_t a_at, b_at;
             bases(buf, a_at, b_at);
-            if constexpr (C::SCALED) {
-#pragma unroll
-                for (int j = 0; j < C::FN; ++j)
-                    C::TB::fragments(tb, b_at, brow, 16 * j, lane, 0, scale[j], fb[0][j], fb[1][j]);
-            }
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-                if constexpr (!C::SCALED) {
 #pragma unroll
-                    for (int j = 0; j < C::FN; ++j) fb[kk][j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
+                for (int j = 0; j < C::FN; ++j) {
+                    if constexpr (C::TB::BASED)
+                        fb[kk][j] = C::TB::fragment_at(b_at, 16 * j, kk);
+                    else
+                        fb[kk][j] = C::TB::fragment(tb, brow + 16 * j, kk, lane);
                 }
 #pragma unroll
                 for (int i = 0; i < C::FM; ++i) {
@@ -440,6 +441,16 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
                         fa[kk][i] = C::TA::fragment_at(a_at, 16 * i, kk);
                     else
                         fa[kk][i] = C::TA::fragment(ta, arow + 16 * i, kk, lane);
+                }
+            }
+            if constexpr (C::SCALED) {
+                // here, beside the other group's products: the compiler would
+                // put it off past the barrier, before this group's own (8192 x
+                // 2048 x 16384: a backward of 3.53 ms against 3.58)
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j) {
+                    C::TB::split(scale[j], fb[0][j], fb[1][j]);
+                    asm volatile("" : "+v"(fb[0][j]), "+v"(fb[1][j]));
                 }
             }
         };
