@@ -566,9 +566,10 @@ TROP_API trop_status tropical_layer_norm_backward(trop_dtype dtype, trop_dtype p
  * loss, lse: float32, tokens elements each.
  * The rows of x that count and w are meant to be finite: where one of their
  *   elements is not, what depends on it may be NaN even where the formula
- *   gives an infinity or, of a label at -inf, a number.  With more than 32
- *   tokens, float32 elements below 2^-18 of their matrix's largest keep an
- *   absolute precision of 2^-39 of that largest.
+ *   gives an infinity or, of a label at -inf, a number.  Exponentials below
+ *   2^-126 count as zero.  With more than 32 tokens, float32 elements below
+ *   2^-18 of their matrix's largest keep an absolute precision of 2^-39 of that
+ *   largest.
  * workspace: at least tropical_linear_cross_entropy_workspace_size bytes of
  *   device memory, used only by work on `stream`.
  * tokens, width, vocab >= 0 (vocab >= 1 and width >= 1 when tokens > 0).

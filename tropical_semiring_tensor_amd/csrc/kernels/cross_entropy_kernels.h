@@ -14,10 +14,10 @@
 // Measured, forward and backward: 8192 x 4096 x 65536 bfloat16 (7780 tokens
 // count) 13.1 to 14.2 ms by the card's power, 1.18 to 1.27 PFLOP/s (logits
 // 3.0, their gradient 3.3, both products of it 6.6 of 13.1 ms); 4096 x 1024 x
-// 32768 float32 2.5 to 2.7 ms, 390 to 420 TFLOP/s (0.62, 0.66, 1.16 of 2.5);
-// 1000 x 1000 x 50001 bfloat16, a third ignored, 0.37 ms, bound by whole
-// rounds of tiles; 256 x 512 x 8000 float32 87 us, by nine short
-// launches.
+// 32768 float32 2.55 to 2.7 ms, 385 to 410 TFLOP/s (0.62, 0.67, 1.35 of 2.84
+// under the profiler); 1000 x 1000 x 50001 bfloat16, a third ignored, 0.37 ms,
+// bound by whole rounds of tiles; 256 x 512 x 8000 float32 88 to 91 us, by nine
+// short launches.
 //
 // Tokens that do not count are left out: the kept ones are listed first
 // (ordered, by one workgroup), and x is packed in that order, so masked
@@ -644,8 +644,8 @@ __device__ __forceinline__ void ce_grad_w_body(const TropCeParams& p, int64_t id
 
 // Both gradients of a piece in one launch: neither reads what the other
 // writes, and their tiles fill one another's last round of workgroups.
-// Two launches against one: 256 x 512 x 8000 float32 25.6 and 20.4 us, 655 x
-// 733 x 46669 float32 335 and 293, 8192 x 4096 x 65536 bfloat16 6.91 and 6.83 ms.
+// Two launches against one: 256 x 512 x 8000 float32 36 and 25 us, 655 x 733 x
+// 46669 float32 354 and 337, 8192 x 4096 x 65536 bfloat16 6.91 and 6.83 ms.
 template <typename CX, typename CW, typename T>
 __device__ __forceinline__ void ce_gradients_body(const TropCeParams& p, char* lds) {
     static_assert(CX::THREADS == CW::THREADS && CX::LDS_BYTES == CW::LDS_BYTES, "one launch");
@@ -706,11 +706,13 @@ __device__ __forceinline__ void ce_finish_w_body(const TropCeParams& p) {
 // Up to 64 tokens (32 in bfloat16's backward and where w is large): w is
 // streamed from HBM straight into the matrix instructions' registers, with no
 // LDS copy and no packing.  The logits' pass reads it once; the backward reads
-// it twice and writes grad_w.  All are bound by those bytes up to 16 tokens (1
-// token x 4096 x 65536 bfloat16: 96 us, 5.6 TB/s), so they want many loads in
-// flight: the four waves of a workgroup share its rows and split the sum.
-// Beyond, by the float32 matrix instructions too (26 tokens x 2560 x 58817
-// float32: logits 206 us, grad_x 135, grad_w 175, where w's bytes take 125).
+// it twice and writes grad_w.  They want many loads in flight: the four waves
+// of a workgroup share its rows and split the sum.  One token is bound by w's
+// bytes (4096 x 65536 bfloat16: 96 us, 5.6 TB/s); 16 tokens take 152 us on the
+// same w, since every workgroup of 32 labels reads all of x too, 268 MB through
+// the caches beside w's 537.  From 17 on the float32 matrix instructions take
+// as long as the reads (26 tokens x 2560 x 58817 float32: logits 206 us, grad_x
+// 135, grad_w 175, where w's bytes take 100 to 125).
 //
 // Logits: a workgroup takes 16 RF labels and all tokens (16 to a block
 // column).  A lane reads 16 bytes of row lane % 16 at k chunk lane / 16, so

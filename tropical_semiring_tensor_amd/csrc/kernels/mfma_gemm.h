@@ -337,8 +337,10 @@ __device__ __forceinline__ f32x4 mg_mfma(s16x8 a, s16x8 b, f32x4 c) {
 // lower where they are busier; with every load hitting the L1 (a timing copy)
 // KM KM reaches 1500.  In 128 x 128, k tiles of 32 or three buffers are slower
 // by up to a fifth.  Two planes: a third fewer loads and reads per product,
-// and 1340 (logits of 4096 x 1024 x 32768, with their epilogue) to 1440 TFLOP/s
-// of 16-bit products against 1140 to 1250 in three walks, a plane pair each.
+// and 1340 TFLOP/s of 16-bit products (logits of 4096 x 1024 x 32768, with their
+// epilogue) against 1140 to 1250 in three walks, a plane pair each; the
+// gradients, which also split float32's halves, 1160 to 1220 of them, the
+// matrix units busy 62% of the cycles (1440 and 70% without the split).
 // (A large library product on the same card: 1430-1470 in bfloat16, 153 in
 // float32.)
 template <int BM_, int BN_, int WM_, int WN_, OperandKind KA_, OperandKind KB_, int PLANES_, int STAGES_ = 2>

@@ -32,7 +32,8 @@ int64_t piece_labels(int64_t vocab, int64_t bytes) {
 // and takes 1.75 us a k tile; a 128 x 128 one 0.7 us alone on a CU, 1.15
 // beside another; a 64 x 64 one 0.3 us alone, 0.5 with two and 0.85 with
 // four on a CU; a tile costs 6, 5 or 4 us besides (first loads, epilogue).
-// A k tile of 32 of float32's two planes takes 1.25 of these.
+// A k tile of 32 of float32's two planes takes 1.25 of these (in the
+// gradients, which also split G, 1.35: alike for every tile, and left out).
 struct TileRate {
     double us;
     int64_t slots;
@@ -203,8 +204,8 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     // Few tokens take the streaming kernels.  Beyond 32 the tiles are faster
     // where they need no packed copy of a large w, and always in bfloat16's
     // backward, whose streaming form sums widened values (both directions, in
-    // tiles and streaming: 65 and 64 tokens x 2560 x 58817 float32 847 and 1085
-    // us, 4096 x 8000 285 and 278; forward, bfloat16, 60 tokens: 4096 x 16100 36 and
+    // tiles and streaming: 65 and 64 tokens x 2560 x 58817 float32 887 and 1085
+    // us, 4096 x 8000 288 and 278; forward, bfloat16, 60 tokens: 4096 x 16100 36 and
     // 80, 4096 x 5000 37 and 43, 1024 x 12000 24 and 22, 4096 x 2600 36 and 27).
     const bool large = !packed && vocab * width >= (backward ? kLargeElements : kTileElements);
     const bool tiles = backward ? dt == TROP_BF16 || large : dt == TROP_BF16 && large;
@@ -215,10 +216,10 @@ bool plan(trop_dtype dt, int64_t tokens, int64_t width, int64_t vocab, bool back
     c->padded = round_up(tokens > 0 ? tokens : 1, 256);
     // float32 w as it lies, split by the tiles that read it, saves its packed
     // copy where two tiles of tokens at most read it, but has them wait for
-    // the split: forward and backward without the magnitudes, packed and as
-    // it lies, 66 tokens x 1856 x 25495: 379 and 293 us; 250 x 1856 x 16810:
-    // 379 and 330; 183 x 320 x 33477 (11 million elements): 134 and 127; 232 x
-    // 2560 x 3457 (9 million): 120 and 130; 150 x 1024 x 259: 44 and 57.
+    // the split: forward and backward, packed and as it lies, 66 tokens x 1856
+    // x 25495: 467 and 364 us; 250 x 1856 x 16810: 420 and 359; 183 x 320 x
+    // 33477 (11 million elements): 171 and 161; 232 x 2560 x 3457 (9 million):
+    // 160 and 174; 150 x 1024 x 259: 62 and 75.
     c->raw = dt == TROP_F32 && !packed && tokens <= 256 && vocab * width >= kLargeElements;
     c->packed = packed || (dt == TROP_F32 && !c->raw);
     bool ok = true;
