@@ -11,7 +11,9 @@
  *   tropical_tree_run              a contraction tree of pairwise einsums
  *                                  with every intermediate kept on device
  * and the operators of a training step around them (see "Training
- * operators" below): layer norm, linear cross entropy, AdamW.
+ * operators" below): layer norm, linear cross entropy, AdamW, activations in
+ * 8 bits with a linear layer's weight gradient from them, and the norms, gate
+ * and sum between two residual blocks.
  *
  * Sources (web pages the method is taken from):
  *   [PR35]  tropical-gemm PR #35 "feat: batched GPU ops with DLPack zero-copy
@@ -689,6 +691,181 @@ TROP_API trop_status tropical_adamw8_step(trop_dtype dtype, const trop_adamw8_te
 TROP_API trop_status tropical_adamw8_unpack(const trop_adamw8_tensor* tensors, int64_t count,
                                    float* const* exp_avg_values, float* const* exp_avg_sq_values, void* stream);
 
+/*
+ * ---- Activations in 8 bits ----
+ *
+ * What a forward keeps for the backward, in a little over a byte an element.
+ * TROP_ACT8_BLOCK consecutive elements of a row (its last block may be short)
+ * share an exponent e in [1, 248]:
+ *   code c = rint(x 2^(127 - e)) in [-127, 127] stands for c 2^(e - 127)
+ * with e the smallest for which no code of the block passes 127 (magnitudes
+ * above 127 2^121, 3.376e38, are taken as that).  So a value
+ * is off by half of 2^(e - 127) at most, which is 1 / 127 of the block's
+ * largest magnitude at most (and 2^-127 in blocks below 2^-120), and it is
+ * exact in bfloat16 and in float32: unpacking rounds nothing.  A block of zeros has
+ * e = 1.  A block with a NaN or an infinity has e = 255 and codes 0; all its
+ * values are NaN.
+ * codes: rows x cols, row stride ld >= cols.  exponents: rows x
+ * ceil(cols / TROP_ACT8_BLOCK), row stride ld_exponents >= that.
+ */
+#define TROP_ACT8_BLOCK 32
+typedef struct {
+    int8_t* codes;
+    uint8_t* exponents;
+    int64_t ld, ld_exponents;
+} trop_act8;
+
+/*
+ * x (rows x cols, row stride ldx, float32 or bfloat16) into `out`, and back
+ * into `out` (row stride ldo, float32 or bfloat16).
+ * rows, cols >= 0.  Errors: TROP_ERR_INVALID_ARGUMENT (bad dtype, NULL
+ *   trop_act8, negative size, row stride below the row's length),
+ *   TROP_ERR_NOT_DEVICE_MEMORY, TROP_ERR_HIP.
+ */
+TROP_API trop_status tropical_act8_pack(trop_dtype dtype, const void* x, int64_t ldx, const trop_act8* out,
+                               int64_t rows, int64_t cols, void* stream);
+TROP_API trop_status tropical_act8_unpack(const trop_act8* in, trop_dtype dtype, void* out, int64_t ldo,
+                                 int64_t rows, int64_t cols, void* stream);
+
+/*
+ * Weight gradient of a linear layer z = x w^T whose input x was kept in 8 bits:
+ *   grad_w[o][c] = sum_n dz[n][o] x[n][c]
+ * dz (tokens x out_features, row stride lddz) and grad_w (out_features x cols,
+ * row stride ldgw): `dtype` (float32 or bfloat16).  x: tokens x cols.
+ * bfloat16: every product is exact, the sums are float32.  float32: dz is
+ * taken as the exact sum of three bfloat16 values, so every product is exact
+ * too; parts of dz below 2^-126 may count as zero.  Where an element of dz or
+ * of x is not finite, what depends on it may be NaN even where the formula
+ * gives an infinity.  With tokens == 0 grad_w is zero.
+ * workspace: at least tropical_act8_linear_grad_w_workspace_size bytes (x as
+ *   bfloat16 in pieces of 256 MiB or 256 columns at most; of dz, where float32
+ *   or not aligned to 16 bytes, likewise; partial sums), used only by work on
+ *   `stream`.
+ * tokens, cols, out_features >= 0.
+ * Errors: TROP_ERR_INVALID_ARGUMENT, TROP_ERR_NOT_DEVICE_MEMORY,
+ *   TROP_ERR_WORKSPACE_TOO_SMALL, TROP_ERR_UNSUPPORTED (more than 2^22 tokens,
+ *   columns or output features), TROP_ERR_HIP.
+ */
+TROP_API trop_status tropical_act8_linear_grad_w(trop_dtype dtype, const void* dz, int64_t lddz, const trop_act8* x,
+                                        void* grad_w, int64_t ldgw, int64_t tokens, int64_t cols,
+                                        int64_t out_features, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/* Workspace (bytes) of the above for this shape and every row stride and
+ * alignment.  Host-only.  Errors: TROP_ERR_INVALID_ARGUMENT (bad dtype,
+ * negative size, NULL bytes), TROP_ERR_UNSUPPORTED. */
+TROP_API trop_status tropical_act8_linear_grad_w_workspace_size(trop_dtype dtype, int64_t tokens, int64_t cols,
+                                                       int64_t out_features, size_t* bytes);
+
+/*
+ * ---- Between two residual blocks ----
+ *
+ * The norm after a block, its gate, the residual sum and the norm before the
+ * next block in one pass over the rows:
+ *   v = post norm of u                              (u the block's output)
+ *   h = residual_scale r + (branch_scale gate) v    (r the block's input)
+ *   y = pre norm of h                               (the next block's input)
+ * A norm is one of
+ *   TROP_NORM_NONE   x itself
+ *   TROP_NORM_LAYER  (x - mean) rstd gamma + beta, the statistics those of
+ *                    tropical_layer_norm_forward
+ *   TROP_NORM_RMS    x rstd gamma + beta, rstd = 1 / sqrt(sum_c x^2 / cols + eps)
+ * v, h and the statistics are float32; h and y are rounded once each where
+ * they are stored, y and its statistics come from h before it is rounded.  A
+ * non-finite element reaches its own row's outputs and no other's.
+ */
+typedef enum { TROP_NORM_NONE = 0, TROP_NORM_LAYER = 1, TROP_NORM_RMS = 2 } trop_norm;
+
+/* What both directions share.  dtype: float32 or bfloat16, of r, u, h, y and
+ * their gradients.  param_dtype: float32 or dtype, of gamma and beta (each may
+ * be NULL: 1 and 0).  gate: NULL (1), or gate_rows x cols of gate_dtype
+ * (float32 or dtype), row stride ldgate; row i has gate row i / gate_group,
+ * and gate_rows = ceil(rows / gate_group).  A gate_group of 1 is a gate for
+ * each element, one of rows or more a vector for all rows.  gate_group >= 1
+ * with a gate.  The scales are finite, the eps finite and >= 0. */
+typedef struct {
+    trop_dtype dtype, param_dtype, gate_dtype;
+    trop_norm post, pre;
+    float residual_scale, branch_scale, post_eps, pre_eps;
+    int64_t rows, cols;
+    const void* gate;
+    int64_t ldgate, gate_group;
+    const void* post_gamma;
+    const void* post_beta;
+    const void* pre_gamma;
+    const void* pre_beta;
+} trop_residual_norm;
+
+/* A row-major matrix of the operator's dtype; data NULL: not there. */
+typedef struct {
+    void* data;
+    int64_t ld;
+} trop_matrix;
+
+/*
+ * Forward.  r may be left out (h = branch_scale gate v), h and y may (y is
+ * when pre is TROP_NORM_NONE, which makes no y).  h may be r itself (same
+ * stride).  post_mean, post_rstd, pre_mean, pre_rstd: float32, rows elements,
+ * each may be NULL; those of a norm that is none, and the mean of an RMS norm,
+ * are not written.  u8, h8: u and h in 8 bits for the backward (h before it is
+ * rounded to dtype), either may be NULL.
+ * Errors: TROP_ERR_INVALID_ARGUMENT, TROP_ERR_NOT_DEVICE_MEMORY, TROP_ERR_HIP.
+ */
+TROP_API trop_status tropical_residual_norm_forward(const trop_residual_norm* op, trop_matrix r, trop_matrix u,
+                                           trop_matrix h, trop_matrix y, float* post_mean, float* post_rstd,
+                                           float* pre_mean, float* pre_rstd, const trop_act8* u8,
+                                           const trop_act8* h8, void* stream);
+
+/*
+ * Backward.  With dy and dh the gradients of y and h (the sum of both paths
+ * is taken), x^ = (x - mean) rstd (x rstd for RMS) and the Jacobian of a norm
+ *   N(d, x) = rstd (w - sum_c w / cols - x^ sum_c (w x^) / cols), w = d gamma
+ * (without the first sum for RMS, d itself for none):
+ *   H = dh + N_pre(dy, h)           dr = residual_scale H
+ *   dgate[g] = branch_scale sum of H v over the rows of gate row g
+ *   dv = branch_scale gate H        du = N_post(dv, u)
+ *   dgamma = sum over rows of d x^, dbeta = sum over rows of d
+ * u and h: the forward's, as `dtype` (u, h) or as 8 bits (u8, h8): one of the
+ * two forms for both.  h is needed with a pre norm, u with a post norm or for
+ * dgate.  post_mean ... pre_rstd: the forward's, where a norm has them.
+ * dy: needed with a pre norm, not there without one.  dh: may be left out
+ * with a pre norm.  dr, du, dgate (of gate_dtype, gate_rows x cols) and the
+ * gradients of gamma and beta (param_dtype): each may be NULL (not computed).
+ * With rows == 0 the gradients of gamma and beta are zero.  All sums over rows
+ * are added in a fixed order.
+ * workspace: at least tropical_residual_norm_backward_workspace_size bytes
+ *   (NULL when only dr and du are asked for), used only by work on `stream`.
+ * Errors: as the forward, and TROP_ERR_WORKSPACE_TOO_SMALL.
+ */
+typedef struct {
+    trop_matrix u, h;
+    const trop_act8* u8;
+    const trop_act8* h8;
+    const float* post_mean;
+    const float* post_rstd;
+    const float* pre_mean;
+    const float* pre_rstd;
+    trop_matrix dy, dh;
+} trop_residual_norm_kept;
+
+typedef struct {
+    trop_matrix dr, du, dgate;
+    void* dpost_gamma;
+    void* dpost_beta;
+    void* dpre_gamma;
+    void* dpre_beta;
+} trop_residual_norm_grads;
+
+TROP_API trop_status tropical_residual_norm_backward(const trop_residual_norm* op, const trop_residual_norm_kept* kept,
+                                            const trop_residual_norm_grads* grads, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
+/* Workspace (bytes) of the backward with any of its gradients asked for
+ * (rows, cols, gate, gate_group and the norms of op are looked at; gate only
+ * for whether it is NULL).  Host-only.
+ * Errors: TROP_ERR_INVALID_ARGUMENT (NULL, negative size, bad norm or group). */
+TROP_API trop_status tropical_residual_norm_backward_workspace_size(const trop_residual_norm* op, size_t* bytes);
+
 /* Kernel families of the training operators, counted apart from trop_stats. */
 typedef enum {
     TROP_T_LAYER_NORM_FORWARD = 0,
@@ -698,7 +875,11 @@ typedef enum {
     TROP_T_CE_MERGE = 4,             /* statistics and partial gradients joined */
     TROP_T_CE_GRAD = 5,              /* the gradients' products */
     TROP_T_ADAMW = 6,
-    TROP_T_FAMILIES = 7
+    TROP_T_ACT8 = 7,                 /* activations packed and unpacked */
+    TROP_T_ACT8_GRAD_W = 8,          /* their weight gradient: operands, product, parts joined */
+    TROP_T_RESIDUAL_FORWARD = 9,
+    TROP_T_RESIDUAL_BACKWARD = 10,   /* row gradients and partial column sums, and their sum */
+    TROP_T_FAMILIES = 11
 } trop_train_family;
 
 typedef struct {

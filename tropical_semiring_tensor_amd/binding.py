@@ -9,6 +9,7 @@ built, the first call raises ``TropicalLibraryMissing``.
 Output tensors are allocated with torch when the caller passes none; torch
 is used only for device memory and streams.
 """
+import collections
 import ctypes
 import functools
 import os
@@ -28,7 +29,7 @@ KERNEL_FAMILIES = ["gemm_tiled", "gemm_simple", "fill", "gather_copy", "gather_t
                    "gather_naive", "gather_reduce", "gemm_backward", "gemm_splitk_merge",
                    "argmax_compose", "gemm_domain"]
 TRAIN_FAMILIES = ["layer_norm_forward", "layer_norm_backward", "ce_pack", "ce_logits", "ce_merge", "ce_grad",
-                  "adamw"]
+                  "adamw", "act8", "act8_grad_w", "residual_forward", "residual_backward"]
 MAX_DIMS = 8
 
 
@@ -72,7 +73,36 @@ class trop_adamw_hyper(ctypes.Structure):
 
 class trop_train_stats(ctypes.Structure):
     _fields_ = [("module_loads", ctypes.c_uint64), ("launches_total", ctypes.c_uint64),
-                ("launches", ctypes.c_uint64 * 7)]
+                ("launches", ctypes.c_uint64 * 11)]
+
+
+class trop_act8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("exponents", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("ld_exponents", ctypes.c_int64)]
+
+
+class trop_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class trop_residual_norm(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("dtype", "param_dtype", "gate_dtype", "post", "pre")] +
+                [(n, ctypes.c_float) for n in ("residual_scale", "branch_scale", "post_eps", "pre_eps")] +
+                [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("gate", ctypes.c_void_p),
+                 ("ldgate", ctypes.c_int64), ("gate_group", ctypes.c_int64)] +
+                [(n, ctypes.c_void_p) for n in ("post_gamma", "post_beta", "pre_gamma", "pre_beta")])
+
+
+class trop_residual_norm_kept(ctypes.Structure):
+    _fields_ = ([("u", trop_matrix), ("h", trop_matrix), ("u8", ctypes.POINTER(trop_act8)),
+                 ("h8", ctypes.POINTER(trop_act8))] +
+                [(n, ctypes.c_void_p) for n in ("post_mean", "post_rstd", "pre_mean", "pre_rstd")] +
+                [("dy", trop_matrix), ("dh", trop_matrix)])
+
+
+class trop_residual_norm_grads(ctypes.Structure):
+    _fields_ = ([(n, trop_matrix) for n in ("dr", "du", "dgate")] +
+                [(n, ctypes.c_void_p) for n in ("dpost_gamma", "dpost_beta", "dpre_gamma", "dpre_beta")])
 
 
 _lib = None
@@ -153,11 +183,23 @@ def lib():
     L.tropical_adamw_step.argtypes = [i32, PP(trop_adamw_tensor), i64, PP(trop_adamw_hyper), vp]
     L.tropical_adamw8_step.argtypes = [i32, PP(trop_adamw8_tensor), i64, PP(trop_adamw_hyper), vp]
     L.tropical_adamw8_unpack.argtypes = [PP(trop_adamw8_tensor), i64, PP(vp), PP(vp), vp]
+    L.tropical_act8_pack.argtypes = [i32, vp, i64, PP(trop_act8), i64, i64, vp]
+    L.tropical_act8_unpack.argtypes = [PP(trop_act8), i32, vp, i64, i64, i64, vp]
+    L.tropical_act8_linear_grad_w.argtypes = [i32, vp, i64, PP(trop_act8), vp, i64, i64, i64, i64, vp, sz, vp]
+    L.tropical_act8_linear_grad_w_workspace_size.argtypes = [i32, i64, i64, i64, PP(sz)]
+    L.tropical_residual_norm_forward.argtypes = [PP(trop_residual_norm), trop_matrix, trop_matrix, trop_matrix,
+                                                 trop_matrix, vp, vp, vp, vp, PP(trop_act8), PP(trop_act8), vp]
+    L.tropical_residual_norm_backward.argtypes = [PP(trop_residual_norm), PP(trop_residual_norm_kept),
+                                                  PP(trop_residual_norm_grads), vp, sz, vp]
+    L.tropical_residual_norm_backward_workspace_size.argtypes = [PP(trop_residual_norm), PP(sz)]
     L.tropical_get_train_stats.argtypes = [PP(trop_train_stats)]
     for fn in ("tropical_train_init", "tropical_layer_norm_forward", "tropical_layer_norm_backward_workspace_size",
                "tropical_layer_norm_backward", "tropical_linear_cross_entropy_forward",
                "tropical_linear_cross_entropy_workspace_size", "tropical_linear_cross_entropy_backward",
-               "tropical_adamw_step", "tropical_adamw8_step", "tropical_adamw8_unpack", "tropical_get_train_stats"):
+               "tropical_adamw_step", "tropical_adamw8_step", "tropical_adamw8_unpack", "tropical_act8_pack",
+               "tropical_act8_unpack", "tropical_act8_linear_grad_w", "tropical_act8_linear_grad_w_workspace_size",
+               "tropical_residual_norm_forward", "tropical_residual_norm_backward",
+               "tropical_residual_norm_backward_workspace_size", "tropical_get_train_stats"):
         getattr(L, fn).restype = ctypes.c_int
     _lib = L
     return L
@@ -874,6 +916,304 @@ def tropical_adamw8_unpack(exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_sca
     if st != OK:
         _check(st, "tropical_adamw8_unpack")
     return exp_avg_values, exp_avg_sq_values
+
+
+ACT8_BLOCK = 32  # TROP_ACT8_BLOCK in include/tropical.h
+
+# A matrix held in 8 bits: int8 codes (rows, cols) and uint8 exponents
+# (rows, ceil(cols / ACT8_BLOCK)).
+Act8 = collections.namedtuple("Act8", ["codes", "exponents"])
+
+
+def _act8(a, rows, cols, what):
+    """The C structure of an Act8 of this shape."""
+    codes, exponents = a
+    if codes.dtype != torch.int8 or tuple(codes.shape) != (rows, cols):
+        raise ValueError(f"{what}: codes must be int8 of shape {(rows, cols)}")
+    blocks = (rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK)
+    if exponents.dtype != torch.uint8 or tuple(exponents.shape) != blocks:
+        raise ValueError(f"{what}: exponents must be uint8 of shape {blocks}")
+    return trop_act8(codes.data_ptr(), exponents.data_ptr(), _row_stride(codes, what + " codes"),
+                     _row_stride(exponents, what + " exponents"))
+
+
+def _new_act8(rows, cols, device):
+    return Act8(torch.empty((rows, cols), dtype=torch.int8, device=device),
+                torch.empty((rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK), dtype=torch.uint8, device=device))
+
+
+@_on_stream
+def tropical_act8_pack(x, out=None):
+    """The rows of x (float32 or bfloat16) in 8 bits: an Act8 (allocated when
+    not given).  Each value is off by 1/127 of its block's largest magnitude at
+    most; see include/tropical.h."""
+    dt = _tdt(x, "x")
+    ldx = _row_stride(x, "x")
+    rows, cols = x.shape
+    if out is None:
+        out = _new_act8(rows, cols, x.device)
+    st = lib().tropical_act8_pack(dt, x.data_ptr(), ldx, _act8(out, rows, cols, "out"), rows, cols,
+                                  _stream_ptr(None, x))
+    if st != OK:
+        _check(st, "tropical_act8_pack")
+    return out
+
+
+@_on_stream
+def tropical_act8_unpack(x8, dtype=torch.float32, out=None):
+    """The values of an Act8 as float32 or bfloat16 (exact in both)."""
+    rows, cols = x8[0].shape
+    if out is not None:
+        dtype = out.dtype
+    if dtype not in _TRAIN_DTYPES:
+        raise TypeError(f"out must be float32 or bfloat16, got {dtype}")
+    out, po, ldo = _out_matrix(out, rows, cols, dtype, x8[0].device, "out")
+    st = lib().tropical_act8_unpack(_act8(x8, rows, cols, "x8"), _TRAIN_DTYPES[dtype], po, ldo, rows, cols,
+                                    _stream_ptr(None, out))
+    if st != OK:
+        _check(st, "tropical_act8_unpack")
+    return out
+
+
+def tropical_act8_linear_grad_w_workspace_size(dtype, tokens, cols, out_features):
+    """Workspace bytes of the weight gradient (dtype: torch.float32 or
+    torch.bfloat16)."""
+    if dtype not in _TRAIN_DTYPES:
+        raise TypeError(f"float32 or bfloat16 only, got {dtype}")
+    nb = ctypes.c_size_t(0)
+    _check(lib().tropical_act8_linear_grad_w_workspace_size(_TRAIN_DTYPES[dtype], int(tokens), int(cols),
+                                                            int(out_features), ctypes.byref(nb)),
+           "tropical_act8_linear_grad_w_workspace_size")
+    return nb.value
+
+
+@_on_stream
+def tropical_act8_linear_grad_w(dz, x8, grad_w=None, workspace=None):
+    """dz.T @ x for a linear layer's input held in 8 bits.
+
+    dz (tokens, out_features): float32 or bfloat16, unit stride along the
+    rows.  x8: Act8 of (tokens, cols).  grad_w (out_features, cols) has dz's
+    type; it and the workspace are allocated with torch when not given.
+    """
+    dt = _tdt(dz, "dz")
+    lddz = _row_stride(dz, "dz")
+    tokens, outs = dz.shape
+    if x8[0].dim() != 2 or x8[0].shape[0] != tokens:
+        raise ValueError(f"x8 must have dz's {tokens} rows")
+    cols = x8[0].shape[1]
+    x = _act8(x8, tokens, cols, "x8")
+    grad_w, pw, ldw = _out_matrix(grad_w, outs, cols, dz.dtype, dz.device, "grad_w")
+    need = 0
+    if workspace is None:
+        need = tropical_act8_linear_grad_w_workspace_size(dz.dtype, tokens, cols, outs)
+    workspace, wp, wn = _workspace(workspace, need, dz.device)
+    st = lib().tropical_act8_linear_grad_w(dt, dz.data_ptr(), lddz, x, pw, ldw, tokens, cols, outs, wp, wn,
+                                           _stream_ptr(None, dz))
+    if st != OK:
+        _check(st, "tropical_act8_linear_grad_w")
+    return grad_w
+
+
+_NORMS = {None: 0, "layer": 1, "rms": 2}
+
+ResidualNorm = collections.namedtuple("ResidualNorm", ["h", "y", "post_mean", "post_rstd", "pre_mean", "pre_rstd",
+                                                       "u8", "h8"])
+ResidualNormGrads = collections.namedtuple("ResidualNormGrads", ["r", "u", "gate", "post_gamma", "post_beta",
+                                                                 "pre_gamma", "pre_beta"])
+
+
+def _residual_op(dt, dtype, rows, cols, gate, gate_group, post, post_gamma, post_beta, post_eps, pre, pre_gamma,
+                 pre_beta, pre_eps, residual_scale, branch_scale):
+    """(C structure, weights' type, gate rows)."""
+    if post not in _NORMS or pre not in _NORMS:
+        raise ValueError("norms are None, 'layer' or 'rms'")
+    op = trop_residual_norm(dt, F32, F32, _NORMS[post], _NORMS[pre], residual_scale, branch_scale, post_eps, pre_eps,
+                            rows, cols)
+    ptype = None
+    for there, name, w in ((post, "post_gamma", post_gamma), (post, "post_beta", post_beta),
+                           (pre, "pre_gamma", pre_gamma), (pre, "pre_beta", pre_beta)):
+        if w is None:
+            continue
+        if there is None:
+            raise ValueError(f"{name} without its norm")
+        if ptype is None:
+            ptype = w.dtype
+            op.param_dtype = _tdt(w, "gamma and beta")
+        setattr(op, name, _flat(w, name, cols, ptype))
+    gates = 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate[None]
+            gate_group = max(rows, 1)
+        op.gate_dtype = _tdt(gate, "gate")
+        gates = gate.shape[0]
+        if gate_group is None:
+            gate_group = rows // gates if gates else 1
+            if gates * gate_group != rows:
+                raise ValueError(f"{gates} gate rows do not divide {rows} rows: give gate_group")
+        if gate_group < 1 or gate.shape[1] != cols or (rows and gates != -(-rows // gate_group)):
+            raise ValueError(f"gate must have a row of {cols} for each {gate_group} of {rows} rows")
+        op.gate = gate.data_ptr()
+        op.ldgate = _row_stride(gate, "gate")
+        op.gate_group = gate_group
+    return op, ptype or torch.float32, gates
+
+
+@_on_stream
+def tropical_residual_norm_forward(u, r=None, gate=None, post=None, post_gamma=None, post_beta=None, post_eps=1e-5,
+                                   pre="layer", pre_gamma=None, pre_beta=None, pre_eps=1e-5, residual_scale=1.0,
+                                   branch_scale=1.0, gate_group=None, h=True, y=True, hold_u=False, hold_h=False):
+    """Between two residual blocks, in one pass:
+
+        h = residual_scale r + branch_scale gate post_norm(u),  y = pre_norm(h)
+
+    u (rows, cols), the block's output, and r, its input (None: left out):
+    float32 or bfloat16, unit stride along the rows.  post, pre: None, 'layer'
+    or 'rms', with weights of cols elements (float32 or u's type) or None.
+    gate: cols elements for all rows, or (gates, cols) with a gate row for each
+    gate_group consecutive rows (rows / gates when not given), float32 or u's
+    type.  h, y: True to allocate, a tensor to fill (h may be r), None to skip.
+    hold_u, hold_h: also leave u and h in 8 bits (True, or an Act8 to fill).
+    Returns a ResidualNorm; what there is none of is None.
+    """
+    dt = _tdt(u, "u")
+    ldu = _row_stride(u, "u")
+    rows, cols = u.shape
+    dev, f32 = u.device, torch.float32
+    op, _, _ = _residual_op(dt, u.dtype, rows, cols, gate, gate_group, post, post_gamma, post_beta, post_eps, pre,
+                            pre_gamma, pre_beta, pre_eps, residual_scale, branch_scale)
+    none = trop_matrix(None, 0)
+    mr = mh = my = none
+    if r is not None:
+        if r.shape != u.shape or r.dtype != u.dtype:
+            raise ValueError("r must have the shape and type of u")
+        mr = trop_matrix(r.data_ptr(), _row_stride(r, "r"))
+    if h is not None:
+        h, ph, ldh = _out_matrix(h, rows, cols, u.dtype, dev, "h")
+        mh = trop_matrix(ph, ldh)
+    if pre is None:
+        if y is not None and y is not True:
+            raise ValueError("y without a norm before the next block")
+        y = None
+    if y is not None:
+        y, py, ldy = _out_matrix(y, rows, cols, u.dtype, dev, "y")
+        my = trop_matrix(py, ldy)
+    stats, ptrs = [], []
+    for norm in (post, pre):
+        for there in (norm == "layer", norm is not None):
+            t = torch.empty(rows, dtype=f32, device=dev) if there else None
+            stats.append(t)
+            ptrs.append(t.data_ptr() if there else None)
+    held, keep = [], []
+    for x, what in ((hold_u, "hold_u"), (hold_h, "hold_h")):
+        x = _new_act8(rows, cols, dev) if x is True else x or None
+        held.append(x)
+        keep.append(_act8(x, rows, cols, what) if x is not None else None)
+    st = lib().tropical_residual_norm_forward(op, mr, trop_matrix(u.data_ptr(), ldu), mh, my, *ptrs, *keep,
+                                              _stream_ptr(None, u))
+    if st != OK:
+        _check(st, "tropical_residual_norm_forward")
+    return ResidualNorm(h, y, *stats, *held)
+
+
+@_on_stream
+def tropical_residual_norm_backward(dy, dh, u, h, post_mean=None, post_rstd=None, pre_mean=None, pre_rstd=None,
+                                    gate=None, post=None, post_gamma=None, post_beta=None, post_eps=1e-5, pre="layer",
+                                    pre_gamma=None, pre_beta=None, pre_eps=1e-5, residual_scale=1.0, branch_scale=1.0,
+                                    gate_group=None, dr=True, du=True, dgate=True, dpost_gamma=True, dpost_beta=True,
+                                    dpre_gamma=True, dpre_beta=True, workspace=None):
+    """Gradients of tropical_residual_norm_forward, from dy and dh, those of y
+    and h (dy is None without a pre norm; dh may be None with one).
+
+    u, h: the forward's, both as they were (u's type) or both held in 8 bits
+    (Act8), each None where it is not needed.  The statistics, weights, gate
+    and scales are the forward's.  dr, du: True to allocate, a tensor to fill,
+    None to skip; the others likewise, True meaning where the forward had that
+    weight or gate.  The workspace is allocated with torch when not given.
+    Returns a ResidualNormGrads.
+    """
+    lead = dy if dy is not None else dh
+    if lead is None:
+        raise ValueError("neither dy nor dh")
+    dt = _tdt(lead, "dy and dh")
+    rows, cols = lead.shape
+    dtype, dev = lead.dtype, lead.device
+    op, ptype, gates = _residual_op(dt, dtype, rows, cols, gate, gate_group, post, post_gamma, post_beta, post_eps, pre,
+                                    pre_gamma, pre_beta, pre_eps, residual_scale, branch_scale)
+    kept, grads = trop_residual_norm_kept(), trop_residual_norm_grads()
+    alive = []
+
+    def matrix(t, what):
+        if t.shape != lead.shape or t.dtype != dtype:
+            raise ValueError(f"{what} must be {dtype} of shape {(rows, cols)}")
+        return trop_matrix(t.data_ptr(), _row_stride(t, what))
+
+    if dy is not None:
+        kept.dy = matrix(dy, "dy")
+    if dh is not None:
+        kept.dh = matrix(dh, "dh")
+    for name, t in (("u", u), ("h", h)):
+        if isinstance(t, torch.Tensor):
+            setattr(kept, name, matrix(t, name))
+        elif t is not None:
+            alive.append(_act8(t, rows, cols, name))
+            setattr(kept, name + "8", ctypes.pointer(alive[-1]))
+    for name, t in (("post_mean", post_mean), ("post_rstd", post_rstd), ("pre_mean", pre_mean), ("pre_rstd", pre_rstd)):
+        if t is not None:
+            setattr(kept, name, _flat(t, name, rows, torch.float32))
+    if dr is not None:
+        dr, p, ld = _out_matrix(dr, rows, cols, dtype, dev, "dr")
+        grads.dr = trop_matrix(p, ld)
+    if du is not None:
+        du, p, ld = _out_matrix(du, rows, cols, dtype, dev, "du")
+        grads.du = trop_matrix(p, ld)
+    if dgate is True and gate is None:
+        dgate = None
+    given = dgate
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate without a gate")
+        flat = gate.dim() == 1
+        if dgate is True:
+            dgate = given = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
+        elif dgate.shape != gate.shape:
+            raise ValueError("dgate must have the gate's shape")
+        dgate, p, ld = _out_matrix(dgate[None] if flat else dgate, gates, cols, gate.dtype, dev, "dgate")
+        grads.dgate = trop_matrix(p, ld)
+    weights = []
+    for name, g, w in (("dpost_gamma", dpost_gamma, post_gamma), ("dpost_beta", dpost_beta, post_beta),
+                       ("dpre_gamma", dpre_gamma, pre_gamma), ("dpre_beta", dpre_beta, pre_beta)):
+        if g is True and w is None:
+            g = None
+        if g is not None:
+            g, p = _out_flat(g, cols, ptype, dev, name)
+            setattr(grads, name, p)
+        weights.append(g)
+    need = 0
+    if workspace is None and (dgate is not None or any(w is not None for w in weights)):
+        need = _residual_workspace(op)
+    workspace, wp, wn = _workspace(workspace, need, dev)
+    st = lib().tropical_residual_norm_backward(op, kept, grads, wp, wn, _stream_ptr(None, lead))
+    if st != OK:
+        _check(st, "tropical_residual_norm_backward")
+    return ResidualNormGrads(dr, du, given, *weights)
+
+
+def _residual_workspace(op):
+    nb = ctypes.c_size_t(0)
+    _check(lib().tropical_residual_norm_backward_workspace_size(op, ctypes.byref(nb)),
+           "tropical_residual_norm_backward_workspace_size")
+    return nb.value
+
+
+def tropical_residual_norm_backward_workspace_size(rows, cols, post=None, pre="layer", gate_group=None):
+    """Workspace bytes of a backward (gate_group: None without a gate)."""
+    if post not in _NORMS or pre not in _NORMS:
+        raise ValueError("norms are None, 'layer' or 'rms'")
+    op = trop_residual_norm(post=_NORMS[post], pre=_NORMS[pre], rows=int(rows), cols=int(cols))
+    if gate_group is not None:
+        op.gate, op.gate_group = 1, int(gate_group)
+    return _residual_workspace(op)
 
 
 def tropical_get_train_stats():

@@ -34,7 +34,7 @@ HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-We
               "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]
 RUNTIME_SRCS = ["status.cpp", "module.cpp", "validate.cpp", "gemm.cpp", "gather.cpp", "contract.cpp",
                 "backward.cpp", "tree.cpp", "train_module.cpp", "layer_norm.cpp", "adamw.cpp",
-                "cross_entropy.cpp"]
+                "cross_entropy.cpp", "act8.cpp", "residual_norm.cpp"]
 # host runtime sources with device data (compiled by hipcc, gfx950 only)
 RUNTIME_HIP_SRCS = ["noalloc.hip"]
 

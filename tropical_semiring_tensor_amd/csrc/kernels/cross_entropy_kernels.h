@@ -282,21 +282,6 @@ __device__ __forceinline__ void ce_pack_body(const TropCeParams& p) {
 }
 
 // ---- tiles -----------------------------------------------------------------
-// Workgroup -> tile of an active tm x tn grid (false: none).  Each XCD (a
-// workgroup's id modulo 8) takes a consecutive range of the tiles, which run
-// down groups of 8 tile rows, so the tiles that an XCD works on at a time
-// share operand panels in its L2.
-__device__ __forceinline__ bool ce_tile(int64_t id, int64_t tm, int64_t tn, int64_t& mi, int64_t& ni) {
-    const int64_t total = tm * tn, per = total / 8, rest = total % 8;
-    const int64_t xcd = id % 8, k = id / 8;
-    if (k >= per + (xcd < rest ? 1 : 0)) return false;
-    const int64_t t = xcd * per + min(xcd, rest) + k;
-    const int64_t group = t / (8 * tn), in = t - group * 8 * tn, rows = min((int64_t)8, tm - group * 8);
-    mi = group * 8 + in % rows;
-    ni = in / rows;
-    return true;
-}
-
 // The label matrix's rows from piece row r0 on as a KM operand (along the width).
 template <typename C>
 __device__ __forceinline__ MgOperand ce_w_rows(const TropCeParams& p, int64_t r0) {
@@ -331,7 +316,7 @@ template <typename C, CeEpilogue EPI>
 __device__ __forceinline__ void ce_logits_body(const TropCeParams& p, char* lds) {
     const int64_t kept = p.control->kept;
     int64_t mi, ni;
-    if (!ce_tile(blockIdx.x, p.piece / C::BM, (kept + C::BN - 1) / C::BN, mi, ni)) return;
+    if (!mg_tile(blockIdx.x, p.piece / C::BM, (kept + C::BN - 1) / C::BN, mi, ni)) return;
     MgOperand b;
     b.ld = p.width_p * C::PLANES;
     b.base = static_cast<const char*>(p.xp) + ni * C::BN * b.ld * 2;
@@ -493,7 +478,7 @@ __device__ __forceinline__ void ce_grad_x_body(const TropCeParams& p, int64_t id
     const int64_t kept = p.control->kept;
     const int64_t tm = (kept + C::BN - 1) / C::BN, tn = (p.width + C::BM - 1) / C::BM;
     int64_t mi, q;
-    if (!ce_tile(id, tm, tn * p.splits, mi, q)) return;
+    if (!mg_tile(id, tm, tn * p.splits, mi, q)) return;
     const int64_t ni = q % tn, split = q / tn;
     // (k tiles that hold a label: a part past them is empty, its sums zero)
     const int64_t ktiles = (min(p.piece, p.vocab - p.v0) + C::KT - 1) / C::KT;
@@ -589,7 +574,7 @@ __device__ __forceinline__ void ce_grad_w_body(const TropCeParams& p, int64_t id
     const int64_t kept = p.control->kept;
     const int64_t tn = (p.width + C::BM - 1) / C::BM;
     int64_t mi, q;
-    if (!ce_tile(id, (min(p.piece, p.vocab - p.v0) + C::BN - 1) / C::BN, tn * p.gw_splits, mi, q)) return;
+    if (!mg_tile(id, (min(p.piece, p.vocab - p.v0) + C::BN - 1) / C::BN, tn * p.gw_splits, mi, q)) return;
     const int64_t ni = q % tn, split = q / tn;
     const int64_t ktiles = (kept + C::KT - 1) / C::KT, per = (ktiles + p.gw_splits - 1) / p.gw_splits;
     const int64_t kt0 = min(split * per, ktiles), kt1 = min(kt0 + per, ktiles), k0 = kt0 * C::KT;

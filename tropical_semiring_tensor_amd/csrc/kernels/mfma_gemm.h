@@ -1,6 +1,6 @@
 // Matrix products on the matrix cores: C[i][j] = sum_k A(i, k) B(j, k) with
 // 16-bit operands and float32 sums, the tile loop shared by the linear cross
-// entropy's kernels.
+// entropy's kernels and the weight gradient from 8-bit activations.
 //
 // A workgroup of WM x WN waves computes a BM x BN tile; a wave computes
 // (BM / WM) x (BN / WN) of it in 16 x 16 blocks (v_mfma_f32_16x16x32).  K is
@@ -343,8 +343,11 @@ __device__ __forceinline__ f32x4 mg_mfma(s16x8 a, s16x8 b, f32x4 c) {
 // matrix units busy 62% of the cycles (1440 and 70% without the split).
 // (A large library product on the same card: 1430-1470 in bfloat16, 153 in
 // float32.)
-template <int BM_, int BN_, int WM_, int WN_, OperandKind KA_, OperandKind KB_, int PLANES_, int STAGES_ = 2>
+// REPEAT: each k tile of A meets that many of B in turn (B's values in parts).
+template <int BM_, int BN_, int WM_, int WN_, OperandKind KA_, OperandKind KB_, int PLANES_, int STAGES_ = 2,
+          int REPEAT_ = 1>
 struct MgConfig {
+    static constexpr int REPEAT = REPEAT_;
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, PLANES = PLANES_;
     static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
     static constexpr int STAGES = STAGES_;  // buffers
@@ -367,6 +370,21 @@ __device__ __forceinline__ void mg_multiply(f32x4 (&acc)[C::FM][C::FN], const s1
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) acc[i][j] = mg_mfma<C::PLANES>(a[i], b[j], acc[i][j]);
+}
+
+// Workgroup -> tile of an active tm x tn grid (false: none).  Each XCD (a
+// workgroup's id modulo 8) takes a consecutive range of the tiles, which run
+// down groups of 8 tile rows, so the tiles that an XCD works on at a time
+// share operand panels in its L2.
+__device__ __forceinline__ bool mg_tile(int64_t id, int64_t tm, int64_t tn, int64_t& mi, int64_t& ni) {
+    const int64_t total = tm * tn, per = total / 8, rest = total % 8;
+    const int64_t xcd = id % 8, k = id / 8;
+    if (k >= per + (xcd < rest ? 1 : 0)) return false;
+    const int64_t t = xcd * per + min(xcd, rest) + k;
+    const int64_t group = t / (8 * tn), in = t - group * 8 * tn, rows = min((int64_t)8, tm - group * 8);
+    mi = group * 8 + in % rows;
+    ni = in / rows;
+    return true;
 }
 
 // Walks the first `ktiles` k tiles of both operands, each of which starts
@@ -417,9 +435,9 @@ __device__ __forceinline__ void mg_walk(f32x4 (&acc)[C::FM][C::FN], const MgOper
     auto load_next = [&](int buf) {
         C::TA::load(a, pa, kt, lds0 + buf * C::STAGE, wave, lane, aoff);
         C::TB::load(b, pb, kt, lds0 + buf * C::STAGE + C::TA::BYTES, wave, lane, boff);
-        pa += a.k_bytes;
-        pb += b.k_bytes;
         ++kt;
+        if (C::REPEAT == 1 || kt % C::REPEAT == 0) pa += a.k_bytes;
+        pb += b.k_bytes;
     };
     if constexpr (C::WAVES == 8) {
         s16x8 fa[2][C::FM], fb[2][C::FN];

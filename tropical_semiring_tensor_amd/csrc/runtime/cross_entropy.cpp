@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <string>
 
+#include "product_tiles.h"
 #include "train.h"
 
 namespace trop {
@@ -15,8 +16,6 @@ constexpr int64_t kMaxTokens = 1 << 22, kMaxWidth = 1 << 22;  // 32-bit offsets 
 constexpr int64_t kLargeElements = 10 << 20;  // of a w that few tokens' tiles read as it lies
 constexpr int64_t kTileElements = 16 << 20;  // of a bfloat16 w for 33 to 64 tokens' logits in tiles
 constexpr int64_t kMaxVocab = ((int64_t)1 << 31) - 512;       // label indices are 32-bit
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 // A piece's labels when a label takes `bytes` of a kPieceBytes buffer: equal
 // pieces, multiples of 256.
@@ -24,30 +23,6 @@ int64_t piece_labels(int64_t vocab, int64_t bytes) {
     int64_t most = kPieceBytes / bytes / 256 * 256;
     if (most < 256) most = 256;
     return round_up(ceil_div(vocab, ceil_div(vocab, most)), 256);
-}
-
-// A tile's time (us) over `k` tiles of 64 along k, and how many run at once,
-// in a launch of `tiles` (kind 0: 256 x 256, 1: 128 x 128, 2: 64 x 64).
-// Measured on one MI355X (256 CUs): a 256 x 256 workgroup has a CU to itself
-// and takes 1.75 us a k tile; a 128 x 128 one 0.7 us alone on a CU, 1.15
-// beside another; a 64 x 64 one 0.3 us alone, 0.5 with two and 0.85 with
-// four on a CU; a tile costs 6, 5 or 4 us besides (first loads, epilogue).
-// A k tile of 32 of float32's two planes takes 1.25 of these (in the
-// gradients, which also split G, 1.35: alike for every tile, and left out).
-struct TileRate {
-    double us;
-    int64_t slots;
-};
-TileRate tile_rate(int kind, int64_t tiles, double k) {
-    if (kind == 0) return {k * 1.75 + 6.0, 256};
-    if (kind == 1) return tiles <= 256 ? TileRate{k * 0.7 + 5.0, 256} : TileRate{k * 1.15 + 5.0, 512};
-    return tiles <= 256   ? TileRate{k * 0.3 + 4.0, 256}
-           : tiles <= 512 ? TileRate{k * 0.5 + 4.0, 512}
-                          : TileRate{k * 0.85 + 4.0, 1024};
-}
-double tile_time(int kind, int64_t tiles, double k) {
-    const TileRate r = tile_rate(kind, tiles, k);
-    return (double)ceil_div(tiles, r.slots) * r.us;
 }
 
 // Time of `tx` tiles over kx, then `tw` over kw in one launch: a slot that
@@ -78,9 +53,6 @@ double logits_time(int kind, int64_t tiles, double k) {
     if (kind == 1) return (double)ceil_div(tiles, 512) * (k * 1.15 + 5.0);
     return tile_time(kind, tiles, k);
 }
-
-int64_t tile_edge(int tile) { return tile == 3 ? 128 : 256 >> tile; }
-uint32_t tile_threads(int tile) { return tile == 0 ? 512 : 256; }
 
 // The gradients of `tokens` x `labels` of G: tile and parts along k with the
 // least time.  kx, kw: k tiles (`unit` of a tile_rate's each).  A part's sums

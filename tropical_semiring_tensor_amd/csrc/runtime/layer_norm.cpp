@@ -8,14 +8,6 @@
 namespace trop {
 namespace {
 
-// 0: f32 f32, 1: bf16 bf16, 2: bf16 f32, -1: none
-int ln_index(trop_dtype dt, trop_dtype pdt) {
-    if (dt == TROP_F32 && pdt == TROP_F32) return 0;
-    if (dt == TROP_BF16 && pdt == TROP_BF16) return 1;
-    if (dt == TROP_BF16 && pdt == TROP_F32) return 2;
-    return -1;
-}
-
 trop_status check_types(trop_dtype dt, trop_dtype pdt, int64_t rows, int64_t cols) {
     if (dt != TROP_F32 && dt != TROP_BF16)
         return fail(TROP_ERR_INVALID_ARGUMENT, "layer norm takes float32 or bfloat16, got dtype " + std::to_string((int)dt));

@@ -42,7 +42,23 @@ enum TrainKernelId : int {
     TK_CE_FEW_GRAD = TK_CE_FEW + 12,   // G; likewise, without bf16 for 4 blocks
     TK_CE_FEW_GX = TK_CE_FEW_GRAD + 10,  // the gradients: without label blocks
     TK_CE_FEW_GW = TK_CE_FEW_GX + 5,
-    TK_COUNT = TK_CE_FEW_GW + 5
+    TK_ACT8_PACK = TK_CE_FEW_GW + 5,  // + (bf16 ? 1 : 0), to TK_GRAD_W
+    TK_ACT8_UNPACK = TK_ACT8_PACK + 2,
+    TK_GRAD_W_PACK = TK_ACT8_UNPACK + 2,
+    TK_GRAD_W_FINISH = TK_GRAD_W_PACK + 2,
+    TK_PART_SUMS = TK_GRAD_W_FINISH + 2,
+    TK_GRAD_W = TK_PART_SUMS + 2,      // + 2 tile (256, 128, 64)
+    TK_RN_FWD_WAVE = TK_GRAD_W + 6,    // + ln_index
+    TK_RN_FWD_BLOCK = TK_RN_FWD_WAVE + 3,
+    TK_RN_FWD_WIDE = TK_RN_FWD_BLOCK + 3,
+    TK_RN_FWD_LOOP = TK_RN_FWD_WIDE + 3,
+    TK_RN_BWD_WAVE = TK_RN_FWD_LOOP + 3,  // + ln_index + 3 (u and h in 8 bits)
+    TK_RN_BWD_BLOCK = TK_RN_BWD_WAVE + 6,
+    TK_RN_BWD_HALF = TK_RN_BWD_BLOCK + 6,
+    TK_RN_BWD_WIDE = TK_RN_BWD_HALF + 6,
+    TK_RN_BWD_LOOP = TK_RN_BWD_WIDE + 6,
+    TK_RN_COLUMNS = TK_RN_BWD_LOOP + 6,
+    TK_COUNT = TK_RN_COLUMNS + 6
 };
 
 // Current device with the training code object loaded on it.
@@ -52,6 +68,15 @@ trop_status train_launch(int dev, TrainKernelId id, trop_train_family fam, int64
 // Workgroups of `block` threads that one launch may have.
 inline int64_t max_groups(uint32_t block) { return 0xffffffffLL / block; }
 void reset_train_launches();
+
+// A norm's kernels by the rows' and the weights' type: 0: f32 f32, 1: bf16
+// bf16, 2: bf16 f32, -1: none
+inline int ln_index(trop_dtype dt, trop_dtype pdt) {
+    if (dt == TROP_F32 && pdt == TROP_F32) return 0;
+    if (dt == TROP_BF16 && pdt == TROP_BF16) return 1;
+    if (dt == TROP_BF16 && pdt == TROP_F32) return 2;
+    return -1;
+}
 
 inline size_t elem_size(trop_dtype dt) { return dt == TROP_BF16 ? 2 : 4; }
 
@@ -70,6 +95,9 @@ class SpanChecker {
     int dev_;
     uintptr_t lo_ = 1, hi_ = 0;
 };
+
+// Both buffers of an 8-bit rows x cols matrix.
+trop_status check_act8(SpanChecker& checker, const trop_act8& a, int64_t rows, int64_t cols, const char* what);
 
 // A C entry point's body: no C++ exception leaves the library.
 template <typename F>

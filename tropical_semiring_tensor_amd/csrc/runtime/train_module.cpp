@@ -64,6 +64,25 @@ const char* const kNames[] = {
     "trop_ce_few_gx_n2_bf16", "trop_ce_few_gx_n4_f32",
     "trop_ce_few_gw_n1_f32", "trop_ce_few_gw_n1_bf16", "trop_ce_few_gw_n2_f32",
     "trop_ce_few_gw_n2_bf16", "trop_ce_few_gw_n4_f32",
+    "trop_act8_pack_f32", "trop_act8_pack_bf16",
+    "trop_act8_unpack_f32", "trop_act8_unpack_bf16",
+    "trop_grad_w_pack_f32", "trop_grad_w_pack_bf16",
+    "trop_grad_w_finish_f32", "trop_grad_w_finish_bf16",
+    "trop_part_sums_f32", "trop_part_sums_bf16",
+    "trop_grad_w256_f32", "trop_grad_w256_bf16",
+    "trop_grad_w128_f32", "trop_grad_w128_bf16",
+    "trop_grad_w64_f32", "trop_grad_w64_bf16",
+#define TROP_RN_TYPES(KERNEL, HELD) \
+    "trop_rn_" KERNEL "_f32_f32" HELD, "trop_rn_" KERNEL "_bf16_bf16" HELD, "trop_rn_" KERNEL "_bf16_f32" HELD,
+    TROP_RN_TYPES("fwd_wave", "") TROP_RN_TYPES("fwd_block", "")
+    TROP_RN_TYPES("fwd_wide", "") TROP_RN_TYPES("fwd_loop", "")
+    TROP_RN_TYPES("bwd_wave", "") TROP_RN_TYPES("bwd_wave", "_held8")
+    TROP_RN_TYPES("bwd_block", "") TROP_RN_TYPES("bwd_block", "_held8")
+    TROP_RN_TYPES("bwd_half", "") TROP_RN_TYPES("bwd_half", "_held8")
+    TROP_RN_TYPES("bwd_wide", "") TROP_RN_TYPES("bwd_wide", "_held8")
+    TROP_RN_TYPES("bwd_loop", "") TROP_RN_TYPES("bwd_loop", "_held8")
+    TROP_RN_TYPES("columns", "") TROP_RN_TYPES("columns", "_held8")
+#undef TROP_RN_TYPES
 };
 static_assert(sizeof(kNames) / sizeof(kNames[0]) == TK_COUNT, "training kernels");
 

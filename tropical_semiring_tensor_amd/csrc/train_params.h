@@ -88,6 +88,106 @@ struct TropAdamw8Params {
     TropAdamw8Entry t[TROP_ADAMW8_TENSORS];
 };
 
+// ---- activations in 8 bits --------------------------------------------------
+// Elements of a row that share an exponent; elements of a wave's chunk of a row.
+#define TROP_ACT8_BLOCK_ELEMS 32
+#define TROP_ACT8_CHUNK 1024
+
+struct TropAct8Params {
+    const void* x;        // packing: the rows; unpacking: written
+    int8_t* codes;
+    uint8_t* exps;
+    int64_t ldx, ldc, lde;
+    int64_t rows, cols;   // of the codes
+    int64_t rows_x, cols_x;  // unpacking: of the rows (zeros past the codes)
+    int64_t chunks;       // of a row
+    int64_t chunk0;       // the launch's first chunk
+    int64_t total;        // chunks in all
+};
+
+// Operands of the weight gradient, then its product: piece [c0, c0 + cols) x
+// [o0, o0 + outs) of the gradient.
+struct TropGradWParams {
+    TropAct8Params x;     // unpacked into xp
+    const void* dz;       // at the piece's first output feature
+    void* grad_w;         // at the piece's first element
+    void* xp;             // [tokens_p][cols_p] bfloat16
+    void* dzp;            // packed dz: [tokens_p / 64][parts][64][outs_p] bfloat16, or null: dz as it lies
+    float* part;          // [splits][outs][cols_p], when splits > 1
+    int64_t lddz, ldgw;
+    int64_t tokens, tokens_p, cols, cols_p, outs, outs_p;
+    int64_t id0;          // finishing: the launch's first workgroup
+    uint32_t x_groups;    // packing: workgroups that unpack x, before those that pack dz
+    int32_t splits;
+};
+
+// ---- between two residual blocks ---------------------------------------------
+// Columns a wave / 256 / 512 / 1024 threads of the backward hold (8 each).
+#define TROP_RN_COLS_WAVE 512
+#define TROP_RN_COLS_BLOCK 2048
+#define TROP_RN_COLS_HALF 4096
+#define TROP_RN_COLS_WIDE 8192
+// Partial column sums a backward call makes at most.
+#define TROP_RN_MAX_PARTS 512
+// Column sums: gradients of the pre norm's weights, the post norm's, the gate.
+enum { TROP_RN_PRE_GAMMA, TROP_RN_PRE_BETA, TROP_RN_POST_GAMMA, TROP_RN_POST_BETA, TROP_RN_GATE, TROP_RN_SUMS };
+
+struct TropResidualParams {
+    const void* r;          // forward, may be null
+    const void* u;
+    const void* gate;       // may be null
+    const void* post_gamma; // may be null
+    const void* post_beta;
+    const void* pre_gamma;
+    const void* pre_beta;
+    const void* dy;         // backward
+    const void* dh;
+    void* h;                // forward: written, may be null; backward: read
+    void* y;
+    void* dr;
+    void* du;
+    void* dgate;            // gate rows that a part takes whole are written here
+    float* post_mean;
+    float* post_rstd;
+    float* pre_mean;
+    float* pre_rstd;
+    int8_t* u_codes;        // forward: written, may be null; backward: read
+    uint8_t* u_exps;
+    int8_t* h_codes;
+    uint8_t* h_exps;
+    float* part[TROP_RN_SUMS];  // backward: [parts][cols] each, null where not asked for
+    float* row_sums;        // backward of wide rows: [rows][2], the pre norm's two means
+    int64_t ldr, ldu, ldgate, lddy, lddh, ldh, ldy, lddr, lddu, lddgate, ldu_codes, ldu_exps, ldh_codes, ldh_exps;
+    int64_t rows, cols;
+    int64_t row0;           // the launch's first row
+    int64_t col0;           // wide rows' column sums: the launch's first column
+    int64_t gate_group;     // rows of a gate row (rows or more: one gate row)
+    int64_t part_rows;      // backward: rows of a part
+    int64_t group_parts;    // backward: parts of a gate row, or 0: a part takes whole gate rows
+    float residual_scale, branch_scale, post_eps, pre_eps, inv_cols;
+    int32_t post, pre;      // trop_norm
+    int32_t gate_f32;
+    int32_t parts;
+    int32_t need_v, need_post;  // backward: the gate's gradient; the post norm's gradients or du through it
+};
+
+// Partial sums of up to TROP_RN_SUMS column sums: entry i has `rows[i]` output
+// rows, each the sum of `parts` consecutive rows of src.
+struct TropRowSumsEntry {
+    const float* src;
+    void* dst;
+    int64_t ldd, rows, parts;
+    uint32_t blocks;        // workgroups of this entry and all before it
+    int32_t f32;
+    float scale;
+    int32_t pad_;
+};
+struct TropRowSumsParams {
+    TropRowSumsEntry e[TROP_RN_SUMS];
+    int64_t cols, id0;      // id0: the launch's first workgroup
+    int32_t count, pad_;
+};
+
 // ---- linear cross entropy --------------------------------------------------
 // Tokens up to this many may take the streaming kernels (no packing).
 #define TROP_CE_FEW 64
