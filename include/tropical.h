@@ -497,7 +497,7 @@ TROP_API trop_status tropical_tree_describe(trop_tree_plan plan, char* buf, size
  * >= the row's length (in elements); every element alignment is served.
  * Outputs must not overlap inputs or each other unless stated.  No kernel
  * uses atomics: a call gives the same bits every time on one device model.
- * Their kernels are a code object of their own, loaded once per device by
+ * Their kernels are code objects of their own, loaded once per device by
  * the first such call (or tropical_train_init, which code that captures
  * graphs calls beforehand).
  */
@@ -811,10 +811,18 @@ typedef struct {
  * rounded to dtype), either may be NULL.
  * Errors: TROP_ERR_INVALID_ARGUMENT, TROP_ERR_NOT_DEVICE_MEMORY, TROP_ERR_HIP.
  */
-TROP_API trop_status tropical_residual_norm_forward(const trop_residual_norm* op, trop_matrix r, trop_matrix u,
-                                           trop_matrix h, trop_matrix y, float* post_mean, float* post_rstd,
-                                           float* pre_mean, float* pre_rstd, const trop_act8* u8,
-                                           const trop_act8* h8, void* stream);
+typedef struct {
+    trop_matrix r, u, h, y;
+    float* post_mean;
+    float* post_rstd;
+    float* pre_mean;
+    float* pre_rstd;
+    const trop_act8* u8;
+    const trop_act8* h8;
+} trop_residual_norm_rows;
+
+TROP_API trop_status tropical_residual_norm_forward(const trop_residual_norm* op, const trop_residual_norm_rows* rows,
+                                           void* stream);
 
 /*
  * Backward.  With dy and dh the gradients of y and h (the sum of both paths

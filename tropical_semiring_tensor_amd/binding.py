@@ -81,10 +81,6 @@ class trop_act8(ctypes.Structure):
                 ("ld_exponents", ctypes.c_int64)]
 
 
-class trop_matrix(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64)]
-
-
 class trop_residual_norm(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int) for n in ("dtype", "param_dtype", "gate_dtype", "post", "pre")] +
                 [(n, ctypes.c_float) for n in ("residual_scale", "branch_scale", "post_eps", "pre_eps")] +
@@ -93,16 +89,9 @@ class trop_residual_norm(ctypes.Structure):
                 [(n, ctypes.c_void_p) for n in ("post_gamma", "post_beta", "pre_gamma", "pre_beta")])
 
 
-class trop_residual_norm_kept(ctypes.Structure):
-    _fields_ = ([("u", trop_matrix), ("h", trop_matrix), ("u8", ctypes.POINTER(trop_act8)),
-                 ("h8", ctypes.POINTER(trop_act8))] +
-                [(n, ctypes.c_void_p) for n in ("post_mean", "post_rstd", "pre_mean", "pre_rstd")] +
-                [("dy", trop_matrix), ("dh", trop_matrix)])
-
-
-class trop_residual_norm_grads(ctypes.Structure):
-    _fields_ = ([(n, trop_matrix) for n in ("dr", "du", "dgate")] +
-                [(n, ctypes.c_void_p) for n in ("dpost_gamma", "dpost_beta", "dpre_gamma", "dpre_beta")])
+# trop_residual_norm_rows, trop_residual_norm_kept, trop_residual_norm_grads:
+# every field is 8 bytes, so a call fills them as flat arrays
+_rows_fields, _kept_fields, _grads_fields = ctypes.c_uint64 * 14, ctypes.c_uint64 * 14, ctypes.c_uint64 * 10
 
 
 _lib = None
@@ -187,10 +176,9 @@ def lib():
     L.tropical_act8_unpack.argtypes = [PP(trop_act8), i32, vp, i64, i64, i64, vp]
     L.tropical_act8_linear_grad_w.argtypes = [i32, vp, i64, PP(trop_act8), vp, i64, i64, i64, i64, vp, sz, vp]
     L.tropical_act8_linear_grad_w_workspace_size.argtypes = [i32, i64, i64, i64, PP(sz)]
-    L.tropical_residual_norm_forward.argtypes = [PP(trop_residual_norm), trop_matrix, trop_matrix, trop_matrix,
-                                                 trop_matrix, vp, vp, vp, vp, PP(trop_act8), PP(trop_act8), vp]
-    L.tropical_residual_norm_backward.argtypes = [PP(trop_residual_norm), PP(trop_residual_norm_kept),
-                                                  PP(trop_residual_norm_grads), vp, sz, vp]
+    L.tropical_residual_norm_forward.argtypes = [PP(trop_residual_norm), PP(ctypes.c_uint64), vp]
+    L.tropical_residual_norm_backward.argtypes = [PP(trop_residual_norm), PP(ctypes.c_uint64), PP(ctypes.c_uint64), vp,
+                                                  sz, vp]
     L.tropical_residual_norm_backward_workspace_size.argtypes = [PP(trop_residual_norm), PP(sz)]
     L.tropical_get_train_stats.argtypes = [PP(trop_train_stats)]
     for fn in ("tropical_train_init", "tropical_layer_norm_forward", "tropical_layer_norm_backward_workspace_size",
@@ -605,26 +593,32 @@ def _tdt(t, what):
 
 def _row_stride(t, what):
     """Row stride of a 2-d tensor with unit stride along its rows."""
-    if t.dim() != 2:
+    strides = t.stride()
+    if len(strides) != 2:
         raise ValueError(f"{what} must be 2-d, got {t.dim()}-d")
+    ld, inner = strides
     rows, cols = t.shape
-    ld, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{what} must have unit stride along its rows")
     return ld if rows > 1 else max(ld, cols)
 
 
 def _flat(t, what, n, dtype):
-    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous 1-d {dtype} tensor of {n} elements")
     return t.data_ptr()
+
+
+def _new_matrix(rows, cols, dtype, device):
+    # (empty_strided reads its arguments in half of empty's time)
+    return torch.empty_strided((rows, cols), (max(cols, 1), 1), dtype=dtype, device=device)
 
 
 def _out_matrix(t, rows, cols, dtype, device, what):
     """(tensor, pointer, row stride) of the caller's output matrix, checked,
     or of a new one for True / None."""
     if t is None or t is True:
-        t = torch.empty((rows, cols), dtype=dtype, device=device)
+        t = _new_matrix(rows, cols, dtype, device)
         return t, t.data_ptr(), cols
     if tuple(t.shape) != (rows, cols) or t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} of shape {(rows, cols)}")
@@ -634,7 +628,7 @@ def _out_matrix(t, rows, cols, dtype, device, what):
 def _out_flat(t, n, dtype, device, what):
     """(tensor, pointer) of a 1-d output, likewise."""
     if t is None or t is True:
-        t = torch.empty(n, dtype=dtype, device=device)
+        t = torch.empty_strided((n,), (1,), dtype=dtype, device=device)
         return t, t.data_ptr()
     return t, _flat(t, what, n, dtype)
 
@@ -644,7 +638,8 @@ def _workspace(workspace, nbytes, device):
     if workspace is None:
         if not nbytes:
             return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), nbytes
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -928,18 +923,16 @@ Act8 = collections.namedtuple("Act8", ["codes", "exponents"])
 def _act8(a, rows, cols, what):
     """The C structure of an Act8 of this shape."""
     codes, exponents = a
-    if codes.dtype != torch.int8 or tuple(codes.shape) != (rows, cols):
+    if codes.dtype != torch.int8 or codes.shape != (rows, cols):
         raise ValueError(f"{what}: codes must be int8 of shape {(rows, cols)}")
-    blocks = (rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK)
-    if exponents.dtype != torch.uint8 or tuple(exponents.shape) != blocks:
-        raise ValueError(f"{what}: exponents must be uint8 of shape {blocks}")
-    return trop_act8(codes.data_ptr(), exponents.data_ptr(), _row_stride(codes, what + " codes"),
-                     _row_stride(exponents, what + " exponents"))
+    if exponents.dtype != torch.uint8 or exponents.shape != (rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK):
+        raise ValueError(f"{what}: exponents must be uint8, one for each {ACT8_BLOCK} elements of a row")
+    return trop_act8(codes.data_ptr(), exponents.data_ptr(), _row_stride(codes, what), _row_stride(exponents, what))
 
 
 def _new_act8(rows, cols, device):
-    return Act8(torch.empty((rows, cols), dtype=torch.int8, device=device),
-                torch.empty((rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK), dtype=torch.uint8, device=device))
+    return Act8(_new_matrix(rows, cols, torch.int8, device),
+                _new_matrix(rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK, torch.uint8, device))
 
 
 @_on_stream
@@ -975,16 +968,20 @@ def tropical_act8_unpack(x8, dtype=torch.float32, out=None):
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def _grad_w_workspace(dt, tokens, cols, out_features):
+    nb = ctypes.c_size_t(0)
+    _check(lib().tropical_act8_linear_grad_w_workspace_size(dt, tokens, cols, out_features, ctypes.byref(nb)),
+           "tropical_act8_linear_grad_w_workspace_size")
+    return nb.value
+
+
 def tropical_act8_linear_grad_w_workspace_size(dtype, tokens, cols, out_features):
     """Workspace bytes of the weight gradient (dtype: torch.float32 or
     torch.bfloat16)."""
     if dtype not in _TRAIN_DTYPES:
         raise TypeError(f"float32 or bfloat16 only, got {dtype}")
-    nb = ctypes.c_size_t(0)
-    _check(lib().tropical_act8_linear_grad_w_workspace_size(_TRAIN_DTYPES[dtype], int(tokens), int(cols),
-                                                            int(out_features), ctypes.byref(nb)),
-           "tropical_act8_linear_grad_w_workspace_size")
-    return nb.value
+    return _grad_w_workspace(_TRAIN_DTYPES[dtype], int(tokens), int(cols), int(out_features))
 
 
 @_on_stream
@@ -1005,7 +1002,7 @@ def tropical_act8_linear_grad_w(dz, x8, grad_w=None, workspace=None):
     grad_w, pw, ldw = _out_matrix(grad_w, outs, cols, dz.dtype, dz.device, "grad_w")
     need = 0
     if workspace is None:
-        need = tropical_act8_linear_grad_w_workspace_size(dz.dtype, tokens, cols, outs)
+        need = _grad_w_workspace(dt, tokens, cols, outs)
     workspace, wp, wn = _workspace(workspace, need, dz.device)
     st = lib().tropical_act8_linear_grad_w(dt, dz.data_ptr(), lddz, x, pw, ldw, tokens, cols, outs, wp, wn,
                                            _stream_ptr(None, dz))
@@ -1015,6 +1012,8 @@ def tropical_act8_linear_grad_w(dz, x8, grad_w=None, workspace=None):
 
 
 _NORMS = {None: 0, "layer": 1, "rms": 2}
+_WEIGHTS = ("post_gamma", "post_beta", "pre_gamma", "pre_beta")
+_STATISTICS = ("post_mean", "post_rstd", "pre_mean", "pre_rstd")
 
 ResidualNorm = collections.namedtuple("ResidualNorm", ["h", "y", "post_mean", "post_rstd", "pre_mean", "pre_rstd",
                                                        "u8", "h8"])
@@ -1022,41 +1021,41 @@ ResidualNormGrads = collections.namedtuple("ResidualNormGrads", ["r", "u", "gate
                                                                  "pre_gamma", "pre_beta"])
 
 
-def _residual_op(dt, dtype, rows, cols, gate, gate_group, post, post_gamma, post_beta, post_eps, pre, pre_gamma,
-                 pre_beta, pre_eps, residual_scale, branch_scale):
-    """(C structure, weights' type, gate rows)."""
+def _residual_op(dt, rows, cols, gate, gate_group, post, post_gamma, post_beta, post_eps, pre, pre_gamma, pre_beta,
+                 pre_eps, residual_scale, branch_scale):
+    """(C structure, weights' type)."""
     if post not in _NORMS or pre not in _NORMS:
         raise ValueError("norms are None, 'layer' or 'rms'")
-    op = trop_residual_norm(dt, F32, F32, _NORMS[post], _NORMS[pre], residual_scale, branch_scale, post_eps, pre_eps,
-                            rows, cols)
-    ptype = None
-    for there, name, w in ((post, "post_gamma", post_gamma), (post, "post_beta", post_beta),
-                           (pre, "pre_gamma", pre_gamma), (pre, "pre_beta", pre_beta)):
-        if w is None:
-            continue
-        if there is None:
-            raise ValueError(f"{name} without its norm")
-        if ptype is None:
-            ptype = w.dtype
-            op.param_dtype = _tdt(w, "gamma and beta")
-        setattr(op, name, _flat(w, name, cols, ptype))
-    gates = 0
+    pdt, gdt, ptype = F32, F32, None
+    weights = [None, None, None, None]
+    i = 0
+    for w in (post_gamma, post_beta, pre_gamma, pre_beta):
+        if w is not None:
+            name = _WEIGHTS[i]
+            if (pre if i > 1 else post) is None:
+                raise ValueError(f"{name} without its norm")
+            if ptype is None:
+                ptype = w.dtype
+                pdt = _tdt(w, "gamma and beta")
+            weights[i] = _flat(w, name, cols, ptype)
+        i += 1
+    pg, ldg, group = None, 0, 0
     if gate is not None:
+        gdt = _tdt(gate, "gate")
         if gate.dim() == 1:
-            gate = gate[None]
-            gate_group = max(rows, 1)
-        op.gate_dtype = _tdt(gate, "gate")
-        gates = gate.shape[0]
-        if gate_group is None:
-            gate_group = rows // gates if gates else 1
-            if gates * gate_group != rows:
-                raise ValueError(f"{gates} gate rows do not divide {rows} rows: give gate_group")
-        if gate_group < 1 or gate.shape[1] != cols or (rows and gates != -(-rows // gate_group)):
-            raise ValueError(f"gate must have a row of {cols} for each {gate_group} of {rows} rows")
-        op.gate = gate.data_ptr()
-        op.ldgate = _row_stride(gate, "gate")
-        op.gate_group = gate_group
-    return op, ptype or torch.float32, gates
+            pg, ldg, group = _flat(gate, "gate", cols, gate.dtype), cols, max(rows, 1)
+        else:
+            pg, ldg, group = gate.data_ptr(), _row_stride(gate, "gate"), gate_group
+            gates, width = gate.shape
+            if group is None:
+                group = rows // gates if gates else 1
+                if gates * group != rows:
+                    raise ValueError(f"{gates} gate rows do not divide {rows} rows: give gate_group")
+            if group < 1 or width != cols or (rows and gates != -(-rows // group)):
+                raise ValueError(f"gate must have a row of {cols} for each {group} of {rows} rows")
+    op = trop_residual_norm(dt, pdt, gdt, _NORMS[post], _NORMS[pre], residual_scale, branch_scale, post_eps, pre_eps,
+                            rows, cols, pg, ldg, group, *weights)
+    return op, ptype or torch.float32
 
 
 @_on_stream
@@ -1079,38 +1078,45 @@ def tropical_residual_norm_forward(u, r=None, gate=None, post=None, post_gamma=N
     dt = _tdt(u, "u")
     ldu = _row_stride(u, "u")
     rows, cols = u.shape
-    dev, f32 = u.device, torch.float32
-    op, _, _ = _residual_op(dt, u.dtype, rows, cols, gate, gate_group, post, post_gamma, post_beta, post_eps, pre,
-                            pre_gamma, pre_beta, pre_eps, residual_scale, branch_scale)
-    none = trop_matrix(None, 0)
-    mr = mh = my = none
+    dev, dtype = u.device, u.dtype
+    op, _ = _residual_op(dt, rows, cols, gate, gate_group, post, post_gamma, post_beta, post_eps, pre, pre_gamma,
+                         pre_beta, pre_eps, residual_scale, branch_scale)
+    pr = ldr = ph = ldh = py = ldy = 0
     if r is not None:
-        if r.shape != u.shape or r.dtype != u.dtype:
+        if r.shape != u.shape or r.dtype != dtype:
             raise ValueError("r must have the shape and type of u")
-        mr = trop_matrix(r.data_ptr(), _row_stride(r, "r"))
+        pr, ldr = r.data_ptr(), _row_stride(r, "r")
     if h is not None:
-        h, ph, ldh = _out_matrix(h, rows, cols, u.dtype, dev, "h")
-        mh = trop_matrix(ph, ldh)
+        h, ph, ldh = _out_matrix(h, rows, cols, dtype, dev, "h")
     if pre is None:
         if y is not None and y is not True:
             raise ValueError("y without a norm before the next block")
         y = None
     if y is not None:
-        y, py, ldy = _out_matrix(y, rows, cols, u.dtype, dev, "y")
-        my = trop_matrix(py, ldy)
-    stats, ptrs = [], []
+        y, py, ldy = _out_matrix(y, rows, cols, dtype, dev, "y")
+    io = [pr, ldr, u.data_ptr(), ldu, ph, ldh, py, ldy]
+    stats = []
     for norm in (post, pre):
         for there in (norm == "layer", norm is not None):
-            t = torch.empty(rows, dtype=f32, device=dev) if there else None
+            t = None
+            if there:
+                t = torch.empty_strided((rows,), (1,), dtype=torch.float32, device=dev)
             stats.append(t)
-            ptrs.append(t.data_ptr() if there else None)
-    held, keep = [], []
-    for x, what in ((hold_u, "hold_u"), (hold_h, "hold_h")):
-        x = _new_act8(rows, cols, dev) if x is True else x or None
-        held.append(x)
-        keep.append(_act8(x, rows, cols, what) if x is not None else None)
-    st = lib().tropical_residual_norm_forward(op, mr, trop_matrix(u.data_ptr(), ldu), mh, my, *ptrs, *keep,
-                                              _stream_ptr(None, u))
+            io.append(t.data_ptr() if there else 0)
+    held, alive = [None, None], []
+    if hold_u is not None and hold_u is not False:
+        held[0] = x = _new_act8(rows, cols, dev) if hold_u is True else hold_u
+        alive.append(_act8(x, rows, cols, "hold_u"))
+        io.append(ctypes.addressof(alive[-1]))
+    else:
+        io.append(0)
+    if hold_h is not None and hold_h is not False:
+        held[1] = x = _new_act8(rows, cols, dev) if hold_h is True else hold_h
+        alive.append(_act8(x, rows, cols, "hold_h"))
+        io.append(ctypes.addressof(alive[-1]))
+    else:
+        io.append(0)
+    st = lib().tropical_residual_norm_forward(op, _rows_fields(*io), _stream_ptr(None, u))
     if st != OK:
         _check(st, "tropical_residual_norm_forward")
     return ResidualNorm(h, y, *stats, *held)
@@ -1136,70 +1142,76 @@ def tropical_residual_norm_backward(dy, dh, u, h, post_mean=None, post_rstd=None
     if lead is None:
         raise ValueError("neither dy nor dh")
     dt = _tdt(lead, "dy and dh")
-    rows, cols = lead.shape
-    dtype, dev = lead.dtype, lead.device
-    op, ptype, gates = _residual_op(dt, dtype, rows, cols, gate, gate_group, post, post_gamma, post_beta, post_eps, pre,
-                                    pre_gamma, pre_beta, pre_eps, residual_scale, branch_scale)
-    kept, grads = trop_residual_norm_kept(), trop_residual_norm_grads()
-    alive = []
+    lead_ld = _row_stride(lead, "dy" if dy is not None else "dh")
+    shape, dtype, dev = lead.shape, lead.dtype, lead.device
+    rows, cols = shape
+    op, ptype = _residual_op(dt, rows, cols, gate, gate_group, post, post_gamma, post_beta, post_eps, pre, pre_gamma,
+                             pre_beta, pre_eps, residual_scale, branch_scale)
 
     def matrix(t, what):
-        if t.shape != lead.shape or t.dtype != dtype:
+        if t.shape != shape or t.dtype != dtype:
             raise ValueError(f"{what} must be {dtype} of shape {(rows, cols)}")
-        return trop_matrix(t.data_ptr(), _row_stride(t, what))
+        return t.data_ptr(), _row_stride(t, what)
 
-    if dy is not None:
-        kept.dy = matrix(dy, "dy")
-    if dh is not None:
-        kept.dh = matrix(dh, "dh")
-    for name, t in (("u", u), ("h", h)):
+    alive = []
+    kept = [0, 0, 0, 0, 0, 0]  # u, h, u8, h8
+    for i, t in ((0, u), (1, h)):
         if isinstance(t, torch.Tensor):
-            setattr(kept, name, matrix(t, name))
+            kept[2 * i], kept[2 * i + 1] = matrix(t, "uh"[i])
         elif t is not None:
-            alive.append(_act8(t, rows, cols, name))
-            setattr(kept, name + "8", ctypes.pointer(alive[-1]))
-    for name, t in (("post_mean", post_mean), ("post_rstd", post_rstd), ("pre_mean", pre_mean), ("pre_rstd", pre_rstd)):
-        if t is not None:
-            setattr(kept, name, _flat(t, name, rows, torch.float32))
+            alive.append(_act8(t, rows, cols, "uh"[i]))
+            kept[4 + i] = ctypes.addressof(alive[-1])
+    i = 0
+    for t in (post_mean, post_rstd, pre_mean, pre_rstd):
+        kept.append(0 if t is None else _flat(t, _STATISTICS[i], rows, torch.float32))
+        i += 1
+    if dy is not None:
+        kept += (dy.data_ptr(), lead_ld)
+        kept += matrix(dh, "dh") if dh is not None else (0, 0)
+    else:
+        kept += (0, 0, dh.data_ptr(), lead_ld)
+    grads = [0] * 10
     if dr is not None:
-        dr, p, ld = _out_matrix(dr, rows, cols, dtype, dev, "dr")
-        grads.dr = trop_matrix(p, ld)
+        dr, grads[0], grads[1] = _out_matrix(dr, rows, cols, dtype, dev, "dr")
     if du is not None:
-        du, p, ld = _out_matrix(du, rows, cols, dtype, dev, "du")
-        grads.du = trop_matrix(p, ld)
-    if dgate is True and gate is None:
-        dgate = None
-    given = dgate
+        du, grads[2], grads[3] = _out_matrix(du, rows, cols, dtype, dev, "du")
+    if dgate is True:
+        dgate = torch.empty(gate.shape, dtype=gate.dtype, device=dev) if gate is not None else None
     if dgate is not None:
         if gate is None:
             raise ValueError("dgate without a gate")
-        flat = gate.dim() == 1
-        if dgate is True:
-            dgate = given = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
-        elif dgate.shape != gate.shape:
-            raise ValueError("dgate must have the gate's shape")
-        dgate, p, ld = _out_matrix(dgate[None] if flat else dgate, gates, cols, gate.dtype, dev, "dgate")
-        grads.dgate = trop_matrix(p, ld)
-    weights = []
-    for name, g, w in (("dpost_gamma", dpost_gamma, post_gamma), ("dpost_beta", dpost_beta, post_beta),
-                       ("dpre_gamma", dpre_gamma, pre_gamma), ("dpre_beta", dpre_beta, pre_beta)):
+        if dgate.shape != gate.shape or dgate.dtype != gate.dtype:
+            raise ValueError("dgate must have the gate's shape and type")
+        flat = dgate.dim() == 1
+        grads[4] = _flat(dgate, "dgate", cols, gate.dtype) if flat else dgate.data_ptr()
+        grads[5] = cols if flat else _row_stride(dgate, "dgate")
+    weights = [dpost_gamma, dpost_beta, dpre_gamma, dpre_beta]
+    sums = dgate is not None
+    i = 0
+    for w in (post_gamma, post_beta, pre_gamma, pre_beta):
+        g = weights[i]
         if g is True and w is None:
-            g = None
-        if g is not None:
-            g, p = _out_flat(g, cols, ptype, dev, name)
-            setattr(grads, name, p)
-        weights.append(g)
+            weights[i] = None
+        elif g is not None:
+            sums = True
+            weights[i], grads[6 + i] = _out_flat(g, cols, ptype, dev, "d" + _WEIGHTS[i])
+        i += 1
     need = 0
-    if workspace is None and (dgate is not None or any(w is not None for w in weights)):
-        need = _residual_workspace(op)
+    if workspace is None and sums:
+        need = _residual_workspace(rows, cols, op.post, op.pre, op.gate_group if gate is not None else None)
     workspace, wp, wn = _workspace(workspace, need, dev)
-    st = lib().tropical_residual_norm_backward(op, kept, grads, wp, wn, _stream_ptr(None, lead))
+    st = lib().tropical_residual_norm_backward(op, _kept_fields(*kept), _grads_fields(*grads), wp, wn,
+                                               _stream_ptr(None, lead))
     if st != OK:
         _check(st, "tropical_residual_norm_backward")
-    return ResidualNormGrads(dr, du, given, *weights)
+    return ResidualNormGrads(dr, du, dgate, *weights)
 
 
-def _residual_workspace(op):
+@functools.lru_cache(maxsize=4096)
+def _residual_workspace(rows, cols, post, pre, gate_group):
+    op = trop_residual_norm(post=post, pre=pre, rows=rows, cols=cols)
+    if gate_group is not None:
+        op.gate, op.gate_group = 1, gate_group
     nb = ctypes.c_size_t(0)
     _check(lib().tropical_residual_norm_backward_workspace_size(op, ctypes.byref(nb)),
            "tropical_residual_norm_backward_workspace_size")
@@ -1210,10 +1222,8 @@ def tropical_residual_norm_backward_workspace_size(rows, cols, post=None, pre="l
     """Workspace bytes of a backward (gate_group: None without a gate)."""
     if post not in _NORMS or pre not in _NORMS:
         raise ValueError("norms are None, 'layer' or 'rms'")
-    op = trop_residual_norm(post=_NORMS[post], pre=_NORMS[pre], rows=int(rows), cols=int(cols))
-    if gate_group is not None:
-        op.gate, op.gate_group = 1, int(gate_group)
-    return _residual_workspace(op)
+    return _residual_workspace(int(rows), int(cols), _NORMS[post], _NORMS[pre],
+                               None if gate_group is None else int(gate_group))
 
 
 def tropical_get_train_stats():

@@ -1,8 +1,8 @@
 """Build libtropical.so: gfx950 code object + host runtime.
 
 1. hipcc --genco compiles csrc/kernels/kernels.hip (the contraction) and
-   csrc/kernels/train_kernels.hip (the training operators) for gfx950 only,
-   one code object each.  Packed FP32 instructions are disabled
+   csrc/kernels/train_kernels.hip and block_kernels.hip (the training
+   operators) for gfx950 only, one code object each.  Packed FP32 instructions are disabled
    (-packed-fp32-ops) and nothing enables fast math, FTZ or FMA contraction:
    every tropical term is one IEEE op.
 2. The code objects are embedded into the library with an assembler .incbin.
@@ -58,6 +58,7 @@ def build(verbose=False):
     os.makedirs(LIBDIR, exist_ok=True)
     co = os.path.join(BUILD, "tropical_kernels.co")
     train_co = os.path.join(BUILD, "train_kernels.co")
+    block_co = os.path.join(BUILD, "block_kernels.co")
     blob = os.path.join(BUILD, "co_blob.S")
 
     def compile_host(name):
@@ -73,7 +74,8 @@ def build(verbose=False):
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, len(RUNTIME_SRCS) + 2)) as ex:
-        fut_co = [ex.submit(build_code_object, co), ex.submit(build_code_object, train_co, "train_kernels.hip")]
+        fut_co = [ex.submit(build_code_object, co), ex.submit(build_code_object, train_co, "train_kernels.hip"),
+                  ex.submit(build_code_object, block_co, "block_kernels.hip")]
         fut_hip = [ex.submit(compile_hip_host, n) for n in RUNTIME_HIP_SRCS]
         objs = list(ex.map(compile_host, RUNTIME_SRCS))
         objs += [f.result() for f in fut_hip]
@@ -82,7 +84,8 @@ def build(verbose=False):
 
     with open(blob, "w") as f:
         f.write("    .section .rodata\n")
-        for symbol, path in (("trop_code_object", co), ("trop_train_code_object", train_co)):
+        for symbol, path in (("trop_code_object", co), ("trop_train_code_object", train_co),
+                             ("trop_block_code_object", block_co)):
             f.write(
                 "    .balign 4096\n"
                 f"    .globl {symbol}\n"

@@ -78,6 +78,11 @@ __device__ __forceinline__ void act8_store(int8_t* codes, uint8_t* exps, int64_t
     }
 }
 
+// Codes as 32-bit words, for a kernel to keep (as bytes each would take a
+// register of its own).
+template <int VEC>
+using CodeWords = typename VecOf<uint32_t, VEC / 4>::raw;
+
 // A lane's codes and exponent, to be turned into values later.
 template <int VEC>
 struct Act8Lane {

@@ -43,28 +43,33 @@ __device__ __forceinline__ float wave_total(float x) {
 }
 
 // Sums over the TPR threads of a row, by way of an LDS slot of their own when
-// the row has several waves.  A slot is written again only after another
-// reduction's barrier.
+// the row has several waves: each wave then reads one wave's sum to a lane and
+// adds them across its lanes, so the sums end in scalar registers.  A slot is
+// written again only after another reduction's barrier.
 template <int TPR, int NVAL>
 struct RowSums {
-    float lds[TPR > 64 ? TPR / 64 : 1][NVAL];
+    float lds[NVAL][TPR > 64 ? TPR / 64 : 1];
 };
 template <int TPR, int NVAL>
 __device__ __forceinline__ void row_sums(float (&v)[NVAL], RowSums<TPR, NVAL>& s) {
 #pragma unroll
     for (int i = 0; i < NVAL; ++i) v[i] = wave_total(v[i]);
     if constexpr (TPR > 64) {
-        const int wave = threadIdx.x / 64;
-        if ((threadIdx.x & 63) == 0) {
+        constexpr int WAVES = TPR / 64;
+        static_assert(WAVES == 2 || WAVES == 4 || WAVES == 8 || WAVES == 16, "steps below");
+        const int wave = threadIdx.x / 64, lane = threadIdx.x & 63;
+        if (lane == 0) {
 #pragma unroll
-            for (int i = 0; i < NVAL; ++i) s.lds[wave][i] = v[i];
+            for (int i = 0; i < NVAL; ++i) s.lds[i][wave] = v[i];
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NVAL; ++i) {
-            v[i] = s.lds[0][i];
-#pragma unroll
-            for (int w = 1; w < TPR / 64; ++w) v[i] += s.lds[w][i];
+            float x = dpp_add<0x111>(s.lds[i][lane & (WAVES - 1)]);  // row_shr:1
+            if constexpr (WAVES > 2) x = dpp_add<0x112>(x);          // row_shr:2
+            if constexpr (WAVES > 4) x = dpp_add<0x114>(x);          // row_shr:4
+            if constexpr (WAVES > 8) x = dpp_add<0x118>(x);          // row_shr:8
+            v[i] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), WAVES - 1));
         }
     }
 }
@@ -88,6 +93,48 @@ __device__ __forceinline__ FloatVec<VEC> rn_gate(const TropResidualParams& p, in
 #pragma unroll
     for (int e = 0; e < VEC; ++e) g[e] *= p.branch_scale;
     return g;
+}
+
+// Row r of a matrix, a uniform pointer in scalar registers, and element c of
+// it, by a 32-bit byte offset that the load takes as it is.  Both are hidden
+// from the compiler, which would rather add each lane's column to the base
+// before the loop over the rows and keep 64-bit lane addresses (60 registers
+// of a backward's 190).
+template <typename T>
+__device__ __forceinline__ T* rn_row(T* base, int64_t r, int64_t ld) {
+    auto row = (__attribute__((address_space(1))) T*)(base + r * ld);
+    asm("" : "+s"(row));
+    return (T*)row;
+}
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ float rn_scalar(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
+template <typename T>
+__device__ __forceinline__ T* rn_at(T* row, uint32_t c) {
+    uint32_t offset = c * (uint32_t)sizeof(T);
+    asm volatile("" : "+v"(offset));
+    return (T*)((__attribute__((address_space(1))) char*)(__attribute__((address_space(1))) T*)row + offset);
+}
+// The same, and norm weights, where the whole vector is inside the row.
+template <typename T, int VEC>
+__device__ __forceinline__ FloatVec<VEC> rn_gate_full(const TropResidualParams& p, int64_t row, uint32_t c) {
+    FloatVec<VEC> g;
+    if (!p.gate)
+        g = FloatVec<VEC>(1.f);
+    else if (sizeof(T) == 4 || p.gate_f32)
+        g = load_vec<float, VEC>(rn_at(rn_row(static_cast<const float*>(p.gate), row, p.ldgate), c));
+    else
+        g = to_float<T, VEC>(load_vec<T, VEC>(rn_at(rn_row(static_cast<const T*>(p.gate), row, p.ldgate), c)));
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) g[e] *= p.branch_scale;
+    return g;
+}
+template <int VEC>
+__device__ __forceinline__ FloatVec<VEC> rn_weight(const TropResidualParams& p, const void* w, uint32_t c, float other) {
+    if (!w) return FloatVec<VEC>(other);
+    if (p.weight_f32) return load_vec<float, VEC>(rn_at(rn_row(static_cast<const float*>(w), 0, 0), c));
+    return to_float<bf16, VEC>(load_vec<bf16, VEC>(rn_at(rn_row(static_cast<const bf16*>(w), 0, 0), c)));
 }
 
 // A row's statistics: mean (0 for RMS) and rstd of x, whose elements past the
@@ -302,76 +349,116 @@ template <typename T, int VEC, bool HELD>
 struct RnKept {
     typename VecOf<T, VEC>::raw v;
     __device__ __forceinline__ void load(const void* m, int64_t ld, const int8_t*, int64_t, const uint8_t*, int64_t,
-                                         int64_t r, int64_t c, int64_t n) {
-        v = load_row_stream<T, VEC>(static_cast<const T*>(m) + r * ld, c, n);
+                                         int64_t r, uint32_t c, bool) {
+        v = load_stream<T, VEC>(rn_at(rn_row(static_cast<const T*>(m), r, ld), c));
     }
-    __device__ __forceinline__ FloatVec<VEC> values() const { return to_float<T, VEC>(v); }
+    // the values less `mean`
+    __device__ __forceinline__ FloatVec<VEC> about(float mean, uint32_t, bool) const {
+        FloatVec<VEC> x = to_float<T, VEC>(v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] -= mean;
+        return x;
+    }
 };
 template <typename T, int VEC>
 struct RnKept<T, VEC, true> {
-    Act8Lane<VEC> v;
-    __device__ __forceinline__ void load(const void*, int64_t, const int8_t* codes, int64_t ldc, const uint8_t* exps,
-                                         int64_t lde, int64_t r, int64_t c, int64_t n) {
-        v.load(codes + r * ldc, exps + r * lde, c, n);
+    CodeWords<VEC> codes;
+    uint32_t exps;  // of the first and (`ragged` rows), from bit 8 on, the last element
+    __device__ __forceinline__ void load(const void*, int64_t, const int8_t* m, int64_t ldc, const uint8_t* e,
+                                         int64_t lde, int64_t r, uint32_t c, bool ragged) {
+        codes = __builtin_bit_cast(CodeWords<VEC>, load_stream<int8_t, VEC>(rn_at(rn_row(m, r, ldc), c)));
+        const uint8_t* row = rn_row(e, r, lde);
+        exps = *rn_at(row, c / TROP_ACT8_BLOCK_ELEMS);
+        if (ragged) exps |= (uint32_t)*rn_at(row, (c + VEC - 1) / TROP_ACT8_BLOCK_ELEMS) << 8;
     }
-    __device__ __forceinline__ FloatVec<VEC> values() const { return v.values(); }
+    __device__ __forceinline__ FloatVec<VEC> about(float mean, uint32_t c, bool ragged) const {
+        const float step = act8_step(exps & 255);
+        const FloatVec<VEC> q = __builtin_convertvector(__builtin_bit_cast(Codes<VEC>, codes), FloatVec<VEC>);
+        FloatVec<VEC> x;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] = __builtin_fmaf(q[e], step, -mean);  // (the product is exact)
+        if (ragged) {
+            int split = TROP_ACT8_BLOCK_ELEMS - (int)(c % TROP_ACT8_BLOCK_ELEMS);
+            asm volatile("" : "+v"(split));  // (the comparisons are not to be kept over the rows)
+            if (split < VEC) {  // a block ends inside the vector
+                const float last = act8_step(exps >> 8);
+                CodeWords<VEC> again;  // (converted anew: no registers for it elsewhere)
+#pragma unroll
+                for (int q = 0; q < VEC / 4; ++q) {
+                    uint32_t word = codes[q];
+                    asm volatile("" : "+v"(word));
+                    again[q] = word;
+                }
+                const FloatVec<VEC> q1 = __builtin_convertvector(__builtin_bit_cast(Codes<VEC>, again), FloatVec<VEC>);
+#pragma unroll
+                for (int e = 1; e < VEC; ++e)
+                    if (e >= split) x[e] = __builtin_fmaf(q1[e], last, -mean);
+            }
+        }
+        return x;
+    }
 };
 
-// The rows of part blockIdx.x, TPR threads to a row, 8 elements to a thread.
-// A part inside a gate row: rows one by one, to the workgroup's row groups in
-// turn (four waves, or one group).  A part of whole gate rows: those in turn,
-// their rows one by one.
-template <typename T, typename P, int TPR, bool HELD>
+// The rows of part blockIdx.x, TPR threads to a row, EPT elements to a thread
+// in vectors of 16 bytes.  A part inside a gate row: rows one by one, to the
+// workgroup's row groups in turn (four waves, or one group).  A part of whole
+// gate rows: those in turn, their rows one by one.
+//
+// A vector that would pass the row's end lies at the end instead: its first
+// elements, which the lane before holds too, come to the same bits in both and
+// are stored twice; only the row's sums leave them out.  So no load or store
+// is taken apart.  Lanes past the end repeat the last vector and store nothing.
+//
+// Within a gate row the gate, gamma and beta are constants of a column, so two
+// sums serve three gradients: with A = sum H x^ and B = sum H,
+//   dgamma = gate A,  dbeta = gate B,  dgate = gamma A + beta B
+// (all but the scales).  A part of whole gate rows adds up the first two in
+// LDS, a slot to each thread, whenever a gate row ends.
+template <typename T, int TPR, int EPT, bool HELD, bool PRE, bool POST>
 __device__ __forceinline__ void residual_norm_backward_body(const TropResidualParams& p) {
-    constexpr int VEC = ln_vec<T>(), NV = 8 / VEC, RPB = TPR == 64 ? 4 : 1;
-    // the weights' registers, where there are enough
-    constexpr bool KEEP = TPR < 1024;
+    constexpr int VEC = ln_vec<T>(), NV = EPT / VEC, RPB = TPR == 64 ? 4 : 1, THREADS = TPR * RPB;
+    using V = typename VecOf<T, VEC>::raw;
     __shared__ RowSums<TPR, 2> sums[2][2];
-    __shared__ float cols_lds[TPR == 64 ? TROP_RN_COLS_WAVE : 1];
+    __shared__ float post_lds[POST ? 2 : 1][POST ? EPT : 1][THREADS];
+    __shared__ float cols_lds[TPR == 64 ? 4 : 1][TPR == 64 ? TPR * EPT : 1];
     const int t = threadIdx.x % TPR, group = RPB == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
-    float acc[TROP_RN_SUMS][NV * VEC] = {};
-    typename VecOf<T, VEC>::raw dyv[NV], dhv[NV];
+    const int cols = (int)p.cols;
+    uint32_t at[NV];
+    int dup[NV];  // first column; elements of the vector that the lane before holds
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + t) * VEC;
+        at[i] = min(c, cols - VEC);
+        dup[i] = c - (int)at[i];
+    }
+    float pg[EPT] = {}, pb[EPT] = {}, sa[EPT] = {}, sb[EPT] = {};  // sums of dy x^, dy; A and B
+    V dyv[NV], dhv[NV] = {};
     RnKept<T, VEC, HELD> hv[NV], uv[NV];
-    float pre_mean = 0.f, pre_rstd = 1.f, post_mean = 0.f, post_rstd = 1.f;
-    const bool need_u = p.need_v || p.need_post;
+    float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f;
+    const bool need_u = POST || p.need_v;
     auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t c = (int64_t)(i * TPR + t) * VEC;
-            if (p.pre) {
-                dyv[i] = load_row_stream<T, VEC>(static_cast<const T*>(p.dy) + r * p.lddy, c, p.cols);
-                hv[i].load(p.h, p.ldh, p.h_codes, p.ldh_codes, p.h_exps, p.ldh_exps, r, c, p.cols);
+            if constexpr (PRE) {
+                dyv[i] = load_stream<T, VEC>(rn_at(rn_row(static_cast<const T*>(p.dy), r, p.lddy), at[i]));
+                hv[i].load(p.h, p.ldh, p.h_codes, p.ldh_codes, p.h_exps, p.ldh_exps, r, at[i], p.ragged);
             }
-            if (p.dh) dhv[i] = load_row_stream<T, VEC>(static_cast<const T*>(p.dh) + r * p.lddh, c, p.cols);
-            if (need_u) uv[i].load(p.u, p.ldu, p.u_codes, p.ldu_codes, p.u_exps, p.ldu_exps, r, c, p.cols);
+            if (!PRE || p.dh) dhv[i] = load_stream<T, VEC>(rn_at(rn_row(static_cast<const T*>(p.dh), r, p.lddh), at[i]));
+            if (need_u) uv[i].load(p.u, p.ldu, p.u_codes, p.ldu_codes, p.u_exps, p.ldu_exps, r, at[i], p.ragged);
         }
-        if (p.pre) {
-            if (p.pre == RN_LAYER) pre_mean = p.pre_mean[r];
-            pre_rstd = p.pre_rstd[r];
+        if constexpr (PRE) {
+            if (p.pre_mean) mean1 = p.pre_mean[r];
+            rstd1 = p.pre_rstd[r];
         }
-        if (p.post && need_u) {
-            if (p.post == RN_LAYER) post_mean = p.post_mean[r];
-            post_rstd = p.post_rstd[r];
+        if constexpr (POST) {
+            if (p.post_mean) mean2 = p.post_mean[r];
+            rstd2 = p.post_rstd[r];
         }
     };
-    FloatVec<VEC> pre_g[NV], post_g[NV], post_b[NV], gate[NV];
-    auto weights = [&](bool pre) {
+    FloatVec<VEC> pre_g[NV], gg[NV];  // gamma of the pre norm; branch_scale gate, times gamma of the post norm
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c = (int64_t)(i * TPR + t) * VEC;
-            if (pre) {
-                pre_g[i] = load_param<P, VEC>(p.pre_gamma, c, p.cols, 1.f);
-            } else {
-                post_g[i] = load_param<P, VEC>(p.post_gamma, c, p.cols, 1.f);
-                post_b[i] = load_param<P, VEC>(p.post_beta, c, p.cols, 0.f);
-            }
-        }
-    };
-    if constexpr (KEEP) {
-        weights(true);
-        weights(false);
-    }
-    // this row group's rows: `units` of unit_rows, `stride` units apart
+    for (int i = 0; i < NV; ++i) pre_g[i] = rn_weight<VEC>(p, p.pre_gamma, at[i], 1.f);
+    // this row group's rows: units of unit_rows, RPB units apart
     const bool whole = p.group_parts == 0;
     const int64_t unit_rows = whole ? p.gate_group : 1;
     int64_t first, end, gate_row;  // rows of the part
@@ -385,207 +472,246 @@ __device__ __forceinline__ void residual_norm_backward_body(const TropResidualPa
         first = min(gate_row * p.gate_group + q * p.part_rows, last);
         end = min(first + p.part_rows, last);
     }
-    int slot = 0;
     int64_t unit = first + group * unit_rows, r = unit, unit_end = min(unit + unit_rows, end);
-    bool new_gate = true;
-    if (whole && r < end) gate_row = rn_divide(r, p.gate_group);
     if (r < end) fetch(r);
+    if (whole) {
+        if (r < end) gate_row = rn_divide(r, p.gate_group);
+        if constexpr (POST) {
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) post_lds[0][e][threadIdx.x] = post_lds[1][e][threadIdx.x] = 0.f;
+        }
+    }
+    // Sums of w and w x over the row, without the elements held twice.
+    auto add = [&](float (&s)[2], const FloatVec<VEC>& w, const FloatVec<VEC>& x, int d) {
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            a += w[e];
+            b = __builtin_fmaf(w[e], x[e], b);
+        }
+        if (cols < TPR * EPT) {
+            asm volatile("" : "+v"(d));  // (the comparisons are not to be kept over the rows)
+            if (d > 0) {
+                a = b = 0.f;
+#pragma unroll
+                for (int e = 1; e < VEC; ++e)
+                    if (e >= d) {
+                        a += w[e];
+                        b = __builtin_fmaf(w[e], x[e], b);
+                    }
+            }
+        }
+        s[0] += a;
+        s[1] += b;
+    };
+    int slot = 0;
+    bool new_gate = true;
     while (r < end) {  // the groups of a workgroup share barriers only when RPB = 1
         if (new_gate) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) gate[i] = rn_gate<T, VEC>(p, gate_row, (int64_t)(i * TPR + t) * VEC);
+            for (int i = 0; i < NV; ++i) {
+                gg[i] = rn_gate_full<T, VEC>(p, gate_row, at[i]);
+                if constexpr (POST) {
+                    const FloatVec<VEC> g = rn_weight<VEC>(p, p.post_gamma, at[i], 1.f);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) gg[i][e] *= g[e];
+                }
+            }
             new_gate = false;
         }
         const int64_t row = r;
-        // the row after this one
         bool flush = false;
-        int64_t next_gate = gate_row;
-        if (++r == unit_end) {
+        if (++r == unit_end) {  // the row after this one
             flush = whole;
             unit += RPB * unit_rows;
             r = unit;
             unit_end = min(unit + unit_rows, end);
-            if (whole) next_gate = gate_row + RPB;
         }
-        FloatVec<VEC> H[NV], x[NV], w[NV];
+        FloatVec<VEC> H[NV], x[NV], w[NV], u[NV];
+        RnKept<T, VEC, HELD> uraw[NV];
         float s[2] = {0.f, 0.f};
-        const float mean1 = pre_mean, rstd1 = pre_rstd, mean2 = post_mean, rstd2 = post_rstd;
-        if constexpr (!KEEP) weights(true);
+        const float mu1 = rn_scalar(mean1), rs1 = rn_scalar(rstd1), mu2 = rn_scalar(mean2), rs2 = rn_scalar(rstd2);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t c = (int64_t)(i * TPR + t) * VEC;
-            if (p.dh)
-                H[i] = to_float<T, VEC>(dhv[i]);
-            else
-                H[i] = FloatVec<VEC>(0.f);
-            if (p.pre) {
-                const FloatVec<VEC> h = hv[i].values(), dy = to_float<T, VEC>(dyv[i]);
+            H[i] = to_float<T, VEC>(dhv[i]);
+            if constexpr (PRE) {
+                const FloatVec<VEC> dy = to_float<T, VEC>(dyv[i]);
+                x[i] = hv[i].about(mu1, at[i], p.ragged);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    // past the row's end everything is held to zero, so that a
-                    // non-finite statistic or weight adds nothing there
-                    const float xx = c + e < p.cols ? (h[e] - mean1) * rstd1 : 0.f;
-                    const float ww = c + e < p.cols ? dy[e] * pre_g[i][e] : 0.f;
-                    x[i][e] = xx;
-                    w[i][e] = ww;
-                    acc[TROP_RN_PRE_GAMMA][i * VEC + e] = __builtin_fmaf(dy[e], xx, acc[TROP_RN_PRE_GAMMA][i * VEC + e]);
-                    acc[TROP_RN_PRE_BETA][i * VEC + e] += dy[e];
-                    s[0] += ww;
-                    s[1] = __builtin_fmaf(ww, xx, s[1]);
+                    x[i][e] *= rs1;
+                    w[i][e] = dy[e] * pre_g[i][e];
+                    pg[i * VEC + e] = __builtin_fmaf(dy[e], x[i][e], pg[i * VEC + e]);
+                    pb[i * VEC + e] += dy[e];
                 }
+                add(s, w[i], x[i], dup[i]);
             }
-        }
-        FloatVec<VEC> u[NV];
-        if (need_u) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) u[i] = uv[i].values();
+            uraw[i] = uv[i];
         }
         if (r < end) fetch(r);
-        if (p.pre) {
+        if constexpr (PRE) {
             row_sums<TPR, 2>(s, sums[slot][0]);
             const float c1 = p.pre == RN_LAYER ? s[0] * p.inv_cols : 0.f, c2 = s[1] * p.inv_cols;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int64_t c = (int64_t)(i * TPR + t) * VEC;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float d = __builtin_fmaf(__builtin_fmaf(-c2, x[i][e], w[i][e] - c1), rstd1, H[i][e]);
-                    H[i][e] = c + e < p.cols ? d : 0.f;
-                }
-            }
-        }
-        if (p.dr) {
-            T* dr = static_cast<T*>(p.dr) + row * p.lddr;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int64_t c = (int64_t)(i * TPR + t) * VEC;
-                FloatVec<VEC> o;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = H[i][e] * p.residual_scale;
-                if (c < p.cols) store_row_stream<T, VEC>(dr, c, p.cols, from_float<T, VEC>(o));
-            }
-        }
-        if constexpr (!KEEP) {
-            if (p.post) weights(false);
-        }
-        if (need_u && p.post) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int64_t c = (int64_t)(i * TPR + t) * VEC;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    x[i][e] = c + e < p.cols ? (u[i][e] - mean2) * rstd2 : 0.f;
-                    u[i][e] = c + e < p.cols ? __builtin_fmaf(x[i][e], post_g[i][e], post_b[i][e]) : 0.f;
-                }
-            }
-        }
-        if (p.need_v) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
-                    acc[TROP_RN_GATE][i * VEC + e] = __builtin_fmaf(H[i][e], u[i][e], acc[TROP_RN_GATE][i * VEC + e]);
+                    H[i][e] = __builtin_fmaf(__builtin_fmaf(-c2, x[i][e], w[i][e] - c1), rs1, H[i][e]);
         }
-        float c1 = 0.f, c2 = 0.f;
-        if (p.need_post) {
-            s[0] = s[1] = 0.f;
+        if (p.dr) {
+            T* dr = rn_row(static_cast<T*>(p.dr), row, p.lddr);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int64_t c = (int64_t)(i * TPR + t) * VEC;
+                FloatVec<VEC> o;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float dv = c + e < p.cols ? H[i][e] * gate[i][e] : 0.f;
-                    const float ww = c + e < p.cols ? dv * post_g[i][e] : 0.f;
-                    w[i][e] = ww;
-                    acc[TROP_RN_POST_GAMMA][i * VEC + e] =
-                        __builtin_fmaf(dv, x[i][e], acc[TROP_RN_POST_GAMMA][i * VEC + e]);
-                    acc[TROP_RN_POST_BETA][i * VEC + e] += dv;
-                    s[0] += ww;
-                    s[1] = __builtin_fmaf(ww, x[i][e], s[1]);
-                }
+                for (int e = 0; e < VEC; ++e) o[e] = H[i][e] * p.residual_scale;
+                if (dup[i] < VEC) store_stream<T, VEC>(rn_at(dr, at[i]), from_float<T, VEC>(o));
             }
+        }
+        if (need_u) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) u[i] = uraw[i].about(mu2, at[i], p.ragged);
+            if constexpr (POST) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) u[i][e] *= rs2;
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) sa[i * VEC + e] = __builtin_fmaf(H[i][e], u[i][e], sa[i * VEC + e]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                if constexpr (POST) sb[i * VEC + e] += H[i][e];
+                w[i][e] = H[i][e] * gg[i][e];
+            }
+        if constexpr (POST) {
+            s[0] = s[1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) add(s, w[i], u[i], dup[i]);
             row_sums<TPR, 2>(s, sums[slot][1]);
-            c1 = p.post == RN_LAYER ? s[0] * p.inv_cols : 0.f;
-            c2 = s[1] * p.inv_cols;
+            const float c1 = p.post == RN_LAYER ? s[0] * p.inv_cols : 0.f, c2 = s[1] * p.inv_cols;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) w[i][e] = __builtin_fmaf(-c2, u[i][e], w[i][e] - c1) * rs2;
         }
         slot ^= 1;
         if (p.du) {
-            T* du = static_cast<T*>(p.du) + row * p.lddu;
+            T* du = rn_row(static_cast<T*>(p.du), row, p.lddu);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int64_t c = (int64_t)(i * TPR + t) * VEC;
-                FloatVec<VEC> o;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    o[e] = p.post ? __builtin_fmaf(-c2, x[i][e], w[i][e] - c1) * rstd2 : H[i][e] * gate[i][e];
-                if (c < p.cols) store_row_stream<T, VEC>(du, c, p.cols, from_float<T, VEC>(o));
-            }
+            for (int i = 0; i < NV; ++i)
+                if (dup[i] < VEC) store_stream<T, VEC>(rn_at(du, at[i]), from_float<T, VEC>(w[i]));
         }
         if (flush) {
-            if (p.dgate) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int64_t c = (int64_t)(i * TPR + t) * VEC;
-                    FloatVec<VEC> o;
+            for (int i = 0; i < NV; ++i) {
+                const FloatVec<VEC> gs = rn_gate_full<T, VEC>(p, gate_row, at[i]);
+                const FloatVec<VEC> g = rn_weight<VEC>(p, p.post_gamma, at[i], 1.f);
+                const FloatVec<VEC> b = rn_weight<VEC>(p, p.post_beta, at[i], 0.f);
+                FloatVec<VEC> o;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        o[e] = acc[TROP_RN_GATE][i * VEC + e] * p.branch_scale;
-                        acc[TROP_RN_GATE][i * VEC + e] = 0.f;
+                for (int e = 0; e < VEC; ++e) {
+                    const int k = i * VEC + e;
+                    o[e] = (g[e] * sa[k] + b[e] * sb[k]) * p.branch_scale;
+                    if constexpr (POST) {
+                        post_lds[0][k][threadIdx.x] += gs[e] * sa[k];
+                        post_lds[1][k][threadIdx.x] += gs[e] * sb[k];
                     }
-                    if (c >= p.cols) continue;
+                    sa[k] = sb[k] = 0.f;
+                }
+                if (p.dgate && dup[i] < VEC) {
                     if (sizeof(T) == 4 || p.gate_f32)
-                        store_row_stream<float, VEC>(static_cast<float*>(p.dgate) + gate_row * p.lddgate, c, p.cols, o);
+                        store_vec<float, VEC>(rn_at(rn_row(static_cast<float*>(p.dgate), gate_row, p.lddgate), at[i]), o);
                     else
-                        store_row_stream<T, VEC>(static_cast<T*>(p.dgate) + gate_row * p.lddgate, c, p.cols,
-                                                 from_float<T, VEC>(o));
+                        store_vec<T, VEC>(rn_at(rn_row(static_cast<T*>(p.dgate), gate_row, p.lddgate), at[i]),
+                                          from_float<T, VEC>(o));
                 }
             }
-            gate_row = next_gate;
+            gate_row += RPB;
             new_gate = true;
         }
     }
-#pragma unroll
-    for (int k = 0; k < TROP_RN_SUMS; ++k) {
-        if (!p.part[k]) continue;
-        float* out = p.part[k] + (int64_t)blockIdx.x * p.cols;
+    // this part's sums
+    auto leave = [&](float* out, const float (&v)[EPT]) {
+        if (!out) return;
+        out += (int64_t)blockIdx.x * cols;
         if constexpr (TPR == 64) {  // the four waves' sums, added in wave order
-            for (int wv = 0; wv < 4; ++wv) {
-                if (group == wv) {
 #pragma unroll
-                    for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                FloatVec<VEC> o;
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const int c = (i * TPR + t) * VEC + e;
-                            cols_lds[c] = wv ? cols_lds[c] + acc[k][i * VEC + e] : acc[k][i * VEC + e];
-                        }
-                }
-                __syncthreads();
+                for (int e = 0; e < VEC; ++e) o[e] = v[i * VEC + e];
+                if (dup[i] < VEC) store_vec<float, VEC>(&cols_lds[group][at[i]], o);
             }
-            for (int c = threadIdx.x; c < p.cols; c += 256) out[c] = cols_lds[c];
+            __syncthreads();
+            for (int c = threadIdx.x; c < cols; c += 256)
+                out[c] = cols_lds[0][c] + cols_lds[1][c] + cols_lds[2][c] + cols_lds[3][c];
             __syncthreads();
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int64_t c = (int64_t)(i * TPR + t) * VEC;
                 FloatVec<VEC> o;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = acc[k][i * VEC + e];
-                if (c < p.cols) store_row<float, VEC>(out, c, p.cols, o);
+                for (int e = 0; e < VEC; ++e) o[e] = v[i * VEC + e];
+                if (dup[i] < VEC) store_vec<float, VEC>(rn_at(out, at[i]), o);
             }
         }
+    };
+    if constexpr (PRE) {
+        leave(p.part[TROP_RN_PRE_GAMMA], pg);
+        leave(p.part[TROP_RN_PRE_BETA], pb);
+    }
+    if (!p.part[TROP_RN_POST_GAMMA] && !p.part[TROP_RN_POST_BETA] && !p.part[TROP_RN_GATE]) return;
+    if (whole) {
+        if constexpr (POST) {
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
+                sa[e] = post_lds[0][e][threadIdx.x];
+                sb[e] = post_lds[1][e][threadIdx.x];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const FloatVec<VEC> gs = rn_gate_full<T, VEC>(p, gate_row, at[i]);
+            const FloatVec<VEC> g = rn_weight<VEC>(p, p.post_gamma, at[i], 1.f);
+            const FloatVec<VEC> b = rn_weight<VEC>(p, p.post_beta, at[i], 0.f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int k = i * VEC + e;
+                pg[k] = g[e] * sa[k] + b[e] * sb[k];
+                sa[k] *= gs[e];
+                sb[k] *= gs[e];
+            }
+        }
+        leave(p.part[TROP_RN_GATE], pg);
+    }
+    if constexpr (POST) {
+        leave(p.part[TROP_RN_POST_GAMMA], sa);
+        leave(p.part[TROP_RN_POST_BETA], sb);
     }
 }
 
-// u or h of a row, elements [c, c + VEC) as values.
+// u or h of a row, elements [c, c + VEC) (VEC 1 or c a multiple of it) as
+// values, zeros past its end.
 template <typename T, int VEC, bool HELD>
 __device__ __forceinline__ FloatVec<VEC> rn_kept(const void* m, int64_t ld, const int8_t* codes, int64_t ldc,
                                                  const uint8_t* exps, int64_t lde, int64_t r, int64_t c, int64_t n) {
-    RnKept<T, VEC, HELD> k;
-    k.load(m, ld, codes, ldc, exps, lde, r, c, n);
-    return k.values();
+    if constexpr (HELD) {
+        Act8Lane<VEC> k;
+        k.load(codes + r * ldc, exps + r * lde, c, n);
+        return k.values();
+    } else {
+        return to_float<T, VEC>(load_row<T, VEC>(static_cast<const T*>(m) + r * ld, c, n));
+    }
 }
 
-// Rows wider than the registers: a walk for the pre norm's means, kept for the
+// Rows wider than the registers (or narrower than a vector): a walk for the pre norm's means, kept for the
 // column sums; one for the post norm's, which writes dr (and du without a post
 // norm); one for du.
 template <typename T, typename P, bool HELD>

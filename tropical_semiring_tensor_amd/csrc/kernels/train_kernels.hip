@@ -1,11 +1,9 @@
-// The gfx950 code object of the training operators: every kernel entry
-// point.  Built with hipcc --genco and embedded in the library beside the
+// The gfx950 code object of layer norm, cross entropy and AdamW: every kernel
+// entry point.  Built with hipcc --genco and embedded in the library beside the
 // contraction's; loaded once per device by the first training call.
-#include "act8_grad_w_kernels.h"
 #include "adamw_kernels.h"
 #include "cross_entropy_kernels.h"
 #include "layer_norm_kernels.h"
-#include "residual_norm_kernels.h"
 
 using namespace trop;
 
@@ -154,56 +152,3 @@ TROP_CE_TILE(grad64_raw, Raw64, (ce_logits_body<Raw64, CE_GRAD>))
 TROP_CE_TILE(grad128d_raw, Raw128d, (ce_logits_body<Raw128d, CE_GRAD>))
 TROP_CE_TILE(gradients128_raw, RawX128, (ce_gradients_body<RawX128, GradW128_f32, float>))
 TROP_CE_TILE(gradients64_raw, RawX64, (ce_gradients_body<RawX64, GradW64_f32, float>))
-
-#define TROP_ACT8_ENTRIES(NAME, T)                                                                          \
-    extern "C" __global__ __launch_bounds__(256) void trop_act8_pack_##NAME(TropAct8Params p) {              \
-        act8_pack_body<T>(p);                                                                                \
-    }                                                                                                        \
-    extern "C" __global__ __launch_bounds__(256) void trop_act8_unpack_##NAME(TropAct8Params p) {            \
-        act8_unpack_body<T>(p);                                                                              \
-    }                                                                                                        \
-    extern "C" __global__ __launch_bounds__(256) void trop_grad_w_pack_##NAME(TropGradWParams p) {           \
-        grad_w_pack_body<T>(p);                                                                              \
-    }                                                                                                        \
-    extern "C" __global__ __launch_bounds__(256) void trop_grad_w_finish_##NAME(TropGradWParams p) {         \
-        grad_w_finish_body<T>(p);                                                                            \
-    }                                                                                                        \
-    extern "C" __global__ __launch_bounds__(1024) void trop_part_sums_##NAME(TropRowSumsParams p) {          \
-        part_sums_body<T>(p);                                                                                \
-    }
-#define TROP_GRAD_W_TILE(NAME, T, EDGE, WM, WN)                                                              \
-    using GradW8_##EDGE##_##NAME = MgConfig<EDGE, EDGE, WM, WN, MM, MM, 1, 2, grad_w_parts<T>()>;            \
-    extern "C" __global__ __launch_bounds__(GradW8_##EDGE##_##NAME::THREADS) void                            \
-        trop_grad_w##EDGE##_##NAME(TropGradWParams p) {                                                      \
-        __shared__ __align__(1024) char lds[GradW8_##EDGE##_##NAME::LDS_BYTES];                              \
-        grad_w_body<GradW8_##EDGE##_##NAME, T>(p, lds);                                                      \
-    }
-TROP_ACT8_ENTRIES(f32, float)
-TROP_ACT8_ENTRIES(bf16, bf16)
-TROP_GRAD_W_TILE(f32, float, 256, 2, 4)
-TROP_GRAD_W_TILE(f32, float, 128, 2, 2)
-TROP_GRAD_W_TILE(f32, float, 64, 2, 2)
-TROP_GRAD_W_TILE(bf16, bf16, 256, 2, 4)
-TROP_GRAD_W_TILE(bf16, bf16, 128, 2, 2)
-TROP_GRAD_W_TILE(bf16, bf16, 64, 2, 2)
-
-// suffix: element type, the weights' type; backward: u and h as they are, or in 8 bits
-#define TROP_RN_ENTRY(KERNEL, THREADS, BODY)                                                                 \
-    extern "C" __global__ __launch_bounds__(THREADS) void trop_rn_##KERNEL(TropResidualParams p) { BODY(p); }
-#define TROP_RN_BACKWARD(NAME, T, P, HELD)                                                                   \
-    TROP_RN_ENTRY(bwd_wave_##NAME, 256, (residual_norm_backward_body<T, P, 64, HELD>))                       \
-    TROP_RN_ENTRY(bwd_block_##NAME, 256, (residual_norm_backward_body<T, P, 256, HELD>))                     \
-    TROP_RN_ENTRY(bwd_half_##NAME, 512, (residual_norm_backward_body<T, P, 512, HELD>))                      \
-    TROP_RN_ENTRY(bwd_wide_##NAME, 1024, (residual_norm_backward_body<T, P, 1024, HELD>))                    \
-    TROP_RN_ENTRY(bwd_loop_##NAME, 1024, (residual_norm_backward_loop_body<T, P, HELD>))                     \
-    TROP_RN_ENTRY(columns_##NAME, 256, (residual_norm_columns_body<T, P, HELD>))
-#define TROP_RN_ENTRIES(NAME, T, P)                                                                          \
-    TROP_RN_ENTRY(fwd_wave_##NAME, 256, (residual_norm_forward_body<T, P, 64>))                              \
-    TROP_RN_ENTRY(fwd_block_##NAME, 256, (residual_norm_forward_body<T, P, 256>))                            \
-    TROP_RN_ENTRY(fwd_wide_##NAME, 1024, (residual_norm_forward_body<T, P, 1024>))                           \
-    TROP_RN_ENTRY(fwd_loop_##NAME, 1024, (residual_norm_forward_loop_body<T, P>))                            \
-    TROP_RN_BACKWARD(NAME, T, P, false)                                                                      \
-    TROP_RN_BACKWARD(NAME##_held8, T, P, true)
-TROP_RN_ENTRIES(f32_f32, float, float)
-TROP_RN_ENTRIES(bf16_bf16, bf16, bf16)
-TROP_RN_ENTRIES(bf16_f32, bf16, float)

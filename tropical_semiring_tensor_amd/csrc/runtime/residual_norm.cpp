@@ -41,13 +41,17 @@ int64_t gate_group(const trop_residual_norm& op) {
 }
 int64_t gate_rows(const trop_residual_norm& op) { return ceil_div(op.rows, gate_group(op)); }
 
-// Row group of the backward by the columns 8 elements per thread cover.
-int backward_group(int64_t cols) {
-    return cols <= TROP_RN_COLS_WAVE    ? 0
-           : cols <= TROP_RN_COLS_BLOCK ? 1
-           : cols <= TROP_RN_COLS_HALF  ? 2
-           : cols <= TROP_RN_COLS_WIDE  ? 3
-                                        : 4;
+// Row group of the backward by the columns 8 elements per thread cover;
+// kLoop: rows too wide, narrower than a vector, or without a norm.
+constexpr int kLoop = 5;
+int backward_group(const trop_residual_norm& op) {
+    if (op.cols < 8 || (op.pre == TROP_NORM_NONE && op.post == TROP_NORM_NONE)) return kLoop;
+    return op.cols <= TROP_RN_COLS_WAVE    ? 0
+           : op.cols <= TROP_RN_COLS_PAIR  ? 1
+           : op.cols <= TROP_RN_COLS_BLOCK ? 2
+           : op.cols <= TROP_RN_COLS_HALF  ? 3
+           : op.cols <= TROP_RN_COLS_WIDE  ? 4
+                                           : kLoop;
 }
 
 // The backward's parts: each inside one gate row (group_parts to one), so
@@ -59,7 +63,7 @@ struct Parts {
 };
 Parts backward_parts(const trop_residual_norm& op) {
     if (op.rows == 0) return {0, 1, 1};
-    const int64_t group = gate_group(op), gates = gate_rows(op), rpb = backward_group(op.cols) == 0 ? 4 : 1;
+    const int64_t group = gate_group(op), gates = gate_rows(op), rpb = backward_group(op) == 0 ? 4 : 1;
     if (gates <= TROP_RN_MAX_PARTS) {
         const int64_t most = std::min<int64_t>(TROP_RN_MAX_PARTS / gates, ceil_div(group, rpb));
         const int64_t rows = ceil_div(group, most), per = ceil_div(group, rows);
@@ -89,7 +93,7 @@ trop_status plan(const trop_residual_norm& op, Layout* l) {
         if (has[i]) total += one;
     }
     l->row_sums = total / 4;
-    if (backward_group(op.cols) == 4 && op.pre != TROP_NORM_NONE) {
+    if (backward_group(op) == kLoop && op.pre != TROP_NORM_NONE) {
         int64_t more;
         if (__builtin_mul_overflow(op.rows, (int64_t)8, &more) || __builtin_add_overflow(total, more, &total))
             return invalid("workspace size overflows");
@@ -114,6 +118,7 @@ trop_status common(const trop_residual_norm& op, SpanChecker& checker, TropResid
         p.ldgate = op.ldgate;
     }
     p.gate_f32 = op.gate_dtype == TROP_F32;
+    p.weight_f32 = op.param_dtype == TROP_F32;
     p.gate_group = gate_group(op);
     auto weight = [&](bool there, const void* w, const char* what) -> const void* {
         if (!there || !w || st != TROP_OK) return nullptr;
@@ -146,10 +151,10 @@ trop_status launch_rows(int dev, int id, trop_train_family fam, TropResidualPara
     return st;
 }
 
-trop_status forward(const trop_residual_norm* opp, trop_matrix r, trop_matrix u, trop_matrix h, trop_matrix y,
-                    float* post_mean, float* post_rstd, float* pre_mean, float* pre_rstd, const trop_act8* u8,
-                    const trop_act8* h8, void* stream) {
-    if (!opp) return invalid("trop_residual_norm is NULL");
+trop_status forward(const trop_residual_norm* opp, const trop_residual_norm_rows* io, void* stream) {
+    if (!opp || !io) return invalid("NULL structure");
+    const trop_matrix &r = io->r, &u = io->u, &h = io->h, &y = io->y;
+    const trop_act8 *u8 = io->u8, *h8 = io->h8;
     const trop_residual_norm& op = *opp;
     trop_status st = check_op(op);
     if (st != TROP_OK) return st;
@@ -173,10 +178,10 @@ trop_status forward(const trop_residual_norm* opp, trop_matrix r, trop_matrix u,
         st = checker.span(v, op.rows, 4, what);
         return v;
     };
-    p.post_mean = rows(op.post == TROP_NORM_LAYER, post_mean, "post_mean");
-    p.post_rstd = rows(op.post != TROP_NORM_NONE, post_rstd, "post_rstd");
-    p.pre_mean = rows(op.pre == TROP_NORM_LAYER, pre_mean, "pre_mean");
-    p.pre_rstd = rows(op.pre != TROP_NORM_NONE, pre_rstd, "pre_rstd");
+    p.post_mean = rows(op.post == TROP_NORM_LAYER, io->post_mean, "post_mean");
+    p.post_rstd = rows(op.post != TROP_NORM_NONE, io->post_rstd, "post_rstd");
+    p.pre_mean = rows(op.pre == TROP_NORM_LAYER, io->pre_mean, "pre_mean");
+    p.pre_rstd = rows(op.pre != TROP_NORM_NONE, io->pre_rstd, "pre_rstd");
     if (st != TROP_OK) return st;
     if (u8) {
         if ((st = check_act8(checker, *u8, op.rows, op.cols, "u8's")) != TROP_OK) return st;
@@ -364,12 +369,14 @@ trop_status backward(const trop_residual_norm* opp, const trop_residual_norm_kep
         for (int i = 0; i < TROP_RN_SUMS; ++i) p.part[i] = asked[i] ? ws + l.at[i] : nullptr;
         p.need_v = g.dgate.data != nullptr;
         p.need_post = through_post;
-        const int kind = backward_group(op.cols), idx = ln_index(op.dtype, op.param_dtype) + (held ? 3 : 0);
-        if (kind < 4) {
-            static const TrainKernelId ids[] = {TK_RN_BWD_WAVE, TK_RN_BWD_BLOCK, TK_RN_BWD_HALF, TK_RN_BWD_WIDE};
-            static const uint32_t threads[] = {256, 256, 512, 1024};
-            st = train_launch(dev, (TrainKernelId)(ids[kind] + idx), TROP_T_RESIDUAL_BACKWARD, l.parts.parts,
-                              threads[kind], &p, s);
+        p.ragged = op.cols % (16 / (int64_t)elem_size(op.dtype)) != 0;
+        const int kind = need_u || pre ? backward_group(op) : kLoop;
+        const int idx = ln_index(op.dtype, op.param_dtype) + (held ? 3 : 0);
+        if (kind != kLoop) {
+            static const uint32_t threads[] = {256, 128, 256, 512, 1024};
+            const int norms = !pre ? 1 : post && need_u ? 2 : 0;
+            st = train_launch(dev, (TrainKernelId)(TK_RN_BWD + 12 * kind + 4 * norms + 2 * held + (op.dtype == TROP_BF16)),
+                              TROP_T_RESIDUAL_BACKWARD, l.parts.parts, threads[kind], &p, s);
         } else {
             p.row_sums = pre && (sum_post || g.dgate.data) ? ws + l.row_sums : nullptr;
             if (g.dr.data || g.du.data || p.row_sums)
@@ -390,13 +397,9 @@ trop_status backward(const trop_residual_norm* opp, const trop_residual_norm_kep
 }  // namespace
 }  // namespace trop
 
-extern "C" trop_status tropical_residual_norm_forward(const trop_residual_norm* op, trop_matrix r, trop_matrix u,
-                                                      trop_matrix h, trop_matrix y, float* post_mean, float* post_rstd,
-                                                      float* pre_mean, float* pre_rstd, const trop_act8* u8,
-                                                      const trop_act8* h8, void* stream) {
-    return trop::guarded("tropical_residual_norm_forward", [&] {
-        return trop::forward(op, r, u, h, y, post_mean, post_rstd, pre_mean, pre_rstd, u8, h8, stream);
-    });
+extern "C" trop_status tropical_residual_norm_forward(const trop_residual_norm* op, const trop_residual_norm_rows* rows,
+                                                      void* stream) {
+    return trop::guarded("tropical_residual_norm_forward", [&] { return trop::forward(op, rows, stream); });
 }
 
 extern "C" trop_status tropical_residual_norm_backward(const trop_residual_norm* op, const trop_residual_norm_kept* kept,

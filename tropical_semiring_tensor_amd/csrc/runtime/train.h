@@ -52,11 +52,8 @@ enum TrainKernelId : int {
     TK_RN_FWD_BLOCK = TK_RN_FWD_WAVE + 3,
     TK_RN_FWD_WIDE = TK_RN_FWD_BLOCK + 3,
     TK_RN_FWD_LOOP = TK_RN_FWD_WIDE + 3,
-    TK_RN_BWD_WAVE = TK_RN_FWD_LOOP + 3,  // + ln_index + 3 (u and h in 8 bits)
-    TK_RN_BWD_BLOCK = TK_RN_BWD_WAVE + 6,
-    TK_RN_BWD_HALF = TK_RN_BWD_BLOCK + 6,
-    TK_RN_BWD_WIDE = TK_RN_BWD_HALF + 6,
-    TK_RN_BWD_LOOP = TK_RN_BWD_WIDE + 6,
+    TK_RN_BWD = TK_RN_FWD_LOOP + 3,  // + 12 row group + 4 (norms: pre, post, both) + 2 (8 bits) + (bf16 ? 1 : 0)
+    TK_RN_BWD_LOOP = TK_RN_BWD + 60,   // + ln_index + 3 (u and h in 8 bits)
     TK_RN_COLUMNS = TK_RN_BWD_LOOP + 6,
     TK_COUNT = TK_RN_COLUMNS + 6
 };
@@ -80,8 +77,8 @@ inline int ln_index(trop_dtype dt, trop_dtype pdt) {
 
 inline size_t elem_size(trop_dtype dt) { return dt == TROP_BF16 ? 2 : 4; }
 
-// Extents and allocations of one call's pointers.  One inside the allocation
-// that the call checked last needs no further query (small tensors share the
+// Extents and allocations of one call's pointers.  One inside an allocation
+// that the call looked up before needs no further query (small tensors share the
 // allocator's segments, a call's own are often neighbours).
 class SpanChecker {
    public:
@@ -93,7 +90,9 @@ class SpanChecker {
 
    private:
     int dev_;
-    uintptr_t lo_ = 1, hi_ = 0;
+    static constexpr int kRanges = 8;
+    int found_ = 0;  // ranges looked up, the first kRanges of them kept
+    uintptr_t lo_[kRanges], hi_[kRanges];
 };
 
 // Both buffers of an 8-bit rows x cols matrix.

@@ -1,6 +1,6 @@
-// The training operators' code object: loaded once per process and device by
+// The training operators' code objects: loaded once per process and device by
 // the first training call, apart from the contraction's, so that programs
-// that only contract never load it.  Launches and loads are counted here.
+// that only contract never load them.  Launches and loads are counted here.
 #include <atomic>
 #include <cstring>
 #include <mutex>
@@ -8,8 +8,9 @@
 
 #include "train.h"
 
-// Embedded code object (co_blob.S).
+// Embedded code objects (co_blob.S): kernels below TK_ACT8_PACK, and from it on.
 extern "C" const unsigned char trop_train_code_object[];
+extern "C" const unsigned char trop_block_code_object[];
 
 namespace trop {
 namespace {
@@ -76,18 +77,22 @@ const char* const kNames[] = {
     "trop_rn_" KERNEL "_f32_f32" HELD, "trop_rn_" KERNEL "_bf16_bf16" HELD, "trop_rn_" KERNEL "_bf16_f32" HELD,
     TROP_RN_TYPES("fwd_wave", "") TROP_RN_TYPES("fwd_block", "")
     TROP_RN_TYPES("fwd_wide", "") TROP_RN_TYPES("fwd_loop", "")
-    TROP_RN_TYPES("bwd_wave", "") TROP_RN_TYPES("bwd_wave", "_held8")
-    TROP_RN_TYPES("bwd_block", "") TROP_RN_TYPES("bwd_block", "_held8")
-    TROP_RN_TYPES("bwd_half", "") TROP_RN_TYPES("bwd_half", "_held8")
-    TROP_RN_TYPES("bwd_wide", "") TROP_RN_TYPES("bwd_wide", "_held8")
+#define TROP_RN_NORMS(KERNEL)                                                              \
+    TROP_RN_KEPT(KERNEL "_pre") TROP_RN_KEPT(KERNEL "_post") TROP_RN_KEPT(KERNEL "_both")
+#define TROP_RN_KEPT(KERNEL) \
+    "trop_rn_bwd_" KERNEL "_f32", "trop_rn_bwd_" KERNEL "_bf16", "trop_rn_bwd_" KERNEL "_f32_held8", \
+    "trop_rn_bwd_" KERNEL "_bf16_held8",
+    TROP_RN_NORMS("wave") TROP_RN_NORMS("pair") TROP_RN_NORMS("block") TROP_RN_NORMS("half") TROP_RN_NORMS("wide")
     TROP_RN_TYPES("bwd_loop", "") TROP_RN_TYPES("bwd_loop", "_held8")
     TROP_RN_TYPES("columns", "") TROP_RN_TYPES("columns", "_held8")
+#undef TROP_RN_KEPT
+#undef TROP_RN_NORMS
 #undef TROP_RN_TYPES
 };
 static_assert(sizeof(kNames) / sizeof(kNames[0]) == TK_COUNT, "training kernels");
 
 struct TrainModule {
-    hipModule_t module = nullptr;
+    hipModule_t module[2] = {};
     hipFunction_t fn[TK_COUNT] = {};
 };
 
@@ -102,16 +107,24 @@ trop_status load(int dev) {
     std::lock_guard<std::mutex> lock(g_mu);
     if (g_dev[dev].load(std::memory_order_acquire)) return TROP_OK;
     TrainModule* m = new TrainModule;
-    hipError_t e = hipModuleLoadData(&m->module, trop_train_code_object);
-    trop_status st = e == hipSuccess ? TROP_OK : hip_fail(e, "hipModuleLoadData (training code object)");
-    if (st == TROP_OK) {
+    const unsigned char* const objects[] = {trop_train_code_object, trop_block_code_object};
+    trop_status st = TROP_OK;
+    for (int k = 0; k < 2 && st == TROP_OK; ++k) {
+        hipError_t e = hipModuleLoadData(&m->module[k], objects[k]);
+        if (e != hipSuccess) {
+            m->module[k] = nullptr;
+            st = hip_fail(e, "hipModuleLoadData (training code object)");
+            break;
+        }
         g_loads.fetch_add(1);
-        for (int i = 0; i < TK_COUNT && st == TROP_OK; ++i) {
-            e = hipModuleGetFunction(&m->fn[i], m->module, kNames[i]);
+        for (int i = k ? TK_ACT8_PACK : 0; i < (k ? TK_COUNT : TK_ACT8_PACK) && st == TROP_OK; ++i) {
+            e = hipModuleGetFunction(&m->fn[i], m->module[k], kNames[i]);
             if (e != hipSuccess) st = hip_fail(e, kNames[i]);
         }
-        if (st != TROP_OK) (void)hipModuleUnload(m->module);
     }
+    if (st != TROP_OK)
+        for (hipModule_t module : m->module)
+            if (module) (void)hipModuleUnload(module);
     if (st != TROP_OK) {
         delete m;
         return st;
@@ -150,7 +163,10 @@ void reset_train_launches() {
 
 trop_status SpanChecker::span(const void* p, int64_t elems, size_t elem_bytes, const char* what, int64_t index) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    if (a >= lo_ && a < hi_ && a % elem_bytes == 0 && (unsigned __int128)elems * elem_bytes <= hi_ - a) return TROP_OK;
+    const int known = found_ < kRanges ? found_ : kRanges;
+    for (int i = known - 1; i >= 0; --i)
+        if (a >= lo_[i] && a < hi_[i] && a % elem_bytes == 0 && (unsigned __int128)elems * elem_bytes <= hi_[i] - a)
+            return TROP_OK;
     const std::string name = index < 0 ? what : std::string(what) + " of tensor " + std::to_string(index);
     if (a % elem_bytes) return fail(TROP_ERR_INVALID_ARGUMENT, name + " is not aligned to its elements");
     const trop_status st = check_device_span(p, dev_, elems, elem_bytes, name.c_str());
@@ -158,8 +174,9 @@ trop_status SpanChecker::span(const void* p, int64_t elems, size_t elem_bytes, c
     hipDeviceptr_t base = nullptr;
     size_t size = 0;
     if (hipMemGetAddressRange(&base, &size, const_cast<void*>(p)) == hipSuccess) {
-        lo_ = reinterpret_cast<uintptr_t>(base);
-        hi_ = lo_ + size;
+        const int at = found_++ % kRanges;
+        lo_[at] = reinterpret_cast<uintptr_t>(base);
+        hi_[at] = lo_[at] + size;
     } else {
         (void)hipGetLastError();
     }

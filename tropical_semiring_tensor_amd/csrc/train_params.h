@@ -122,8 +122,9 @@ struct TropGradWParams {
 };
 
 // ---- between two residual blocks ---------------------------------------------
-// Columns a wave / 256 / 512 / 1024 threads of the backward hold (8 each).
+// Columns a wave / 128 / 256 / 512 / 1024 threads of the backward hold (8 each).
 #define TROP_RN_COLS_WAVE 512
+#define TROP_RN_COLS_PAIR 1024
 #define TROP_RN_COLS_BLOCK 2048
 #define TROP_RN_COLS_HALF 4096
 #define TROP_RN_COLS_WIDE 8192
@@ -166,9 +167,11 @@ struct TropResidualParams {
     int64_t group_parts;    // backward: parts of a gate row, or 0: a part takes whole gate rows
     float residual_scale, branch_scale, post_eps, pre_eps, inv_cols;
     int32_t post, pre;      // trop_norm
-    int32_t gate_f32;
+    int32_t gate_f32, weight_f32;
     int32_t parts;
     int32_t need_v, need_post;  // backward: the gate's gradient; the post norm's gradients or du through it
+    int32_t ragged;         // backward: rows that are no multiple of a 16-byte vector
+    int32_t pad_;
 };
 
 // Partial sums of up to TROP_RN_SUMS column sums: entry i has `rows[i]` output
