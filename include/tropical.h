@@ -869,9 +869,10 @@ TROP_API trop_status tropical_residual_norm_backward(const trop_residual_norm* o
                                             size_t workspace_bytes, void* stream);
 
 /* Workspace (bytes) of the backward with any of its gradients asked for
- * (rows, cols, gate, gate_group and the norms of op are looked at; gate only
- * for whether it is NULL).  Host-only.
- * Errors: TROP_ERR_INVALID_ARGUMENT (NULL, negative size, bad norm or group). */
+ * (dtype, rows, cols, gate, gate_group and the norms of op are looked at; gate
+ * only for whether it is NULL).  Host-only.
+ * Errors: TROP_ERR_INVALID_ARGUMENT (NULL, bad dtype, norm or group, negative
+ *   size). */
 TROP_API trop_status tropical_residual_norm_backward_workspace_size(const trop_residual_norm* op, size_t* bytes);
 
 /* Kernel families of the training operators, counted apart from trop_stats. */

@@ -459,7 +459,7 @@ def test_graph_and_streams(tb, cols):
     q = Problem(64, cols, BF16, F32, "rms", "layer", gates=2)
     h, y = torch.empty_like(q.u), torch.empty_like(q.u)
     u8, h8 = tb.tropical_act8_pack(q.u), tb.tropical_act8_pack(q.u)
-    ws = torch.empty(tb.tropical_residual_norm_backward_workspace_size(64, cols, "rms", "layer", 32), dtype=torch.uint8,
+    ws = torch.empty(tb.tropical_residual_norm_backward_workspace_size(BF16, 64, cols, "rms", "layer", 32), dtype=torch.uint8,
                      device=DEV)
 
     def step(**kw):

@@ -1198,7 +1198,7 @@ def tropical_residual_norm_backward(dy, dh, u, h, post_mean=None, post_rstd=None
         i += 1
     need = 0
     if workspace is None and sums:
-        need = _residual_workspace(rows, cols, op.post, op.pre, op.gate_group if gate is not None else None)
+        need = _residual_workspace(dt, rows, cols, op.post, op.pre, op.gate_group if gate is not None else None)
     workspace, wp, wn = _workspace(workspace, need, dev)
     st = lib().tropical_residual_norm_backward(op, _kept_fields(*kept), _grads_fields(*grads), wp, wn,
                                                _stream_ptr(None, lead))
@@ -1208,8 +1208,8 @@ def tropical_residual_norm_backward(dy, dh, u, h, post_mean=None, post_rstd=None
 
 
 @functools.lru_cache(maxsize=4096)
-def _residual_workspace(rows, cols, post, pre, gate_group):
-    op = trop_residual_norm(post=post, pre=pre, rows=rows, cols=cols)
+def _residual_workspace(dt, rows, cols, post, pre, gate_group):
+    op = trop_residual_norm(dtype=dt, post=post, pre=pre, rows=rows, cols=cols)
     if gate_group is not None:
         op.gate, op.gate_group = 1, gate_group
     nb = ctypes.c_size_t(0)
@@ -1218,11 +1218,14 @@ def _residual_workspace(rows, cols, post, pre, gate_group):
     return nb.value
 
 
-def tropical_residual_norm_backward_workspace_size(rows, cols, post=None, pre="layer", gate_group=None):
-    """Workspace bytes of a backward (gate_group: None without a gate)."""
+def tropical_residual_norm_backward_workspace_size(dtype, rows, cols, post=None, pre="layer", gate_group=None):
+    """Workspace bytes of a backward (dtype: torch.float32 or torch.bfloat16;
+    gate_group: None without a gate)."""
+    if dtype not in _TRAIN_DTYPES:
+        raise TypeError(f"float32 or bfloat16 only, got {dtype}")
     if post not in _NORMS or pre not in _NORMS:
         raise ValueError("norms are None, 'layer' or 'rms'")
-    return _residual_workspace(int(rows), int(cols), _NORMS[post], _NORMS[pre],
+    return _residual_workspace(_TRAIN_DTYPES[dtype], int(rows), int(cols), _NORMS[post], _NORMS[pre],
                                None if gate_group is None else int(gate_group))
 
 

@@ -49,6 +49,7 @@ TROP_GRAD_W_TILE(bf16, bf16, 64, 2, 2)
 #define TROP_RN_ENTRIES(NAME, T, P)                                                                          \
     TROP_RN_ENTRY(fwd_wave_##NAME, 256, (residual_norm_forward_body<T, P, 64>))                              \
     TROP_RN_ENTRY(fwd_block_##NAME, 256, (residual_norm_forward_body<T, P, 256>))                            \
+    TROP_RN_ENTRY_WAVES(fwd_half_##NAME, 512, 4, (residual_norm_forward_body<T, P, 512>))                    \
     TROP_RN_ENTRY(fwd_wide_##NAME, 1024, (residual_norm_forward_body<T, P, 1024>))                           \
     TROP_RN_ENTRY(fwd_loop_##NAME, 1024, (residual_norm_forward_loop_body<T, P>))                            \
     TROP_RN_WIDE(NAME, T, P, false)                                                                          \
@@ -56,18 +57,24 @@ TROP_GRAD_W_TILE(bf16, bf16, 64, 2, 2)
 TROP_RN_ENTRIES(f32_f32, float, float)
 TROP_RN_ENTRIES(bf16_bf16, bf16, bf16)
 TROP_RN_ENTRIES(bf16_f32, bf16, float)
-// rows in registers: which norms there are, element type
+// rows in registers: which norms there are, element type (at least four waves
+// to a SIMD in bfloat16)
+#define TROP_RN_ROWS(KERNEL, NAME, THREADS, T, TPR, EPT, HELD, PRE, POST, WORK)                              \
+    TROP_RN_ENTRY_WAVES(bwd_##KERNEL##_##NAME, THREADS, sizeof(T) == 2 ? 4 : 1,                              \
+                        (residual_norm_backward_body<T, TPR, EPT, HELD, PRE, POST, WORK>))
 #define TROP_RN_BACKWARD(NAME, T, HELD, PRE, POST)                                                           \
-    TROP_RN_ENTRY(bwd_wave_##NAME, 256, (residual_norm_backward_body<T, 64, 8, HELD, PRE, POST>))            \
-    TROP_RN_ENTRY(bwd_pair_##NAME, 128, (residual_norm_backward_body<T, 128, 8, HELD, PRE, POST>))           \
-    TROP_RN_ENTRY(bwd_block_##NAME, 256, (residual_norm_backward_body<T, 256, 8, HELD, PRE, POST>))          \
-    TROP_RN_ENTRY_WAVES(bwd_half_##NAME, 512, sizeof(T) == 2 ? 4 : 1,                                        \
-                        (residual_norm_backward_body<T, 512, 8, HELD, PRE, POST>))                           \
-    TROP_RN_ENTRY(bwd_wide_##NAME, 1024, (residual_norm_backward_body<T, 1024, 8, HELD, PRE, POST>))
+    TROP_RN_ROWS(wave, NAME, 256, T, 64, 8, HELD, PRE, POST, RN_ALL)                                         \
+    TROP_RN_ROWS(pair, NAME, 128, T, 128, 8, HELD, PRE, POST, RN_ALL)                                        \
+    TROP_RN_ROWS(block, NAME, 256, T, 256, 8, HELD, PRE, POST, RN_ALL)                                       \
+    TROP_RN_ROWS(half, NAME, 512, T, 512, 8, HELD, PRE, POST, RN_ALL)                                        \
+    TROP_RN_ROWS(wide, NAME, 1024, T, 1024, 8, HELD, PRE, POST, RN_ALL)                                      \
+    TROP_RN_ROWS(rows, NAME, 1024, T, 1024, 16, HELD, PRE, POST, RN_ROWS)                                    \
+    TROP_RN_ROWS(sums, NAME, 256, T, 256, 8, HELD, PRE, POST, RN_COLUMNS)
 #define TROP_RN_NORMS(NAME, T, HELD)                                                                         \
     TROP_RN_BACKWARD(pre_##NAME, T, HELD, true, false)                                                       \
     TROP_RN_BACKWARD(post_##NAME, T, HELD, false, true)                                                      \
-    TROP_RN_BACKWARD(both_##NAME, T, HELD, true, true)
+    TROP_RN_BACKWARD(both_##NAME, T, HELD, true, true)                                                       \
+    TROP_RN_ROWS(sums, none_##NAME, 256, T, 256, 8, HELD, false, false, RN_COLUMNS)
 TROP_RN_NORMS(f32, float, false)
 TROP_RN_NORMS(bf16, bf16, false)
 TROP_RN_NORMS(f32_held8, float, true)

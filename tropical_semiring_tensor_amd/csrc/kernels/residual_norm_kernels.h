@@ -399,6 +399,11 @@ struct RnKept<T, VEC, true> {
     }
 };
 
+// What a kernel does with its rows: everything; for rows too wide to keep their
+// sums in registers, the rows' gradients (and the pre norm's two means, left for
+// the sums); their sums, each workgroup TPR EPT columns of a part's rows.
+enum RnWork { RN_ALL, RN_ROWS, RN_COLUMNS };
+
 // The rows of part blockIdx.x, TPR threads to a row, EPT elements to a thread
 // in vectors of 16 bytes.  A part inside a gate row: rows one by one, to the
 // workgroup's row groups in turn (four waves, or one group).  A part of whole
@@ -414,28 +419,37 @@ struct RnKept<T, VEC, true> {
 //   dgamma = gate A,  dbeta = gate B,  dgate = gamma A + beta B
 // (all but the scales).  A part of whole gate rows adds up the first two in
 // LDS, a slot to each thread, whenever a gate row ends.
-template <typename T, int TPR, int EPT, bool HELD, bool PRE, bool POST>
+template <typename T, int TPR, int EPT, bool HELD, bool PRE, bool POST, RnWork WORK>
 __device__ __forceinline__ void residual_norm_backward_body(const TropResidualParams& p) {
     constexpr int VEC = ln_vec<T>(), NV = EPT / VEC, RPB = TPR == 64 ? 4 : 1, THREADS = TPR * RPB;
     using V = typename VecOf<T, VEC>::raw;
     __shared__ RowSums<TPR, 2> sums[2][2];
-    __shared__ float post_lds[POST ? 2 : 1][POST ? EPT : 1][THREADS];
+    constexpr bool SUMS = WORK != RN_ROWS, ROWS = WORK != RN_COLUMNS;
+    // a row of 16 elements to a thread leaves no registers for its weights
+    constexpr bool KEEP = EPT <= 8;
+    __shared__ float post_lds[POST && SUMS ? 2 : 1][POST && SUMS ? EPT : 1][THREADS];
     __shared__ float cols_lds[TPR == 64 ? 4 : 1][TPR == 64 ? TPR * EPT : 1];
     const int t = threadIdx.x % TPR, group = RPB == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
     const int cols = (int)p.cols;
+    int part = blockIdx.x, col0 = 0;
+    if constexpr (!ROWS) {
+        const int block = (int)p.col0 + part / p.parts;
+        part %= p.parts;
+        col0 = block * (TPR * EPT);
+    }
     uint32_t at[NV];
     int dup[NV];  // first column; elements of the vector that the lane before holds
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + t) * VEC;
+        const int c = col0 + (i * TPR + t) * VEC;
         at[i] = min(c, cols - VEC);
         dup[i] = c - (int)at[i];
     }
-    float pg[EPT] = {}, pb[EPT] = {}, sa[EPT] = {}, sb[EPT] = {};  // sums of dy x^, dy; A and B
+    float pg[SUMS ? EPT : 1] = {}, pb[SUMS ? EPT : 1] = {}, sa[SUMS ? EPT : 1] = {}, sb[SUMS ? EPT : 1] = {};  // sums of dy x^, dy; A and B
     V dyv[NV], dhv[NV] = {};
     RnKept<T, VEC, HELD> hv[NV], uv[NV];
-    float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f;
-    const bool need_u = POST || p.need_v;
+    float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f, c1_row = 0.f, c2_row = 0.f;
+    const bool need_u = POST || (SUMS && p.need_v);
     auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -449,6 +463,10 @@ __device__ __forceinline__ void residual_norm_backward_body(const TropResidualPa
         if constexpr (PRE) {
             if (p.pre_mean) mean1 = p.pre_mean[r];
             rstd1 = p.pre_rstd[r];
+            if (!ROWS && p.row_sums) {  // (not there where no sum needs H)
+                c1_row = p.row_sums[2 * r];
+                c2_row = p.row_sums[2 * r + 1];
+            }
         }
         if constexpr (POST) {
             if (p.post_mean) mean2 = p.post_mean[r];
@@ -456,19 +474,31 @@ __device__ __forceinline__ void residual_norm_backward_body(const TropResidualPa
         }
     };
     FloatVec<VEC> pre_g[NV], gg[NV];  // gamma of the pre norm; branch_scale gate, times gamma of the post norm
+    auto weights = [&](bool pre, bool post, int64_t gate_row) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) pre_g[i] = rn_weight<VEC>(p, p.pre_gamma, at[i], 1.f);
+        for (int i = 0; i < NV; ++i) {
+            if (pre && PRE) pre_g[i] = rn_weight<VEC>(p, p.pre_gamma, at[i], 1.f);
+            if (!post) continue;
+            gg[i] = rn_gate_full<T, VEC>(p, gate_row, at[i]);
+            if constexpr (POST) {
+                const FloatVec<VEC> g = rn_weight<VEC>(p, p.post_gamma, at[i], 1.f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) gg[i][e] *= g[e];
+            }
+        }
+    };
+    if constexpr (KEEP) weights(true, false, 0);
     // this row group's rows: units of unit_rows, RPB units apart
     const bool whole = p.group_parts == 0;
     const int64_t unit_rows = whole ? p.gate_group : 1;
     int64_t first, end, gate_row;  // rows of the part
     if (whole) {
-        first = blockIdx.x * p.part_rows;
+        first = part * p.part_rows;
         end = min(first + p.part_rows, p.rows);
         gate_row = 0;
     } else {
-        gate_row = rn_divide(blockIdx.x, p.group_parts);
-        const int64_t q = blockIdx.x - gate_row * p.group_parts, last = min((gate_row + 1) * p.gate_group, p.rows);
+        gate_row = rn_divide(part, p.group_parts);
+        const int64_t q = part - gate_row * p.group_parts, last = min((gate_row + 1) * p.gate_group, p.rows);
         first = min(gate_row * p.gate_group + q * p.part_rows, last);
         end = min(first + p.part_rows, last);
     }
@@ -476,7 +506,7 @@ __device__ __forceinline__ void residual_norm_backward_body(const TropResidualPa
     if (r < end) fetch(r);
     if (whole) {
         if (r < end) gate_row = rn_divide(r, p.gate_group);
-        if constexpr (POST) {
+        if constexpr (POST && SUMS) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) post_lds[0][e][threadIdx.x] = post_lds[1][e][threadIdx.x] = 0.f;
         }
@@ -507,16 +537,8 @@ __device__ __forceinline__ void residual_norm_backward_body(const TropResidualPa
     int slot = 0;
     bool new_gate = true;
     while (r < end) {  // the groups of a workgroup share barriers only when RPB = 1
-        if (new_gate) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                gg[i] = rn_gate_full<T, VEC>(p, gate_row, at[i]);
-                if constexpr (POST) {
-                    const FloatVec<VEC> g = rn_weight<VEC>(p, p.post_gamma, at[i], 1.f);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) gg[i][e] *= g[e];
-                }
-            }
+        if (KEEP && new_gate) {
+            weights(false, true, gate_row);
             new_gate = false;
         }
         const int64_t row = r;
@@ -537,28 +559,39 @@ __device__ __forceinline__ void residual_norm_backward_body(const TropResidualPa
             if constexpr (PRE) {
                 const FloatVec<VEC> dy = to_float<T, VEC>(dyv[i]);
                 x[i] = hv[i].about(mu1, at[i], p.ragged);
+                if constexpr (!KEEP) pre_g[i] = rn_weight<VEC>(p, p.pre_gamma, at[i], 1.f);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     x[i][e] *= rs1;
                     w[i][e] = dy[e] * pre_g[i][e];
-                    pg[i * VEC + e] = __builtin_fmaf(dy[e], x[i][e], pg[i * VEC + e]);
-                    pb[i * VEC + e] += dy[e];
+                    if constexpr (SUMS) {
+                        pg[i * VEC + e] = __builtin_fmaf(dy[e], x[i][e], pg[i * VEC + e]);
+                        pb[i * VEC + e] += dy[e];
+                    }
                 }
-                add(s, w[i], x[i], dup[i]);
+                if constexpr (ROWS) add(s, w[i], x[i], dup[i]);
             }
             uraw[i] = uv[i];
         }
+        float c1 = rn_scalar(c1_row), c2 = rn_scalar(c2_row);
         if (r < end) fetch(r);
         if constexpr (PRE) {
-            row_sums<TPR, 2>(s, sums[slot][0]);
-            const float c1 = p.pre == RN_LAYER ? s[0] * p.inv_cols : 0.f, c2 = s[1] * p.inv_cols;
+            if constexpr (ROWS) {
+                row_sums<TPR, 2>(s, sums[slot][0]);
+                c1 = p.pre == RN_LAYER ? s[0] * p.inv_cols : 0.f;
+                c2 = s[1] * p.inv_cols;
+                if (WORK == RN_ROWS && p.row_sums && t == 0) {
+                    p.row_sums[2 * row] = c1;
+                    p.row_sums[2 * row + 1] = c2;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
                     H[i][e] = __builtin_fmaf(__builtin_fmaf(-c2, x[i][e], w[i][e] - c1), rs1, H[i][e]);
         }
-        if (p.dr) {
+        if (ROWS && p.dr) {
             T* dr = rn_row(static_cast<T*>(p.dr), row, p.lddr);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -577,123 +610,131 @@ __device__ __forceinline__ void residual_norm_backward_body(const TropResidualPa
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) u[i][e] *= rs2;
             }
+            if constexpr (SUMS) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+                for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) sa[i * VEC + e] = __builtin_fmaf(H[i][e], u[i][e], sa[i * VEC + e]);
+                    for (int e = 0; e < VEC; ++e) sa[i * VEC + e] = __builtin_fmaf(H[i][e], u[i][e], sa[i * VEC + e]);
+            }
         }
+        if constexpr (!KEEP) weights(false, true, gate_row);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                if constexpr (POST) sb[i * VEC + e] += H[i][e];
-                w[i][e] = H[i][e] * gg[i][e];
+                if constexpr (POST && SUMS) sb[i * VEC + e] += H[i][e];
+                if constexpr (ROWS) w[i][e] = H[i][e] * gg[i][e];
             }
-        if constexpr (POST) {
+        if constexpr (POST && ROWS) {
             s[0] = s[1] = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) add(s, w[i], u[i], dup[i]);
             row_sums<TPR, 2>(s, sums[slot][1]);
-            const float c1 = p.post == RN_LAYER ? s[0] * p.inv_cols : 0.f, c2 = s[1] * p.inv_cols;
+            c1 = p.post == RN_LAYER ? s[0] * p.inv_cols : 0.f;
+            c2 = s[1] * p.inv_cols;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) w[i][e] = __builtin_fmaf(-c2, u[i][e], w[i][e] - c1) * rs2;
         }
         slot ^= 1;
-        if (p.du) {
+        if (ROWS && p.du) {
             T* du = rn_row(static_cast<T*>(p.du), row, p.lddu);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (dup[i] < VEC) store_stream<T, VEC>(rn_at(du, at[i]), from_float<T, VEC>(w[i]));
         }
         if (flush) {
+            if constexpr (SUMS) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const FloatVec<VEC> gs = rn_gate_full<T, VEC>(p, gate_row, at[i]);
-                const FloatVec<VEC> g = rn_weight<VEC>(p, p.post_gamma, at[i], 1.f);
-                const FloatVec<VEC> b = rn_weight<VEC>(p, p.post_beta, at[i], 0.f);
-                FloatVec<VEC> o;
+                for (int i = 0; i < NV; ++i) {
+                    const FloatVec<VEC> gs = rn_gate_full<T, VEC>(p, gate_row, at[i]);
+                    const FloatVec<VEC> g = rn_weight<VEC>(p, p.post_gamma, at[i], 1.f);
+                    const FloatVec<VEC> b = rn_weight<VEC>(p, p.post_beta, at[i], 0.f);
+                    FloatVec<VEC> o;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const int k = i * VEC + e;
-                    o[e] = (g[e] * sa[k] + b[e] * sb[k]) * p.branch_scale;
-                    if constexpr (POST) {
-                        post_lds[0][k][threadIdx.x] += gs[e] * sa[k];
-                        post_lds[1][k][threadIdx.x] += gs[e] * sb[k];
+                    for (int e = 0; e < VEC; ++e) {
+                        const int k = i * VEC + e;
+                        o[e] = (g[e] * sa[k] + b[e] * sb[k]) * p.branch_scale;
+                        if constexpr (POST) {
+                            post_lds[0][k][threadIdx.x] += gs[e] * sa[k];
+                            post_lds[1][k][threadIdx.x] += gs[e] * sb[k];
+                        }
+                        sa[k] = sb[k] = 0.f;
                     }
-                    sa[k] = sb[k] = 0.f;
-                }
-                if (p.dgate && dup[i] < VEC) {
-                    if (sizeof(T) == 4 || p.gate_f32)
-                        store_vec<float, VEC>(rn_at(rn_row(static_cast<float*>(p.dgate), gate_row, p.lddgate), at[i]), o);
-                    else
-                        store_vec<T, VEC>(rn_at(rn_row(static_cast<T*>(p.dgate), gate_row, p.lddgate), at[i]),
-                                          from_float<T, VEC>(o));
+                    if (p.dgate && dup[i] < VEC) {
+                        if (sizeof(T) == 4 || p.gate_f32)
+                            store_vec<float, VEC>(rn_at(rn_row(static_cast<float*>(p.dgate), gate_row, p.lddgate), at[i]), o);
+                        else
+                            store_vec<T, VEC>(rn_at(rn_row(static_cast<T*>(p.dgate), gate_row, p.lddgate), at[i]),
+                                              from_float<T, VEC>(o));
+                    }
                 }
             }
             gate_row += RPB;
             new_gate = true;
         }
     }
-    // this part's sums
-    auto leave = [&](float* out, const float (&v)[EPT]) {
-        if (!out) return;
-        out += (int64_t)blockIdx.x * cols;
-        if constexpr (TPR == 64) {  // the four waves' sums, added in wave order
+    if constexpr (SUMS) {
+        // this part's sums
+        auto leave = [&](float* out, const float (&v)[EPT]) {
+            if (!out) return;
+            out += (int64_t)part * cols;
+            if constexpr (TPR == 64) {  // the four waves' sums, added in wave order
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                FloatVec<VEC> o;
+                for (int i = 0; i < NV; ++i) {
+                    FloatVec<VEC> o;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = v[i * VEC + e];
-                if (dup[i] < VEC) store_vec<float, VEC>(&cols_lds[group][at[i]], o);
+                    for (int e = 0; e < VEC; ++e) o[e] = v[i * VEC + e];
+                    if (dup[i] < VEC) store_vec<float, VEC>(&cols_lds[group][at[i]], o);
+                }
+                __syncthreads();
+                for (int c = threadIdx.x; c < cols; c += 256)
+                    out[c] = cols_lds[0][c] + cols_lds[1][c] + cols_lds[2][c] + cols_lds[3][c];
+                __syncthreads();
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    FloatVec<VEC> o;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o[e] = v[i * VEC + e];
+                    if (dup[i] < VEC) store_vec<float, VEC>(rn_at(out, at[i]), o);
+                }
             }
-            __syncthreads();
-            for (int c = threadIdx.x; c < cols; c += 256)
-                out[c] = cols_lds[0][c] + cols_lds[1][c] + cols_lds[2][c] + cols_lds[3][c];
-            __syncthreads();
+        };
+        if constexpr (PRE) {
+            leave(p.part[TROP_RN_PRE_GAMMA], pg);
+            leave(p.part[TROP_RN_PRE_BETA], pb);
+        }
+        if (!p.part[TROP_RN_POST_GAMMA] && !p.part[TROP_RN_POST_BETA] && !p.part[TROP_RN_GATE]) return;
+        if (whole) {
+            if constexpr (POST) {
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) {
+                    sa[e] = post_lds[0][e][threadIdx.x];
+                    sb[e] = post_lds[1][e][threadIdx.x];
+                }
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                FloatVec<VEC> o;
+                const FloatVec<VEC> gs = rn_gate_full<T, VEC>(p, gate_row, at[i]);
+                const FloatVec<VEC> g = rn_weight<VEC>(p, p.post_gamma, at[i], 1.f);
+                const FloatVec<VEC> b = rn_weight<VEC>(p, p.post_beta, at[i], 0.f);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = v[i * VEC + e];
-                if (dup[i] < VEC) store_vec<float, VEC>(rn_at(out, at[i]), o);
+                for (int e = 0; e < VEC; ++e) {
+                    const int k = i * VEC + e;
+                    pg[k] = g[e] * sa[k] + b[e] * sb[k];
+                    sa[k] *= gs[e];
+                    sb[k] *= gs[e];
+                }
             }
+            leave(p.part[TROP_RN_GATE], pg);
         }
-    };
-    if constexpr (PRE) {
-        leave(p.part[TROP_RN_PRE_GAMMA], pg);
-        leave(p.part[TROP_RN_PRE_BETA], pb);
-    }
-    if (!p.part[TROP_RN_POST_GAMMA] && !p.part[TROP_RN_POST_BETA] && !p.part[TROP_RN_GATE]) return;
-    if (whole) {
         if constexpr (POST) {
-#pragma unroll
-            for (int e = 0; e < EPT; ++e) {
-                sa[e] = post_lds[0][e][threadIdx.x];
-                sb[e] = post_lds[1][e][threadIdx.x];
-            }
+            leave(p.part[TROP_RN_POST_GAMMA], sa);
+            leave(p.part[TROP_RN_POST_BETA], sb);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const FloatVec<VEC> gs = rn_gate_full<T, VEC>(p, gate_row, at[i]);
-            const FloatVec<VEC> g = rn_weight<VEC>(p, p.post_gamma, at[i], 1.f);
-            const FloatVec<VEC> b = rn_weight<VEC>(p, p.post_beta, at[i], 0.f);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int k = i * VEC + e;
-                pg[k] = g[e] * sa[k] + b[e] * sb[k];
-                sa[k] *= gs[e];
-                sb[k] *= gs[e];
-            }
-        }
-        leave(p.part[TROP_RN_GATE], pg);
-    }
-    if constexpr (POST) {
-        leave(p.part[TROP_RN_POST_GAMMA], sa);
-        leave(p.part[TROP_RN_POST_BETA], sb);
     }
 }
 
@@ -711,7 +752,7 @@ __device__ __forceinline__ FloatVec<VEC> rn_kept(const void* m, int64_t ld, cons
     }
 }
 
-// Rows wider than the registers (or narrower than a vector): a walk for the pre norm's means, kept for the
+// Rows wider than that, narrower than a vector, or without a norm: a walk for the pre norm's means, kept for the
 // column sums; one for the post norm's, which writes dr (and du without a post
 // norm); one for du.
 template <typename T, typename P, bool HELD>
@@ -882,35 +923,37 @@ __device__ __forceinline__ void residual_norm_columns_body(const TropResidualPar
         if (p.part[k]) p.part[k][part * p.cols + c] = acc[k];
 }
 
-// Sums of parts.  A workgroup takes 64 columns of an output row, 16 waves the
-// parts wave, wave + 16, ...; the waves' sums are added in wave order.
+// Sums of parts.  A workgroup takes 2^column_bits columns of an output row and
+// shares the parts out among its 1024 / 2^column_bits groups of threads (group g
+// adds parts g, g + groups, ...), whose sums are added pairwise: few columns
+// where there are many parts, so that no thread has many loads in a row.
 template <typename T>
 __device__ __forceinline__ void part_sums_body(const TropRowSumsParams& p) {
-    __shared__ float lds[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    __shared__ float lds[1024];
     const uint32_t id = (uint32_t)p.id0 + blockIdx.x;
     int k = 0;
     while (k + 1 < p.count && id >= p.e[k].blocks) ++k;
     const TropRowSumsEntry& e = p.e[k];
-    const uint32_t at = id - (k ? p.e[k - 1].blocks : 0), columns = (uint32_t)((p.cols + 63) / 64);
-    const int64_t row = at / columns, c = (int64_t)(at % columns) * 64 + lane;
+    const int bits = e.column_bits, width = 1 << bits, groups = 1024 >> bits;
+    const uint32_t at = id - (k ? p.e[k - 1].blocks : 0), columns = (uint32_t)((p.cols + width - 1) >> bits);
+    const int64_t row = at / columns, c = ((int64_t)(at % columns) << bits) + (threadIdx.x & (width - 1));
     float s = 0.f;
     if (c < p.cols) {
         const float* q = e.src + row * e.parts * p.cols + c;
-#pragma unroll 4
-        for (int64_t i = wave; i < e.parts; i += 16) s += q[i * p.cols];
+#pragma unroll 8
+        for (int64_t i = threadIdx.x >> bits; i < e.parts; i += groups) s += q[i * p.cols];
     }
-    lds[wave][lane] = s;
-    __syncthreads();
-    if (wave == 0 && c < p.cols) {
-        float a = lds[0][lane];
-#pragma unroll
-        for (int w = 1; w < 16; ++w) a += lds[w][lane];
-        a *= e.scale;
+    lds[threadIdx.x] = s;
+    for (int n = 512; n >= width; n >>= 1) {
+        __syncthreads();
+        if ((int)threadIdx.x < n) lds[threadIdx.x] = s = s + lds[threadIdx.x + n];
+    }
+    if ((int)threadIdx.x < width && c < p.cols) {
+        s *= e.scale;
         if (e.f32)
-            static_cast<float*>(e.dst)[row * e.ldd + c] = a;
+            static_cast<float*>(e.dst)[row * e.ldd + c] = s;
         else
-            static_cast<T*>(e.dst)[row * e.ldd + c] = (T)a;
+            static_cast<T*>(e.dst)[row * e.ldd + c] = (T)s;
     }
 }
 

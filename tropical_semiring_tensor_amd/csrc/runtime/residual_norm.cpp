@@ -13,6 +13,8 @@ namespace {
 trop_status invalid(const std::string& what) { return fail(TROP_ERR_INVALID_ARGUMENT, what); }
 
 trop_status check_norms(const trop_residual_norm& op) {
+    if (op.dtype != TROP_F32 && op.dtype != TROP_BF16)
+        return invalid("residual norms take float32 or bfloat16, got dtype " + std::to_string((int)op.dtype));
     for (const trop_norm n : {op.post, op.pre})
         if (n != TROP_NORM_NONE && n != TROP_NORM_LAYER && n != TROP_NORM_RMS)
             return invalid("no norm " + std::to_string((int)n));
@@ -22,12 +24,10 @@ trop_status check_norms(const trop_residual_norm& op) {
 }
 
 trop_status check_op(const trop_residual_norm& op) {
-    if (op.dtype != TROP_F32 && op.dtype != TROP_BF16)
-        return invalid("residual norms take float32 or bfloat16, got dtype " + std::to_string((int)op.dtype));
-    if (ln_index(op.dtype, op.param_dtype) < 0) return invalid("norm weights are float32 or of the rows' type");
-    if (op.gate && ln_index(op.dtype, op.gate_dtype) < 0) return invalid("the gate is float32 or of the rows' type");
     const trop_status st = check_norms(op);
     if (st != TROP_OK) return st;
+    if (ln_index(op.dtype, op.param_dtype) < 0) return invalid("norm weights are float32 or of the rows' type");
+    if (op.gate && ln_index(op.dtype, op.gate_dtype) < 0) return invalid("the gate is float32 or of the rows' type");
     for (const float f : {op.residual_scale, op.branch_scale})
         if (!std::isfinite(f)) return invalid("the scales must be finite");
     for (const float f : {op.post_eps, op.pre_eps})
@@ -42,16 +42,32 @@ int64_t gate_group(const trop_residual_norm& op) {
 int64_t gate_rows(const trop_residual_norm& op) { return ceil_div(op.rows, gate_group(op)); }
 
 // Row group of the backward by the columns 8 elements per thread cover;
-// kLoop: rows too wide, narrower than a vector, or without a norm.
-constexpr int kLoop = 5;
+// kWide: rows too wide to keep their sums as well; kNarrow: narrower than a
+// vector; kPlain: without a norm.
+enum { kRegisters = 5, kWide = 5, kNarrow = 6, kPlain = 7 };
 int backward_group(const trop_residual_norm& op) {
-    if (op.cols < 8 || (op.pre == TROP_NORM_NONE && op.post == TROP_NORM_NONE)) return kLoop;
+    if (op.cols < 8) return kNarrow;
+    if (op.pre == TROP_NORM_NONE && op.post == TROP_NORM_NONE) return kPlain;
     return op.cols <= TROP_RN_COLS_WAVE    ? 0
            : op.cols <= TROP_RN_COLS_PAIR  ? 1
            : op.cols <= TROP_RN_COLS_BLOCK ? 2
            : op.cols <= TROP_RN_COLS_HALF  ? 3
            : op.cols <= TROP_RN_COLS_WIDE  ? 4
-                                           : kLoop;
+                                           : kWide;
+}
+
+// Parts a backward makes at most, by row group: more keep more loads in flight,
+// but each leaves its sums for a second kernel to add.  Rows and sums in 512,
+// 768, 1024 and 2048 parts: 16384 x 1024 bfloat16 68, 56, 48 and 50 us, 16384 x
+// 1000 float32 91, 74, 75 and 82 (two waves to a row); 8192 x 2048 bfloat16 48,
+// 49, 50 and 62 (four); 16384 x 512 26, 27, 28 and 35 (one).  1024 threads to a
+// row fill a CU.  Where the sums have a kernel of their own its blocks of
+// columns make more workgroups.
+int64_t most_parts(const trop_residual_norm& op) {
+    static constexpr int64_t parts[] = {512, 1024, 512, 512, 256};
+    const int group = backward_group(op);
+    if (group < kRegisters) return parts[group];
+    return std::max<int64_t>(128, 1024 / ceil_div(std::max<int64_t>(op.cols, 1), TROP_RN_COLS_SUMS));
 }
 
 // The backward's parts: each inside one gate row (group_parts to one), so
@@ -61,15 +77,15 @@ int backward_group(const trop_residual_norm& op) {
 struct Parts {
     int64_t parts, part_rows, group_parts;
 };
-Parts backward_parts(const trop_residual_norm& op) {
+Parts parts_of(const trop_residual_norm& op, int64_t limit) {
     if (op.rows == 0) return {0, 1, 1};
     const int64_t group = gate_group(op), gates = gate_rows(op), rpb = backward_group(op) == 0 ? 4 : 1;
-    if (gates <= TROP_RN_MAX_PARTS) {
-        const int64_t most = std::min<int64_t>(TROP_RN_MAX_PARTS / gates, ceil_div(group, rpb));
+    if (gates <= limit) {
+        const int64_t most = std::min(limit / gates, ceil_div(group, rpb));
         const int64_t rows = ceil_div(group, most), per = ceil_div(group, rows);
         return {gates * per, rows, per};
     }
-    const int64_t whole = ceil_div(gates, TROP_RN_MAX_PARTS);
+    const int64_t whole = ceil_div(gates, limit);
     return {ceil_div(gates, whole), whole * group, 0};
 }
 
@@ -82,7 +98,7 @@ struct Layout {
     size_t bytes;
 };
 trop_status plan(const trop_residual_norm& op, Layout* l) {
-    l->parts = backward_parts(op);
+    l->parts = parts_of(op, most_parts(op));
     const bool has[TROP_RN_SUMS] = {op.pre != TROP_NORM_NONE, op.pre != TROP_NORM_NONE, op.post != TROP_NORM_NONE,
                                     op.post != TROP_NORM_NONE, op.gate && l->parts.group_parts > 0};
     int64_t one, total = 0;
@@ -93,7 +109,7 @@ trop_status plan(const trop_residual_norm& op, Layout* l) {
         if (has[i]) total += one;
     }
     l->row_sums = total / 4;
-    if (backward_group(op) == kLoop && op.pre != TROP_NORM_NONE) {
+    if (backward_group(op) >= kRegisters && op.pre != TROP_NORM_NONE) {
         int64_t more;
         if (__builtin_mul_overflow(op.rows, (int64_t)8, &more) || __builtin_add_overflow(total, more, &total))
             return invalid("workspace size overflows");
@@ -205,13 +221,12 @@ trop_status forward(const trop_residual_norm* opp, const trop_residual_norm_rows
     p.ldu = u.ld;
     p.ldh = h.ld;
     p.ldy = y.ld;
-    static const TrainKernelId ids[] = {TK_RN_FWD_WAVE, TK_RN_FWD_BLOCK, TK_RN_FWD_WIDE, TK_RN_FWD_LOOP};
-    const int g = op.cols <= TROP_LN_COLS_WAVE    ? 0
-                  : op.cols <= TROP_LN_COLS_BLOCK ? 1
-                  : op.cols <= TROP_LN_COLS_WIDE  ? 2
-                                                  : 3;
+    // 16 elements to a thread
+    static const TrainKernelId ids[] = {TK_RN_FWD_WAVE, TK_RN_FWD_BLOCK, TK_RN_FWD_HALF, TK_RN_FWD_WIDE, TK_RN_FWD_LOOP};
+    static const uint32_t threads[] = {256, 256, 512, 1024, 1024};
+    const int g = op.cols <= 64 * 16 ? 0 : op.cols <= 256 * 16 ? 1 : op.cols <= 512 * 16 ? 2 : op.cols <= 1024 * 16 ? 3 : 4;
     st = launch_rows(dev, ids[g] + ln_index(op.dtype, op.param_dtype), TROP_T_RESIDUAL_FORWARD, p, g == 0 ? 4 : 1,
-                     g < 2 ? 256 : 1024, static_cast<hipStream_t>(stream));
+                     threads[g], static_cast<hipStream_t>(stream));
     return st == TROP_OK ? ok() : st;
 }
 
@@ -231,7 +246,8 @@ trop_status sum_parts(int dev, const trop_residual_norm& op, const trop_residual
         e.parts = parts;
         e.scale = scale;
         e.f32 = dt == TROP_F32;
-        blocks += rows * ceil_div(op.cols, 64);
+        e.column_bits = parts > 64 ? 4 : parts > 16 ? 6 : 8;
+        blocks += rows * ceil_div(op.cols, (int64_t)1 << e.column_bits);
         e.blocks = (uint32_t)blocks;
     };
     const int64_t parts = l.parts.parts;
@@ -370,23 +386,39 @@ trop_status backward(const trop_residual_norm* opp, const trop_residual_norm_kep
         p.need_v = g.dgate.data != nullptr;
         p.need_post = through_post;
         p.ragged = op.cols % (16 / (int64_t)elem_size(op.dtype)) != 0;
-        const int kind = need_u || pre ? backward_group(op) : kLoop;
-        const int idx = ln_index(op.dtype, op.param_dtype) + (held ? 3 : 0);
-        if (kind != kLoop) {
+        const int kind = backward_group(op), variant = 2 * held + (op.dtype == TROP_BF16);
+        const int loop = ln_index(op.dtype, op.param_dtype) + (held ? 3 : 0);
+        // norms of the rows' gradients, and of the sums: 0 pre, 1 post, 2 both, 3 none
+        const int norms = pre ? (post && need_u ? 2 : 0) : post && need_u ? 1 : 3;
+        if (kind < kRegisters && norms < 3) {
             static const uint32_t threads[] = {256, 128, 256, 512, 1024};
-            const int norms = !pre ? 1 : post && need_u ? 2 : 0;
-            st = train_launch(dev, (TrainKernelId)(TK_RN_BWD + 12 * kind + 4 * norms + 2 * held + (op.dtype == TROP_BF16)),
-                              TROP_T_RESIDUAL_BACKWARD, l.parts.parts, threads[kind], &p, s);
+            st = train_launch(dev, (TrainKernelId)(TK_RN_BWD + 12 * kind + 4 * norms + variant), TROP_T_RESIDUAL_BACKWARD,
+                              l.parts.parts, threads[kind], &p, s);
         } else {
             p.row_sums = pre && (sum_post || g.dgate.data) ? ws + l.row_sums : nullptr;
-            if (g.dr.data || g.du.data || p.row_sums)
-                st = launch_rows(dev, TK_RN_BWD_LOOP + idx, TROP_T_RESIDUAL_BACKWARD, p, 1, 1024, s);
+            if (g.dr.data || g.du.data || p.row_sums) {
+                if (kind == kWide && op.cols <= TROP_RN_COLS_ROWS && norms < 3) {
+                    TropResidualParams q = p;
+                    const Parts rows = parts_of(op, 256);
+                    q.part_rows = rows.part_rows;
+                    q.group_parts = rows.group_parts;
+                    st = train_launch(dev, (TrainKernelId)(TK_RN_BWD_ROWS + 4 * norms + variant),
+                                      TROP_T_RESIDUAL_BACKWARD, rows.parts, 1024, &q, s);
+                } else {
+                    st = launch_rows(dev, TK_RN_BWD_LOOP + loop, TROP_T_RESIDUAL_BACKWARD, p, 1, 1024, s);
+                }
+            }
             if (st == TROP_OK && sums) {
                 p.need_post = sum_post;
-                const int64_t most = max_groups(256) / l.parts.parts * 256;
-                for (; st == TROP_OK && p.col0 < op.cols; p.col0 += most)
-                    st = train_launch(dev, (TrainKernelId)(TK_RN_COLUMNS + idx), TROP_T_RESIDUAL_BACKWARD,
-                                      l.parts.parts * ceil_div(std::min(op.cols - p.col0, most), 256), 256, &p, s);
+                // (the vectors' kernel counts bytes of a row in 32 bits)
+                const bool vectors = kind != kNarrow && op.cols <= (int64_t)1 << 29;
+                const int64_t width = vectors ? TROP_RN_COLS_SUMS : 256, blocks = ceil_div(op.cols, width);
+                const int64_t most = max_groups(256) / l.parts.parts;
+                for (int64_t b = 0; st == TROP_OK && b < blocks; b += most) {
+                    p.col0 = vectors ? b : b * width;
+                    st = train_launch(dev, (TrainKernelId)(vectors ? TK_RN_BWD_SUMS + 4 * norms + variant : TK_RN_COLUMNS + loop),
+                                      TROP_T_RESIDUAL_BACKWARD, l.parts.parts * std::min(blocks - b, most), 256, &p, s);
+                }
             }
         }
     }

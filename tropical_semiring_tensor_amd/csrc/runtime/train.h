@@ -50,10 +50,13 @@ enum TrainKernelId : int {
     TK_GRAD_W = TK_PART_SUMS + 2,      // + 2 tile (256, 128, 64)
     TK_RN_FWD_WAVE = TK_GRAD_W + 6,    // + ln_index
     TK_RN_FWD_BLOCK = TK_RN_FWD_WAVE + 3,
-    TK_RN_FWD_WIDE = TK_RN_FWD_BLOCK + 3,
+    TK_RN_FWD_HALF = TK_RN_FWD_BLOCK + 3,
+    TK_RN_FWD_WIDE = TK_RN_FWD_HALF + 3,
     TK_RN_FWD_LOOP = TK_RN_FWD_WIDE + 3,
     TK_RN_BWD = TK_RN_FWD_LOOP + 3,  // + 12 row group + 4 (norms: pre, post, both) + 2 (8 bits) + (bf16 ? 1 : 0)
-    TK_RN_BWD_LOOP = TK_RN_BWD + 60,   // + ln_index + 3 (u and h in 8 bits)
+    TK_RN_BWD_ROWS = TK_RN_BWD + 60,   // likewise, without row groups
+    TK_RN_BWD_SUMS = TK_RN_BWD_ROWS + 12,  // + 4 (norms: pre, post, both, none) + 2 (8 bits) + (bf16 ? 1 : 0)
+    TK_RN_BWD_LOOP = TK_RN_BWD_SUMS + 16,  // + ln_index + 3 (u and h in 8 bits)
     TK_RN_COLUMNS = TK_RN_BWD_LOOP + 6,
     TK_COUNT = TK_RN_COLUMNS + 6
 };

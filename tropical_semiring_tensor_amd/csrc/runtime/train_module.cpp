@@ -76,13 +76,14 @@ const char* const kNames[] = {
 #define TROP_RN_TYPES(KERNEL, HELD) \
     "trop_rn_" KERNEL "_f32_f32" HELD, "trop_rn_" KERNEL "_bf16_bf16" HELD, "trop_rn_" KERNEL "_bf16_f32" HELD,
     TROP_RN_TYPES("fwd_wave", "") TROP_RN_TYPES("fwd_block", "")
-    TROP_RN_TYPES("fwd_wide", "") TROP_RN_TYPES("fwd_loop", "")
+    TROP_RN_TYPES("fwd_half", "") TROP_RN_TYPES("fwd_wide", "") TROP_RN_TYPES("fwd_loop", "")
 #define TROP_RN_NORMS(KERNEL)                                                              \
     TROP_RN_KEPT(KERNEL "_pre") TROP_RN_KEPT(KERNEL "_post") TROP_RN_KEPT(KERNEL "_both")
 #define TROP_RN_KEPT(KERNEL) \
     "trop_rn_bwd_" KERNEL "_f32", "trop_rn_bwd_" KERNEL "_bf16", "trop_rn_bwd_" KERNEL "_f32_held8", \
     "trop_rn_bwd_" KERNEL "_bf16_held8",
     TROP_RN_NORMS("wave") TROP_RN_NORMS("pair") TROP_RN_NORMS("block") TROP_RN_NORMS("half") TROP_RN_NORMS("wide")
+    TROP_RN_NORMS("rows") TROP_RN_NORMS("sums") TROP_RN_KEPT("sums_none")
     TROP_RN_TYPES("bwd_loop", "") TROP_RN_TYPES("bwd_loop", "_held8")
     TROP_RN_TYPES("columns", "") TROP_RN_TYPES("columns", "_held8")
 #undef TROP_RN_KEPT

@@ -128,8 +128,10 @@ struct TropGradWParams {
 #define TROP_RN_COLS_BLOCK 2048
 #define TROP_RN_COLS_HALF 4096
 #define TROP_RN_COLS_WIDE 8192
-// Partial column sums a backward call makes at most.
-#define TROP_RN_MAX_PARTS 512
+// and 1024 threads of its rows' gradients alone (16 each).
+#define TROP_RN_COLS_ROWS 16384
+// Columns of a workgroup of wide rows' sums.
+#define TROP_RN_COLS_SUMS 2048
 // Column sums: gradients of the pre norm's weights, the post norm's, the gate.
 enum { TROP_RN_PRE_GAMMA, TROP_RN_PRE_BETA, TROP_RN_POST_GAMMA, TROP_RN_POST_BETA, TROP_RN_GATE, TROP_RN_SUMS };
 
@@ -161,7 +163,7 @@ struct TropResidualParams {
     int64_t ldr, ldu, ldgate, lddy, lddh, ldh, ldy, lddr, lddu, lddgate, ldu_codes, ldu_exps, ldh_codes, ldh_exps;
     int64_t rows, cols;
     int64_t row0;           // the launch's first row
-    int64_t col0;           // wide rows' column sums: the launch's first column
+    int64_t col0;           // wide rows' sums: the launch's first block of columns (narrow ones': column)
     int64_t gate_group;     // rows of a gate row (rows or more: one gate row)
     int64_t part_rows;      // backward: rows of a part
     int64_t group_parts;    // backward: parts of a gate row, or 0: a part takes whole gate rows
@@ -183,7 +185,7 @@ struct TropRowSumsEntry {
     uint32_t blocks;        // workgroups of this entry and all before it
     int32_t f32;
     float scale;
-    int32_t pad_;
+    int32_t column_bits;    // log2 of a workgroup's columns
 };
 struct TropRowSumsParams {
     TropRowSumsEntry e[TROP_RN_SUMS];
