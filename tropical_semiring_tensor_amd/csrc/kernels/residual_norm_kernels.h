@@ -363,16 +363,21 @@ struct RnKept {
 template <typename T, int VEC>
 struct RnKept<T, VEC, true> {
     CodeWords<VEC> codes;
-    uint32_t exps;  // of the first and (`ragged` rows), from bit 8 on, the last element
+    // Exponents of the first element and, in rows that end inside a vector
+    // (`ragged`: the last vectors may lie across two blocks), of the last.  Kept
+    // as the bytes they are: put together, or widened, they would be waited
+    // for where they are loaded, a row ahead of their use (16384 x 1024
+    // bfloat16 57 us against 49).
+    uint8_t first, last;
     __device__ __forceinline__ void load(const void*, int64_t, const int8_t* m, int64_t ldc, const uint8_t* e,
                                          int64_t lde, int64_t r, uint32_t c, bool ragged) {
         codes = __builtin_bit_cast(CodeWords<VEC>, load_stream<int8_t, VEC>(rn_at(rn_row(m, r, ldc), c)));
         const uint8_t* row = rn_row(e, r, lde);
-        exps = *rn_at(row, c / TROP_ACT8_BLOCK_ELEMS);
-        if (ragged) exps |= (uint32_t)*rn_at(row, (c + VEC - 1) / TROP_ACT8_BLOCK_ELEMS) << 8;
+        first = *rn_at(row, c / TROP_ACT8_BLOCK_ELEMS);
+        if (ragged) last = *rn_at(row, (c + VEC - 1) / TROP_ACT8_BLOCK_ELEMS);
     }
     __device__ __forceinline__ FloatVec<VEC> about(float mean, uint32_t c, bool ragged) const {
-        const float step = act8_step(exps & 255);
+        const float step = act8_step(first);
         const FloatVec<VEC> q = __builtin_convertvector(__builtin_bit_cast(Codes<VEC>, codes), FloatVec<VEC>);
         FloatVec<VEC> x;
 #pragma unroll
@@ -381,18 +386,18 @@ struct RnKept<T, VEC, true> {
             int split = TROP_ACT8_BLOCK_ELEMS - (int)(c % TROP_ACT8_BLOCK_ELEMS);
             asm volatile("" : "+v"(split));  // (the comparisons are not to be kept over the rows)
             if (split < VEC) {  // a block ends inside the vector
-                const float last = act8_step(exps >> 8);
+                const float other = act8_step(last);
                 CodeWords<VEC> again;  // (converted anew: no registers for it elsewhere)
 #pragma unroll
-                for (int q = 0; q < VEC / 4; ++q) {
-                    uint32_t word = codes[q];
+                for (int i = 0; i < VEC / 4; ++i) {
+                    uint32_t word = codes[i];
                     asm volatile("" : "+v"(word));
-                    again[q] = word;
+                    again[i] = word;
                 }
                 const FloatVec<VEC> q1 = __builtin_convertvector(__builtin_bit_cast(Codes<VEC>, again), FloatVec<VEC>);
 #pragma unroll
                 for (int e = 1; e < VEC; ++e)
-                    if (e >= split) x[e] = __builtin_fmaf(q1[e], last, -mean);
+                    if (e >= split) x[e] = __builtin_fmaf(q1[e], other, -mean);
             }
         }
         return x;
@@ -487,7 +492,6 @@ __device__ __forceinline__ void residual_norm_backward_body(const TropResidualPa
             }
         }
     };
-    if constexpr (KEEP) weights(true, false, 0);
     // this row group's rows: units of unit_rows, RPB units apart
     const bool whole = p.group_parts == 0;
     const int64_t unit_rows = whole ? p.gate_group : 1;
@@ -503,9 +507,10 @@ __device__ __forceinline__ void residual_norm_backward_body(const TropResidualPa
         end = min(first + p.part_rows, last);
     }
     int64_t unit = first + group * unit_rows, r = unit, unit_end = min(unit + unit_rows, end);
+    if (whole && r < end) gate_row = rn_divide(r, p.gate_group);
+    if (KEEP && r < end) weights(true, false, 0);
     if (r < end) fetch(r);
     if (whole) {
-        if (r < end) gate_row = rn_divide(r, p.gate_group);
         if constexpr (POST && SUMS) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) post_lds[0][e][threadIdx.x] = post_lds[1][e][threadIdx.x] = 0.f;

@@ -79,9 +79,11 @@ struct Parts {
 };
 Parts parts_of(const trop_residual_norm& op, int64_t limit) {
     if (op.rows == 0) return {0, 1, 1};
-    const int64_t group = gate_group(op), gates = gate_rows(op), rpb = backward_group(op) == 0 ? 4 : 1;
+    // (four rows at least, a wave each or one after another: 1537 x 1001 with 29
+    // gate rows in 783 parts of two 20 + 9 us, in 406 of four 20 + 5)
+    const int64_t group = gate_group(op), gates = gate_rows(op);
     if (gates <= limit) {
-        const int64_t most = std::min(limit / gates, ceil_div(group, rpb));
+        const int64_t most = std::min(limit / gates, ceil_div(group, 4));
         const int64_t rows = ceil_div(group, most), per = ceil_div(group, rows);
         return {gates * per, rows, per};
     }
@@ -246,7 +248,7 @@ trop_status sum_parts(int dev, const trop_residual_norm& op, const trop_residual
         e.parts = parts;
         e.scale = scale;
         e.f32 = dt == TROP_F32;
-        e.column_bits = parts > 64 ? 4 : parts > 16 ? 6 : 8;
+        e.column_bits = parts <= 16 ? 8 : parts <= 64 || rows * op.cols >= 4096 ? 6 : 4;
         blocks += rows * ceil_div(op.cols, (int64_t)1 << e.column_bits);
         e.blocks = (uint32_t)blocks;
     };

@@ -172,7 +172,7 @@ struct TropResidualParams {
     int32_t gate_f32, weight_f32;
     int32_t parts;
     int32_t need_v, need_post;  // backward: the gate's gradient; the post norm's gradients or du through it
-    int32_t ragged;         // backward: rows that are no multiple of a 16-byte vector
+    int32_t ragged;         // backward: rows that end inside a 16-byte vector
     int32_t pad_;
 };
 
