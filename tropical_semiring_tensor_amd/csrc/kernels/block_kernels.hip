@@ -22,21 +22,22 @@ using namespace trop;
     extern "C" __global__ __launch_bounds__(1024) void trop_part_sums_##NAME(TropRowSumsParams p) {          \
         part_sums_body<T>(p);                                                                                \
     }
-#define TROP_GRAD_W_TILE(NAME, T, EDGE, WM, WN)                                                              \
-    using GradW8_##EDGE##_##NAME = MgConfig<EDGE, EDGE, WM, WN, MM, MM, 1, 2, grad_w_parts<T>()>;            \
-    extern "C" __global__ __launch_bounds__(GradW8_##EDGE##_##NAME::THREADS) void                            \
-        trop_grad_w##EDGE##_##NAME(TropGradWParams p) {                                                      \
-        __shared__ __align__(1024) char lds[GradW8_##EDGE##_##NAME::LDS_BYTES];                              \
-        grad_w_body<GradW8_##EDGE##_##NAME, T>(p, lds);                                                      \
+#define TROP_GRAD_W_TILE(NAME, T, TILE, EDGE, WM, WN, BUFFERS)                                               \
+    using GradW8_##TILE##_##NAME = MgConfig<EDGE, EDGE, WM, WN, MM, MM, 1, BUFFERS, grad_w_parts<T>()>;      \
+    extern "C" __global__ __launch_bounds__(GradW8_##TILE##_##NAME::THREADS) void                            \
+        trop_grad_w##TILE##_##NAME(TropGradWParams p) {                                                      \
+        __shared__ __align__(1024) char lds[GradW8_##TILE##_##NAME::LDS_BYTES];                              \
+        grad_w_body<GradW8_##TILE##_##NAME, T>(p, lds);                                                      \
     }
+#define TROP_GRAD_W_TILES(NAME, T)                                                                           \
+    TROP_GRAD_W_TILE(NAME, T, 256, 256, 2, 4, 2)                                                             \
+    TROP_GRAD_W_TILE(NAME, T, 128, 128, 2, 2, 2)                                                             \
+    TROP_GRAD_W_TILE(NAME, T, 64, 64, 2, 2, 2)                                                               \
+    TROP_GRAD_W_TILE(NAME, T, 64d, 64, 2, 2, 4)
 TROP_ACT8_ENTRIES(f32, float)
 TROP_ACT8_ENTRIES(bf16, bf16)
-TROP_GRAD_W_TILE(f32, float, 256, 2, 4)
-TROP_GRAD_W_TILE(f32, float, 128, 2, 2)
-TROP_GRAD_W_TILE(f32, float, 64, 2, 2)
-TROP_GRAD_W_TILE(bf16, bf16, 256, 2, 4)
-TROP_GRAD_W_TILE(bf16, bf16, 128, 2, 2)
-TROP_GRAD_W_TILE(bf16, bf16, 64, 2, 2)
+TROP_GRAD_W_TILES(f32, float)
+TROP_GRAD_W_TILES(bf16, bf16)
 
 // suffix: element type, the weights' type; backward: u and h as they are, or in 8 bits
 #define TROP_RN_ENTRY(KERNEL, THREADS, BODY) TROP_RN_ENTRY_WAVES(KERNEL, THREADS, 1, BODY)

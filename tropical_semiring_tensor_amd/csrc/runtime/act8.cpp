@@ -70,6 +70,19 @@ trop_status pack_or_unpack(bool pack, trop_dtype dt, const void* x, int64_t ldx,
 
 // ---- weight gradient ---------------------------------------------------------
 
+// Tiles of the product: 0: 256 x 256, 1: 128 x 128, 2: 64 x 64, 3: 64 x 64 with
+// four buffers, for few tiles: alone on a CU, or beside one other, a tile waits
+// for its loads (1000 tokens x 1001 x 777 bfloat16, 208 tiles: 11.1 us with two
+// buffers, 8.1 with four; 512 x 1024 x 1024 float32, 256: 15.0 and 11.0; but 64 x
+// 2048 x 2048 bfloat16, 1024: 7.3 and 8.2; and 128 x 128 gain nothing: 26 and 27
+// us for 2048 x 2048 x 2048).
+constexpr int kTiles = 4;
+int64_t grad_w_edge(int tile) { return tile == 3 ? 64 : tile_edge(tile); }
+double grad_w_time(int tile, int64_t tiles, double k) {
+    if (tile == 3) return tiles <= 256 ? k * 0.27 + 4.0 : (double)ceil_div(tiles, 512) * (k * 0.41 + 4.0);
+    return tile_time(tile, tiles, k);
+}
+
 struct GradWPlan {
     int64_t parts;             // of dz's values
     int64_t tokens_p;
@@ -96,11 +109,11 @@ void plan_grad_w(trop_dtype dt, bool packed, int64_t tokens, int64_t cols, int64
     // tile and parts along the tokens with the least time; the parts' sums
     // are written and read again at 4 TB/s, by one more launch
     double least = -1;
-    for (int kind = 0; kind < 3; ++kind) {
-        const int64_t edge = tile_edge(kind), tiles = ceil_div(c->cols, edge) * ceil_div(c->outs, edge);
+    for (int kind = 0; kind < kTiles; ++kind) {
+        const int64_t edge = grad_w_edge(kind), tiles = ceil_div(c->cols, edge) * ceil_div(c->outs, edge);
         for (int64_t n = 1; n <= 32 && (n == 1 || (ktiles >= 2 * n && tiles * n <= 2048)); ++n) {
             const double extra = n == 1 ? 0.0 : 4.0 + (double)(2 * n * c->outs * cols_p * 4) / 4e6;
-            const double t = tile_time(kind, tiles * n, (double)(ceil_div(ktiles, n) * c->parts)) + extra;
+            const double t = grad_w_time(kind, tiles * n, (double)(ceil_div(ktiles, n) * c->parts)) + extra;
             if (least < 0 || t < least) {
                 least = t;
                 c->tile = kind;
@@ -109,7 +122,7 @@ void plan_grad_w(trop_dtype dt, bool packed, int64_t tokens, int64_t cols, int64
         }
     }
     // a piece's tiles in one launch
-    const int64_t edge = tile_edge(c->tile);
+    const int64_t edge = grad_w_edge(c->tile);
     const int64_t most = max_groups(tile_threads(c->tile)) / (ceil_div(c->cols, edge) * c->splits) * edge / 256 * 256;
     if (c->outs > most) c->outs = most;
     c->bytes = 256;  // room to align the caller's pointer
@@ -189,7 +202,7 @@ trop_status grad_w(trop_dtype dt, const void* dz, int64_t lddz, const trop_act8*
     p.xp = ws + c.xp;
     p.dzp = packed ? ws + c.dzp : nullptr;
     p.part = reinterpret_cast<float*>(ws + c.part);
-    const int64_t edge = tile_edge(c.tile);
+    const int64_t edge = grad_w_edge(c.tile);
     for (int64_t c0 = 0; st == TROP_OK && c0 < cols; c0 += c.cols) {
         p.cols = std::min(c.cols, cols - c0);
         p.cols_p = round_up(p.cols, 64);

@@ -47,8 +47,8 @@ enum TrainKernelId : int {
     TK_GRAD_W_PACK = TK_ACT8_UNPACK + 2,
     TK_GRAD_W_FINISH = TK_GRAD_W_PACK + 2,
     TK_PART_SUMS = TK_GRAD_W_FINISH + 2,
-    TK_GRAD_W = TK_PART_SUMS + 2,      // + 2 tile (256, 128, 64)
-    TK_RN_FWD_WAVE = TK_GRAD_W + 6,    // + ln_index
+    TK_GRAD_W = TK_PART_SUMS + 2,      // + 2 tile (256, 128, 64, 64 with four buffers)
+    TK_RN_FWD_WAVE = TK_GRAD_W + 8,    // + ln_index
     TK_RN_FWD_BLOCK = TK_RN_FWD_WAVE + 3,
     TK_RN_FWD_HALF = TK_RN_FWD_BLOCK + 3,
     TK_RN_FWD_WIDE = TK_RN_FWD_HALF + 3,

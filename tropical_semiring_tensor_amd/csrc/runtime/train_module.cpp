@@ -73,6 +73,7 @@ const char* const kNames[] = {
     "trop_grad_w256_f32", "trop_grad_w256_bf16",
     "trop_grad_w128_f32", "trop_grad_w128_bf16",
     "trop_grad_w64_f32", "trop_grad_w64_bf16",
+    "trop_grad_w64d_f32", "trop_grad_w64d_bf16",
 #define TROP_RN_TYPES(KERNEL, HELD) \
     "trop_rn_" KERNEL "_f32_f32" HELD, "trop_rn_" KERNEL "_bf16_bf16" HELD, "trop_rn_" KERNEL "_bf16_f32" HELD,
     TROP_RN_TYPES("fwd_wave", "") TROP_RN_TYPES("fwd_block", "")
