@@ -430,8 +430,10 @@ __device__ __forceinline__ void residual_norm_backward_body(const TropResidualPa
     using V = typename VecOf<T, VEC>::raw;
     __shared__ RowSums<TPR, 2> sums[2][2];
     constexpr bool SUMS = WORK != RN_ROWS, ROWS = WORK != RN_COLUMNS;
-    // a row of 16 elements to a thread leaves no registers for its weights
-    constexpr bool KEEP = EPT <= 8;
+    // Weights and gate stay in registers where there are enough: not with 16
+    // elements to a thread, nor in float32 with 1024 threads (128 registers each;
+    // 4096 x 8192: 183 us kept and spilled, 156 read again for each row).
+    constexpr bool KEEP = EPT <= 8 && !(TPR == 1024 && sizeof(T) == 4);
     __shared__ float post_lds[POST && SUMS ? 2 : 1][POST && SUMS ? EPT : 1][THREADS];
     __shared__ float cols_lds[TPR == 64 ? 4 : 1][TPR == 64 ? TPR * EPT : 1];
     const int t = threadIdx.x % TPR, group = RPB == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
