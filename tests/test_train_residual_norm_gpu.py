@@ -6,8 +6,14 @@ Tolerances, with u = 2^-24 (one float32 rounding, relative):
     steps across lanes, 16 waves; with the product and the factor 1 / cols
     fewer than 48 roundings touch a term (rows past the registers add cols /
     1024 sequential terms): n u sum |terms|;
-  - a sum over rows has at most `rows` sequential terms in a part, then 4
-    waves' sums and 512 / 16 + 16 parts: (rows + 64) u sum |terms|;
+  - a sum over rows in P <= rows parts has at most rows / P + P / 4 sequential
+    terms, and fewer than 32 more in joining waves and parts: below rows + 64,
+    so (rows + 64) u sum |terms|;
+  - dgate is gamma A + beta B with A = sum H x^ and B = sum H over a gate row's
+    rows, each off by (group + 64) u times its terms' magnitudes; two products,
+    their sum and branch_scale add four roundings of |gamma A| + |beta B| at
+    most: (group + 68) u sum |H| (|x^ gamma| + |beta|), and sum |H v| in place
+    of the last without a post norm, where v is u;
   - elementwise errors are carried through the formulas to first order;
   - an output is rounded to its type once (torch.finfo(t).eps / 2).
 """
@@ -192,12 +198,11 @@ def backward_reference(q, f, u, h):
         H, eH = H + t, et + U * (H + t).abs()
     rs = f32(op["residual_scale"])
     out["r"] = (H * rs, eH * abs(rs) + U * (H * rs).abs())
-    v, ev = u, zero
+    v, ev, av = u, zero, u.abs()
     if op["post"]:
         xu, exu, rstd_u = standard(u, "post")
-        g = q.weight("post_gamma", 1.0)
-        v = xu * g + q.weight("post_beta", 0.0)
-        ev = exu * g.abs() + 2 * U * ((xu * g).abs() + v.abs())
+        g, b = q.weight("post_gamma", 1.0), q.weight("post_beta", 0.0)
+        v, ev, av = xu * g + b, exu * g.abs(), (xu * g).abs() + b.abs()
     gates = -(-q.rows // q.group) if q.rows else 0
     index = torch.arange(q.rows, device=DEV) // q.group
 
@@ -205,7 +210,7 @@ def backward_reference(q, f, u, h):
         return torch.zeros(gates, cols, dtype=torch.float64, device=DEV).index_add_(0, index, x)
 
     bs = f32(op["branch_scale"])
-    eg = group_sum(eH * v.abs() + H.abs() * ev) + (q.group + 66) * U * group_sum((H * v).abs())
+    eg = group_sum(eH * av + H.abs() * ev) + (q.group + 68) * U * group_sum(H.abs() * av)
     gate = group_sum(H * v) * bs
     out["gate"] = (gate, eg * abs(bs) + U * gate.abs())
     gs = q.gate_rows()

@@ -12,6 +12,10 @@
 // sign.  So unpacking rounds nothing, a matrix instruction takes the values as
 // they are, and products with them are exact in float32.  32 elements to a
 // step (a 32nd byte each) win back what the power of two costs.
+//
+// Bound by HBM: 16384 x 4096 bfloat16 (203 MB each way) packed in 33 us and
+// unpacked in 31, 6.1 and 6.6 TB/s (42 us right behind the kernel that wrote
+// the codes among much else); 33 x 1000: 4 us each, latency.
 #pragma once
 #include "train_common.h"
 

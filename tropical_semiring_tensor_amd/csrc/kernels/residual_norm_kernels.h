@@ -18,6 +18,18 @@
 // run of rows inside one gate row, or several whole gate rows, whose gradient
 // it then writes by itself.  The parts' sums are added in order by a second
 // kernel: no atomics, the same bits every time.
+//
+// Measured (one MI355X; a large copy moves 5.0 TB/s): 16384 x 4096 bfloat16, u
+// and h kept in 8 bits, 675 MB each way: forward with a gate and a pre norm
+// 126-137 us (4.9-5.4 TB/s), backward with a post norm as well 131-135 us
+// (5.0-5.2) and 6 us for the parts' sums.  1537 x 1001 float32: forward 9 us (25
+// MB), backward 20 + 6 us (28 MB; 406 parts of four rows, latency).  One row of
+// 4096: 4 us, the way from the load through two norms' reductions to the store.
+//
+// Row groups: forward 16 elements to a thread, which reaches the copy's rate;
+// backward 8, since a thread holds dy, dh, h and u of its next row besides its
+// columns' sums: bfloat16 rows then fit 128 registers, four waves to a SIMD
+// (16384 x 4096: 152 us, with three waves 186, before later steps).
 #pragma once
 #include "act8_kernels.h"
 #include "layer_norm_kernels.h"
@@ -452,7 +464,8 @@ __device__ __forceinline__ void residual_norm_backward_body(const TropResidualPa
         at[i] = min(c, cols - VEC);
         dup[i] = c - (int)at[i];
     }
-    float pg[SUMS ? EPT : 1] = {}, pb[SUMS ? EPT : 1] = {}, sa[SUMS ? EPT : 1] = {}, sb[SUMS ? EPT : 1] = {};  // sums of dy x^, dy; A and B
+    // sums of dy x^ and dy; A and B
+    float pg[SUMS ? EPT : 1] = {}, pb[SUMS ? EPT : 1] = {}, sa[SUMS ? EPT : 1] = {}, sb[SUMS ? EPT : 1] = {};
     V dyv[NV], dhv[NV] = {};
     RnKept<T, VEC, HELD> hv[NV], uv[NV];
     float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f, c1_row = 0.f, c2_row = 0.f;
@@ -759,9 +772,9 @@ __device__ __forceinline__ FloatVec<VEC> rn_kept(const void* m, int64_t ld, cons
     }
 }
 
-// Rows wider than that, narrower than a vector, or without a norm: a walk for the pre norm's means, kept for the
-// column sums; one for the post norm's, which writes dr (and du without a post
-// norm); one for du.
+// Rows wider than that, narrower than a vector, or without a norm: a walk for
+// the pre norm's means, kept for the column sums; one for the post norm's,
+// which writes dr (and du without a post norm); one for du.
 template <typename T, typename P, bool HELD>
 __device__ __forceinline__ void residual_norm_backward_loop_body(const TropResidualParams& p) {
     constexpr int VEC = ln_vec<T>(), TPR = 1024;
