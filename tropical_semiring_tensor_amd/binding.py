@@ -633,6 +633,17 @@ def _out_flat(t, n, dtype, device, what):
     return t, _flat(t, what, n, dtype)
 
 
+def _new_flats(there, n, dtype, device):
+    """A new vector of n elements for each that is there, None for the others;
+    of several the rows of one matrix (four vectors 2.9 us of host time against
+    4.8)."""
+    count = sum(there)
+    if count > 2:
+        rows = iter(torch.empty_strided((count, n), (max(n, 1), 1), dtype=dtype, device=device).unbind(0))
+        return [next(rows) if t else None for t in there]
+    return [torch.empty_strided((n,), (1,), dtype=dtype, device=device) if t else None for t in there]
+
+
 def _workspace(workspace, nbytes, device):
     """(tensor to keep alive, pointer, bytes) of a workspace given or made."""
     if workspace is None:
@@ -1095,14 +1106,9 @@ def tropical_residual_norm_forward(u, r=None, gate=None, post=None, post_gamma=N
     if y is not None:
         y, py, ldy = _out_matrix(y, rows, cols, dtype, dev, "y")
     io = [pr, ldr, u.data_ptr(), ldu, ph, ldh, py, ldy]
-    stats = []
-    for norm in (post, pre):
-        for there in (norm == "layer", norm is not None):
-            t = None
-            if there:
-                t = torch.empty_strided((rows,), (1,), dtype=torch.float32, device=dev)
-            stats.append(t)
-            io.append(t.data_ptr() if there else 0)
+    stats = _new_flats((post == "layer", post is not None, pre == "layer", pre is not None), rows, torch.float32, dev)
+    for t in stats:
+        io.append(0 if t is None else t.data_ptr())
     held, alive = [None, None], []
     if hold_u is not None and hold_u is not False:
         held[0] = x = _new_act8(rows, cols, dev) if hold_u is True else hold_u
@@ -1176,7 +1182,10 @@ def tropical_residual_norm_backward(dy, dh, u, h, post_mean=None, post_rstd=None
     if du is not None:
         du, grads[2], grads[3] = _out_matrix(du, rows, cols, dtype, dev, "du")
     if dgate is True:
-        dgate = torch.empty(gate.shape, dtype=gate.dtype, device=dev) if gate is not None else None
+        dgate = None
+        if gate is not None:
+            dgate = (torch.empty_strided((cols,), (1,), dtype=gate.dtype, device=dev) if gate.dim() == 1 else
+                     _new_matrix(*gate.shape, gate.dtype, dev))
     if dgate is not None:
         if gate is None:
             raise ValueError("dgate without a gate")
@@ -1185,17 +1194,19 @@ def tropical_residual_norm_backward(dy, dh, u, h, post_mean=None, post_rstd=None
         flat = dgate.dim() == 1
         grads[4] = _flat(dgate, "dgate", cols, gate.dtype) if flat else dgate.data_ptr()
         grads[5] = cols if flat else _row_stride(dgate, "dgate")
-    weights = [dpost_gamma, dpost_beta, dpre_gamma, dpre_beta]
+    given = (dpost_gamma, dpost_beta, dpre_gamma, dpre_beta)
+    weights = _new_flats([g is True and w is not None for g, w in
+                          zip(given, (post_gamma, post_beta, pre_gamma, pre_beta))], cols, ptype, dev)
     sums = dgate is not None
-    i = 0
-    for w in (post_gamma, post_beta, pre_gamma, pre_beta):
+    for i in range(4):
         g = weights[i]
-        if g is True and w is None:
-            weights[i] = None
-        elif g is not None:
-            sums = True
-            weights[i], grads[6 + i] = _out_flat(g, cols, ptype, dev, "d" + _WEIGHTS[i])
-        i += 1
+        if g is not None:
+            grads[6 + i] = g.data_ptr()
+        elif given[i] is not None and given[i] is not True:
+            weights[i], grads[6 + i] = given[i], _flat(given[i], "d" + _WEIGHTS[i], cols, ptype)
+        else:
+            continue
+        sums = True
     need = 0
     if workspace is None and sums:
         need = _residual_workspace(dt, rows, cols, op.post, op.pre, op.gate_group if gate is not None else None)

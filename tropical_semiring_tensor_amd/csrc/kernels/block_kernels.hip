@@ -63,12 +63,18 @@ TROP_RN_ENTRIES(bf16_f32, bf16, float)
 #define TROP_RN_ROWS(KERNEL, NAME, THREADS, T, TPR, EPT, HELD, PRE, POST, WORK)                              \
     TROP_RN_ENTRY_WAVES(bwd_##KERNEL##_##NAME, THREADS, sizeof(T) == 2 ? 4 : 1,                              \
                         (residual_norm_backward_body<T, TPR, EPT, HELD, PRE, POST, WORK>))
+// c512 ... c8k: by the widest row.  float32 rows of 512 to 2048 columns have twice
+// the threads, 4 elements (one vector, as in bfloat16) to each: a row's way from
+// load to store is shorter and 5 waves fit a SIMD instead of 3 (1537 x 1001 16
+// us against 20, 16384 x 1001 78 against 84, x 2000 alike; 16384 x 500, with two
+// waves to a row for one, 46 against 40).
+#define RN_MORE(T) (sizeof(T) / 2)
 #define TROP_RN_BACKWARD(NAME, T, HELD, PRE, POST)                                                           \
-    TROP_RN_ROWS(wave, NAME, 256, T, 64, 8, HELD, PRE, POST, RN_ALL)                                         \
-    TROP_RN_ROWS(pair, NAME, 128, T, 128, 8, HELD, PRE, POST, RN_ALL)                                        \
-    TROP_RN_ROWS(block, NAME, 256, T, 256, 8, HELD, PRE, POST, RN_ALL)                                       \
-    TROP_RN_ROWS(half, NAME, 512, T, 512, 8, HELD, PRE, POST, RN_ALL)                                        \
-    TROP_RN_ROWS(wide, NAME, 1024, T, 1024, 8, HELD, PRE, POST, RN_ALL)                                      \
+    TROP_RN_ROWS(c512, NAME, 256, T, 64, 8, HELD, PRE, POST, RN_ALL)                                        \
+    TROP_RN_ROWS(c1k, NAME, 128 * RN_MORE(T), T, 128 * RN_MORE(T), 8 / RN_MORE(T), HELD, PRE, POST, RN_ALL) \
+    TROP_RN_ROWS(c2k, NAME, 256 * RN_MORE(T), T, 256 * RN_MORE(T), 8 / RN_MORE(T), HELD, PRE, POST, RN_ALL) \
+    TROP_RN_ROWS(c4k, NAME, 512, T, 512, 8, HELD, PRE, POST, RN_ALL)                                        \
+    TROP_RN_ROWS(c8k, NAME, 1024, T, 1024, 8, HELD, PRE, POST, RN_ALL)                                      \
     TROP_RN_ROWS(rows, NAME, 1024, T, 1024, 16, HELD, PRE, POST, RN_ROWS)                                    \
     TROP_RN_ROWS(sums, NAME, 256, T, 256, 8, HELD, PRE, POST, RN_COLUMNS)
 #define TROP_RN_NORMS(NAME, T, HELD)                                                                         \

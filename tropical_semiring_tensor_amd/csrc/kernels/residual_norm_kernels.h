@@ -23,11 +23,11 @@
 // and h kept in 8 bits, 675 MB each way: forward with a gate and a pre norm
 // 126-137 us (4.9-5.4 TB/s), backward with a post norm as well 131-135 us
 // (5.0-5.2) and 6 us for the parts' sums.  1537 x 1001 float32: forward 9 us (25
-// MB), backward 20 + 6 us (28 MB; 406 parts of four rows, latency).  One row of
+// MB), backward 16 + 6 us (28 MB; 406 parts of four rows, latency).  One row of
 // 4096: 4 us, the way from the load through two norms' reductions to the store.
 //
 // Row groups: forward 16 elements to a thread, which reaches the copy's rate;
-// backward 8, since a thread holds dy, dh, h and u of its next row besides its
+// backward 8 (float32 rows of 512 to 2048 columns 4), since a thread holds dy, dh, h and u of its next row besides its
 // columns' sums: bfloat16 rows then fit 128 registers, four waves to a SIMD
 // (16384 x 4096: 152 us, with three waves 186, before later steps).
 #pragma once

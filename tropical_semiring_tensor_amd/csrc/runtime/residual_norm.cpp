@@ -41,32 +41,29 @@ int64_t gate_group(const trop_residual_norm& op) {
 }
 int64_t gate_rows(const trop_residual_norm& op) { return ceil_div(op.rows, gate_group(op)); }
 
-// Row group of the backward by the columns 8 elements per thread cover;
-// kWide: rows too wide to keep their sums as well; kNarrow: narrower than a
-// vector; kPlain: without a norm.
+// Row group of the backward: 0 to 4 a wave, 128, 256, 512 and 1024 threads of 8
+// columns (float32 1 and 2: twice the threads, 4 columns); kWide: rows too wide
+// to keep their sums as well; kNarrow: narrower than a vector; kPlain: without
+// a norm.
 enum { kRegisters = 5, kWide = 5, kNarrow = 6, kPlain = 7 };
 int backward_group(const trop_residual_norm& op) {
     if (op.cols < 8) return kNarrow;
     if (op.pre == TROP_NORM_NONE && op.post == TROP_NORM_NONE) return kPlain;
-    return op.cols <= TROP_RN_COLS_WAVE    ? 0
-           : op.cols <= TROP_RN_COLS_PAIR  ? 1
-           : op.cols <= TROP_RN_COLS_BLOCK ? 2
-           : op.cols <= TROP_RN_COLS_HALF  ? 3
-           : op.cols <= TROP_RN_COLS_WIDE  ? 4
-                                           : kWide;
+    int group = 0;
+    while (group < kRegisters && op.cols > (TROP_RN_COLS_ALL >> 4) << group) ++group;
+    return group;
 }
 
 // Parts a backward makes at most, by row group: more keep more loads in flight,
 // but each leaves its sums for a second kernel to add.  Rows and sums in 512,
-// 768, 1024 and 2048 parts: 16384 x 1024 bfloat16 68, 56, 48 and 50 us, 16384 x
-// 1000 float32 91, 74, 75 and 82 (two waves to a row); 8192 x 2048 bfloat16 48,
-// 49, 50 and 62 (four); 16384 x 512 26, 27, 28 and 35 (one).  1024 threads to a
-// row fill a CU.  Where the sums have a kernel of their own its blocks of
-// columns make more workgroups.
+// 768, 1024 and 2048 parts: 16384 x 1024 bfloat16 68, 56, 48 and 50 us (two
+// waves to a row); 8192 x 2048 bfloat16 48, 49, 50 and 62 (four); 16384 x 512 26,
+// 27, 28 and 35 (one); 16384 x 1001 float32 in 512 and 1024 78 and 87 (four).
+// 1024 threads to a row fill a CU.  Where the sums have a kernel of their own
+// its blocks of columns make more workgroups.
 int64_t most_parts(const trop_residual_norm& op) {
-    static constexpr int64_t parts[] = {512, 1024, 512, 512, 256};
     const int group = backward_group(op);
-    if (group < kRegisters) return parts[group];
+    if (group < kRegisters) return group == 4 ? 256 : group == 1 && op.dtype == TROP_BF16 ? 1024 : 512;
     return std::max<int64_t>(128, 1024 / ceil_div(std::max<int64_t>(op.cols, 1), TROP_RN_COLS_SUMS));
 }
 
@@ -394,8 +391,9 @@ trop_status backward(const trop_residual_norm* opp, const trop_residual_norm_kep
         const int norms = pre ? (post && need_u ? 2 : 0) : post && need_u ? 1 : 3;
         if (kind < kRegisters && norms < 3) {
             static const uint32_t threads[] = {256, 128, 256, 512, 1024};
+            const uint32_t more = op.dtype == TROP_F32 && (kind == 1 || kind == 2) ? 2 : 1;
             st = train_launch(dev, (TrainKernelId)(TK_RN_BWD + 12 * kind + 4 * norms + variant), TROP_T_RESIDUAL_BACKWARD,
-                              l.parts.parts, threads[kind], &p, s);
+                              l.parts.parts, threads[kind] * more, &p, s);
         } else {
             p.row_sums = pre && (sum_post || g.dgate.data) ? ws + l.row_sums : nullptr;
             if (g.dr.data || g.du.data || p.row_sums) {

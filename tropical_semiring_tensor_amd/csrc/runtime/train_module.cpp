@@ -83,7 +83,7 @@ const char* const kNames[] = {
 #define TROP_RN_KEPT(KERNEL) \
     "trop_rn_bwd_" KERNEL "_f32", "trop_rn_bwd_" KERNEL "_bf16", "trop_rn_bwd_" KERNEL "_f32_held8", \
     "trop_rn_bwd_" KERNEL "_bf16_held8",
-    TROP_RN_NORMS("wave") TROP_RN_NORMS("pair") TROP_RN_NORMS("block") TROP_RN_NORMS("half") TROP_RN_NORMS("wide")
+    TROP_RN_NORMS("c512") TROP_RN_NORMS("c1k") TROP_RN_NORMS("c2k") TROP_RN_NORMS("c4k") TROP_RN_NORMS("c8k")
     TROP_RN_NORMS("rows") TROP_RN_NORMS("sums") TROP_RN_KEPT("sums_none")
     TROP_RN_TYPES("bwd_loop", "") TROP_RN_TYPES("bwd_loop", "_held8")
     TROP_RN_TYPES("columns", "") TROP_RN_TYPES("columns", "_held8")

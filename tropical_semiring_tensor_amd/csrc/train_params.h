@@ -122,13 +122,9 @@ struct TropGradWParams {
 };
 
 // ---- between two residual blocks ---------------------------------------------
-// Columns a wave / 128 / 256 / 512 / 1024 threads of the backward hold (8 each).
-#define TROP_RN_COLS_WAVE 512
-#define TROP_RN_COLS_PAIR 1024
-#define TROP_RN_COLS_BLOCK 2048
-#define TROP_RN_COLS_HALF 4096
-#define TROP_RN_COLS_WIDE 8192
-// and 1024 threads of its rows' gradients alone (16 each).
+// Widest row whose sums the backward keeps in registers, and the widest of its
+// rows' gradients alone (1024 threads of 8 and of 16 columns).
+#define TROP_RN_COLS_ALL 8192
 #define TROP_RN_COLS_ROWS 16384
 // Columns of a workgroup of wide rows' sums.
 #define TROP_RN_COLS_SUMS 2048
