@@ -14,8 +14,7 @@
 // step (a 32nd byte each) win back what the power of two costs.
 //
 // Bound by HBM: 16384 x 4096 bfloat16 (203 MB each way) packed in 33 us and
-// unpacked in 31, 6.1 and 6.6 TB/s (42 us right behind the kernel that wrote
-// the codes among much else); 33 x 1000: 4 us each, latency.
+// unpacked in 31, 6.1 and 6.6 TB/s; 33 x 1000: 4 us each, latency.
 #pragma once
 #include "train_common.h"
 
@@ -139,7 +138,10 @@ __device__ __forceinline__ void act8_pack_body(const TropAct8Params& p) {
                         to_float<T, VEC>(v[i]));
 }
 
-// Likewise back; rows and columns past the codes' are written as zeros.
+// Likewise back; rows and columns past the codes' are written as zeros.  Past
+// the caches' reuse order in bfloat16, so that codes just written stay there
+// (16384 x 4096 twice behind a forward: 202 us in all, then 184); not in float32,
+// where rows are not whole lines as often (8192 x 4001: 69 us, 75 so).
 template <typename T>
 __device__ __forceinline__ void act8_unpack_chunk(const TropAct8Params& p, int64_t id) {
     constexpr int VEC = 8, NV = 2;
@@ -155,7 +157,12 @@ __device__ __forceinline__ void act8_unpack_chunk(const TropAct8Params& p, int64
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t c = c0 + (i * 64 + lane) * VEC;
-        if (c < p.cols_x) store_row<T, VEC>(out, c, p.cols_x, from_float<T, VEC>(v[i].values()));
+        if (c >= p.cols_x) continue;
+        const typename VecOf<T, VEC>::raw o = from_float<T, VEC>(v[i].values());
+        if constexpr (sizeof(T) == 2)
+            store_row_stream<T, VEC>(out, c, p.cols_x, o);
+        else
+            store_row<T, VEC>(out, c, p.cols_x, o);
     }
 }
 template <typename T>

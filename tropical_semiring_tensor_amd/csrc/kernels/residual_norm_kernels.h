@@ -21,7 +21,7 @@
 //
 // Measured (one MI355X; a large copy moves 5.0 TB/s): 16384 x 4096 bfloat16, u
 // and h kept in 8 bits, 675 MB each way: forward with a gate and a pre norm
-// 126-137 us (4.9-5.4 TB/s), backward with a post norm as well 131-135 us
+// 119-124 us (5.5-5.7 TB/s), backward with a post norm as well 131-135 us
 // (5.0-5.2) and 6 us for the parts' sums.  1537 x 1001 float32: forward 9 us (25
 // MB), backward 16 + 6 us (28 MB; 406 parts of four rows, latency).  One row of
 // 4096: 4 us, the way from the load through two norms' reductions to the store.
@@ -179,6 +179,9 @@ __device__ __forceinline__ void rn_statistics(const TropResidualParams& p, const
     rstd = 1.0f / sqrtf(s[0] * p.inv_cols + eps);
 }
 
+// Rows are read and written past the caches' reuse order, which leaves the
+// caches to the 8-bit codes that the backward reads (16384 x 4096 bfloat16 with
+// u and h left in 8 bits 137 us, so 124; their unpacking 42 us, so 33).
 template <typename T, typename P, int TPR>
 __device__ __forceinline__ void residual_norm_forward_body(const TropResidualParams& p) {
     constexpr int VEC = ln_vec<T>(), NV = 16 / VEC, RPB = TPR == 64 ? 4 : 1;
@@ -190,11 +193,11 @@ __device__ __forceinline__ void residual_norm_forward_body(const TropResidualPar
     FloatVec<VEC> x[NV], gate[NV];
     const T* u = static_cast<const T*>(p.u) + r * p.ldu;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] = to_float<T, VEC>(load_row<T, VEC>(u, (int64_t)(i * TPR + t) * VEC, p.cols));
+    for (int i = 0; i < NV; ++i) x[i] = to_float<T, VEC>(load_row_stream<T, VEC>(u, (int64_t)(i * TPR + t) * VEC, p.cols));
     if (p.r) {
         const T* res = static_cast<const T*>(p.r) + r * p.ldr;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) raw[i] = load_row<T, VEC>(res, (int64_t)(i * TPR + t) * VEC, p.cols);
+        for (int i = 0; i < NV; ++i) raw[i] = load_row_stream<T, VEC>(res, (int64_t)(i * TPR + t) * VEC, p.cols);
     }
     const int64_t gate_row = rn_gate_row(p, r);
 #pragma unroll
@@ -246,7 +249,7 @@ __device__ __forceinline__ void residual_norm_forward_body(const TropResidualPar
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = (int64_t)(i * TPR + t) * VEC;
-            if (c < p.cols) store_row<T, VEC>(h, c, p.cols, from_float<T, VEC>(x[i]));
+            if (c < p.cols) store_row_stream<T, VEC>(h, c, p.cols, from_float<T, VEC>(x[i]));
         }
     }
     if (!p.pre) return;
@@ -267,7 +270,7 @@ __device__ __forceinline__ void residual_norm_forward_body(const TropResidualPar
             FloatVec<VEC> o;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) o[e] = __builtin_fmaf((x[i][e] - mean) * rstd, g[e], b[e]);
-            store_row<T, VEC>(y, c, p.cols, from_float<T, VEC>(o));
+            store_row_stream<T, VEC>(y, c, p.cols, from_float<T, VEC>(o));
         }
     }
 }
