@@ -499,6 +499,33 @@ def test_graph_and_streams(tb, cols):
     assert torch.equal(f.y, y) and all(torch.equal(a, b) for a, b in zip([x for x in g if x is not None], want))
 
 
+@pytest.mark.parametrize("cols", [300, 2000, 9000])
+def test_calls_at_once_on_two_streams(tb, cols):
+    """Forward, backward and weight gradient of different inputs, issued in turn
+    to two streams without a wait between them, against one after another."""
+    problems = [Problem(200, cols, BF16, F32, "rms", "layer", gates=g, seed=g) for g in (2, 200)]
+
+    def step(q):
+        f = tb.tropical_residual_norm_forward(q.u, q.r, **q.op, hold_u=True, hold_h=True)
+        stats = {k: getattr(f, k) for k in ("post_rstd", "pre_mean", "pre_rstd")}
+        g = tb.tropical_residual_norm_backward(q.dy, q.dh, f.u8, f.h8, **stats, **q.op)
+        return [f.h, f.y, *(x for x in g if x is not None), tb.tropical_act8_linear_grad_w(q.dy, f.u8)]
+
+    want = [step(q) for q in problems]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for k, q in enumerate(problems):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(step(q))
+    for s in streams:
+        s.synchronize()
+    for k in range(2):
+        for out in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[k]))
+
+
 def test_offsets_past_32_bits(tb):
     """Rows that lie more than 2^31 elements apart."""
     ld = (1 << 31) + 64
