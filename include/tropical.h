@@ -497,9 +497,10 @@ TROP_API trop_status tropical_tree_describe(trop_tree_plan plan, char* buf, size
  * >= the row's length (in elements); every element alignment is served.
  * Outputs must not overlap inputs or each other unless stated.  No kernel
  * uses atomics: a call gives the same bits every time on one device model.
- * Their kernels are code objects of their own, loaded once per device by
- * the first such call (or tropical_train_init, which code that captures
- * graphs calls beforehand).
+ * Their kernels are two code objects of their own (layer norm, cross entropy and
+ * AdamW; 8-bit activations and residual norms), each loaded once per device by
+ * the first call of its operators (or both by tropical_train_init, which code
+ * that captures graphs calls beforehand).
  */
 TROP_API trop_status tropical_train_init(int device);
 

@@ -9,11 +9,15 @@ most 3 tokens / 32 + 32 + 32 roundings, each at most 2 u (the instruction's
 own sums may truncate); the result's rounding to its type follows.
 """
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 DEV = "cuda:0"
 U = 2.0 ** -24
 F32, BF16 = torch.float32, torch.bfloat16
@@ -264,6 +268,27 @@ def test_graph_and_streams(tb):
     out = tb.tropical_act8_linear_grad_w(dz, out8, stream=side)
     side.synchronize()
     assert torch.equal(out, gw)
+
+
+def test_each_code_object_is_loaded_by_its_first_call():
+    """A layer norm loads its own code object, 8-bit activations theirs."""
+    program = """
+import torch
+from tropical_semiring_tensor_amd import binding as tb
+x = torch.randn(4, 64, device="cuda:0")
+loads = [tb.tropical_get_train_stats()["module_loads"]]
+tb.tropical_layer_norm_forward(x)
+loads.append(tb.tropical_get_train_stats()["module_loads"])
+for _ in range(2):
+    tb.tropical_act8_pack(x)
+    loads.append(tb.tropical_get_train_stats()["module_loads"])
+tb.tropical_train_init(0)
+loads.append(tb.tropical_get_train_stats()["module_loads"])
+torch.cuda.synchronize()
+print("LOADS", *loads)
+"""
+    out = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, timeout=110, cwd=ROOT)
+    assert out.returncode == 0 and "LOADS 0 1 2 2 2" in out.stdout, out.stdout + out.stderr
 
 
 def test_offsets_past_32_bits(tb):

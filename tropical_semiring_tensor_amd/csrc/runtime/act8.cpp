@@ -38,7 +38,7 @@ trop_status pack_or_unpack(bool pack, trop_dtype dt, const void* x, int64_t ldx,
     if (rows < 0 || cols < 0) return fail(TROP_ERR_INVALID_ARGUMENT, "negative size");
     if (rows == 0 || cols == 0) return ok();
     int dev = -1;
-    trop_status st = train_device(&dev);
+    trop_status st = block_device(&dev);
     if (st != TROP_OK) return st;
     SpanChecker checker(dev);
     if ((st = checker.matrix(x, rows, cols, ldx, elem_size(dt), pack ? "x" : "out")) != TROP_OK) return st;
@@ -167,7 +167,7 @@ trop_status grad_w(trop_dtype dt, const void* dz, int64_t lddz, const trop_act8*
     if (!x) return fail(TROP_ERR_INVALID_ARGUMENT, "trop_act8 is NULL");
     if (cols == 0 || outs == 0) return ok();
     int dev = -1;
-    if ((st = train_device(&dev)) != TROP_OK) return st;
+    if ((st = block_device(&dev)) != TROP_OK) return st;
     const size_t eb = elem_size(dt);
     SpanChecker checker(dev);
     if (tokens > 0) {

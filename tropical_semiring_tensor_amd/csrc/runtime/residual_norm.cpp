@@ -176,7 +176,7 @@ trop_status forward(const trop_residual_norm* opp, const trop_residual_norm_rows
     if (y.data && op.pre == TROP_NORM_NONE) return invalid("y without a norm before the next block");
     if (op.rows == 0 || op.cols == 0) return ok();
     int dev = -1;
-    if ((st = train_device(&dev)) != TROP_OK) return st;
+    if ((st = block_device(&dev)) != TROP_OK) return st;
     SpanChecker checker(dev);
     TropResidualParams p = {};
     if ((st = common(op, checker, p)) != TROP_OK) return st;
@@ -282,7 +282,7 @@ trop_status backward(const trop_residual_norm* opp, const trop_residual_norm_kep
     const bool params = g.dpre_gamma || g.dpre_beta || g.dpost_gamma || g.dpost_beta;
     if (op.cols == 0 || (!params && (op.rows == 0 || (!g.dr.data && !g.du.data && !g.dgate.data)))) return ok();
     int dev = -1;
-    if ((st = train_device(&dev)) != TROP_OK) return st;
+    if ((st = block_device(&dev)) != TROP_OK) return st;
     const size_t pb = elem_size(op.param_dtype);
     SpanChecker checker(dev);
     TropResidualParams p = {};

@@ -61,8 +61,10 @@ enum TrainKernelId : int {
     TK_COUNT = TK_RN_COLUMNS + 6
 };
 
-// Current device with the training code object loaded on it.
+// Current device with the code object of layer norm, cross entropy and AdamW
+// loaded on it, or that of the kernels from TK_ACT8_PACK on.
 trop_status train_device(int* dev);
+trop_status block_device(int* dev);
 trop_status train_launch(int dev, TrainKernelId id, trop_train_family fam, int64_t grid, uint32_t block,
                          const void* params, hipStream_t stream);
 // Workgroups of `block` threads that one launch may have.
@@ -94,7 +96,7 @@ class SpanChecker {
    private:
     int dev_;
     static constexpr int kRanges = 8;
-    int found_ = 0;  // ranges looked up, the first kRanges of them kept
+    int found_ = 0;  // ranges looked up, the last kRanges of them kept
     uintptr_t lo_[kRanges], hi_[kRanges];
 };
 

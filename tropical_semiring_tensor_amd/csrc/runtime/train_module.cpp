@@ -1,6 +1,7 @@
-// The training operators' code objects: loaded once per process and device by
-// the first training call, apart from the contraction's, so that programs
-// that only contract never load them.  Launches and loads are counted here.
+// The training operators' code objects: each loaded once per process and device
+// by the first call of its operators, apart from the contraction's, so that
+// programs that only contract never load them.  Launches and loads are counted
+// here.
 #include <atomic>
 #include <cstring>
 #include <mutex>
@@ -94,8 +95,8 @@ const char* const kNames[] = {
 static_assert(sizeof(kNames) / sizeof(kNames[0]) == TK_COUNT, "training kernels");
 
 struct TrainModule {
-    hipModule_t module[2] = {};
-    hipFunction_t fn[TK_COUNT] = {};
+    std::atomic<bool> loaded[2] = {};
+    hipFunction_t fn[TK_COUNT] = {};  // of the objects that are loaded
 };
 
 std::mutex g_mu;
@@ -103,50 +104,49 @@ std::atomic<TrainModule*> g_dev[kMaxDevices];
 std::atomic<uint64_t> g_loads{0}, g_total{0};
 std::atomic<uint64_t> g_launches[TROP_T_FAMILIES];
 
-trop_status load(int dev) {
+// Object 0: kernels below TK_ACT8_PACK, 1: from it on.
+trop_status load(int dev, int object) {
     if (dev < 0 || dev >= kMaxDevices) return fail(TROP_ERR_INVALID_ARGUMENT, "device index out of range");
-    if (g_dev[dev].load(std::memory_order_acquire)) return TROP_OK;
+    TrainModule* m = g_dev[dev].load(std::memory_order_acquire);
+    if (m && m->loaded[object].load(std::memory_order_acquire)) return TROP_OK;
     std::lock_guard<std::mutex> lock(g_mu);
-    if (g_dev[dev].load(std::memory_order_acquire)) return TROP_OK;
-    TrainModule* m = new TrainModule;
-    const unsigned char* const objects[] = {trop_train_code_object, trop_block_code_object};
-    trop_status st = TROP_OK;
-    for (int k = 0; k < 2 && st == TROP_OK; ++k) {
-        hipError_t e = hipModuleLoadData(&m->module[k], objects[k]);
+    m = g_dev[dev].load(std::memory_order_acquire);
+    if (!m) {
+        m = new TrainModule;
+        g_dev[dev].store(m, std::memory_order_release);
+    }
+    if (m->loaded[object].load(std::memory_order_acquire)) return TROP_OK;
+    hipModule_t module = nullptr;
+    hipError_t e = hipModuleLoadData(&module, object ? trop_block_code_object : trop_train_code_object);
+    if (e != hipSuccess) return hip_fail(e, "hipModuleLoadData (training code object)");
+    g_loads.fetch_add(1);
+    for (int i = object ? TK_ACT8_PACK : 0; i < (object ? TK_COUNT : TK_ACT8_PACK); ++i) {
+        e = hipModuleGetFunction(&m->fn[i], module, kNames[i]);
         if (e != hipSuccess) {
-            m->module[k] = nullptr;
-            st = hip_fail(e, "hipModuleLoadData (training code object)");
-            break;
-        }
-        g_loads.fetch_add(1);
-        for (int i = k ? TK_ACT8_PACK : 0; i < (k ? TK_COUNT : TK_ACT8_PACK) && st == TROP_OK; ++i) {
-            e = hipModuleGetFunction(&m->fn[i], m->module[k], kNames[i]);
-            if (e != hipSuccess) st = hip_fail(e, kNames[i]);
+            (void)hipModuleUnload(module);
+            return hip_fail(e, kNames[i]);
         }
     }
-    if (st != TROP_OK)
-        for (hipModule_t module : m->module)
-            if (module) (void)hipModuleUnload(module);
-    if (st != TROP_OK) {
-        delete m;
-        return st;
-    }
-    g_dev[dev].store(m, std::memory_order_release);
+    m->loaded[object].store(true, std::memory_order_release);
     return TROP_OK;
+}
+
+trop_status device(int* dev, int object) {
+    hipError_t e = hipGetDevice(dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    return load(*dev, object);
 }
 
 }  // namespace
 
-trop_status train_device(int* dev) {
-    hipError_t e = hipGetDevice(dev);
-    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-    return load(*dev);
-}
+trop_status train_device(int* dev) { return device(dev, 0); }
+trop_status block_device(int* dev) { return device(dev, 1); }
 
 trop_status train_launch(int dev, TrainKernelId id, trop_train_family fam, int64_t grid, uint32_t block,
                          const void* params, hipStream_t stream) {
     TrainModule* m = g_dev[dev].load(std::memory_order_acquire);
-    if (!m) return fail(TROP_ERR_HIP, "training code object not loaded on this device");
+    if (!m || !m->loaded[id >= TK_ACT8_PACK].load(std::memory_order_acquire))
+        return fail(TROP_ERR_HIP, "training code object not loaded on this device");
     if (grid <= 0) return TROP_OK;
     if (grid > max_groups(block))
         return fail(TROP_ERR_INVALID_ARGUMENT, std::string(kNames[id]) + ": too many workgroups");
@@ -207,7 +207,8 @@ extern "C" trop_status tropical_train_init(int device) {
         e = hipGetDevice(&cur);
         if (e == hipSuccess && cur != device) e = hipSetDevice(device);
         if (e != hipSuccess) return hip_fail(e, "hipSetDevice");
-        const trop_status st = load(device);
+        trop_status st = load(device, 0);
+        if (st == TROP_OK) st = load(device, 1);
         if (cur != device) (void)hipSetDevice(cur);
         return st == TROP_OK ? ok() : st;
     });
