@@ -27,9 +27,10 @@
 // 4096: 4 us, the way from the load through two norms' reductions to the store.
 //
 // Row groups: forward 16 elements to a thread, which reaches the copy's rate;
-// backward 8 (float32 rows of 512 to 2048 columns 4), since a thread holds dy, dh, h and u of its next row besides its
-// columns' sums: bfloat16 rows then fit 128 registers, four waves to a SIMD
-// (16384 x 4096: 152 us, with three waves 186, before later steps).
+// backward 8 (float32 rows of 512 to 2048 columns 4), since a thread holds dy,
+// dh, h and u of its next row besides its columns' sums: bfloat16 rows then fit
+// 128 registers, four waves to a SIMD (16384 x 4096: 152 us, with three waves
+// 186, before later steps).
 #pragma once
 #include "act8_kernels.h"
 #include "layer_norm_kernels.h"
