@@ -840,10 +840,12 @@ TROP_API trop_status tropical_residual_norm_forward(const trop_residual_norm* op
  * dy: needed with a pre norm, not there without one.  dh: may be left out
  * with a pre norm.  dr, du, dgate (of gate_dtype, gate_rows x cols) and the
  * gradients of gamma and beta (param_dtype): each may be NULL (not computed).
- * With rows == 0 the gradients of gamma and beta are zero.  All sums over rows
- * are added in a fixed order.  Where an element is not finite, what depends on
- * it (its row of dr and du, its column's sums, the row's every column with a
- * norm) may be NaN even where the formula gives an infinity.
+ * With rows == 0 the gradients of gamma and beta are zero; there is no gate row
+ * then, so dgate is not written (a caller that keeps a gate vector for all rows
+ * clears its gradient).  All sums over rows are added in a fixed order.  Where
+ * an element is not finite, what depends on it (its row of dr and du, its
+ * column's sums, the row's every column with a norm) may be NaN even where the
+ * formula gives an infinity.
  * workspace: at least tropical_residual_norm_backward_workspace_size bytes
  *   (NULL when only dr and du are asked for), used only by work on `stream`.
  * Errors: as the forward, and TROP_ERR_WORKSPACE_TOO_SMALL.

@@ -197,6 +197,21 @@ def test_binding_checks(tb):
         tb.tropical_act8_linear_grad_w(x.half(), tb.Act8(codes, exps))
 
 
+@pytest.mark.parametrize("shape,kw", [((64,), {}), ((3, 64), dict(gate_group=5)), ((0, 64), {})])
+def test_gate_gradient_without_rows(tb, monkeypatch, shape, kw):
+    """An empty batch: the library has no gate row to write, the gradient of a
+    gate that is there all the same is zero.  Asked for alone, which needs no
+    device."""
+    monkeypatch.setattr(tb, "_stream_ptr", lambda stream, t: None)
+    x, gate = torch.zeros(0, 64), torch.ones(shape)
+    others = dict(dr=None, du=None, dpost_gamma=None, dpost_beta=None, dpre_gamma=None, dpre_beta=None)
+    for dgate in (torch.full(shape, 5.0), torch.full(shape, math.nan)):
+        g = tb.tropical_residual_norm_backward(x, x, x, x, gate=gate, dgate=dgate, **others, **kw)
+        assert g.gate is dgate and bool((dgate == 0).all())
+    g = tb.tropical_residual_norm_backward(x, x, x, x, gate=gate, **others, **kw)
+    assert g.gate.shape == gate.shape and bool((g.gate == 0).all())
+
+
 def test_code_object_is_gfx950_only():
     import os
 

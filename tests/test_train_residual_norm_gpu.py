@@ -403,6 +403,35 @@ def test_no_rows(tb):
         assert all((t == 0).all() for t in out) and g.r.shape == (rows, cols)
 
 
+@pytest.mark.parametrize("cols", [5, 40, 9000])
+@pytest.mark.parametrize("gates,group", [(1, None), (3, 7)])
+@pytest.mark.parametrize("post", [None, "layer"])
+def test_gate_gradient_without_rows(tb, cols, gates, group, post):
+    """Zeros for every gate row that is there, as for the weights, asked for
+    with them or alone, and on a stream of its own."""
+    q = Problem(0, cols, F32, F32, post, "rms", gates=0)
+    gate = torch.ones(gates, cols, device=DEV)
+    q.op["gate"] = gate if group else gate[0]
+    if group:
+        q.op["gate_group"] = group
+    f = tb.tropical_residual_norm_forward(q.u, q.r, **q.op)
+    stats = {k: getattr(f, k) for k in ("post_mean", "post_rstd", "pre_rstd")}
+    names = ["dr", "du", "dpost_gamma", "dpost_beta", "dpre_gamma", "dpre_beta"]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for kw in ({}, {n: None for n in names}, dict(stream=side)):
+        dgate = torch.full_like(q.op["gate"], math.nan)
+        side.wait_stream(torch.cuda.current_stream())
+        g = tb.tropical_residual_norm_backward(q.dy, q.dh, q.u, f.h, **stats, **q.op, dgate=dgate, **kw)
+        side.synchronize()
+        assert g.gate is dgate and (dgate == 0).all()
+        assert all(x is None or (x == 0).all() for x in g[3:])
+    # allocated by the call, in memory that held something else
+    torch.full_like(q.op["gate"], math.nan)
+    g = tb.tropical_residual_norm_backward(q.dy, q.dh, q.u, f.h, **stats, **q.op)
+    assert g.gate.shape == q.op["gate"].shape and (g.gate == 0).all()
+
+
 @pytest.mark.parametrize("rows,cols,gates", [(2049, 24, 1), (700, 520, 700), (300, 4096, 3), (90, 8192, 1), (50, 9000, 5)])
 def test_the_same_bits_every_time(tb, rows, cols, gates):
     q = Problem(rows, cols, BF16, F32, "rms", "rms", gates)

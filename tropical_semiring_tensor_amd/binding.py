@@ -1141,7 +1141,8 @@ def tropical_residual_norm_backward(dy, dh, u, h, post_mean=None, post_rstd=None
     (Act8), each None where it is not needed.  The statistics, weights, gate
     and scales are the forward's.  dr, du: True to allocate, a tensor to fill,
     None to skip; the others likewise, True meaning where the forward had that
-    weight or gate.  The workspace is allocated with torch when not given.
+    weight or gate.  Without rows the gradients of weights and gate are zeros.
+    The workspace is allocated with torch when not given.
     Returns a ResidualNormGrads.
     """
     lead = dy if dy is not None else dh
@@ -1215,6 +1216,9 @@ def tropical_residual_norm_backward(dy, dh, u, h, post_mean=None, post_rstd=None
                                                _stream_ptr(None, lead))
     if st != OK:
         _check(st, "tropical_residual_norm_backward")
+    if rows == 0 and dgate is not None:
+        # (no row has a gate row: the call wrote none of those that are there)
+        dgate.detach().zero_()
     return ResidualNormGrads(dr, du, dgate, *weights)
 
 
