@@ -212,6 +212,26 @@ def test_gate_gradient_without_rows(tb, monkeypatch, shape, kw):
     assert g.gate.shape == gate.shape and bool((g.gate == 0).all())
 
 
+@pytest.mark.parametrize("gates", [1, 3])
+def test_gate_rows_without_rows(tb, monkeypatch, gates):
+    """Gate rows whose batch is empty are taken as a gate vector is: each is for
+    none of the rows."""
+    monkeypatch.setattr(tb, "_stream_ptr", lambda stream, t: None)
+    x, gate = torch.zeros(0, 64), torch.ones(gates, 64)
+    f = tb.tropical_residual_norm_forward(x, x, gate=gate, post="rms")
+    assert f.h.shape == f.y.shape == x.shape
+    others = dict(dr=None, du=None, dpost_gamma=None, dpost_beta=None, dpre_gamma=None, dpre_beta=None)
+    g = tb.tropical_residual_norm_backward(x, x, x, x, gate=gate, dgate=torch.full((gates, 64), 5.0), **others)
+    assert bool((g.gate == 0).all())
+    # a width or a group that no batch has is refused all the same
+    for kw in (dict(gate=torch.ones(gates, 63)), dict(gate=gate, gate_group=0)):
+        with pytest.raises(ValueError):
+            tb.tropical_residual_norm_forward(x, x, **kw)
+    # and so are gate rows that do not divide the rows there are
+    with pytest.raises(ValueError):
+        tb.tropical_residual_norm_forward(torch.zeros(gates + 1, 64), gate=torch.ones(gates + 2, 64))
+
+
 def test_code_object_is_gfx950_only():
     import os
 

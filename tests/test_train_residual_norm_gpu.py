@@ -432,6 +432,19 @@ def test_gate_gradient_without_rows(tb, cols, gates, group, post):
     assert g.gate.shape == q.op["gate"].shape and (g.gate == 0).all()
 
 
+@pytest.mark.parametrize("gates", [1, 3])
+def test_gate_rows_without_rows(tb, gates):
+    """Gate rows whose batch is empty: outputs of no rows, gradients of zeros."""
+    q = Problem(0, 40, F32, F32, "layer", "rms", gates=0)
+    q.op["gate"] = torch.ones(gates, 40, device=DEV)
+    f = tb.tropical_residual_norm_forward(q.u, q.r, **q.op)
+    assert f.h.shape == f.y.shape == (0, 40)
+    stats = {k: getattr(f, k) for k in ("post_mean", "post_rstd", "pre_rstd")}
+    g = tb.tropical_residual_norm_backward(q.dy, q.dh, q.u, f.h, **stats, **q.op,
+                                           dgate=torch.full((gates, 40), math.nan, device=DEV))
+    assert g.r.shape == (0, 40) and all((x == 0).all() for x in g[2:] if x is not None)
+
+
 @pytest.mark.parametrize("rows,cols,gates", [(2049, 24, 1), (700, 520, 700), (300, 4096, 3), (90, 8192, 1), (50, 9000, 5)])
 def test_the_same_bits_every_time(tb, rows, cols, gates):
     q = Problem(rows, cols, BF16, F32, "rms", "rms", gates)

@@ -1059,8 +1059,8 @@ def _residual_op(dt, rows, cols, gate, gate_group, post, post_gamma, post_beta, 
             pg, ldg, group = gate.data_ptr(), _row_stride(gate, "gate"), gate_group
             gates, width = gate.shape
             if group is None:
-                group = rows // gates if gates else 1
-                if gates * group != rows:
+                group = rows // gates if rows and gates else 1
+                if rows and gates * group != rows:
                     raise ValueError(f"{gates} gate rows do not divide {rows} rows: give gate_group")
             if group < 1 or width != cols or (rows and gates != -(-rows // group)):
                 raise ValueError(f"gate must have a row of {cols} for each {group} of {rows} rows")
