@@ -232,6 +232,30 @@ def test_gate_rows_without_rows(tb, monkeypatch, gates):
         tb.tropical_residual_norm_forward(torch.zeros(gates + 1, 64), gate=torch.ones(gates + 2, 64))
 
 
+@pytest.mark.parametrize("n", [0, 1, 5, 64])
+@pytest.mark.parametrize("there", [(True, True, True, True), (True, False, True, True), (False, True, False, True)])
+def test_new_vectors_are_tensors_of_their_own(tb, there, n):
+    """Vectors that a call allocates together: no views of one another's matrix,
+    so each may be changed in place, by what needs a gradient too, while
+    another is kept for a backward."""
+    v = tb._new_flats(there, n, F32, torch.device("cpu"))
+    assert [t is not None for t in v] == list(there)
+    v = [t for t in v if t is not None]
+    for k, t in enumerate(v):
+        assert t.shape == (n,) and t.is_contiguous() and t.dtype == F32 and not t._is_view()
+        t.fill_(float(k))
+    assert all(bool((t == k).all()) for k, t in enumerate(v))
+    a = torch.ones(n, requires_grad=True)
+    kept = v[0].clone()
+    out = (a * v[0]).sum()
+    for t in v[1:]:
+        t.zero_()
+    out.backward()
+    assert torch.equal(a.grad, kept)
+    v[1].add_(torch.ones(n, requires_grad=True))
+    assert v[1].requires_grad and not v[0].requires_grad
+
+
 def test_code_object_is_gfx950_only():
     import os
 

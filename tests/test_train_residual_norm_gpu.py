@@ -445,6 +445,26 @@ def test_gate_rows_without_rows(tb, gates):
     assert g.r.shape == (0, 40) and all((x == 0).all() for x in g[2:] if x is not None)
 
 
+@pytest.mark.parametrize("cols", [33, 1001, 9000])
+def test_vectors_changed_in_place(tb, cols):
+    """Statistics and weight gradients are tensors of their own: one changed in
+    place, by what needs a gradient too, leaves the others and what autograd
+    kept of them."""
+    q = Problem(12, cols, F32, F32, "layer", "layer", gates=1)
+    f = check_forward(tb, q)
+    g = check_backward(tb, q, f)
+    for vectors in (f[2:6], g[3:]):
+        want = [t.clone() for t in vectors]
+        a = torch.ones_like(vectors[1], requires_grad=True)
+        out = (a * vectors[1]).sum()
+        vectors[0].add_(torch.ones_like(vectors[0], requires_grad=True))
+        vectors[2].zero_()
+        out.backward()
+        assert torch.equal(a.grad, want[1]) and torch.equal(vectors[1], want[1]) and torch.equal(vectors[3], want[3])
+        assert torch.equal(vectors[0], want[0] + 1) and (vectors[2] == 0).all()
+        assert [t.requires_grad for t in vectors] == [True, False, False, False]
+
+
 @pytest.mark.parametrize("rows,cols,gates", [(2049, 24, 1), (700, 520, 700), (300, 4096, 3), (90, 8192, 1), (50, 9000, 5)])
 def test_the_same_bits_every_time(tb, rows, cols, gates):
     q = Problem(rows, cols, BF16, F32, "rms", "rms", gates)

@@ -635,12 +635,13 @@ def _out_flat(t, n, dtype, device, what):
 
 def _new_flats(there, n, dtype, device):
     """A new vector of n elements for each that is there, None for the others;
-    of several the rows of one matrix (four vectors 2.9 us of host time against
-    4.8)."""
+    of several one after another in one allocation (four vectors 3.2 us of host
+    time against 5.0).  unsafe_chunk makes them tensors of their own: views of
+    one matrix would share its version, and refuse some changes in place."""
     count = sum(there)
     if count > 2:
-        rows = iter(torch.empty_strided((count, n), (max(n, 1), 1), dtype=dtype, device=device).unbind(0))
-        return [next(rows) if t else None for t in there]
+        parts = iter(torch.unsafe_chunk(torch.empty_strided((count * n,), (1,), dtype=dtype, device=device), count))
+        return [next(parts) if t else None for t in there]
     return [torch.empty_strided((n,), (1,), dtype=dtype, device=device) if t else None for t in there]
 
 
@@ -1084,7 +1085,9 @@ def tropical_residual_norm_forward(u, r=None, gate=None, post=None, post_gamma=N
     gate_group consecutive rows (rows / gates when not given), float32 or u's
     type.  h, y: True to allocate, a tensor to fill (h may be r), None to skip.
     hold_u, hold_h: also leave u and h in 8 bits (True, or an Act8 to fill).
-    Returns a ResidualNorm; what there is none of is None.
+    Returns a ResidualNorm; what there is none of is None.  Statistics that the
+    call allocates lie one after another in one allocation, which lives as long
+    as any of them.
     """
     dt = _tdt(u, "u")
     ldu = _row_stride(u, "u")
@@ -1142,7 +1145,9 @@ def tropical_residual_norm_backward(dy, dh, u, h, post_mean=None, post_rstd=None
     and scales are the forward's.  dr, du: True to allocate, a tensor to fill,
     None to skip; the others likewise, True meaning where the forward had that
     weight or gate.  Without rows the gradients of weights and gate are zeros.
-    The workspace is allocated with torch when not given.
+    Gradients of gamma and beta that the call allocates lie one after another in
+    one allocation, which lives as long as any of them.  The workspace is
+    allocated with torch when not given.
     Returns a ResidualNormGrads.
     """
     lead = dy if dy is not None else dh
