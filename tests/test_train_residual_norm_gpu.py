@@ -391,6 +391,28 @@ def test_non_finite_rows_stay_apart(tb, cols, bad):
     assert torch.equal(g.pre_beta[only], clean.pre_beta[only]) and not torch.isfinite(g.pre_beta[1])
 
 
+@pytest.mark.parametrize("cols", [50, 3000, 9000, 20000])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_non_finite_rows_whole(tb, cols, bad):
+    """What a non-finite element makes of its own row.  In u before a layer norm
+    it makes the mean and all of the row NaN.  In r before an RMS norm a NaN does
+    so too; an infinity makes rstd 0, its own y NaN and the others beta."""
+    q = Problem(8, cols, F32, F32, "layer", "rms", gates=1)
+    clean = tb.tropical_residual_norm_forward(q.u, q.r, **q.op)
+    q.u[2, cols // 2] = bad
+    q.r[5, 0] = bad
+    f = tb.tropical_residual_norm_forward(q.u, q.r, **q.op)
+    for t in (f.h, f.y):
+        assert t[2].isnan().all()
+    assert f.post_rstd[2].isnan() and f.pre_rstd[2].isnan() and not torch.isfinite(f.post_mean[2])
+    assert torch.equal(f.post_mean[5], clean.post_mean[5]) and torch.equal(f.post_rstd[5], clean.post_rstd[5])
+    assert torch.equal(f.h[5, 1:], clean.h[5, 1:]) and not torch.isfinite(f.h[5, 0])
+    if math.isnan(bad):
+        assert f.pre_rstd[5].isnan() and f.y[5].isnan().all()
+    else:
+        assert f.pre_rstd[5] == 0 and f.y[5, 0].isnan() and torch.equal(f.y[5, 1:], q.op["pre_beta"][1:])
+
+
 def test_no_rows(tb):
     for rows, cols in ((0, 40), (3, 0), (0, 9000)):
         q = Problem(rows, cols, F32, F32, "layer", "rms", gates=1)
