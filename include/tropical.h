@@ -808,8 +808,8 @@ typedef struct {
  * when pre is TROP_NORM_NONE, which makes no y).  h may be r itself (same
  * stride).  post_mean, post_rstd, pre_mean, pre_rstd: float32, rows elements,
  * each may be NULL; those of a norm that is none, and the mean of an RMS norm,
- * are not written.  u8, h8: u and h in 8 bits for the backward (h before it is
- * rounded to dtype), either may be NULL.
+ * are not written, and with cols == 0 none is.  u8, h8: u and h in 8 bits for the
+ * backward (h before it is rounded to dtype), either may be NULL.
  * Errors: TROP_ERR_INVALID_ARGUMENT, TROP_ERR_NOT_DEVICE_MEMORY, TROP_ERR_HIP.
  */
 typedef struct {

@@ -9,10 +9,14 @@
 // exactly; a tile of x meets the three of dz in turn.
 //
 // Measured (one MI355X): 8192 tokens x 4096 x 16384 bfloat16 841-871 us in all,
-// 20-27 of them unpacking (1.26-1.31 PFLOP/s); call after call on other values,
-// where the clock falls further, 1010-1030, and the library's product of
-// unpacked bfloat16 operands in turn with it 1070-1200.  4096 x 1024 x 4096
-// float32 123-143 us: 27 to unpack and take apart (175 MB), 90 for three products
+// 20-27 of them unpacking (1.26-1.31 PFLOP/s); on other values three calls in a
+// row 1000-1030 and twenty 880-900, the library's product of unpacked bfloat16
+// operands in turn with it 1060-1090 and 930.  Smaller ones are level with that
+// product: 4096 x 4096 x 4096 135-145 us against 139-143, 2048 x 1024 x 1024
+// 19.5-22 against 18-25.  One token x 8192 x 16384: 106 us, float32 215 (the
+// output alone 54 and 108: 64 rows are unpacked, packed and multiplied, and a
+// store writes 32 or 64 bytes of 16 rows).  4096 x 1024 x 4096
+// float32 123-143 us: 27 to unpack and take apart (181 MB), 90 for three products
 // (1.15 PFLOP/s, the matrix units busy half of the cycles: one round of 48 k
 // tiles, with first loads and a last store that nothing hides), 13 to add four
 // parts; the library's float32 product takes 258-290.  Two bfloat16 parts of dz

@@ -180,9 +180,19 @@ __device__ __forceinline__ void rn_statistics(const TropResidualParams& p, const
     rstd = 1.0f / sqrtf(s[0] * p.inv_cols + eps);
 }
 
-// Rows are read and written past the caches' reuse order, which leaves the
-// caches to the 8-bit codes that the backward reads (16384 x 4096 bfloat16 with
-// u and h left in 8 bits 137 us, so 124; their unpacking 42 us, so 33).
+// Rows are read and written past the caches' reuse order: 16384 x 4096 bfloat16
+// with u and h left in 8 bits 137 us otherwise, so 124.  What reads y next may
+// find less of it in the caches.  Streaming stores of h and y against ordinary
+// ones, us, pairs in a graph; alone, then with an elementwise reader of y behind
+// it, then with a product by a square matrix (bfloat16 but for the last):
+//   16384 x 4096, 8 bits left   130 136   184 186   555 558
+//   16384 x 4096                102 100   143 137   529 526
+//   4096 x 4096, 8 bits left     40  39    51  49   149 148
+//   4096 x 4096                  30  31    43  41   141 139
+//   1 x 4096                    3.8 3.8   5.7 5.4    20  20
+//   1537 x 1001 float32         8.0 8.1  11.5 12.5   44  45
+// Ahead where 8-bit rows are left of a large batch and in float32, a few percent
+// behind elsewhere; one form serves all.
 template <typename T, typename P, int TPR>
 __device__ __forceinline__ void residual_norm_forward_body(const TropResidualParams& p) {
     constexpr int VEC = ln_vec<T>(), NV = 16 / VEC, RPB = TPR == 64 ? 4 : 1;

@@ -1,6 +1,6 @@
 // The gfx950 code object of layer norm, cross entropy and AdamW: every kernel
 // entry point.  Built with hipcc --genco and embedded in the library beside the
-// contraction's; loaded once per device by the first training call.
+// contraction's; loaded once per device by the first call of these operators.
 #include "adamw_kernels.h"
 #include "cross_entropy_kernels.h"
 #include "layer_norm_kernels.h"
